@@ -62,6 +62,13 @@ typedef enum {
   PC_PREC_FP32 = 2  /* 3xTF32 products */
 } pc_precision_t;
 
+/* Element type of the activations and matrices of the factor network's operators
+ * (layer norm, linear attention, orthogonalised updates). */
+typedef enum {
+  PC_F32 = 0, /* float32 */
+  PC_BF16 = 1 /* bfloat16 */
+} pc_dtype_t;
+
 typedef enum {
   PC_OK = 0,
   PC_ERR_NULL = 1,              /* a required pointer is NULL */
@@ -128,7 +135,7 @@ typedef enum {
   PC_KIND_HMM_FWD = 3, PC_KIND_HMM_ELEM = 4, PC_KIND_HMM_PARAM = 5,
   PC_KIND_HCLT_FWD = 6, PC_KIND_HCLT_ELEM = 7, PC_KIND_HCLT_PARAM = 8,
   PC_KIND_LOWRANK_FWD = 9, PC_KIND_LOWRANK_BWD = 10, PC_KIND_EM_MSTEP = 11,
-  PC_KIND_HMM_MEM = 12, PC_KIND_HCLT_MEM = 13
+  PC_KIND_HMM_MEM = 12, PC_KIND_HCLT_MEM = 13, PC_KIND_ORTHOGONALIZE = 14
 } pc_kind_t;
 PCSUM_API pc_status_t pc_profile_start(int capacity);
 PCSUM_API pc_status_t pc_profile_stop(int* count, float* ms, int* kind, long long* flops,
@@ -401,6 +408,104 @@ PCSUM_API pc_status_t pc_hmm_lowrank_fwd_bwd(int H, int T, int V, int B, int K, 
  * nothing is launched then. */
 PCSUM_API pc_status_t pc_em_normalize(int G, int M, int N, const float* F, const float* W, float* theta,
                                       pc_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * The factor network's operators: what a sequence model that supplies the LowRank
+ * factors FA, FB of pc_hmm_lowrank_fwd_bwd from the positions so far is made of, and
+ * what trains it from dFA, dFB. Tensors named "elements" hold pc_dtype_t values
+ * (aligned to their own size); everything else is as its type says. Statistics, states,
+ * sums and parameter gradients are float32 whatever the element type. Offsets are
+ * 64-bit.
+ * ---------------------------------------------------------------------------- */
+
+/* Layer norm of `rows` rows of `dim` elements, row r at r * ld:
+ *   mean = avg(x), rstd = (avg((x - mean)^2) + eps)^(-1/2), y = (x - mean) rstd weight + bias
+ *   x, y (elements)                row strides x_ld, y_ld >= dim; y may be x
+ *   weight, bias [dim]             NULL: 1, 0
+ *   mean, rstd [rows]              outputs, each may be NULL; the backward reads them
+ * rows may be 0. Errors: PC_ERR_UNSUPPORTED (element type), PC_ERR_SHAPE, PC_ERR_NULL,
+ * PC_ERR_ALIGNMENT. Rows of whole 16-byte pieces from 16-byte aligned starts are the fast
+ * case; any other is taken as it comes. */
+PCSUM_API pc_status_t pc_layer_norm_fwd(long long rows, int dim, const void* x, long long x_ld, const float* weight,
+                                        const float* bias, float eps, void* y, long long y_ld, float* mean,
+                                        float* rstd, pc_dtype_t dtype, pc_stream_t stream);
+
+/* Its gradient from the forward's statistics, z = (x - mean) rstd, g = dy weight:
+ *   dx = rstd (g - avg(g) - z avg(g z))       (elements, row stride dx_ld; dx may be dy)
+ *   dweight [dim] = sum_r dy z,  dbias [dim] = sum_r dy
+ * dweight and dbias may be NULL; with accumulate != 0 they are added to. The row sums are
+ * taken in a fixed order: equal inputs give equal bits. Workspace (needed with dweight or
+ * dbias): pc_layer_norm_bwd_workspace bytes, 16-byte aligned. */
+PCSUM_API pc_status_t pc_layer_norm_bwd_workspace(long long rows, int dim, size_t* bytes);
+
+PCSUM_API pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy, long long dy_ld, const void* x,
+                                        long long x_ld, const float* weight, const float* mean, const float* rstd,
+                                        void* dx, long long dx_ld, float* dweight, float* dbias, int accumulate,
+                                        pc_dtype_t dtype, void* ws, size_t ws_bytes, pc_stream_t stream);
+
+/* Linear attention with a decay for each head: for sequence b, head h, l =
+ * exp(log_decay[h]) and n = lengths[b] tokens (T where lengths is NULL; values outside
+ * [0, T] are taken to its ends),
+ *   S_t = l S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t,   t = 1 .. n,  S_0 = state
+ *   q, k (elements) [B][T][H][Dk], v, o (elements) [B][T][H][Dv]
+ *   strides (HOST)                 (batch, token, head) strides in elements, in the order
+ *                                  q, k, v, o; the innermost dimension is contiguous
+ *   log_decay [H]                  <= 0; -inf: only the current token counts
+ *   state [B][H][Dk][Dv]           S_0, NULL: zeros
+ *   state_out [B][H][Dk][Dv]       S_n, NULL: not wanted; may not be `state`
+ * Rows of o past a sequence's length are zero; what q, k and v hold there is not read.
+ * B and T may be 0. Products of bf16 elements are formed on the tensor cores where the
+ * head sizes allow (multiples of 8 up to 128, 16-byte aligned rows): scores and the state
+ * that the queries read are rounded to bf16 there, the state itself is carried in
+ * float32 from products of full precision; otherwise all arithmetic is float32. Equal
+ * inputs give equal bits.
+ * Errors: PC_ERR_UNSUPPORTED (element type, head sizes above 256, state_out == state),
+ * PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_ALIGNMENT, PC_ERR_WORKSPACE. Workspace:
+ * pc_linear_attention_workspace bytes (may be 0), 16-byte aligned. */
+PCSUM_API pc_status_t pc_linear_attention_workspace(int B, int T, int H, int Dk, int Dv, int with_backward,
+                                                    pc_dtype_t dtype, size_t* bytes);
+
+PCSUM_API pc_status_t pc_linear_attention_fwd(int B, int T, int H, int Dk, int Dv, const void* q, const void* k,
+                                              const void* v, const long long* strides, const float* log_decay,
+                                              float scale, const float* state, const int32_t* lengths, void* o,
+                                              float* state_out, pc_dtype_t dtype, void* ws, size_t ws_bytes,
+                                              pc_stream_t stream);
+
+/* Its gradients (the decay is a constant of the model), given do and, optionally, the
+ * gradient dstate_out of S_n (NULL: zeros):
+ *   dq, dk, dv (elements), rows past a sequence's length zero
+ *   dstate [B][H][Dk][Dv]          gradient of S_0, NULL: not wanted; may not be dstate_out
+ *   strides (HOST)                 as above, in the order q, k, v, do, dq, dk, dv
+ * The states are computed again from q, k, v: the forward keeps nothing. */
+PCSUM_API pc_status_t pc_linear_attention_bwd(int B, int T, int H, int Dk, int Dv, const void* q, const void* k,
+                                              const void* v, const void* d_o, const long long* strides,
+                                              const float* log_decay, float scale, const float* state,
+                                              const float* dstate_out, const int32_t* lengths, void* dq, void* dk,
+                                              void* dv, float* dstate, pc_dtype_t dtype, void* ws, size_t ws_bytes,
+                                              pc_stream_t stream);
+
+/* One token of each sequence, the state updated in place (float32 arithmetic):
+ *   q, k (elements) [B][H][Dk], v, o (elements) [B][H][Dv]; strides (HOST): (batch, head)
+ *   in the order q, k, v, o; state [B][H][Dk][Dv]. */
+PCSUM_API pc_status_t pc_linear_attention_step(int B, int H, int Dk, int Dv, const void* q, const void* k,
+                                               const void* v, const long long* strides, const float* log_decay,
+                                               float scale, float* state, void* o, pc_dtype_t dtype,
+                                               pc_stream_t stream);
+
+/* Orthogonalised update of `batch` matrices G [rows][cols] (elements): X_0 = G / (|G|_F +
+ * eps), then `steps` times A = X X^T, X <- a X + (b A + c A A) X (of the transposed matrix
+ * where rows > cols); out [rows][cols] (elements) = X. a s + b s^3 + c s^5 acts on the
+ * singular values. |G|_F^2 is summed in float32; a matrix of zeros gives zeros.
+ * Precision: PC_PREC_AUTO and PC_PREC_TF32 form every product from operands of 11
+ * significant bits, PC_PREC_FP32 from operands of 22 (hi + lo); float32 accumulation.
+ * out may be G. G and out are 16-byte aligned. Errors: PC_ERR_UNKNOWN_PRECISION,
+ * PC_ERR_UNSUPPORTED, PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_ALIGNMENT, PC_ERR_WORKSPACE.
+ * Workspace: pc_orthogonalize_workspace bytes, 16-byte aligned. */
+PCSUM_API pc_status_t pc_orthogonalize_workspace(int batch, int rows, int cols, pc_precision_t prec, size_t* bytes);
+
+PCSUM_API pc_status_t pc_orthogonalize(int batch, int rows, int cols, const void* G, int steps, float a, float b,
+                                       float c, float eps, void* out, pc_dtype_t dtype, pc_precision_t prec, void* ws,
+                                       size_t ws_bytes, pc_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,10 +14,16 @@ from .api import (  # noqa: F401
     hclt_prepare,
     hmm_fwd_bwd,
     hmm_lowrank_fwd_bwd,
+    layer_norm_bwd,
+    layer_norm_fwd,
+    linear_attention_bwd,
+    linear_attention_fwd,
+    linear_attention_step,
     lowrank_exp_sum_bwd,
     lowrank_exp_sum_fwd,
     lowrank_sum_exp_bwd,
     lowrank_sum_exp_fwd,
+    orthogonalize,
     precision_code,
     profile_start,
     set_wait_limit_ns,

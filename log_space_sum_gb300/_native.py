@@ -23,6 +23,7 @@ KINDS = {
     0: "layer_fwd", 1: "layer_elem", 2: "layer_param", 3: "hmm_fwd", 4: "hmm_elem",
     5: "hmm_param", 6: "hclt_fwd", 7: "hclt_elem", 8: "hclt_param", 9: "lowrank_fwd",
     10: "lowrank_bwd", 11: "em_mstep", 12: "hmm_mem", 13: "hclt_mem",
+    14: "orthogonalize",
 }
 # kinds whose flops field holds algorithmic bytes
 MEMORY_KINDS = {"em_mstep", "hmm_mem", "hclt_mem"}
@@ -62,6 +63,16 @@ SIGNATURES = {
                                _sz, _p],
     "pc_lowrank_exp_sum_bwd": [_i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _i, _i, _p, _sz,
                                _p],
+    "pc_layer_norm_fwd": [_ll, _i, _p, _ll, _p, _p, _f, _p, _ll, _p, _p, _i, _p],
+    "pc_layer_norm_bwd_workspace": [_ll, _i, _p],
+    "pc_layer_norm_bwd": [_ll, _i, _p, _ll, _p, _ll, _p, _p, _p, _p, _ll, _p, _p, _i, _i, _p, _sz, _p],
+    "pc_linear_attention_workspace": [_i, _i, _i, _i, _i, _i, _i, _p],
+    "pc_linear_attention_fwd": [_i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _f, _p, _p, _p, _p, _i, _p, _sz, _p],
+    "pc_linear_attention_bwd": [_i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _f, _p, _p, _p, _p, _p, _p, _p, _i, _p,
+                                _sz, _p],
+    "pc_linear_attention_step": [_i, _i, _i, _i, _p, _p, _p, _p, _p, _f, _p, _p, _i, _p],
+    "pc_orthogonalize_workspace": [_i, _i, _i, _i, _p],
+    "pc_orthogonalize": [_i, _i, _i, _p, _i, _f, _f, _f, _f, _p, _i, _i, _p, _sz, _p],
 }
 _STR = {"pc_version", "pc_status_string", "pc_last_error"}
 

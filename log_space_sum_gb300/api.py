@@ -408,6 +408,222 @@ def em_normalize(F: torch.Tensor, theta: torch.Tensor, W: torch.Tensor | None = 
     return theta
 
 
+# --------------------------------------------------- the factor network's operators
+# What a sequence model that supplies hmm_lowrank_fwd_bwd's factors FA, FB is made of, and
+# what trains it from dFA, dFB. Elements are float32 or bfloat16.
+DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _elements(t, name, dtype=None, device=None):
+    """An activation: float32 or bfloat16 on the GPU, contiguous along its last dimension."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+    if t.dtype not in DTYPES if dtype is None else t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype or 'torch.float32 or torch.bfloat16'}, got {t.dtype}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return t
+
+
+def _shaped(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t
+
+
+def _rows(t, name):
+    """(rows, row stride) of a tensor seen as rows of its last dimension."""
+    if t.dim() == 2:
+        return t.shape[0], t.stride(0)
+    if t.is_contiguous():
+        return (t.numel() // t.shape[-1] if t.shape[-1] else 0), t.shape[-1]
+    try:
+        flat = t.view(-1, t.shape[-1])
+    except RuntimeError:
+        raise ValueError(f"{name}'s leading dimensions must collapse to rows of one stride") from None
+    return flat.shape[0], flat.stride(0)
+
+
+def _param(t, name, dim, device):
+    if t is not None:
+        _shaped(_check(t, name, device=device), name, (dim,))
+    return t
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rstd=None):
+    """Layer norm over the last dimension (pc_layer_norm_fwd): x [..., D] float32 or
+    bfloat16, rows of any one stride; weight, bias [D] float32 or None. Returns (y, mean,
+    rstd); the statistics [...] are float32 and what layer_norm_bwd reads."""
+    _elements(x, "x")
+    dev, D = x.device, (x.shape[-1] if x.dim() else 0)
+    if D < 1:
+        raise ValueError("x must have a last dimension of at least one")
+    _param(weight, "weight", D, dev)
+    _param(bias, "bias", D, dev)
+    rows, ld = _rows(x, "x")
+    out = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else _shaped(
+        _elements(out, "out", x.dtype, dev), "out", x.shape)
+    lead = x.shape[:-1]
+    mean = torch.empty(lead, dtype=torch.float32, device=dev) if mean is None else _shaped(
+        _check(mean, "mean", device=dev), "mean", lead)
+    rstd = torch.empty(lead, dtype=torch.float32, device=dev) if rstd is None else _shaped(
+        _check(rstd, "rstd", device=dev), "rstd", lead)
+    N.call("pc_layer_norm_fwd", rows, D, _ptr(x), ld, _ptr(weight), _ptr(bias), eps, _ptr(out),
+           _rows(out, "out")[1], _ptr(mean), _ptr(rstd), DTYPES[x.dtype], _stream(dev))
+    return out, mean, rstd
+
+
+def layer_norm_bwd(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, params=True, accumulate=False):
+    """Gradients of layer_norm_fwd (pc_layer_norm_bwd) from its statistics: returns (dx,
+    dweight [D], dbias [D]), the last two float32 sums over all rows (None with ``params``
+    False; added to the given tensors with ``accumulate``)."""
+    _elements(x, "x")
+    dev, D = x.device, (x.shape[-1] if x.dim() else 0)
+    if D < 1:
+        raise ValueError("x must have a last dimension of at least one")
+    _shaped(_elements(dy, "dy", x.dtype, dev), "dy", x.shape)
+    _param(weight, "weight", D, dev)
+    for t, n in ((mean, "mean"), (rstd, "rstd")):
+        _shaped(_check(t, n, device=dev), n, x.shape[:-1])
+    if accumulate and params and (dweight is None or dbias is None):
+        raise ValueError("accumulate needs dweight and dbias to add to")
+    rows, ld = _rows(x, "x")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if dx is None else _shaped(
+        _elements(dx, "dx", x.dtype, dev), "dx", x.shape)
+    ws, nb = None, 0
+    if params:
+        dweight = torch.empty(D, dtype=torch.float32, device=dev) if dweight is None else _param(
+            dweight, "dweight", D, dev)
+        dbias = torch.empty(D, dtype=torch.float32, device=dev) if dbias is None else _param(dbias, "dbias", D, dev)
+        ws = workspace(_query("pc_layer_norm_bwd_workspace", rows, D), dev)
+        nb = ws.numel()
+    else:
+        dweight = dbias = None
+    N.call("pc_layer_norm_bwd", rows, D, _ptr(dy), _rows(dy, "dy")[1], _ptr(x), ld, _ptr(weight), _ptr(mean),
+           _ptr(rstd), _ptr(dx), _rows(dx, "dx")[1], _ptr(dweight), _ptr(dbias), int(bool(accumulate)),
+           DTYPES[x.dtype], _ptr(ws), nb, _stream(dev))
+    return dx, dweight, dbias
+
+
+def _strides(*tensors):
+    flat = [s for t in tensors for s in t.stride()[:-1]]
+    return (C.c_longlong * len(flat))(*flat)
+
+
+def _attention_inputs(q, k, v, log_decay, state, lengths, lead):
+    """Checks of q, k [*lead, H, Dk], v [*lead, H, Dv] and what goes with them."""
+    _elements(q, "q")
+    dev, dt = q.device, q.dtype
+    if q.dim() != lead + 2:
+        raise ValueError(f"q must have {lead + 2} dimensions, got {q.dim()}")
+    H, Dk = q.shape[-2:]
+    _shaped(_elements(k, "k", dt, dev), "k", q.shape)
+    _elements(v, "v", dt, dev)
+    if v.dim() != q.dim() or v.shape[:-1] != q.shape[:-1]:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected {tuple(q.shape[:-1])} and a head size")
+    Dv = v.shape[-1]
+    _shaped(_check(log_decay, "log_decay", device=dev), "log_decay", (H,))
+    if state is not None:
+        _shaped(_check(state, "state", device=dev), "state", (q.shape[0], H, Dk, Dv))
+    if lengths is not None:
+        _shaped(_check(lengths, "lengths", dtype=torch.int32, device=dev), "lengths", (q.shape[0],))
+    return dev, dt, H, Dk, Dv
+
+
+def _given(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _shaped(_elements(t, name, dtype, device), name, shape)
+
+
+def linear_attention_fwd(q, k, v, log_decay, scale=1.0, state=None, lengths=None, out=None, state_out=None):
+    """Linear attention with a decay for each head over whole sequences
+    (pc_linear_attention_fwd): S_t = exp(log_decay) S_{t-1} + k_t v_t^T, o_t = scale q_t^T
+    S_t. q, k [B,T,H,Dk], v [B,T,H,Dv] float32 or bfloat16, any strides with the last
+    dimension contiguous; log_decay [H] <= 0, ``state`` [B,H,Dk,Dv] float32 (None: zeros),
+    ``lengths`` [B] int32 (None: T). Returns (o [B,T,H,Dv], state after each sequence's
+    last token)."""
+    dev, dt, H, Dk, Dv = _attention_inputs(q, k, v, log_decay, state, lengths, 2)
+    B, T = q.shape[:2]
+    out = _given(out, "out", v.shape, dt, dev)
+    if state_out is None:
+        state_out = torch.empty(B, H, Dk, Dv, dtype=torch.float32, device=dev)
+    _shaped(_check(state_out, "state_out", device=dev), "state_out", (B, H, Dk, Dv))
+    code = DTYPES[dt]
+    nb = _query("pc_linear_attention_workspace", B, T, H, Dk, Dv, 0, code)
+    ws = workspace(nb, dev)
+    N.call("pc_linear_attention_fwd", B, T, H, Dk, Dv, _ptr(q), _ptr(k), _ptr(v), _strides(q, k, v, out),
+           _ptr(log_decay), scale, _ptr(state), _ptr(lengths), _ptr(out), _ptr(state_out), code, _ptr(ws),
+           ws.numel(), _stream(dev))
+    return out, state_out
+
+
+def linear_attention_bwd(q, k, v, log_decay, do, scale=1.0, state=None, dstate=None, lengths=None, dq=None, dk=None,
+                         dv=None, dstate_in=None):
+    """Gradients of linear_attention_fwd (pc_linear_attention_bwd) from ``do`` [B,T,H,Dv]
+    and, optionally, ``dstate`` [B,H,Dk,Dv], the gradient of the state it returned. Returns
+    a dict with dq, dk, dv and dstate, the gradient of its initial state. dq, dk, dv may be
+    passed in with any strides (slices of one projection's gradient)."""
+    dev, dt, H, Dk, Dv = _attention_inputs(q, k, v, log_decay, state, lengths, 2)
+    B, T = q.shape[:2]
+    _shaped(_elements(do, "do", dt, dev), "do", v.shape)
+    if dstate is not None:
+        _shaped(_check(dstate, "dstate", device=dev), "dstate", (B, H, Dk, Dv))
+    dq, dk, dv = (_given(t, n, like.shape, dt, dev)
+                  for t, n, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
+    if dstate_in is None:
+        dstate_in = torch.empty(B, H, Dk, Dv, dtype=torch.float32, device=dev)
+    _shaped(_check(dstate_in, "dstate_in", device=dev), "dstate_in", (B, H, Dk, Dv))
+    code = DTYPES[dt]
+    nb = _query("pc_linear_attention_workspace", B, T, H, Dk, Dv, 1, code)
+    ws = workspace(nb, dev)
+    N.call("pc_linear_attention_bwd", B, T, H, Dk, Dv, _ptr(q), _ptr(k), _ptr(v), _ptr(do),
+           _strides(q, k, v, do, dq, dk, dv), _ptr(log_decay), scale, _ptr(state), _ptr(dstate), _ptr(lengths),
+           _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dstate_in), code, _ptr(ws), ws.numel(), _stream(dev))
+    return dict(dq=dq, dk=dk, dv=dv, dstate=dstate_in)
+
+
+def linear_attention_step(q, k, v, log_decay, state, scale=1.0, out=None):
+    """One token of each sequence (pc_linear_attention_step): q, k [B,H,Dk], v [B,H,Dv];
+    ``state`` [B,H,Dk,Dv] float32 is updated in place. Returns o [B,H,Dv]."""
+    dev, dt, H, Dk, Dv = _attention_inputs(q, k, v, log_decay, state, None, 1)
+    if state is None:
+        raise TypeError("state must be a torch.Tensor")
+    out = _given(out, "out", v.shape, dt, dev)
+    N.call("pc_linear_attention_step", q.shape[0], H, Dk, Dv, _ptr(q), _ptr(k), _ptr(v), _strides(q, k, v, out),
+           _ptr(log_decay), scale, _ptr(state), _ptr(out), DTYPES[dt], _stream(dev))
+    return out
+
+
+def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, precision="auto", out=None):
+    """Orthogonalised update of a matrix or a stack of them (pc_orthogonalize): G [..., R,
+    C] float32 or bfloat16, contiguous; ``steps`` Newton-Schulz products X <- a X + (b A +
+    c A A) X, A = X X^T, from X = G / (|G|_F + eps). Returns X in G's shape and type."""
+    prec = precision_code(precision)
+    _elements(G, "G")
+    dev = G.device
+    if G.dim() < 2:
+        raise ValueError("G must have at least two dimensions")
+    if not G.is_contiguous():
+        raise ValueError("G must be contiguous")
+    out = _given(out, "out", G.shape, G.dtype, dev)
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    a, b, c = coefficients
+    R, Cc = G.shape[-2:]
+    if R < 1 or Cc < 1:
+        raise ValueError("G's matrices must not be empty")
+    batch = G.numel() // (R * Cc)
+    ws = workspace(_query("pc_orthogonalize_workspace", batch, R, Cc, prec), dev)
+    N.call("pc_orthogonalize", batch, R, Cc, _ptr(G), steps, a, b, c, eps, _ptr(out), DTYPES[G.dtype], prec,
+           _ptr(ws), ws.numel(), _stream(dev))
+    return out
+
+
 # -------------------------------------------------------------------- diagnostics
 def device_status(device=None) -> None:
     """Synchronises the current stream and raises PCError if a kernel gave up a bounded wait."""

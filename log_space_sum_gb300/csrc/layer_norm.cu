@@ -1,0 +1,509 @@
+// Layer norm of rows, forward and backward.
+//
+//   forward   mean = avg(x), rstd = (avg((x - mean)^2) + eps)^(-1/2), z = (x - mean) rstd,
+//             y = z w + b
+//   backward  g = dy w,  dx = rstd (g - avg(g) - z avg(g z)),
+//             dw = sum over rows of dy z,  db = sum over rows of dy
+//
+// Memory-bound: x (and dy) are read once and y (dx) written once, about ten flops per
+// element. A row lives in the registers of one warp or one CTA between its load and its
+// store, so the variance is that of the centred values (no cancellation) at no extra
+// traffic. Statistics, sums and the weight's gradients are float32 throughout; the only
+// rounding to bf16 is that of y and dx.
+#include "pc_device.cuh"
+#include "pc_host.h"
+
+namespace pc {
+namespace {
+
+template <class T>
+constexpr int kLanes = 16 / sizeof(T);  // values of one 16-byte access
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[8]) {  // bf16 x 8
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[4]) {
+  v[0] = __uint_as_float(u.x);
+  v[1] = __uint_as_float(u.y);
+  v[2] = __uint_as_float(u.z);
+  v[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ uint4 pack(const float (&v)[4]) {
+  return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+}
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_float(float v, float* p) { *p = v; }
+__device__ __forceinline__ void from_float(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
+
+// kLanes<T> float32 parameters starting at column c (16-byte aligned: c is a multiple of 4).
+template <int L>
+__device__ __forceinline__ void load_params(const float* p, int c, float (&v)[L]) {
+#pragma unroll
+  for (int i = 0; i < L; i += 4) {
+    const float4 f = __ldg(reinterpret_cast<const float4*>(p + c + i));
+    v[i] = f.x;
+    v[i + 1] = f.y;
+    v[i + 2] = f.z;
+    v[i + 3] = f.w;
+  }
+}
+
+// Sum of a and b over the kWarps warps that share a row (every thread receives both).
+// red: kWarps float2 of shared memory per call site, not reused before the next barrier.
+template <int kWarps>
+__device__ __forceinline__ float2 row_sum(float a, float b, float2* red) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(0xffffffffu, a, o);
+    b += __shfl_xor_sync(0xffffffffu, b, o);
+  }
+  if constexpr (kWarps > 1) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      a += red[w].x;
+      b += red[w].y;
+    }
+  }
+  return make_float2(a, b);
+}
+
+// ------------------------------------------------------------------------ forward
+// kWarps = 1: a warp per row, kRows rows per CTA; kWarps > 1: a CTA per row. A thread
+// holds kVecs 16-byte pieces of its row (piece i at (i * threads + t)).
+template <class T, int kWarps, int kVecs, int kRows>
+__global__ void __launch_bounds__(32 * kWarps * kRows)
+    k_ln_fwd(long long rows, int dim, const T* __restrict__ x, long long x_ld, const float* __restrict__ w,
+             const float* __restrict__ b, float eps, T* __restrict__ y, long long y_ld, float* __restrict__ mean,
+             float* __restrict__ rstd) {
+  constexpr int L = kLanes<T>, kThreads = 32 * kWarps;
+  static_assert(kWarps == 1 || kRows == 1, "a warp's row or a CTA's row");
+  __shared__ float2 red[2][kWarps];
+  const int t = kWarps == 1 ? (threadIdx.x & 31) : threadIdx.x;
+  const long long r = static_cast<long long>(blockIdx.x) * kRows + (kWarps == 1 ? threadIdx.x >> 5 : 0);
+  if (r >= rows) return;
+  const T* xr = x + r * x_ld;
+  uint4 raw[kVecs];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = (i * kThreads + t) * L;
+    raw[i] = c < dim ? __ldcs(reinterpret_cast<const uint4*>(xr + c)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    float v[L];
+    unpack(raw[i], v);
+#pragma unroll
+    for (int j = 0; j < L; ++j) s += v[j];
+  }
+  const float m = row_sum<kWarps>(s, 0.f, red[0]).x / dim;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    float v[L];
+    unpack(raw[i], v);
+    if ((i * kThreads + t) * L < dim) {
+#pragma unroll
+      for (int j = 0; j < L; ++j) s += (v[j] - m) * (v[j] - m);
+    }
+  }
+  const float rs = 1.f / sqrtf(row_sum<kWarps>(s, 0.f, red[1]).x / dim + eps);
+  if (t == 0) {
+    if (mean) mean[r] = m;
+    if (rstd) rstd[r] = rs;
+  }
+  T* yr = y + r * y_ld;
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = (i * kThreads + t) * L;
+    if (c < dim) {
+      float v[L], g[L];
+      unpack(raw[i], v);
+#pragma unroll
+      for (int j = 0; j < L; ++j) v[j] = (v[j] - m) * rs;
+      if (w) {
+        load_params<L>(w, c, g);
+#pragma unroll
+        for (int j = 0; j < L; ++j) v[j] *= g[j];
+      }
+      if (b) {
+        load_params<L>(b, c, g);
+#pragma unroll
+        for (int j = 0; j < L; ++j) v[j] += g[j];
+      }
+      __stcs(reinterpret_cast<uint4*>(yr + c), pack(v));
+    }
+  }
+}
+
+constexpr int kAnyThreads = 256;
+
+// Any row: longer than the registers hold, or not a whole number of aligned 16-byte
+// pieces. A CTA per row reads it three times (L1 and L2 serve the second and third).
+template <class T>
+__global__ void __launch_bounds__(kAnyThreads)
+    k_ln_fwd_any(int dim, const T* __restrict__ x, long long x_ld, const float* __restrict__ w,
+                 const float* __restrict__ b, float eps, T* __restrict__ y, long long y_ld, float* __restrict__ mean,
+                 float* __restrict__ rstd) {
+  __shared__ float2 red[2][kAnyThreads / 32];
+  const long long r = blockIdx.x;
+  const T* xr = x + r * x_ld;
+  float s = 0.f;
+  for (int c = threadIdx.x; c < dim; c += kAnyThreads) s += to_float(xr[c]);
+  const float m = row_sum<kAnyThreads / 32>(s, 0.f, red[0]).x / dim;
+  s = 0.f;
+  for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
+    const float d = to_float(xr[c]) - m;
+    s += d * d;
+  }
+  const float rs = 1.f / sqrtf(row_sum<kAnyThreads / 32>(s, 0.f, red[1]).x / dim + eps);
+  if (threadIdx.x == 0) {
+    if (mean) mean[r] = m;
+    if (rstd) rstd[r] = rs;
+  }
+  T* yr = y + r * y_ld;
+  for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
+    float v = (to_float(xr[c]) - m) * rs;
+    if (w) v *= w[c];
+    if (b) v += b[c];
+    from_float(v, yr + c);
+  }
+}
+
+// ----------------------------------------------------------------------- backward
+// A CTA walks the rows blockIdx.x, + gridDim.x, ...; a thread keeps its columns' sums of
+// dy z and dy in registers over all of them and writes them once, as one row of the
+// partial sums part[2][gridDim.x][dim] (k_ln_reduce adds those rows in a fixed order).
+template <class T, int kWarps, int kVecs>
+__global__ void __launch_bounds__(32 * kWarps)
+    k_ln_bwd(long long rows, int dim, const T* __restrict__ dy, long long dy_ld, const T* __restrict__ x,
+             long long x_ld, const float* __restrict__ w, const float* __restrict__ mean,
+             const float* __restrict__ rstd, T* __restrict__ dx, long long dx_ld, float* __restrict__ part) {
+  constexpr int L = kLanes<T>, kThreads = 32 * kWarps;
+  __shared__ float2 red[2][kWarps];
+  const int t = threadIdx.x;
+  float wv[kVecs][L], aw[kVecs][L], ab[kVecs][L];
+#pragma unroll
+  for (int i = 0; i < kVecs; ++i) {
+    const int c = (i * kThreads + t) * L;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+      aw[i][j] = ab[i][j] = 0.f;
+      wv[i][j] = 1.f;
+    }
+    if (w && c < dim) load_params<L>(w, c, wv[i]);
+  }
+  int flip = 0;
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
+    const float m = mean[r], rs = rstd[r];
+    uint4 rx[kVecs], rd[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = (i * kThreads + t) * L;
+      rx[i] = rd[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c < dim) {
+        rx[i] = __ldcs(reinterpret_cast<const uint4*>(x + r * x_ld + c));
+        rd[i] = __ldcs(reinterpret_cast<const uint4*>(dy + r * dy_ld + c));
+      }
+    }
+    float sg = 0.f, sz = 0.f;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      float xv[L], dv[L];
+      unpack(rx[i], xv);
+      unpack(rd[i], dv);
+#pragma unroll
+      for (int j = 0; j < L; ++j) {  // past dim: dy = 0 adds nothing
+        const float z = (xv[j] - m) * rs, g = dv[j] * wv[i][j];
+        aw[i][j] += dv[j] * z;
+        ab[i][j] += dv[j];
+        sg += g;
+        sz += g * z;
+      }
+    }
+    const float2 sums = row_sum<kWarps>(sg, sz, red[flip]);
+    const float mg = sums.x / dim, mz = sums.y / dim;
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = (i * kThreads + t) * L;
+      if (c < dim) {
+        float xv[L], dv[L];
+        unpack(rx[i], xv);
+        unpack(rd[i], dv);
+#pragma unroll
+        for (int j = 0; j < L; ++j) dv[j] = rs * (dv[j] * wv[i][j] - mg - (xv[j] - m) * rs * mz);
+        __stcs(reinterpret_cast<uint4*>(dx + r * dx_ld + c), pack(dv));
+      }
+    }
+  }
+  if (part) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = (i * kThreads + t) * L;
+      if (c < dim) {
+        float* pw = part + static_cast<long long>(blockIdx.x) * dim + c;
+        float* pb = pw + static_cast<long long>(gridDim.x) * dim;
+#pragma unroll
+        for (int j = 0; j < L; j += 4) {
+          *reinterpret_cast<float4*>(pw + j) = make_float4(aw[i][j], aw[i][j + 1], aw[i][j + 2], aw[i][j + 3]);
+          *reinterpret_cast<float4*>(pb + j) = make_float4(ab[i][j], ab[i][j + 1], ab[i][j + 2], ab[i][j + 3]);
+        }
+      }
+    }
+  }
+}
+
+// Any row length and alignment: the columns' sums live in the CTA's own row of `part`
+// (each column is one thread's, so the read-modify-write needs no atomics).
+template <class T>
+__global__ void __launch_bounds__(kAnyThreads)
+    k_ln_bwd_any(long long rows, int dim, const T* __restrict__ dy, long long dy_ld, const T* __restrict__ x,
+                 long long x_ld, const float* __restrict__ w, const float* __restrict__ mean,
+                 const float* __restrict__ rstd, T* __restrict__ dx, long long dx_ld, float* part) {
+  __shared__ float2 red[2][kAnyThreads / 32];
+  float* pw = part ? part + static_cast<long long>(blockIdx.x) * dim : nullptr;
+  float* pb = part ? pw + static_cast<long long>(gridDim.x) * dim : nullptr;
+  if (part)
+    for (int c = threadIdx.x; c < dim; c += kAnyThreads) pw[c] = pb[c] = 0.f;
+  int flip = 0;
+  for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
+    const float m = mean[r], rs = rstd[r];
+    const T *xr = x + r * x_ld, *dr = dy + r * dy_ld;
+    float sg = 0.f, sz = 0.f;
+    for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
+      const float z = (to_float(xr[c]) - m) * rs, d = to_float(dr[c]), g = w ? d * w[c] : d;
+      if (part) {
+        pw[c] += d * z;
+        pb[c] += d;
+      }
+      sg += g;
+      sz += g * z;
+    }
+    const float2 sums = row_sum<kAnyThreads / 32>(sg, sz, red[flip]);
+    const float mg = sums.x / dim, mz = sums.y / dim;
+    for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
+      const float z = (to_float(xr[c]) - m) * rs, d = to_float(dr[c]), g = w ? d * w[c] : d;
+      from_float(rs * (g - mg - z * mz), dx + r * dx_ld + c);
+    }
+  }
+}
+
+// dweight[c] (+)= sum over n partial rows of part[0][.][c], dbias likewise from part[1].
+constexpr int kReduceCols = 32, kReduceRows = 16;
+__global__ void __launch_bounds__(kReduceCols* kReduceRows)
+    k_ln_reduce(int n, int dim, const float* __restrict__ part, float* __restrict__ dweight,
+                float* __restrict__ dbias, int accumulate) {
+  __shared__ float s[kReduceRows][kReduceCols + 1];
+  float* out = blockIdx.y ? dbias : dweight;
+  if (!out) return;
+  const int c = blockIdx.x * kReduceCols + threadIdx.x;
+  const float* p = part + (blockIdx.y ? static_cast<long long>(n) * dim : 0);
+  float a = 0.f;
+  if (c < dim)
+    for (int r = threadIdx.y; r < n; r += kReduceRows) a += p[static_cast<long long>(r) * dim + c];
+  s[threadIdx.y][threadIdx.x] = a;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < dim) {
+    a = 0.f;
+#pragma unroll
+    for (int r = 0; r < kReduceRows; ++r) a += s[r][threadIdx.x];
+    out[c] = accumulate ? out[c] + a : a;
+  }
+}
+
+// ------------------------------------------------------------------------- launches
+// Rows of whole, aligned 16-byte pieces: base and row stride.
+inline bool rows_aligned(const void* p, long long ld, int es) { return aligned16(p) && (ld * es) % 16 == 0; }
+
+struct LnFwd {
+  long long rows;
+  int dim;
+  const void* x;
+  long long x_ld;
+  const float *w, *b;
+  float eps;
+  void* y;
+  long long y_ld;
+  float *mean, *rstd;
+};
+
+template <class T, int kWarps, int kVecs, int kRows>
+void fwd_kernel(const LnFwd& a, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>((a.rows + kRows - 1) / kRows);
+  k_ln_fwd<T, kWarps, kVecs, kRows><<<grid, 32 * kWarps * kRows, 0, s>>>(
+      a.rows, a.dim, static_cast<const T*>(a.x), a.x_ld, a.w, a.b, a.eps, static_cast<T*>(a.y), a.y_ld, a.mean,
+      a.rstd);
+}
+
+template <class T>
+void launch_fwd(const LnFwd& a, cudaStream_t s) {
+  const bool vec = a.dim % kLanes<T> == 0 && rows_aligned(a.x, a.x_ld, sizeof(T)) &&
+                   rows_aligned(a.y, a.y_ld, sizeof(T)) && (!a.w || aligned16(a.w)) && (!a.b || aligned16(a.b));
+  const int pieces = a.dim / kLanes<T>;
+  if (vec && pieces <= 32)
+    fwd_kernel<T, 1, 1, 4>(a, s);
+  else if (vec && pieces <= 64)
+    fwd_kernel<T, 1, 2, 4>(a, s);
+  else if (vec && pieces <= 128)
+    fwd_kernel<T, 1, 4, 4>(a, s);
+  else if (vec && pieces <= 256)
+    fwd_kernel<T, 4, 2, 1>(a, s);
+  else if (vec && pieces <= 512)
+    fwd_kernel<T, 4, 4, 1>(a, s);
+  else if (vec && pieces <= 1024)
+    fwd_kernel<T, 8, 4, 1>(a, s);
+  else if (vec && pieces <= 2048)
+    fwd_kernel<T, 16, 4, 1>(a, s);
+  else
+    k_ln_fwd_any<T><<<static_cast<unsigned>(a.rows), kAnyThreads, 0, s>>>(
+        a.dim, static_cast<const T*>(a.x), a.x_ld, a.w, a.b, a.eps, static_cast<T*>(a.y), a.y_ld, a.mean, a.rstd);
+}
+
+struct LnBwd {
+  long long rows;
+  int dim;
+  const void* dy;
+  long long dy_ld;
+  const void* x;
+  long long x_ld;
+  const float *w, *mean, *rstd;
+  void* dx;
+  long long dx_ld;
+  float* part;
+  unsigned grid;
+};
+
+// CTAs of the backward: enough to fill the GPU, few enough that the partial sums stay
+// small beside the rows. (The same for every variant: the workspace query uses it.)
+unsigned bwd_grid(long long rows) {
+  const long long most = 4ll * num_sms();
+  return static_cast<unsigned>(rows < most ? rows : most);
+}
+
+template <class T, int kWarps, int kVecs>
+void bwd_kernel(const LnBwd& a, cudaStream_t s) {
+  k_ln_bwd<T, kWarps, kVecs><<<a.grid, 32 * kWarps, 0, s>>>(
+      a.rows, a.dim, static_cast<const T*>(a.dy), a.dy_ld, static_cast<const T*>(a.x), a.x_ld, a.w, a.mean, a.rstd,
+      static_cast<T*>(a.dx), a.dx_ld, a.part);
+}
+
+template <class T>
+void launch_bwd(const LnBwd& a, cudaStream_t s) {
+  const bool vec = a.dim % kLanes<T> == 0 && rows_aligned(a.x, a.x_ld, sizeof(T)) &&
+                   rows_aligned(a.dy, a.dy_ld, sizeof(T)) && rows_aligned(a.dx, a.dx_ld, sizeof(T)) &&
+                   (!a.w || aligned16(a.w));
+  const int pieces = a.dim / kLanes<T>;
+  if (vec && pieces <= 64)
+    bwd_kernel<T, 2, 1>(a, s);
+  else if (vec && pieces <= 128)
+    bwd_kernel<T, 4, 1>(a, s);
+  else if (vec && pieces <= 256)
+    bwd_kernel<T, 8, 1>(a, s);
+  else if (vec && pieces <= 512)
+    bwd_kernel<T, 8, 2>(a, s);
+  else if (vec && pieces <= 1024)
+    bwd_kernel<T, 16, 2>(a, s);
+  else
+    k_ln_bwd_any<T><<<a.grid, kAnyThreads, 0, s>>>(
+        a.rows, a.dim, static_cast<const T*>(a.dy), a.dy_ld, static_cast<const T*>(a.x), a.x_ld, a.w, a.mean, a.rstd,
+        static_cast<T*>(a.dx), a.dx_ld, a.part);
+}
+
+pc_status_t check_shape(long long rows, int dim) {
+  PC_CHECK(rows >= 0 && rows < (1ll << 31), PC_ERR_SHAPE, "rows must be in [0, 2^31) (got %lld)", rows);
+  PC_CHECK(dim >= 1 && dim <= (1 << 24), PC_ERR_SHAPE, "dim must be in [1, 2^24] (got %d)", dim);
+  return PC_OK;
+}
+
+pc_status_t check_rows(const char* name, const void* p, long long ld, long long rows, int dim, pc_dtype_t dt) {
+  PC_CHECK(p, PC_ERR_NULL, "%s must not be NULL", name);
+  PC_CHECK(rows <= 1 || ld >= dim, PC_ERR_SHAPE, "%s: row stride %lld is shorter than a row of %d", name, ld, dim);
+  PC_CHECK(reinterpret_cast<uintptr_t>(p) % dtype_bytes(dt) == 0, PC_ERR_ALIGNMENT, "%s is not aligned to its type",
+           name);
+  return PC_OK;
+}
+
+}  // namespace
+}  // namespace pc
+
+extern "C" {
+
+pc_status_t pc_layer_norm_fwd(long long rows, int dim, const void* x, long long x_ld, const float* weight,
+                              const float* bias, float eps, void* y, long long y_ld, float* mean, float* rstd,
+                              pc_dtype_t dtype, cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_dtype(dtype));
+  PC_TRY(pc::check_shape(rows, dim));
+  PC_CHECK(eps >= 0.f, PC_ERR_SHAPE, "eps must not be negative (got %g)", static_cast<double>(eps));
+  if (rows == 0) return PC_OK;
+  PC_TRY(pc::check_rows("x", x, x_ld, rows, dim, dtype));
+  PC_TRY(pc::check_rows("y", y, y_ld, rows, dim, dtype));
+  const pc::LnFwd a{rows, dim, x, x_ld, weight, bias, eps, y, y_ld, mean, rstd};
+  if (dtype == PC_BF16)
+    pc::launch_fwd<__nv_bfloat16>(a, stream);
+  else
+    pc::launch_fwd<float>(a, stream);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+pc_status_t pc_layer_norm_bwd_workspace(long long rows, int dim, size_t* bytes) {
+  pc::clear_error();
+  PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
+  PC_TRY(pc::check_shape(rows, dim));
+  *bytes = 2 * sizeof(float) * static_cast<size_t>(pc::bwd_grid(rows)) * dim;
+  return PC_OK;
+}
+
+pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy, long long dy_ld, const void* x, long long x_ld,
+                              const float* weight, const float* mean, const float* rstd, void* dx, long long dx_ld,
+                              float* dweight, float* dbias, int accumulate, pc_dtype_t dtype, void* ws,
+                              size_t ws_bytes, cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_dtype(dtype));
+  PC_TRY(pc::check_shape(rows, dim));
+  const bool params = dweight || dbias;
+  if (rows > 0) {
+    PC_TRY(pc::check_rows("dy", dy, dy_ld, rows, dim, dtype));
+    PC_TRY(pc::check_rows("x", x, x_ld, rows, dim, dtype));
+    PC_TRY(pc::check_rows("dx", dx, dx_ld, rows, dim, dtype));
+    PC_CHECK(mean && rstd, PC_ERR_NULL, "mean and rstd must not be NULL");
+  }
+  const unsigned grid = pc::bwd_grid(rows);
+  if (params && rows > 0) {
+    PC_CHECK(ws && ws_bytes >= 2 * sizeof(float) * static_cast<size_t>(grid) * dim, PC_ERR_WORKSPACE,
+             "workspace of %zu bytes is too small", ws_bytes);
+    PC_CHECK(pc::aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  }
+  if (rows > 0) {
+    const pc::LnBwd a{rows, dim, dy, dy_ld, x, x_ld, weight, mean, rstd, dx, dx_ld,
+                      params ? static_cast<float*>(ws) : nullptr, grid};
+    if (dtype == PC_BF16)
+      pc::launch_bwd<__nv_bfloat16>(a, stream);
+    else
+      pc::launch_bwd<float>(a, stream);
+    PC_LAUNCH_CHECK();
+  }
+  if (params) {  // no rows: the sums are zero
+    pc::k_ln_reduce<<<dim3((dim + pc::kReduceCols - 1) / pc::kReduceCols, 2),
+                      dim3(pc::kReduceCols, pc::kReduceRows), 0, stream>>>(
+        static_cast<int>(grid), dim, static_cast<const float*>(ws), dweight, dbias, accumulate);
+    PC_LAUNCH_CHECK();
+  }
+  return PC_OK;
+}
+
+}  // extern "C"

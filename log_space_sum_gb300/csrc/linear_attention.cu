@@ -1,0 +1,375 @@
+// Linear attention with a decay for each head: per sequence b and head h, with
+// l = exp(log_decay[h]) and n = lengths[b] tokens,
+//
+//   S_t = l S_{t-1} + k_t v_t^T        o_t = scale q_t^T S_t        t = 1 .. n, S_0 given
+//
+// Every direction is one pass of the same form. With the gradient of S_t,
+//   R_t = scale q_t do_t^T + l R_{t+1},  R_n = scale q_n do_n^T + dS_n,
+// the backward is  dq_t = scale S_t do_t,  dk_t = R_t v_t,  dv_t = R_t^T k_t,  dS_0 = l R_1:
+//   dq = the forward of (do, v, k) with the state transposed,
+//   dk = the time-reversed forward of (v, do, q) with the state transposed,
+//   dv = the time-reversed forward of (k, q, do).
+// A pass runs in chunks of C tokens (i, j: positions in a tile, in order of time):
+//   O = (P . L) V + diag(in) Q S,   S' = l^m S + (diag(up) K)^T V,   P = Q K^T,
+// with m real tokens in the tile and, in order of time, L_ij = l^(i-j) for i >= j,
+// in_i = l^(i-pad+1), up_i = l^(C-1-i); reversed, L_ij = l^(j-i) for j >= i and in, up
+// exchanged. No exponent is negative, so nothing overflows for l <= 1. Tiles end at
+// the sequence's end: a length that is no multiple of C leaves its `pad` missing rows at
+// the front of the first tile (zeros that add nothing), so no row past the length is
+// ever read.
+#include "pc_device.cuh"
+#include "pc_host.h"
+
+namespace pc {
+namespace {
+
+// One pass, in the terms above.
+struct LaPass {
+  const void *q, *k, *v;
+  void* o;
+  long long qs[3], ks[3], vs[3], os[3];  // strides of batch, token, head (elements)
+  int dk, dv;
+  const float* s_in;  // [B][H][dk][dv], or transposed; NULL: zeros
+  float* s_out;       // [B][H][dk][dv]; NULL: not wanted
+  int s_in_transposed, reverse;
+  float c_intra, c_inter, c_up;  // factors of P, of Q S, and of the outer products
+};
+
+struct LaArgs {
+  LaPass pass[3];
+  int B, T, H;
+  const float* log_decay;
+  const int* lengths;
+};
+
+// l^n, with l^0 = 1 also for l = 0 (log_decay = -inf)
+__device__ __forceinline__ float decay_pow(float g, int n) { return n == 0 ? 1.f : expf(g * static_cast<float>(n)); }
+
+__device__ __forceinline__ float la_load(const float* p) { return *p; }
+__device__ __forceinline__ float la_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void la_store(float* p, float v) { *p = v; }
+__device__ __forceinline__ void la_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ int la_length(const LaArgs& a, int b) {
+  return a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
+}
+
+// ------------------------------------------------------------- any type and head size
+// All products in float32 on the CUDA cores. A CTA owns one (b, h) and kDvs columns of v
+// and walks the chunks with its columns of S in shared memory; the scores are formed
+// again for each slice of columns.
+constexpr int kSimtThreads = 256, kSimtC = 32, kSimtDvs = 64;
+constexpr int kMaxHeadDim = 256;
+
+size_t simt_smem(int dk) {
+  return sizeof(float) * (2 * size_t(kSimtC) * (dk + 1) + size_t(kSimtC) * kSimtDvs + size_t(kSimtC) * (kSimtC + 1) +
+                          size_t(dk) * kSimtDvs + kSimtC + 1);
+}
+
+template <class T>
+__global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant__ LaArgs a) {
+  extern __shared__ float sm[];
+  const LaPass& p = a.pass[blockIdx.z];
+  const int c0 = blockIdx.y * kSimtDvs;
+  if (c0 >= p.dv) return;
+  constexpr int C = kSimtC;
+  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, dk = p.dk, pitch = dk + 1, tid = threadIdx.x;
+  const int cols = min(kSimtDvs, p.dv - c0);
+  float* Q = sm;
+  float* K = Q + C * pitch;
+  float* V = K + C * pitch;
+  float* P = V + C * kSimtDvs;
+  float* S = P + C * (C + 1);
+  float* pw = S + dk * kSimtDvs;  // l^0 .. l^C
+  const float g = a.log_decay[h];
+  if (tid <= C) pw[tid] = decay_pow(g, tid);
+  const long long bh = blockIdx.x;
+  for (int e = tid; e < dk * kSimtDvs; e += kSimtThreads) {
+    const int d = e / kSimtDvs, c = e % kSimtDvs;
+    float v = 0.f;
+    if (p.s_in && c < cols)
+      v = p.s_in[bh * dk * p.dv + (p.s_in_transposed ? static_cast<long long>(c0 + c) * dk + d
+                                                     : static_cast<long long>(d) * p.dv + c0 + c)];
+    S[e] = v;
+  }
+  const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + h * p.qs[2];
+  const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + h * p.ks[2];
+  const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + h * p.vs[2] + c0;
+  T* o = static_cast<T*>(p.o) + b * p.os[0] + h * p.os[2] + c0;
+  const int len = la_length(a, b), nch = (len + C - 1) / C;
+  for (int step = 0; step < nch; ++step) {
+    const int tile = p.reverse ? nch - 1 - step : step;
+    const int t0 = len - (nch - tile) * C, pad = max(0, -t0);
+    __syncthreads();  // the last chunk's reads are done
+    for (int e = tid; e < C * dk; e += kSimtThreads) {
+      const int i = e / dk, d = e % dk;
+      const bool in = i >= pad;
+      Q[i * pitch + d] = in ? la_load(q + (t0 + i) * p.qs[1] + d) : 0.f;
+      K[i * pitch + d] = in ? la_load(k + (t0 + i) * p.ks[1] + d) : 0.f;
+    }
+    for (int e = tid; e < C * kSimtDvs; e += kSimtThreads) {
+      const int i = e / kSimtDvs, c = e % kSimtDvs;
+      V[e] = i >= pad && c < cols ? la_load(v + (t0 + i) * p.vs[1] + c) : 0.f;
+    }
+    __syncthreads();
+    const int i = tid >> 3, lane8 = tid & 7;
+    {
+      float acc[C / 8] = {};
+      for (int d = 0; d < dk; ++d) {
+        const float x = Q[i * pitch + d];
+#pragma unroll
+        for (int jj = 0; jj < C / 8; ++jj) acc[jj] += x * K[(lane8 + 8 * jj) * pitch + d];
+      }
+#pragma unroll
+      for (int jj = 0; jj < C / 8; ++jj) {
+        const int j = lane8 + 8 * jj, gap = p.reverse ? j - i : i - j;
+        P[i * (C + 1) + j] = gap >= 0 ? acc[jj] * (pw[gap] * p.c_intra) : 0.f;
+      }
+    }
+    __syncwarp();  // a warp reads only the rows of P that it wrote
+    const int early = max(i - pad + 1, 0), late = C - 1 - i;
+    {
+      float acc[kSimtDvs / 8] = {};
+      for (int d = 0; d < dk; ++d) {
+        const float x = Q[i * pitch + d];
+#pragma unroll
+        for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] += x * S[d * kSimtDvs + lane8 + 8 * cc];
+      }
+      const float w = pw[p.reverse ? late : early] * p.c_inter;
+#pragma unroll
+      for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] *= w;
+      for (int j = 0; j < C; ++j) {
+        const float x = P[i * (C + 1) + j];
+#pragma unroll
+        for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] += x * V[j * kSimtDvs + lane8 + 8 * cc];
+      }
+      if (i >= pad) {
+#pragma unroll
+        for (int cc = 0; cc < kSimtDvs / 8; ++cc)
+          if (lane8 + 8 * cc < cols) la_store(o + (t0 + i) * p.os[1] + lane8 + 8 * cc, acc[cc]);
+      }
+    }
+    __syncthreads();  // every read of S, before its update
+    {
+      const int c = tid % kSimtDvs;
+      float vr[C];
+#pragma unroll
+      for (int j = 0; j < C; ++j) {
+        const int up = p.reverse ? max(j - pad + 1, 0) : C - 1 - j;
+        vr[j] = V[j * kSimtDvs + c] * (pw[up] * p.c_up);
+      }
+      const float carry = pw[C - pad];
+      for (int d = tid / kSimtDvs; d < dk; d += kSimtThreads / kSimtDvs) {
+        float acc = 0.f;
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc += K[j * pitch + d] * vr[j];
+        S[d * kSimtDvs + c] = carry * S[d * kSimtDvs + c] + acc;
+      }
+    }
+  }
+  __syncthreads();
+  if (p.s_out)
+    for (int e = tid; e < dk * kSimtDvs; e += kSimtThreads) {
+      const int d = e / kSimtDvs, c = e % kSimtDvs;
+      if (c < cols) p.s_out[bh * dk * p.dv + static_cast<long long>(d) * p.dv + c0 + c] = S[e];
+    }
+  // rows past the length hold zeros
+  for (long long e = tid; e < static_cast<long long>(a.T - len) * cols; e += kSimtThreads)
+    la_store(o + (len + e / cols) * p.os[1] + e % cols, 0.f);
+}
+
+template <class T>
+pc_status_t launch_simt(const LaArgs& a, int passes, cudaStream_t s) {
+  int dk = 0, dv = 0;
+  for (int i = 0; i < passes; ++i) {
+    dk = a.pass[i].dk > dk ? a.pass[i].dk : dk;
+    dv = a.pass[i].dv > dv ? a.pass[i].dv : dv;
+  }
+  const size_t smem = simt_smem(dk);
+  PC_CUDA(cudaFuncSetAttribute(k_la_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               static_cast<int>(simt_smem(kMaxHeadDim))));
+  k_la_simt<T><<<dim3(a.B * a.H, (dv + kSimtDvs - 1) / kSimtDvs, passes), kSimtThreads, smem, s>>>(a);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+// ------------------------------------------------------------------- a single token
+// S <- l S + k v^T and o = scale q^T S, in place. Memory-bound: 8 bytes of state per
+// 4 flops. A CTA takes one (b, h): each warp some rows of S, a lane 16 bytes of a row.
+constexpr int kStepThreads = 256;
+template <class T>
+__global__ void __launch_bounds__(kStepThreads)
+    k_la_step(int H, int dk, int dv, const T* __restrict__ q, long long q_b, long long q_h, const T* __restrict__ k,
+              long long k_b, long long k_h, const T* __restrict__ v, long long v_b, long long v_h,
+              const float* __restrict__ log_decay, float scale, float* __restrict__ state, T* __restrict__ o,
+              long long o_b, long long o_h) {
+  __shared__ float part[kStepThreads / 32][kMaxHeadDim];
+  const int b = blockIdx.x / H, h = blockIdx.x % H;
+  const float l = decay_pow(log_decay[h], 1);
+  const T *qp = q + b * q_b + h * q_h, *kp = k + b * k_b + h * k_h, *vp = v + b * v_b + h * v_h;
+  float* S = state + static_cast<long long>(blockIdx.x) * dk * dv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int c = lane; c < dv; c += 32) {
+    const float x = la_load(vp + c);
+    float acc = 0.f;
+    for (int d = warp; d < dk; d += kStepThreads / 32) {
+      const float s = l * S[d * dv + c] + la_load(kp + d) * x;
+      S[d * dv + c] = s;
+      acc += la_load(qp + d) * s;
+    }
+    part[warp][c] = acc;
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < dv; c += kStepThreads) {
+    float acc = 0.f;
+#pragma unroll
+    for (int w = 0; w < kStepThreads / 32; ++w) acc += part[w][c];
+    la_store(o + b * o_b + h * o_h + c, acc * scale);
+  }
+}
+
+// ------------------------------------------------------------------------- checks
+pc_status_t check_la(int B, int T, int H, int dk, int dv, pc_dtype_t dt) {
+  PC_TRY(check_dtype(dt));
+  PC_CHECK(B >= 0 && T >= 0 && H >= 1 && static_cast<long long>(B) * H < (1ll << 31) && T < (1 << 30), PC_ERR_SHAPE,
+           "B, T >= 0, H >= 1, B * H < 2^31 and T < 2^30 wanted (got %d, %d, %d)", B, T, H);
+  PC_CHECK(dk >= 1 && dv >= 1, PC_ERR_SHAPE, "head sizes must be >= 1 (got %d, %d)", dk, dv);
+  PC_CHECK(dk <= kMaxHeadDim && dv <= kMaxHeadDim, PC_ERR_UNSUPPORTED, "head sizes up to %d (got %d, %d)",
+           kMaxHeadDim, dk, dv);
+  return PC_OK;
+}
+
+pc_status_t check_tensor(const char* name, const void* p, pc_dtype_t dt) {
+  PC_CHECK(p, PC_ERR_NULL, "%s must not be NULL", name);
+  PC_CHECK(reinterpret_cast<uintptr_t>(p) % dtype_bytes(dt) == 0, PC_ERR_ALIGNMENT, "%s is not aligned to its type",
+           name);
+  return PC_OK;
+}
+
+pc_status_t run_passes(const LaArgs& a, int passes, pc_dtype_t dt, cudaStream_t s) {
+  return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, passes, s) : launch_simt<float>(a, passes, s);
+}
+
+LaPass make_pass(const void* q, const long long* qs, const void* k, const long long* ks, const void* v,
+                 const long long* vs, void* o, const long long* os, int dk, int dv, const float* s_in,
+                 float* s_out, bool s_in_transposed, bool reverse, float scale) {
+  LaPass p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.o = o;
+  for (int i = 0; i < 3; ++i) {
+    p.qs[i] = qs[i];
+    p.ks[i] = ks[i];
+    p.vs[i] = vs[i];
+    p.os[i] = os[i];
+  }
+  p.dk = dk;
+  p.dv = dv;
+  p.s_in = s_in;
+  p.s_out = s_out;
+  p.s_in_transposed = s_in_transposed;
+  p.reverse = reverse;
+  // in order of time the state is unscaled and read with the scale; R carries the scale
+  p.c_intra = scale;
+  p.c_inter = reverse ? 1.f : scale;
+  p.c_up = reverse ? scale : 1.f;
+  return p;
+}
+
+}  // namespace
+}  // namespace pc
+
+extern "C" {
+
+pc_status_t pc_linear_attention_workspace(int B, int T, int H, int Dk, int Dv, int with_backward, pc_dtype_t dtype,
+                                          size_t* bytes) {
+  pc::clear_error();
+  PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
+  PC_TRY(pc::check_la(B, T, H, Dk, Dv, dtype));
+  *bytes = 0;
+  return PC_OK;
+}
+
+pc_status_t pc_linear_attention_fwd(int B, int T, int H, int Dk, int Dv, const void* q, const void* k, const void* v,
+                                    const long long* strides, const float* log_decay, float scale,
+                                    const float* state, const int32_t* lengths, void* o, float* state_out,
+                                    pc_dtype_t dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_la(B, T, H, Dk, Dv, dtype));
+  if (B == 0) return PC_OK;
+  PC_CHECK(strides && log_decay, PC_ERR_NULL, "strides and log_decay must not be NULL");
+  if (T > 0) {
+    PC_TRY(pc::check_tensor("q", q, dtype));
+    PC_TRY(pc::check_tensor("k", k, dtype));
+    PC_TRY(pc::check_tensor("v", v, dtype));
+    PC_TRY(pc::check_tensor("o", o, dtype));
+  }
+  PC_CHECK(!state || state != state_out, PC_ERR_UNSUPPORTED, "state_out may not be state itself");
+  pc::LaArgs a{};
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.log_decay = log_decay;
+  a.lengths = lengths;
+  a.pass[0] = pc::make_pass(q, strides, k, strides + 3, v, strides + 6, o, strides + 9, Dk, Dv, state, state_out,
+                            false, false, scale);
+  return pc::run_passes(a, 1, dtype, stream);
+}
+
+pc_status_t pc_linear_attention_bwd(int B, int T, int H, int Dk, int Dv, const void* q, const void* k, const void* v,
+                                    const void* d_o, const long long* strides, const float* log_decay, float scale,
+                                    const float* state, const float* dstate_out, const int32_t* lengths, void* dq,
+                                    void* dk, void* dv, float* dstate, pc_dtype_t dtype, void* ws, size_t ws_bytes,
+                                    cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_la(B, T, H, Dk, Dv, dtype));
+  if (B == 0) return PC_OK;
+  PC_CHECK(strides && log_decay, PC_ERR_NULL, "strides and log_decay must not be NULL");
+  if (T > 0) {
+    const char* names[7] = {"q", "k", "v", "do", "dq", "dk", "dv"};
+    const void* all[7] = {q, k, v, d_o, dq, dk, dv};
+    for (int i = 0; i < 7; ++i) PC_TRY(pc::check_tensor(names[i], all[i], dtype));
+  }
+  PC_CHECK(!dstate_out || dstate_out != dstate, PC_ERR_UNSUPPORTED, "dstate may not be dstate_out itself");
+  const long long *qs = strides, *ks = strides + 3, *vs = strides + 6, *gs = strides + 9;
+  pc::LaArgs a{};
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.log_decay = log_decay;
+  a.lengths = lengths;
+  a.pass[0] = pc::make_pass(d_o, gs, v, vs, k, ks, dq, strides + 12, Dv, Dk, state, nullptr, true, false, scale);
+  a.pass[1] = pc::make_pass(v, vs, d_o, gs, q, qs, dk, strides + 15, Dv, Dk, dstate_out, nullptr, true, true, scale);
+  a.pass[2] = pc::make_pass(k, ks, q, qs, d_o, gs, dv, strides + 18, Dk, Dv, dstate_out, dstate, false, true, scale);
+  return pc::run_passes(a, 3, dtype, stream);
+}
+
+pc_status_t pc_linear_attention_step(int B, int H, int Dk, int Dv, const void* q, const void* k, const void* v,
+                                     const long long* strides, const float* log_decay, float scale, float* state,
+                                     void* o, pc_dtype_t dtype, cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_la(B, 1, H, Dk, Dv, dtype));
+  if (B == 0) return PC_OK;
+  PC_CHECK(strides && log_decay && state, PC_ERR_NULL, "strides, log_decay and state must not be NULL");
+  PC_TRY(pc::check_tensor("q", q, dtype));
+  PC_TRY(pc::check_tensor("k", k, dtype));
+  PC_TRY(pc::check_tensor("v", v, dtype));
+  PC_TRY(pc::check_tensor("o", o, dtype));
+  const long long* s = strides;
+  if (dtype == PC_BF16) {
+    using T = __nv_bfloat16;
+    pc::k_la_step<T><<<B * H, pc::kStepThreads, 0, stream>>>(
+        H, Dk, Dv, static_cast<const T*>(q), s[0], s[1], static_cast<const T*>(k), s[2], s[3],
+        static_cast<const T*>(v), s[4], s[5], log_decay, scale, state, static_cast<T*>(o), s[6], s[7]);
+  } else {
+    using T = float;
+    pc::k_la_step<T><<<B * H, pc::kStepThreads, 0, stream>>>(
+        H, Dk, Dv, static_cast<const T*>(q), s[0], s[1], static_cast<const T*>(k), s[2], s[3],
+        static_cast<const T*>(v), s[4], s[5], log_decay, scale, state, static_cast<T*>(o), s[6], s[7]);
+  }
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+}  // extern "C"

@@ -69,6 +69,12 @@ struct ProfileScope {
       return ::pc::set_error(PC_ERR_CUDA, "%s failed: %s", #call, cudaGetErrorString(e_)); \
   } while (0)
 
+#define PC_TRY(call)                              \
+  do {                                            \
+    const pc_status_t st_ = (call);               \
+    if (st_ != PC_OK) return st_;                 \
+  } while (0)
+
 // Counts every kernel the library launches (pc_launch_count) after checking the launch.
 void count_launch();
 #define PC_LAUNCH_CHECK()         \
@@ -85,6 +91,14 @@ inline pc_status_t check_precision(pc_precision_t p) {
                      static_cast<int>(p));
   return PC_OK;
 }
+
+inline pc_status_t check_dtype(pc_dtype_t t) {
+  if (t != PC_F32 && t != PC_BF16)
+    return set_error(PC_ERR_UNSUPPORTED, "unknown element type %d; valid types are PC_F32 (0) and PC_BF16 (1)",
+                     static_cast<int>(t));
+  return PC_OK;
+}
+inline int dtype_bytes(pc_dtype_t t) { return t == PC_BF16 ? 2 : 4; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
