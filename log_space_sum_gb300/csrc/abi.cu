@@ -162,8 +162,8 @@ pc_status_t SideStream::fork(cudaStream_t main) {
 
 pc_status_t SideStream::join(cudaStream_t main) { return stream_after(main, s); }
 
-pc_status_t encode_operand_map(CUtensorMap* map, const Operand& op, pc_precision_t p,
-                               int box_rows, int part, bool swizzle, long long group_stride) {
+namespace {
+pc_status_t find_encode() {
   std::call_once(g_encode_once, [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -173,6 +173,29 @@ pc_status_t encode_operand_map(CUtensorMap* map, const Operand& op, pc_precision
       g_encode = reinterpret_cast<EncodeTiledFn>(fn);
   });
   if (!g_encode) return set_error(PC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  return PC_OK;
+}
+}  // namespace
+
+pc_status_t encode_bf16_map4(CUtensorMap* map, const void* base, const long long (&dims)[4],
+                             const long long (&strides)[3], int box_cols, int box_rows) {
+  PC_TRY(find_encode());
+  const cuuint64_t d[4] = {cuuint64_t(dims[0]), cuuint64_t(dims[1]), cuuint64_t(dims[2]), cuuint64_t(dims[3])};
+  const cuuint64_t st[3] = {cuuint64_t(strides[0]) * 2, cuuint64_t(strides[1]) * 2, cuuint64_t(strides[2]) * 2};
+  const cuuint32_t box[4] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return set_error(PC_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) for a %lldx%lldx%lldx%lld tensor", int(r),
+                     dims[3], dims[2], dims[1], dims[0]);
+  return PC_OK;
+}
+
+pc_status_t encode_operand_map(CUtensorMap* map, const Operand& op, pc_precision_t p,
+                               int box_rows, int part, bool swizzle, long long group_stride) {
+  PC_TRY(find_encode());
   const int es = operand_elem_bytes(p);
   uint8_t* base = static_cast<uint8_t*>(op.ptr) + (part ? op.lo_elems * size_t(es) : 0);
   const cuuint64_t dims[3] = {cuuint64_t(op.cols), cuuint64_t(op.rows), cuuint64_t(op.groups)};
