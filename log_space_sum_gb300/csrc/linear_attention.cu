@@ -17,42 +17,15 @@
 // the sequence's end: a length that is no multiple of C leaves its `pad` missing rows at
 // the front of the first tile (zeros that add nothing), so no row past the length is
 // ever read.
-#include "pc_device.cuh"
-#include "pc_host.h"
+#include "linear_attention_tc.cuh"
 
 namespace pc {
 namespace {
-
-// One pass, in the terms above.
-struct LaPass {
-  const void *q, *k, *v;
-  void* o;
-  long long qs[3], ks[3], vs[3], os[3];  // strides of batch, token, head (elements)
-  int dk, dv;
-  const float* s_in;  // [B][H][dk][dv], or transposed; NULL: zeros
-  float* s_out;       // [B][H][dk][dv]; NULL: not wanted
-  int s_in_transposed, reverse;
-  float c_intra, c_inter, c_up;  // factors of P, of Q S, and of the outer products
-};
-
-struct LaArgs {
-  LaPass pass[3];
-  int B, T, H;
-  const float* log_decay;
-  const int* lengths;
-};
-
-// l^n, with l^0 = 1 also for l = 0 (log_decay = -inf)
-__device__ __forceinline__ float decay_pow(float g, int n) { return n == 0 ? 1.f : expf(g * static_cast<float>(n)); }
 
 __device__ __forceinline__ float la_load(const float* p) { return *p; }
 __device__ __forceinline__ float la_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void la_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void la_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-__device__ __forceinline__ int la_length(const LaArgs& a, int b) {
-  return a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
-}
 
 // ------------------------------------------------------------- any type and head size
 // All products in float32 on the CUDA cores. A CTA owns one (b, h) and kDvs columns of v
@@ -193,6 +166,121 @@ pc_status_t launch_simt(const LaArgs& a, int passes, cudaStream_t s) {
   return PC_OK;
 }
 
+// ------------------------------------------------------------------- tensor cores
+// A tensor's map, or false where it has no aligned one. A dimension of one step or of
+// stride 0 (shared by all heads or sequences) is left out of the map.
+bool tc_map(CUtensorMap* map, int (&ext)[2], const void* base, const long long (&st)[3], int d, int T, int H, int B,
+            pc_status_t* status) {
+  ext[0] = H > 1 && st[2] != 0;
+  ext[1] = B > 1 && st[0] != 0;
+  const long long row = T > 1 ? st[1] : 8;
+  const long long strides[3] = {row, ext[0] ? st[2] : 8, ext[1] ? st[0] : 8};
+  if (!aligned16(base) || d % 8) return false;
+  for (const long long s : strides)
+    if (s <= 0 || s % 8 || s >= (1ll << 38)) return false;
+  const long long dims[4] = {d, T, ext[0] ? H : 1, ext[1] ? B : 1};
+  *status = encode_bf16_map4(map, base, dims, strides, 64, kTcC);
+  return *status == PC_OK;
+}
+
+// Outputs are stored in 16-byte pieces.
+bool tc_output(const LaPass& p, int T, int H, int B) {
+  return aligned16(p.o) && p.dv % 8 == 0 && (T <= 1 || p.os[1] % 8 == 0) && (H <= 1 || p.os[2] % 8 == 0) &&
+         (B <= 1 || p.os[0] % 8 == 0);
+}
+
+bool tc_heads(int dk, int dv, pc_dtype_t dt) {
+  return dt == PC_BF16 && dk % 8 == 0 && dv % 8 == 0 && dk <= 128 && dv <= 128;
+}
+int tc_pad(int d) { return d <= 64 ? 64 : 128; }
+
+// Segments of a sequence. One CTA per SM takes a segment; cutting a sequence into S makes
+// the first launch's states cost about 0.6 of a pass's chunks, and each CTA a start of
+// about one and a half chunks (measured at head size 128: 2 us a chunk, 1.2 us of states
+// alone, 3 us from a CTA's launch to its first product), and joining a segment's share 0.3.
+int tc_segments(long long heads, int T) {
+  const int nch = (T + kTcC - 1) / kTcC;
+  const long long sms = num_sms();
+  double best = 1e30;
+  int at = 1;
+  for (int s = 1; s <= nch && s <= 64; ++s) {
+    const int per = (nch + s - 1) / s;
+    if ((nch + per - 1) / per != s) continue;  // the same cut as fewer segments
+    double t = static_cast<double>((heads * s + sms - 1) / sms) * (per + 1.5 + 0.3 * (s - 1));
+    if (s > 1) t += static_cast<double>((heads * (s - 1) + sms - 1) / sms) * (0.6 * per + 1.5);
+    if (t < 0.97 * best) {  // a finer cut has to earn its first launch
+      best = t;
+      at = s;
+    }
+  }
+  return at;
+}
+
+size_t tc_partial_bytes(long long heads, int passes, int segments, int dk, int dv) {
+  return sizeof(float) * static_cast<size_t>(heads) * passes * (segments - 1) * tc_pad(dk) * tc_pad(dv);
+}
+
+template <int DK, int DV>
+pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s) {
+  using Shape = TcShape<DK, DV>;
+  PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes));
+  const unsigned heads = static_cast<unsigned>(t.a.B) * t.a.H;
+  if (t.segments > 1) {
+    PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes));
+    k_la_tc<DK, DV, true><<<dim3(heads, t.segments - 1, passes), kTcThreads, Shape::kBytes, s>>>(t);
+    PC_LAUNCH_CHECK();
+  }
+  k_la_tc<DK, DV, false><<<dim3(heads, t.segments, passes), kTcThreads, Shape::kBytes, s>>>(t);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+// Runs the passes on the tensor cores; *done = false (and nothing launched) where a tensor's
+// alignment does not allow it.
+pc_status_t run_tc(const LaArgs& a, int passes, void* ws, cudaStream_t s, bool* done) {
+  *done = false;
+  LaTcArgs t{};
+  t.a = a;
+  for (int i = 0; i < passes; ++i) {
+    const LaPass& p = a.pass[i];
+    LaMaps& m = t.maps[i];
+    pc_status_t st = PC_OK;
+    if (!tc_output(p, a.T, a.H, a.B) || !tc_map(&m.q, m.q_ext, p.q, p.qs, p.dk, a.T, a.H, a.B, &st) ||
+        !tc_map(&m.k, m.k_ext, p.k, p.ks, p.dk, a.T, a.H, a.B, &st) ||
+        !tc_map(&m.v, m.v_ext, p.v, p.vs, p.dv, a.T, a.H, a.B, &st))
+      return st;
+  }
+  const long long heads = static_cast<long long>(a.B) * a.H;
+  t.segments = tc_segments(heads * passes, a.T);
+  const int nch = (a.T + kTcC - 1) / kTcC;
+  t.chunks_per_segment = (nch + t.segments - 1) / t.segments;
+  t.partial = static_cast<float*>(ws);
+  t.status = device_status_word();
+  *done = true;
+  // passes of one padded shape go in one launch
+  for (int i = 0; i < passes;) {
+    const int dk = tc_pad(a.pass[i].dk), dv = tc_pad(a.pass[i].dv);
+    int n = i + 1;
+    while (n < passes && tc_pad(a.pass[n].dk) == dk && tc_pad(a.pass[n].dv) == dv) ++n;
+    LaTcArgs part = t;
+    for (int j = i; j < n; ++j) {
+      part.a.pass[j - i] = t.a.pass[j];
+      part.maps[j - i] = t.maps[j];
+    }
+    part.partial = t.partial + tc_partial_bytes(heads, i, t.segments, dk, dv) / sizeof(float);
+    if (dk == 64 && dv == 64)
+      PC_TRY((launch_tc<64, 64>(part, n - i, s)));
+    else if (dk == 64)
+      PC_TRY((launch_tc<64, 128>(part, n - i, s)));
+    else if (dv == 64)
+      PC_TRY((launch_tc<128, 64>(part, n - i, s)));
+    else
+      PC_TRY((launch_tc<128, 128>(part, n - i, s)));
+    i = n;
+  }
+  return PC_OK;
+}
+
 // ------------------------------------------------------------------- a single token
 // S <- l S + k v^T and o = scale q^T S, in place. Memory-bound: 8 bytes of state per
 // 4 flops. A CTA takes one (b, h): each warp some rows of S, a lane 16 bytes of a row.
@@ -246,7 +334,24 @@ pc_status_t check_tensor(const char* name, const void* p, pc_dtype_t dt) {
   return PC_OK;
 }
 
-pc_status_t run_passes(const LaArgs& a, int passes, pc_dtype_t dt, cudaStream_t s) {
+// Workspace: the segments' shares of the state.
+size_t la_workspace(int B, int T, int H, int dk, int dv, int passes, pc_dtype_t dt) {
+  const long long heads = static_cast<long long>(B) * H;
+  if (!tc_heads(dk, dv, dt) || T == 0 || heads == 0) return 0;
+  return tc_partial_bytes(heads, passes, tc_segments(heads * passes, T), dk, dv);
+}
+
+pc_status_t run_passes(const LaArgs& a, int passes, pc_dtype_t dt, void* ws, size_t ws_bytes, cudaStream_t s) {
+  const LaPass& p = a.pass[0];
+  const size_t need = la_workspace(a.B, a.T, a.H, p.dk, p.dv, passes, dt);
+  PC_CHECK(need == 0 || (ws && ws_bytes >= need), PC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes,
+           need);
+  PC_CHECK(need == 0 || aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  if (a.T > 0 && tc_heads(p.dk, p.dv, dt)) {
+    bool done = false;
+    PC_TRY(run_tc(a, passes, ws, s, &done));
+    if (done) return PC_OK;
+  }
   return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, passes, s) : launch_simt<float>(a, passes, s);
 }
 
@@ -287,7 +392,7 @@ pc_status_t pc_linear_attention_workspace(int B, int T, int H, int Dk, int Dv, i
   pc::clear_error();
   PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
   PC_TRY(pc::check_la(B, T, H, Dk, Dv, dtype));
-  *bytes = 0;
+  *bytes = pc::la_workspace(B, T, H, Dk, Dv, with_backward ? 3 : 1, dtype);
   return PC_OK;
 }
 
@@ -314,7 +419,7 @@ pc_status_t pc_linear_attention_fwd(int B, int T, int H, int Dk, int Dv, const v
   a.lengths = lengths;
   a.pass[0] = pc::make_pass(q, strides, k, strides + 3, v, strides + 6, o, strides + 9, Dk, Dv, state, state_out,
                             false, false, scale);
-  return pc::run_passes(a, 1, dtype, stream);
+  return pc::run_passes(a, 1, dtype, ws, ws_bytes, stream);
 }
 
 pc_status_t pc_linear_attention_bwd(int B, int T, int H, int Dk, int Dv, const void* q, const void* k, const void* v,
@@ -342,7 +447,7 @@ pc_status_t pc_linear_attention_bwd(int B, int T, int H, int Dk, int Dv, const v
   a.pass[0] = pc::make_pass(d_o, gs, v, vs, k, ks, dq, strides + 12, Dv, Dk, state, nullptr, true, false, scale);
   a.pass[1] = pc::make_pass(v, vs, d_o, gs, q, qs, dk, strides + 15, Dv, Dk, dstate_out, nullptr, true, true, scale);
   a.pass[2] = pc::make_pass(k, ks, q, qs, d_o, gs, dv, strides + 18, Dk, Dv, dstate_out, dstate, false, true, scale);
-  return pc::run_passes(a, 3, dtype, stream);
+  return pc::run_passes(a, 3, dtype, ws, ws_bytes, stream);
 }
 
 pc_status_t pc_linear_attention_step(int B, int H, int Dk, int Dv, const void* q, const void* k, const void* v,
