@@ -204,6 +204,7 @@ pc_status_t encode_operand_map(CUtensorMap* map, const Operand& op, pc_precision
   const cuuint32_t box[3] = {cuuint32_t(128 / es), cuuint32_t(box_rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   const CUtensorMapDataType dt = p == PC_PREC_AUTO  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                 : p == kPrecF16Ops ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                  : p == kPrecFp8Ops ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                                     : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   const CUresult r = g_encode(map, dt,

@@ -1,26 +1,35 @@
-// Orthogonalised update: the nearest semi-orthogonal matrix direction of G by Newton-Schulz
-// products. X_0 = G / (|G|_F + eps), transposed when G is taller than wide (so that X is
-// M x N with M <= N), then `steps` times
+// Orthogonalised update: X_0 = G / (|G|_F + eps), transposed when G is taller than wide (so
+// that X is M x N with M <= N), then `steps` times
 //
 //   A = X X^T,   B = b A + c A A,   X <- a X + B X.
 //
-// The polynomial a s + b s^3 + c s^5 acts on the singular values of X and drives them to
-// one. Compute-bound from a few hundred rows on: M^2 N + M^3 + 2 M^2 N flops a step
-// when the symmetric halves of A and A A are taken once.
+// The polynomial a s + b s^3 + c s^5 acts on the singular values of X and drives them
+// towards one. Compute-bound from a few hundred rows on: M^2 N + M^3 + 2 M^2 N flops a
+// step, the symmetric halves of A and A A taken once (tiles on and above the diagonal,
+// mirrored by the epilogue).
 //
-// Every product runs on the tensor-core contraction with X and B in operand form; X is
-// kept both as rows (A = X X^T) and transposed (the right operand of B X).
-#include "pc_launch.cuh"
+// Operands are float16: the iteration's values are bounded (singular values below about
+// 1.3), so its 11 significant bits can be had at the tensor core's 16-bit rate, eight times
+// finer than bf16; precision PC_PREC_FP32 keeps hi + lo parts (22 bits) and three products.
+// Power-of-two factors keep every operand in float16's range: X is stored as Xs with X =
+// 2^-s Xs, 2^s ~ sqrt(N) (a row of X then has entries of about one), A as 2^12 A, B as
+// 2^10 B. The first Xs is G times a power of two alone (exact for bf16 G); the rest of
+// the norm, nu, enters with the first products in float32.
+#include <cuda_fp16.h>
+
+#include "pc_gemm.cuh"
+#include "pc_host.h"
 
 namespace pc {
 namespace {
 
-constexpr int kNormThreads = 256, kNormBlocks = 64;
+constexpr float kScaleA = 4096.f, kScaleB = 1024.f;
+
+// ------------------------------------------------------------------ norm and operands
+constexpr int kNormThreads = 256, kNormBlocks = 256;
 
 __device__ __forceinline__ float orth_value(const float* p) { return *p; }
-__device__ __forceinline__ float orth_value(const uint16_t* p) {
-  return __uint_as_float(static_cast<uint32_t>(*p) << 16);
-}
+__device__ __forceinline__ float orth_value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
 __device__ __forceinline__ float block_total(float v, float* red) {
 #pragma unroll
@@ -36,11 +45,20 @@ __device__ __forceinline__ float block_total(float v, float* red) {
 // part[g][block]: partial sums of squares, in an order that depends on the size alone.
 template <class T>
 __global__ void __launch_bounds__(kNormThreads) k_orth_squares(long long n, const T* __restrict__ g, float* part) {
+  grid_dependents_launch();
   __shared__ float red[kNormThreads / 32];
   const T* p = g + static_cast<long long>(blockIdx.y) * n;
+  const long long stride = static_cast<long long>(gridDim.x) * kNormThreads;
   float s = 0.f;
-  for (long long i = blockIdx.x * static_cast<long long>(kNormThreads) + threadIdx.x; i < n;
-       i += static_cast<long long>(gridDim.x) * kNormThreads) {
+  long long i = blockIdx.x * static_cast<long long>(kNormThreads) + threadIdx.x;
+  for (; i + 7 * stride < n; i += 8 * stride) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = orth_value(p + i + k * stride);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += v[k] * v[k];
+  }
+  for (; i < n; i += stride) {
     const float v = orth_value(p + i);
     s += v * v;
   }
@@ -48,189 +66,687 @@ __global__ void __launch_bounds__(kNormThreads) k_orth_squares(long long n, cons
   if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = s;
 }
 
-// inv[g] = 1 / (sqrt(sum of part[g]) + eps)
-__global__ void k_orth_inverse(int blocks, const float* part, float eps, float* inv) {
-  float s = 0.f;
-  for (int i = threadIdx.x; i < blocks; i += 32) s += part[blockIdx.x * kNormBlocks + i];
-#pragma unroll
-  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (threadIdx.x == 0) inv[blockIdx.x] = 1.f / (sqrtf(s) + eps);
+// A matrix of float16 operands: rows of ld elements, hi, then lo at +lo (0: none).
+struct HalfMat {
+  __half* ptr;
+  long long rows, cols, ld;
+  size_t lo;
+};
+
+__device__ __forceinline__ void half_split(float v, __half* hi, __half* lo) {
+  *hi = __float2half_rn(v);
+  *lo = __float2half_rn(v - __half2float(*hi));
 }
 
-// The operand writers of k_transpose64, scaled by inv[g].
-template <int P>
-struct ScaledStore {
-  StoreOperand<P> st;
-  const float* inv;
-  __device__ void operator()(int g, int c, int r, const float (&v)[8], int n) const {
-    const float k = inv[g];
-    float w[8];
+// Xs = 2^e G (or its transpose) over 64 x 64 tiles; nu[g] = 2^-e / (|G|_F + eps). 2^e brings
+// the root mean square of the entries near one, within float16's range for the largest.
+template <class T, int kParts>
+__global__ void __launch_bounds__(kNormThreads)
+    k_orth_load(int rows, int cols, const T* __restrict__ g, int blocks, const float* part, float eps, int tall,
+                HalfMat x, float* nu) {
+  __shared__ float red[kNormThreads / 32];
+  __shared__ float tile[64][65];
+  const int m = blockIdx.z, t = threadIdx.x;
+  const T* src = g + static_cast<long long>(m) * rows * cols;
+  const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = v[i] * k;
-    st(g, c, r, w, n);
+  for (int i = t; i < 64 * 64; i += kNormThreads) {
+    const int r = r0 + (i >> 6), c = c0 + (i & 63);
+    tile[i >> 6][i & 63] = r < rows && c < cols ? orth_value(src + static_cast<long long>(r) * cols + c) : 0.f;
   }
-};
-template <int P>
-struct ScaledRows {
-  StoreOperandRows<P> st;
-  const float* inv;
-  __device__ void operator()(int g, int r, int c, const float4& v, int n) const {
-    const float k = inv[g];
-    st(g, r, c, make_float4(v.x * k, v.y * k, v.z * k, v.w * k), n);
+  grid_dependency_wait();  // the sums of squares
+  grid_dependents_launch();
+  const float total = block_total(t < blocks ? part[m * kNormBlocks + t] : 0.f, red);
+  const float norm = sqrtf(total) + eps;
+  // 2^e sqrt(total) <= 2^15 and 2^e rms <= 2: exponents only. Zero (or a norm that is not
+  // finite): e = 0, and nu carries what comes of it.
+  int e = 0;
+  if (norm > 0.f && norm < 3e38f) {
+    int at;
+    frexpf(norm, &at);  // norm = f 2^at, f in [1/2, 1)
+    const int spread = (32 - __clz(rows) + 32 - __clz(cols)) / 2;  // sqrt(rows cols) within a factor of two
+    e = min(spread, 15) - at;
+    e = max(-126, min(e, 126));
   }
+  const float up = ldexpf(1.f, e);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) nu[m] = total == 0.f ? 0.f : ldexpf(1.f, -e) / norm;
+  __half* hi = x.ptr + static_cast<size_t>(m) * x.rows * x.ld;
+#pragma unroll
+  for (int i = t; i < 64 * 32; i += kNormThreads) {  // pairs of columns of the operand
+    const int rr = i >> 5, cc = 2 * (i & 31);
+    const int r = (tall ? c0 : r0) + rr, c = (tall ? r0 : c0) + cc;
+    if (r >= x.rows || c >= x.cols) continue;
+    const float v0 = up * (tall ? tile[cc][rr] : tile[rr][cc]);
+    const float v1 = up * (tall ? tile[cc + 1][rr] : tile[rr][cc + 1]);
+    __half h0, l0, h1, l1;
+    half_split(v0, &h0, &l0);
+    half_split(v1, &h1, &l1);
+    // the row padding (ld is even) takes the second value of an odd last column
+    const size_t at = static_cast<size_t>(r) * x.ld + c;
+    *reinterpret_cast<__half2*>(hi + at) = __halves2half2(h0, h1);
+    if constexpr (kParts == 2) *reinterpret_cast<__half2*>(hi + x.lo + at) = __halves2half2(l0, l1);
+  }
+}
+
+// ---------------------------------------------------------------------- the products
+enum OrthOp : int { kGram = 0, kPoly = 1, kApply = 2 };
+
+struct OrthArgs {
+  int tiles_m, tiles_n, batch;  // kGram, kPoly: tiles_m = tiles_n, pairs m <= n only
+  int num_kb;
+  int M, N;                     // valid rows and columns of the result
+  HalfMat prev;                 // kPoly: A; kApply: X
+  HalfMat to;                   // the result, in operand form
+  const float* nu;              // first step: the norm's factor, else NULL
+  float k0, k1;                 // see the epilogue
+  void* out;                    // last kApply: the caller's matrix, else NULL
+  int tall;
+  unsigned* status;
 };
 
-// --------------------------------------------------------------------- epilogues
-template <int P>
-struct EpiOrthGram : EpiNoHooks {  // A = D
-  struct Params {
-    void* A;
-    long long ld;
-    size_t lo;
-    int M;
-  };
-  __device__ static void apply(const Params& p, int g, int m0, int n0, int row, int col0, float (&v)[32], uint8_t*,
-                               float*) {
-    const int m = m0 + row, n = n0 + col0;
-    if (m >= p.M || n >= p.M) return;
-    const size_t idx = (static_cast<size_t>(g) * p.M + m) * p.ld + n;
-    store_operand_run<P>(p.A, idx, p.lo, v, min(32, p.M - n));
-  }
+template <int kParts, int BN>
+struct OrthShape {
+  static constexpr uint32_t kA = kBM * 128, kB = BN * 128;  // one part's 64 values of K
+  static constexpr uint32_t kStage = kParts * (kA + kB);
 };
 
-template <int P>
-struct EpiOrthPoly : EpiNoHooks {  // B = b A + c D
-  struct Params {
-    const void* A;
-    void* Bm;
-    long long ld;
-    size_t lo;
-    int M;
-    float b, c;
-  };
-  __device__ static void apply(const Params& p, int g, int m0, int n0, int row, int col0, float (&v)[32], uint8_t*,
-                               float*) {
-    const int m = m0 + row, n = n0 + col0;
-    if (m >= p.M || n >= p.M) return;
-    const size_t idx = (static_cast<size_t>(g) * p.M + m) * p.ld + n;
-    const int k = min(32, p.M - n);
-    float a[32];
-    load_operand_run<P>(p.A, idx, p.lo, a, k);
+__device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  umma_bf16(d, a, b, idesc, acc);  // kind::f16: the instruction descriptor names the type
+}
+
+// 32 consecutive values of a row of an operand, n of them valid.
+template <int kParts>
+__device__ __forceinline__ void load_half_run(const HalfMat& x, size_t at, float (&v)[32], int n) {
+  if (n == 32) {  // ld and the column are multiples of 32
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = p.b * a[i] + p.c * v[i];
-    store_operand_run<P>(p.Bm, idx, p.lo, v, k);
+    for (int q = 0; q < 4; ++q) {
+      const uint4 w = *reinterpret_cast<const uint4*>(x.ptr + at + 8 * q);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[k]));
+        v[8 * q + 2 * k] = f.x;
+        v[8 * q + 2 * k + 1] = f.y;
+      }
+      if constexpr (kParts == 2) {
+        const uint4 l = *reinterpret_cast<const uint4*>(x.ptr + x.lo + at + 8 * q);
+        const uint32_t ll[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ll[k]));
+          v[8 * q + 2 * k] += f.x;
+          v[8 * q + 2 * k + 1] += f.y;
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i] = i < n ? __half2float(x.ptr[at + i]) : 0.f;
+      if (kParts == 2 && i < n) v[i] += __half2float(x.ptr[x.lo + at + i]);
+    }
   }
-};
+}
+
+template <int kParts>
+__device__ __forceinline__ void store_half_run(const HalfMat& x, size_t at, const float (&v)[32], int n) {
+  uint32_t hi[16], lo[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    hi[i] = *reinterpret_cast<const uint32_t*>(&h);
+    if constexpr (kParts == 2) {
+      const float2 f = __half22float2(h);
+      const __half2 l = __floats2half2_rn(v[2 * i] - f.x, v[2 * i + 1] - f.y);
+      lo[i] = *reinterpret_cast<const uint32_t*>(&l);
+    }
+  }
+  if (n == 32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      *reinterpret_cast<uint4*>(x.ptr + at + 8 * q) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
+      if constexpr (kParts == 2)
+        *reinterpret_cast<uint4*>(x.ptr + x.lo + at + 8 * q) =
+            make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < n) {
+        x.ptr[at + i] = __ushort_as_half(static_cast<unsigned short>(hi[i >> 1] >> (16 * (i & 1))));
+        if constexpr (kParts == 2)
+          x.ptr[x.lo + at + i] = __ushort_as_half(static_cast<unsigned short>(lo[i >> 1] >> (16 * (i & 1))));
+      }
+  }
+}
 
 __device__ __forceinline__ void orth_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void orth_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-template <int P, class T>
-struct EpiOrthX : EpiNoHooks {  // X' = a X + D, as rows and transposed, or to the caller's matrix
-  struct Params {
-    const void* X;
-    void *Y, *YT;  // NULL on the last step
-    long long ld, ldt;
-    size_t lo, lot;
-    int M, N;
-    float a;
-    T* out;  // last step: [M][N], or [N][M] when tall
-    int tall;
-  };
-  __device__ static void apply(const Params& p, int g, int m0, int n0, int row, int col0, float (&v)[32], uint8_t*,
-                               float*) {
-    const int m = m0 + row, n = n0 + col0;
-    if (m >= p.M || n >= p.N) return;
-    const size_t idx = (static_cast<size_t>(g) * p.M + m) * p.ld + n;
-    const int k = min(32, p.N - n);
+// 32 columns from n of row m of D:
+//   kGram   2^12 A = k0 nu^2 D
+//   kPoly   2^10 B = k0 (2^12 A) + k1 D
+//   kApply  X' = k0 nu (k1 Xs + 2^-10 D), to Xs' or to the caller
+template <int kParts, int kOp, class T>
+__device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, int n, bool mirror, float (&v)[32]) {
+  if (m >= p.M || n >= p.N) return;
+  const int k = min(32, p.N - n);
+  const float nu = p.nu ? p.nu[g] : 1.f;
+  const size_t base = static_cast<size_t>(g) * p.to.rows * p.to.ld, at = base + static_cast<size_t>(m) * p.to.ld + n;
+  if constexpr (kOp == kGram) {
+    const float f = p.k0 * nu * nu;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= f;
+  } else {
     float x[32];
-    load_operand_run<P>(p.X, idx, p.lo, x, k);
+    load_half_run<kParts>(p.prev, static_cast<size_t>(g) * p.prev.rows * p.prev.ld +
+                                      static_cast<size_t>(m) * p.prev.ld + n, x, k);
+    if constexpr (kOp == kPoly) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] += p.a * x[i];
-    if (p.out) {
-      T* o = p.out + static_cast<size_t>(g) * p.M * p.N;
-#pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < k)
-          orth_store(o + (p.tall ? static_cast<size_t>(n + i) * p.M + m : static_cast<size_t>(m) * p.N + n + i), v[i]);
+      for (int i = 0; i < 32; ++i) v[i] = p.k0 * x[i] + p.k1 * v[i];
     } else {
-      store_operand_run<P>(p.Y, idx, p.lo, v, k);
-      // lanes hold consecutive m: each store covers one contiguous run of a row of X^T
+      const float f = p.k0 * nu;
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < k) store_operand<P>(p.YT, (static_cast<size_t>(g) * p.N + n + i) * p.ldt + m, p.lot, v[i]);
+      for (int i = 0; i < 32; ++i) v[i] = f * (p.k1 * x[i] + v[i] * (1.f / kScaleB));
     }
   }
+  if constexpr (kOp == kApply) {
+    if (p.out) {
+      T* o = static_cast<T*>(p.out) + static_cast<size_t>(g) * p.M * p.N;
+      if (p.tall) {  // lanes hold consecutive m: a store covers a run of one row
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < k) orth_store(o + static_cast<size_t>(n + i) * p.M + m, v[i]);
+      } else {
+        T* row = o + static_cast<size_t>(m) * p.N + n;
+        if (k == 32 && (reinterpret_cast<uintptr_t>(row) & 15) == 0) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 16 / sizeof(T)) {
+            if constexpr (sizeof(T) == 2)
+              *reinterpret_cast<uint4*>(row + i) =
+                  make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
+                             pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
+            else
+              *reinterpret_cast<float4*>(row + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (i < k) orth_store(row + i, v[i]);
+        }
+      }
+      return;
+    }
+  }
+  store_half_run<kParts>(p.to, at, v, k);
+  if constexpr (kOp != kApply) {
+    if (mirror) {  // lanes hold consecutive m: each store covers a run of row n + i
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < k) {
+          const size_t to = base + static_cast<size_t>(n + i) * p.to.ld + m;
+          __half hi, lo;
+          half_split(v[i], &hi, &lo);
+          p.to.ptr[to] = hi;
+          if constexpr (kParts == 2) p.to.ptr[p.to.lo + to] = lo;
+        }
+    }
+  }
+}
+
+// D = A B^T (kGram, kPoly: both K-major rows) or A B (kApply: B's rows run along K), tiles of
+// 128 x BN. kSplit CTAs of a cluster share a tile, each over its part of K, and exchange
+// their partial sums through distributed shared memory, each finishing BN / kSplit columns;
+// with kSplit = 1 the CTAs are persistent and the accumulator alternates between two
+// buffers, so that one tile's epilogue runs under the next one's products.
+//   warp 0 TMA, warp 1 MMA, warps 2-9 epilogue (two per lane quarter)
+// Two parts (hi + lo): three products a step, in slices of kSliceKb blocks of K that are
+// added up in registers, because the accumulator truncates.
+constexpr int kSliceKb = 2;
+constexpr int kOrthThreads = 64 + 8 * 32;
+
+template <int kParts, int BN, int kSplit>
+struct OrthRing {
+  // split tiles run one after the other in a chain of small launches: two CTAs per SM let
+  // a launch set up while the one before it finishes
+  static constexpr int kFit = ((kSplit > 1 && kParts == 1 ? 113 : 227) * 1024 - 2048) / OrthShape<kParts, BN>::kStage;
+  static constexpr int kStages = kFit < 6 ? kFit : 6;
+  static constexpr uint32_t kBytes = kStages * OrthShape<kParts, BN>::kStage + 2048;
 };
 
+template <int kParts, int BN, int kSplit, int kOp, class T>
+__global__ void __launch_bounds__(kOrthThreads, 1)
+    k_orth_gemm(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__ CUtensorMap a_lo,
+                const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
+                const __grid_constant__ OrthArgs p) {
+  using S = OrthShape<kParts, BN>;
+  constexpr int kStages = OrthRing<kParts, BN, kSplit>::kStages;
+  constexpr bool kPairs = kOp != kApply;
+  constexpr bool kSliced = kParts == 2;
+  constexpr uint32_t kCols = 2 * BN;  // two accumulators
+  static_assert(kStages >= 2 && kCols <= 512, "two stages, two accumulators");
+  static_assert(kSplit == 1 || (BN % (32 * kSplit) == 0 && (kSplit - 1) * kBM * (BN / kSplit) * 4 <= kStages * S::kStage),
+                "the ring holds the partial sums of the other CTAs");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * S::kStage);
+  uint64_t *empty = full + kStages, *acc_full = empty + kStages, *acc_empty = acc_full + 2, *mma_done = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = kSplit > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&acc_full[i], 1);
+        mbar_init(&acc_empty[i], 8);
+      }
+      mbar_init(mma_done, 1);
+      fence_barrier_init();
+      tma_prefetch_map(&a_hi);
+      tma_prefetch_map(&b_hi);
+    }
+    __syncwarp();
+    tmem_alloc(tmem_slot, kCols);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  grid_dependents_launch();
+
+  const int per_matrix = kPairs ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
+  const int num_tiles = per_matrix * p.batch;
+  const int tile0 = blockIdx.x / kSplit, tile_step = gridDim.x / kSplit;
+  auto tile_at = [&](int t, int& g, int& m0, int& n0) {
+    g = t / per_matrix;
+    int r = t - g * per_matrix;
+    if constexpr (kPairs) {  // pairs (i, j >= i), row by row
+      int i = 0;
+      while (r >= p.tiles_m - i) r -= p.tiles_m - i++;
+      m0 = i * kBM;
+      n0 = (i + r) * BN;
+    } else {  // neighbours share the columns' panel of X
+      m0 = (r % p.tiles_m) * kBM;
+      n0 = (r / p.tiles_m) * BN;
+    }
+  };
+  const int kb0 = p.num_kb * rank / kSplit, kb1 = p.num_kb * (rank + 1) / kSplit;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      grid_dependency_wait();
+      int it = 0, issued = 0;
+      bool ok = true;
+      for (int t = tile0; ok && t < num_tiles; t += tile_step) {
+        int g, m0, n0;
+        tile_at(t, g, m0, n0);
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(&empty[s], ((it / kStages) & 1) ^ 1, p.status, kErrTimeoutProducer)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[s], S::kStage);
+          uint8_t* base = smem + s * S::kStage;
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            const CUtensorMap* am = part ? &a_lo : &a_hi;
+            const CUtensorMap* bm = part ? &b_lo : &b_hi;
+            tma_load_3d(base + part * S::kA, am, &full[s], kb * 64, m0, g);
+            uint8_t* bt = base + kParts * S::kA + part * S::kB;
+            if constexpr (kOp == kApply) {
+#pragma unroll
+              for (int c = 0; c < BN; c += 64) tma_load_3d(bt + c * 128, bm, &full[s], n0 + c, kb * 64, g);
+            } else {
+              tma_load_3d(bt, bm, &full[s], kb * 64, n0, g);
+            }
+          }
+          issued = it + 1;
+        }
+      }
+      for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+        mbar_wait(&full[k % kStages], (k / kStages) & 1, p.status, kErrTimeoutDrain);
+    }
+    if constexpr (kSplit > 1) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // -------------------------------------------------------------- MMA issuer
+      constexpr uint32_t idesc = umma_idesc(0, kBM, BN) | (kOp == kApply ? kIdescBMN : 0u);  // 0: float16
+      int it = 0, unit = 0;
+      bool ok = true;
+      for (int t = tile0; ok && t < num_tiles; t += tile_step) {
+        for (int kb = kb0; ok && kb < kb1; ++unit) {
+          const int end = kSliced ? min(kb + kSliceKb, kb1) : kb1;
+          const int buf = unit & 1;
+          if (!mbar_wait(&acc_empty[buf], ((unit >> 1) & 1) ^ 1, p.status, kErrTimeoutMma)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + buf * BN;
+          uint32_t acc = 0;
+          for (; kb < end; ++kb, ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait(&full[s], (it / kStages) & 1, p.status, kErrTimeoutMma)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a = smem_addr(smem + s * S::kStage), b = a + kParts * S::kA;
+            auto product = [&](int pa, int pb) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint32_t bk = b + pb * S::kB;
+                const uint64_t bd = kOp == kApply ? umma_desc_sw128_mn(bk + kk * 2048, 64 * 128)
+                                                  : umma_desc_sw128(bk + kk * 32);
+                umma_f16(d, umma_desc_sw128(a + pa * S::kA + kk * 32), bd, idesc, acc);
+                acc = 1;
+              }
+            };
+            if constexpr (kParts == 2) {  // the small products first
+              product(1, 0);
+              product(0, 1);
+            }
+            product(0, 0);
+            umma_commit(&empty[s]);
+          }
+          umma_commit(&acc_full[buf]);  // also after a wait that gave up: the epilogue is released
+        }
+      }
+      umma_commit(mma_done);
+      mbar_wait(mma_done, 0, p.status, kErrTimeoutDrain);
+    }
+    if constexpr (kSplit > 1) {
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
+  } else {
+    // ------------------------------------------------------------------- epilogue
+    const int q = warp & 3, part = (warp - 2) >> 2;
+    const int row = q * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    constexpr int kChunks = BN / 64;  // 32-column chunks of this warp: part, part + 2, ..
+    grid_dependency_wait();
+    int unit = 0;
+    bool ok = true;
+    auto wait_unit = [&]() {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(&acc_full[unit & 1], (unit >> 1) & 1, p.status,
+                                                         kErrTimeoutEpilogue));
+      tc_fence_after();
+      return got;
+    };
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&acc_empty[unit & 1]);
+      ++unit;
+    };
+    for (int t = tile0; ok && t < num_tiles; t += tile_step) {
+      int g, m0, n0;
+      tile_at(t, g, m0, n0);
+      const bool mirror = kPairs && n0 != m0;
+      if constexpr (kSplit == 1 && !kSliced) {
+        ok = wait_unit();
+        if (!ok) break;
+#pragma unroll 1
+        for (int c = part * 32; c < BN; c += 64) {
+          float v[32];
+          tmem_ld_32x32(lanes + (unit & 1) * BN + c, v);
+          if (c + 64 >= BN) release();
+          orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + c, mirror, v);
+        }
+      } else {
+        float acc[kChunks][32];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[c][i] = 0.f;
+        const int slices = kSliced ? (kb1 - kb0 + kSliceKb - 1) / kSliceKb : (kb1 > kb0 ? 1 : 0);
+        for (int sl = 0; sl < slices && ok; ++sl) {
+          ok = wait_unit();
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c) {
+            float v[32];
+            tmem_ld_32x32(lanes + (unit & 1) * BN + (2 * c + part) * 32, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c][i] += v[i];
+          }
+          release();
+        }
+        if constexpr (kSplit == 1) {
+          if (ok) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c)
+              orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + (2 * c + part) * 32, mirror, acc[c]);
+          }
+        } else {
+          // chunk x belongs to rank x / kOwn; the others' sums land at [source][chunk][column][row]
+          constexpr int kOwn = BN / 32 / kSplit;
+          cluster_sync();  // every ring of the cluster is idle
+          auto slot = [&](int src, int own) { return ((src * kOwn + own) * 32 * kBM + row) * 4; };
+          if (ok) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const int x = 2 * c + part, owner = x / kOwn;
+              if (owner == rank) continue;
+              const uint32_t to = cluster_map(smem_addr(smem), owner) + slot(rank - (rank > owner), x % kOwn);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * kBM * 4), "f"(acc[c][i]) : "memory");
+            }
+          }
+          cluster_sync();  // the others' sums of this CTA's columns have landed
+          if (ok) {
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) {
+              const int x = 2 * c + part;
+              if (x / kOwn != rank) continue;
+#pragma unroll
+              for (int src = 0; src < kSplit - 1; ++src) {
+                const float* from = reinterpret_cast<const float*>(smem + slot(src, x % kOwn));
+#pragma unroll
+                for (int i = 0; i < 32; ++i) acc[c][i] += from[i * kBM];
+              }
+              orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + x * 32, mirror, acc[c]);
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kCols);
+  }
+}
+
+// --------------------------------------------------------------------------- launches
+inline unsigned blocks_of(long long a, long long b) { return static_cast<unsigned>((a + b - 1) / b); }
+
+template <int kParts, int BN, int kSplit, int kOp, class T>
+pc_status_t launch_orth(const OrthArgs& p, const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], cudaStream_t s,
+                        long long flops) {
+  constexpr uint32_t smem = OrthRing<kParts, BN, kSplit>::kBytes;
+  static_assert(smem <= 232448, "shared memory per CTA");
+  auto* kernel = k_orth_gemm<kParts, BN, kSplit, kOp, T>;
+  PC_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  const long long tiles =
+      static_cast<long long>(kOp == kApply ? p.tiles_m * static_cast<long long>(p.tiles_n)
+                                           : p.tiles_m * (p.tiles_m + 1ll) / 2) * p.batch;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kSplit;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(kSplit > 1 ? tiles * kSplit : (tiles < num_sms() ? tiles : num_sms())));
+  cfg.blockDim = dim3(kOrthThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = kSplit > 1 ? 2 : 1;
+  const int slot = profile_begin(s);
+  PC_CUDA(cudaLaunchKernelEx(&cfg, kernel, a[0], a[1], b[0], b[1], p));
+  PC_LAUNCH_CHECK();
+  profile_end(slot, s, PC_KIND_ORTHOGONALIZE, flops);
+  return PC_OK;
+}
+
+// CTAs of a cluster that share a tile: while they all fit the GPU at once and each keeps two
+// blocks of K or more.
+inline int split_of(long long tiles, int num_kb) {
+  int s = 1;
+  while (s < 4 && tiles * s * 2 <= num_sms() && num_kb >= 4 * s) s *= 2;
+  return s;
+}
+
+template <int kParts, int kOp, class T>
+pc_status_t run_product(OrthArgs p, const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], cudaStream_t s,
+                        long long flops) {
+  p.tiles_m = static_cast<int>(blocks_of(p.M, kBM));
+  const long long wide = static_cast<long long>(p.tiles_m) * blocks_of(p.N, 256) * p.batch;
+  if constexpr (kOp == kApply && kParts == 1) {
+    if (wide >= num_sms()) {
+      p.tiles_n = static_cast<int>(blocks_of(p.N, 256));
+      return launch_orth<kParts, 256, 1, kOp, T>(p, a, b, s, flops);
+    }
+  }
+  p.tiles_n = static_cast<int>(blocks_of(p.N, 128));
+  const long long tiles = (kOp == kApply ? p.tiles_m * static_cast<long long>(p.tiles_n)
+                                         : p.tiles_m * (p.tiles_m + 1ll) / 2) * p.batch;
+  switch (split_of(tiles, p.num_kb)) {
+    case 4: return launch_orth<kParts, 128, 4, kOp, T>(p, a, b, s, flops);
+    case 2: return launch_orth<kParts, 128, 2, kOp, T>(p, a, b, s, flops);
+    default: return launch_orth<kParts, 128, 1, kOp, T>(p, a, b, s, flops);
+  }
+}
+
 struct OrthPlan {
-  Operand X[2], XT[2], A, Bm;
-  float *part, *inv;
+  HalfMat X[2], A, Bm;
+  float *part, *nu;
   size_t bytes;
 };
 
-OrthPlan plan_orth(void* ws, int batch, int M, int N, pc_precision_t prec) {
+OrthPlan plan_orth(void* ws, int batch, int M, int N, int parts) {
   Carver c(ws);
   OrthPlan p;
+  auto mat = [&](int rows, int cols) {
+    HalfMat m;
+    m.rows = rows;
+    m.cols = cols;
+    m.ld = round_up(cols, 64);
+    const size_t n = static_cast<size_t>(batch) * rows * m.ld;
+    m.lo = parts == 2 ? n : 0;
+    m.ptr = static_cast<__half*>(c.take(n * parts * sizeof(__half)));
+    return m;
+  };
   p.part = static_cast<float*>(c.take(sizeof(float) * kNormBlocks * batch));
-  p.inv = static_cast<float*>(c.take(sizeof(float) * batch));
-  for (int i = 0; i < 2; ++i) {
-    p.X[i] = c.operand(prec, batch, M, N);
-    p.XT[i] = c.operand(prec, batch, N, M);
-  }
-  p.A = c.operand(prec, batch, M, M);
-  p.Bm = c.operand(prec, batch, M, M);
+  p.nu = static_cast<float*>(c.take(sizeof(float) * batch));
+  p.X[0] = mat(M, N);
+  p.X[1] = mat(M, N);
+  p.A = mat(M, M);
+  p.Bm = mat(M, M);
   p.bytes = c.used;
   return p;
 }
 
-// The products' precision: PC_PREC_AUTO takes TF32 operands.
-pc_precision_t operand_precision(pc_precision_t prec) { return prec == PC_PREC_AUTO ? PC_PREC_TF32 : prec; }
+// Maps of an operand's parts: boxes of 64 columns (128 bytes) x box_rows.
+pc_status_t half_maps(CUtensorMap (&map)[2], const HalfMat& x, int batch, int box_rows) {
+  for (int part = 0; part < 2; ++part) {
+    Operand o;
+    o.ptr = x.ptr + (part ? x.lo : 0);
+    o.rows = x.rows;
+    o.cols = x.cols;
+    o.ld = x.ld;
+    o.groups = batch;
+    PC_TRY(encode_operand_map(&map[part], o, kPrecF16Ops, box_rows, 0));
+  }
+  return PC_OK;
+}
 
-template <int P, class T>
+template <int kParts, class T>
 pc_status_t run_orth(int batch, int rows, int cols, const T* G, int steps, float a, float b, float c, float eps,
-                     T* out, pc_precision_t prec, void* ws, cudaStream_t s) {
-  using Src = typename std::conditional<sizeof(T) == 2, uint16_t, float>::type;
+                     T* out, void* ws, cudaStream_t s) {
   const int tall = rows > cols;
   const int M = tall ? cols : rows, N = tall ? rows : cols;
-  const OrthPlan p = plan_orth(ws, batch, M, N, prec);
-  const Src* src = reinterpret_cast<const Src*>(G);
+  const OrthPlan p = plan_orth(ws, batch, M, N, kParts);
   const long long n = static_cast<long long>(rows) * cols;
-  const int blocks = static_cast<int>(cdiv(n, 4 * kNormThreads) < kNormBlocks ? cdiv(n, 4 * kNormThreads) : kNormBlocks);
-  k_orth_squares<Src><<<dim3(blocks, batch), kNormThreads, 0, s>>>(n, src, p.part);
+  const int blocks = static_cast<int>(blocks_of(n, 8 * kNormThreads) < kNormBlocks ? blocks_of(n, 8 * kNormThreads)
+                                                                                   : kNormBlocks);
+  k_orth_squares<T><<<dim3(blocks, batch), kNormThreads, 0, s>>>(n, G, p.part);
   PC_LAUNCH_CHECK();
-  k_orth_inverse<<<batch, 32, 0, s>>>(blocks, p.part, eps, p.inv);
-  PC_LAUNCH_CHECK();
-  const Operand &same = tall ? p.XT[0] : p.X[0], &turned = tall ? p.X[0] : p.XT[0];
-  k_transpose64<ScaledStore<P>, ScaledRows<P>, Src><<<dim3(cdiv(cols, 64), cdiv(rows, 64), batch), 256, 0, s>>>(
-      src, cols, n, rows, cols, nullptr,
-      ScaledStore<P>{{turned.ptr, turned.ld, turned.lo_elems, static_cast<long long>(cols)}, p.inv},
-      ScaledRows<P>{{same.ptr, same.ld, same.lo_elems, static_cast<long long>(rows)}, p.inv});
-  PC_LAUNCH_CHECK();
-  constexpr int BN = 128;
-  OperandMaps mX[2], mXT[2], mA, mB;
-  for (int i = 0; i < 2; ++i) {
-    PC_TRY(encode_maps(&mX[i], p.X[i], prec, 128));
-    PC_TRY(encode_maps(&mXT[i], p.XT[i], prec, 128));
+  {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks_of(cols, 64), blocks_of(rows, 64), batch);
+    cfg.blockDim = dim3(kNormThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    PC_CUDA(cudaLaunchKernelEx(&cfg, k_orth_load<T, kParts>, rows, cols, G, blocks, static_cast<const float*>(p.part),
+                               eps, tall, p.X[0], p.nu));
+    PC_LAUNCH_CHECK();
   }
-  PC_TRY(encode_maps(&mA, p.A, prec, 128));
-  PC_TRY(encode_maps(&mB, p.Bm, prec, 128));
-  const dim3 square(cdiv(M, 128), cdiv(M, BN), batch), wide(cdiv(M, 128), cdiv(N, BN), batch);
+  CUtensorMap x_rows[2][2], x_cols[2][2], ma[2], mb[2];  // X as K-major rows, and as rows along K
+  for (int i = 0; i < 2; ++i) {
+    PC_TRY(half_maps(x_rows[i], p.X[i], batch, kBM));
+    PC_TRY(half_maps(x_cols[i], p.X[i], batch, 64));
+  }
+  PC_TRY(half_maps(ma, p.A, batch, kBM));
+  PC_TRY(half_maps(mb, p.Bm, batch, kBM));
+  int bits = 0;  // 2^s ~ sqrt(N)
+  while ((4ll << (2 * bits)) <= N) ++bits;
+  const float up = static_cast<float>(1 << bits), down = 1.f / up;
   const long long mm = static_cast<long long>(batch) * M * M;
+  OrthArgs q{};
+  q.batch = batch;
+  q.M = M;
+  q.status = device_status_word();
   for (int it = 0; it < steps; ++it) {
     const int i = it & 1;
     const bool last = it + 1 == steps;
-    PC_TRY((launch_gemm<P, BN, EpiOrthGram<P>>(square, mX[i].hi, mX[i].lo, mX[i].hi, mX[i].lo, num_k_blocks(N, prec),
-                                               {p.A.ptr, p.A.ld, p.A.lo_elems, M}, s, PC_KIND_ORTHOGONALIZE,
-                                               2 * mm * N)));
-    PC_TRY((launch_gemm<P, BN, EpiOrthPoly<P>>(square, mA.hi, mA.lo, mA.hi, mA.lo, num_k_blocks(M, prec),
-                                               {p.A.ptr, p.Bm.ptr, p.A.ld, p.A.lo_elems, M, b, c}, s,
-                                               PC_KIND_ORTHOGONALIZE, 2 * mm * M)));
-    PC_TRY((launch_gemm<P, BN, EpiOrthX<P, T>>(
-        wide, mB.hi, mB.lo, mXT[i].hi, mXT[i].lo, num_k_blocks(M, prec),
-        {p.X[i].ptr, p.X[i ^ 1].ptr, p.XT[i ^ 1].ptr, p.X[i].ld, p.XT[i].ld, p.X[i].lo_elems, p.XT[i].lo_elems, M, N,
-         a, last ? out : nullptr, tall},
-        s, PC_KIND_ORTHOGONALIZE, 2 * mm * N)));
+    OrthArgs gram = q;
+    gram.N = M;
+    gram.num_kb = static_cast<int>(blocks_of(N, 64));
+    gram.to = p.A;
+    gram.nu = it == 0 ? p.nu : nullptr;
+    gram.k0 = kScaleA * (it == 0 ? 1.f : down * down);
+    PC_TRY((run_product<kParts, kGram, T>(gram, x_rows[i], x_rows[i], s, mm * N)));
+    OrthArgs poly = q;
+    poly.N = M;
+    poly.num_kb = static_cast<int>(blocks_of(M, 64));
+    poly.prev = p.A;
+    poly.to = p.Bm;
+    poly.k0 = kScaleB / kScaleA * b;
+    poly.k1 = kScaleB / (kScaleA * kScaleA) * c;
+    PC_TRY((run_product<kParts, kPoly, T>(poly, ma, ma, s, mm * M)));
+    OrthArgs apply = q;
+    apply.N = N;
+    apply.num_kb = poly.num_kb;
+    apply.prev = p.X[i];
+    apply.to = p.X[i ^ 1];
+    apply.nu = gram.nu;
+    apply.k0 = (it == 0 ? 1.f : down) * (last ? 1.f : up);
+    apply.k1 = a;
+    apply.out = last ? out : nullptr;
+    apply.tall = tall;
+    PC_TRY((run_product<kParts, kApply, T>(apply, mb, x_cols[i], s, 2 * mm * N)));
   }
   return PC_OK;
 }
@@ -241,6 +757,8 @@ pc_status_t check_orth(int batch, int rows, int cols, int steps, pc_precision_t 
   PC_CHECK(batch >= 0 && batch <= 65535, PC_ERR_SHAPE, "batch must be in [0, 65535] (got %d)", batch);
   PC_CHECK(rows >= 1 && cols >= 1, PC_ERR_SHAPE, "rows and columns must be >= 1 (got %d, %d)", rows, cols);
   PC_CHECK(rows <= (1 << 20) && cols <= (1 << 20), PC_ERR_SHAPE, "rows and columns up to 2^20 (got %d, %d)", rows, cols);
+  const long long tiles = static_cast<long long>(blocks_of(rows, kBM)) * blocks_of(cols, kBM) * batch;
+  PC_CHECK(tiles < (1ll << 29), PC_ERR_SHAPE, "batch * rows * cols too large (%d matrices of %d x %d)", batch, rows, cols);
   PC_CHECK(steps >= 1 && steps <= 100, PC_ERR_SHAPE, "steps must be in [1, 100] (got %d)", steps);
   return PC_OK;
 }
@@ -255,7 +773,7 @@ pc_status_t pc_orthogonalize_workspace(int batch, int rows, int cols, pc_precisi
   PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
   PC_TRY(pc::check_orth(batch, rows, cols, 1, prec, PC_F32));
   const int M = rows < cols ? rows : cols, N = rows < cols ? cols : rows;
-  *bytes = pc::plan_orth(nullptr, batch, M, N, pc::operand_precision(prec)).bytes;
+  *bytes = pc::plan_orth(nullptr, batch, M, N, prec == PC_PREC_FP32 ? 2 : 1).bytes;
   return PC_OK;
 }
 
@@ -272,18 +790,18 @@ pc_status_t pc_orthogonalize(int batch, int rows, int cols, const void* G, int s
   PC_TRY(pc_orthogonalize_workspace(batch, rows, cols, prec, &need));
   PC_CHECK(ws && ws_bytes >= need, PC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   PC_CHECK(pc::aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
-  const pc_precision_t op = pc::operand_precision(prec);
+  const bool two = prec == PC_PREC_FP32;
   using bf16 = __nv_bfloat16;
   if (dtype == PC_BF16) {
     const auto* g = static_cast<const bf16*>(G);
     auto* o = static_cast<bf16*>(out);
-    return op == PC_PREC_FP32 ? pc::run_orth<pc::kTF32x3>(batch, rows, cols, g, steps, a, b, c, eps, o, op, ws, stream)
-                              : pc::run_orth<pc::kTF32>(batch, rows, cols, g, steps, a, b, c, eps, o, op, ws, stream);
+    return two ? pc::run_orth<2>(batch, rows, cols, g, steps, a, b, c, eps, o, ws, stream)
+               : pc::run_orth<1>(batch, rows, cols, g, steps, a, b, c, eps, o, ws, stream);
   }
   const auto* g = static_cast<const float*>(G);
   auto* o = static_cast<float*>(out);
-  return op == PC_PREC_FP32 ? pc::run_orth<pc::kTF32x3>(batch, rows, cols, g, steps, a, b, c, eps, o, op, ws, stream)
-                            : pc::run_orth<pc::kTF32>(batch, rows, cols, g, steps, a, b, c, eps, o, op, ws, stream);
+  return two ? pc::run_orth<2>(batch, rows, cols, g, steps, a, b, c, eps, o, ws, stream)
+             : pc::run_orth<1>(batch, rows, cols, g, steps, a, b, c, eps, o, ws, stream);
 }
 
 }  // extern "C"
