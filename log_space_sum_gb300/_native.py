@@ -113,7 +113,7 @@ def load() -> C.CDLL:
 
 def call(name: str, *args) -> None:
     """Calls an entry point and raises PCError on a non-PC_OK status."""
-    lib = load()
+    lib = _lib or load()
     st = getattr(lib, name)(*args)
     if st != 0:
         raise PCError(name, st, lib.pc_last_error().decode())

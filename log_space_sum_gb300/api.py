@@ -12,6 +12,7 @@ change).
 from __future__ import annotations
 
 import ctypes as C
+import functools
 
 import torch
 
@@ -58,16 +59,18 @@ def _check(t: torch.Tensor, name: str, dtype=torch.float32, device=None):
 
 
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device) -> C.c_void_p:
-    return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    # the handle alone: torch.cuda.current_stream would build a Stream object for each call
+    index = device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
     """Scratch buffer of at least nbytes, cached per (device, stream)."""
-    key = (device, torch.cuda.current_stream(device).cuda_stream)
+    key = (device, _stream(device))
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
@@ -75,7 +78,10 @@ def workspace(nbytes: int, device) -> torch.Tensor:
     return ws
 
 
+@functools.lru_cache(maxsize=4096)
 def _query(name: str, *args) -> int:
+    """A workspace size: a function of its arguments and of the GPU's SM count (one model
+    of GPU per process)."""
     out = C.c_size_t(0)
     N.call(name, *args, C.byref(out))
     return out.value
@@ -430,7 +436,7 @@ def _elements(t, name, dtype=None, device=None):
 
 
 def _shaped(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t
 

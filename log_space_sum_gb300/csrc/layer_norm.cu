@@ -151,9 +151,10 @@ __global__ void __launch_bounds__(32 * kWarps * kRows)
 
 constexpr int kAnyThreads = 256;
 
-// Any row: longer than the registers hold, or not a whole number of aligned 16-byte
-// pieces. A CTA per row reads it three times (L1 and L2 serve the second and third).
-template <class T>
+// Any row: not a whole number of aligned 16-byte pieces, or longer than the registers hold.
+// A CTA per row; rows of up to kCols * 256 values are loaded once, longer ones (kCols = 0)
+// are read three times (L1 and L2 serve the second and third).
+template <class T, int kCols>
 __global__ void __launch_bounds__(kAnyThreads)
     k_ln_fwd_any(int dim, const T* __restrict__ x, long long x_ld, const float* __restrict__ w,
                  const float* __restrict__ b, float eps, T* __restrict__ y, long long y_ld, float* __restrict__ mean,
@@ -161,39 +162,67 @@ __global__ void __launch_bounds__(kAnyThreads)
   __shared__ float2 red[2][kAnyThreads / 32];
   const long long r = blockIdx.x;
   const T* xr = x + r * x_ld;
+  T* yr = y + r * y_ld;
+  float v[kCols > 0 ? kCols : 1];
   float s = 0.f;
-  for (int c = threadIdx.x; c < dim; c += kAnyThreads) s += to_float(xr[c]);
+  if constexpr (kCols > 0) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const int c = i * kAnyThreads + threadIdx.x;
+      v[i] = c < dim ? to_float(xr[c]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) s += v[i];
+  } else {
+    for (int c = threadIdx.x; c < dim; c += kAnyThreads) s += to_float(xr[c]);
+  }
   const float m = row_sum<kAnyThreads / 32>(s, 0.f, red[0]).x / dim;
   s = 0.f;
-  for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
-    const float d = to_float(xr[c]) - m;
-    s += d * d;
+  if constexpr (kCols > 0) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i)
+      if (i * kAnyThreads + threadIdx.x < dim) s += (v[i] - m) * (v[i] - m);
+  } else {
+    for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
+      const float d = to_float(xr[c]) - m;
+      s += d * d;
+    }
   }
   const float rs = 1.f / sqrtf(row_sum<kAnyThreads / 32>(s, 0.f, red[1]).x / dim + eps);
   if (threadIdx.x == 0) {
     if (mean) mean[r] = m;
     if (rstd) rstd[r] = rs;
   }
-  T* yr = y + r * y_ld;
-  for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
-    float v = (to_float(xr[c]) - m) * rs;
-    if (w) v *= w[c];
-    if (b) v += b[c];
-    from_float(v, yr + c);
+  auto put = [&](int c, float value) {
+    float z = (value - m) * rs;
+    if (w) z *= w[c];
+    if (b) z += b[c];
+    from_float(z, yr + c);
+  };
+  if constexpr (kCols > 0) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const int c = i * kAnyThreads + threadIdx.x;
+      if (c < dim) put(c, v[i]);
+    }
+  } else {
+    for (int c = threadIdx.x; c < dim; c += kAnyThreads) put(c, to_float(xr[c]));
   }
 }
 
 // ----------------------------------------------------------------------- backward
-// A CTA walks the rows blockIdx.x, + gridDim.x, ...; a thread keeps its columns' sums of
-// dy z and dy in registers over all of them and writes them once, as one row of the
-// partial sums part[2][gridDim.x][dim] (k_ln_reduce adds those rows in a fixed order).
-template <class T, int kWarps, int kVecs>
+// A CTA walks groups of kRows rows; a thread keeps its columns' sums of dy z and dy in
+// registers over all of them and writes them once, as one row of the partial sums
+// part[2][gridDim.x][dim] (k_ln_reduce adds those rows in a fixed order). All loads of
+// a group are in flight together and one barrier serves its rows' sums.
+template <class T, int kWarps, int kVecs, int kRows>
 __global__ void __launch_bounds__(32 * kWarps)
     k_ln_bwd(long long rows, int dim, const T* __restrict__ dy, long long dy_ld, const T* __restrict__ x,
              long long x_ld, const float* __restrict__ w, const float* __restrict__ mean,
              const float* __restrict__ rstd, T* __restrict__ dx, long long dx_ld, float* __restrict__ part) {
   constexpr int L = kLanes<T>, kThreads = 32 * kWarps;
-  __shared__ float2 red[2][kWarps];
+  grid_dependents_launch();
+  __shared__ float2 red[2][kWarps][kRows];
   const int t = threadIdx.x;
   float wv[kVecs][L], aw[kVecs][L], ab[kVecs][L];
 #pragma unroll
@@ -207,45 +236,76 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (w && c < dim) load_params<L>(w, c, wv[i]);
   }
   int flip = 0;
-  for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
-    const float m = mean[r], rs = rstd[r];
-    uint4 rx[kVecs], rd[kVecs];
+  for (long long r0 = static_cast<long long>(blockIdx.x) * kRows; r0 < rows;
+       r0 += static_cast<long long>(gridDim.x) * kRows, flip ^= 1) {
+    uint4 rx[kRows][kVecs], rd[kRows][kVecs];
+    float m[kRows], rs[kRows];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = (i * kThreads + t) * L;
-      rx[i] = rd[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (c < dim) {
-        rx[i] = __ldcs(reinterpret_cast<const uint4*>(x + r * x_ld + c));
-        rd[i] = __ldcs(reinterpret_cast<const uint4*>(dy + r * dy_ld + c));
+    for (int k = 0; k < kRows; ++k) {
+      const long long r = r0 + k;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int c = (i * kThreads + t) * L;
+        rx[k][i] = rd[k][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (c < dim && r < rows) {
+          rx[k][i] = __ldcs(reinterpret_cast<const uint4*>(x + r * x_ld + c));
+          rd[k][i] = __ldcs(reinterpret_cast<const uint4*>(dy + r * dy_ld + c));
+        }
       }
+      m[k] = r < rows ? mean[r] : 0.f;
+      rs[k] = r < rows ? rstd[r] : 0.f;
     }
-    float sg = 0.f, sz = 0.f;
+    float sg[kRows], sz[kRows];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      float xv[L], dv[L];
-      unpack(rx[i], xv);
-      unpack(rd[i], dv);
+    for (int k = 0; k < kRows; ++k) {
+      sg[k] = sz[k] = 0.f;
 #pragma unroll
-      for (int j = 0; j < L; ++j) {  // past dim: dy = 0 adds nothing
-        const float z = (xv[j] - m) * rs, g = dv[j] * wv[i][j];
-        aw[i][j] += dv[j] * z;
-        ab[i][j] += dv[j];
-        sg += g;
-        sz += g * z;
-      }
-    }
-    const float2 sums = row_sum<kWarps>(sg, sz, red[flip]);
-    const float mg = sums.x / dim, mz = sums.y / dim;
-#pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-      const int c = (i * kThreads + t) * L;
-      if (c < dim) {
+      for (int i = 0; i < kVecs; ++i) {
         float xv[L], dv[L];
-        unpack(rx[i], xv);
-        unpack(rd[i], dv);
+        unpack(rx[k][i], xv);
+        unpack(rd[k][i], dv);
+        if (r0 + k < rows) {
 #pragma unroll
-        for (int j = 0; j < L; ++j) dv[j] = rs * (dv[j] * wv[i][j] - mg - (xv[j] - m) * rs * mz);
-        __stcs(reinterpret_cast<uint4*>(dx + r * dx_ld + c), pack(dv));
+          for (int j = 0; j < L; ++j) {  // past dim: dy = 0 adds nothing
+            const float z = (xv[j] - m[k]) * rs[k], g = dv[j] * wv[i][j];
+            aw[i][j] += dv[j] * z;
+            ab[i][j] += dv[j];
+            sg[k] += g;
+            sz[k] += g * z;
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        sg[k] += __shfl_xor_sync(0xffffffffu, sg[k], o);
+        sz[k] += __shfl_xor_sync(0xffffffffu, sz[k], o);
+      }
+      if ((t & 31) == 0) red[flip][t >> 5][k] = make_float2(sg[k], sz[k]);
+    }
+    __syncthreads();  // the other copy of red is rewritten only after the next barrier
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const long long r = r0 + k;
+      if (r >= rows) break;
+      float mg = 0.f, mz = 0.f;
+#pragma unroll
+      for (int q = 0; q < kWarps; ++q) {
+        mg += red[flip][q][k].x;
+        mz += red[flip][q][k].y;
+      }
+      mg /= dim;
+      mz /= dim;
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const int c = (i * kThreads + t) * L;
+        if (c < dim) {
+          float xv[L], dv[L];
+          unpack(rx[k][i], xv);
+          unpack(rd[k][i], dv);
+#pragma unroll
+          for (int j = 0; j < L; ++j) dv[j] = rs[k] * (dv[j] * wv[i][j] - mg - (xv[j] - m[k]) * rs[k] * mz);
+          __stcs(reinterpret_cast<uint4*>(dx + r * dx_ld + c), pack(dv));
+        }
       }
     }
   }
@@ -266,62 +326,124 @@ __global__ void __launch_bounds__(32 * kWarps)
   }
 }
 
-// Any row length and alignment: the columns' sums live in the CTA's own row of `part`
-// (each column is one thread's, so the read-modify-write needs no atomics).
-template <class T>
+// Any row length and alignment, a CTA per row at a time. Rows of up to kCols * 256 values
+// live in registers as above, loaded one value at a time (consecutive lanes, consecutive
+// addresses); for longer ones (kCols = 0) the row is read twice and the columns' sums live
+// in the CTA's own row of `part` (each column is one thread's: no atomics).
+template <class T, int kCols>
 __global__ void __launch_bounds__(kAnyThreads)
     k_ln_bwd_any(long long rows, int dim, const T* __restrict__ dy, long long dy_ld, const T* __restrict__ x,
                  long long x_ld, const float* __restrict__ w, const float* __restrict__ mean,
                  const float* __restrict__ rstd, T* __restrict__ dx, long long dx_ld, float* part) {
+  grid_dependents_launch();
   __shared__ float2 red[2][kAnyThreads / 32];
   float* pw = part ? part + static_cast<long long>(blockIdx.x) * dim : nullptr;
   float* pb = part ? pw + static_cast<long long>(gridDim.x) * dim : nullptr;
-  if (part)
-    for (int c = threadIdx.x; c < dim; c += kAnyThreads) pw[c] = pb[c] = 0.f;
   int flip = 0;
-  for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
-    const float m = mean[r], rs = rstd[r];
-    const T *xr = x + r * x_ld, *dr = dy + r * dy_ld;
-    float sg = 0.f, sz = 0.f;
-    for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
-      const float z = (to_float(xr[c]) - m) * rs, d = to_float(dr[c]), g = w ? d * w[c] : d;
-      if (part) {
-        pw[c] += d * z;
-        pb[c] += d;
-      }
-      sg += g;
-      sz += g * z;
+  if constexpr (kCols > 0) {
+    float wv[kCols], aw[kCols], ab[kCols];
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const int c = i * kAnyThreads + threadIdx.x;
+      aw[i] = ab[i] = 0.f;
+      wv[i] = w && c < dim ? w[c] : 1.f;
     }
-    const float2 sums = row_sum<kAnyThreads / 32>(sg, sz, red[flip]);
-    const float mg = sums.x / dim, mz = sums.y / dim;
-    for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
-      const float z = (to_float(xr[c]) - m) * rs, d = to_float(dr[c]), g = w ? d * w[c] : d;
-      from_float(rs * (g - mg - z * mz), dx + r * dx_ld + c);
+    for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
+      const T *xr = x + r * x_ld, *dr = dy + r * dy_ld;
+      float z[kCols], g[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const int c = i * kAnyThreads + threadIdx.x;
+        z[i] = c < dim ? to_float(xr[c]) : 0.f;
+        g[i] = c < dim ? to_float(dr[c]) : 0.f;
+      }
+      const float m = mean[r], rs = rstd[r];
+      float sg = 0.f, sz = 0.f;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        z[i] = (z[i] - m) * rs;
+        aw[i] += g[i] * z[i];
+        ab[i] += g[i];
+        g[i] *= wv[i];
+        sg += g[i];
+        sz += g[i] * z[i];
+      }
+      const float2 sums = row_sum<kAnyThreads / 32>(sg, sz, red[flip]);
+      const float mg = sums.x / dim, mz = sums.y / dim;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const int c = i * kAnyThreads + threadIdx.x;
+        if (c < dim) from_float(rs * (g[i] - mg - z[i] * mz), dx + r * dx_ld + c);
+      }
+    }
+    if (part) {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const int c = i * kAnyThreads + threadIdx.x;
+        if (c < dim) {
+          pw[c] = aw[i];
+          pb[c] = ab[i];
+        }
+      }
+    }
+  } else {
+    if (part)
+      for (int c = threadIdx.x; c < dim; c += kAnyThreads) pw[c] = pb[c] = 0.f;
+    for (long long r = blockIdx.x; r < rows; r += gridDim.x, flip ^= 1) {
+      const float m = mean[r], rs = rstd[r];
+      const T *xr = x + r * x_ld, *dr = dy + r * dy_ld;
+      float sg = 0.f, sz = 0.f;
+      for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
+        const float z = (to_float(xr[c]) - m) * rs, d = to_float(dr[c]), g = w ? d * w[c] : d;
+        if (part) {
+          pw[c] += d * z;
+          pb[c] += d;
+        }
+        sg += g;
+        sz += g * z;
+      }
+      const float2 sums = row_sum<kAnyThreads / 32>(sg, sz, red[flip]);
+      const float mg = sums.x / dim, mz = sums.y / dim;
+      for (int c = threadIdx.x; c < dim; c += kAnyThreads) {
+        const float z = (to_float(xr[c]) - m) * rs, d = to_float(dr[c]), g = w ? d * w[c] : d;
+        from_float(rs * (g - mg - z * mz), dx + r * dx_ld + c);
+      }
     }
   }
 }
 
 // dweight[c] (+)= sum over n partial rows of part[0][.][c], dbias likewise from part[1].
-constexpr int kReduceCols = 32, kReduceRows = 16;
+constexpr int kReduceCols = 32, kReduceRows = 32;
 __global__ void __launch_bounds__(kReduceCols* kReduceRows)
     k_ln_reduce(int n, int dim, const float* __restrict__ part, float* __restrict__ dweight,
                 float* __restrict__ dbias, int accumulate) {
+  grid_dependency_wait();
   __shared__ float s[kReduceRows][kReduceCols + 1];
   float* out = blockIdx.y ? dbias : dweight;
   if (!out) return;
   const int c = blockIdx.x * kReduceCols + threadIdx.x;
   const float* p = part + (blockIdx.y ? static_cast<long long>(n) * dim : 0);
   float a = 0.f;
-  if (c < dim)
-    for (int r = threadIdx.y; r < n; r += kReduceRows) a += p[static_cast<long long>(r) * dim + c];
+  if (c < dim) {
+    int r = threadIdx.y;
+    for (; r + 7 * kReduceRows < n; r += 8 * kReduceRows) {  // eight loads in flight
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = p[static_cast<long long>(r + k * kReduceRows) * dim + c];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) a += v[k];
+    }
+#pragma unroll 4
+    for (; r < n; r += kReduceRows) a += p[static_cast<long long>(r) * dim + c];
+  }
   s[threadIdx.y][threadIdx.x] = a;
   __syncthreads();
-  if (threadIdx.y == 0 && c < dim) {
-    a = 0.f;
+  // warp y sums column y over the rows of s
+  a = s[threadIdx.x][threadIdx.y];
 #pragma unroll
-    for (int r = 0; r < kReduceRows; ++r) a += s[r][threadIdx.x];
-    out[c] = accumulate ? out[c] + a : a;
-  }
+  for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  const int col = blockIdx.x * kReduceCols + threadIdx.y;
+  if (threadIdx.x == 0 && col < dim) out[col] = accumulate ? out[col] + a : a;
 }
 
 // ------------------------------------------------------------------------- launches
@@ -348,6 +470,12 @@ void fwd_kernel(const LnFwd& a, cudaStream_t s) {
       a.rstd);
 }
 
+template <class T, int kCols>
+void fwd_any(const LnFwd& a, cudaStream_t s) {
+  k_ln_fwd_any<T, kCols><<<static_cast<unsigned>(a.rows), kAnyThreads, 0, s>>>(
+      a.dim, static_cast<const T*>(a.x), a.x_ld, a.w, a.b, a.eps, static_cast<T*>(a.y), a.y_ld, a.mean, a.rstd);
+}
+
 template <class T>
 void launch_fwd(const LnFwd& a, cudaStream_t s) {
   const bool vec = a.dim % kLanes<T> == 0 && rows_aligned(a.x, a.x_ld, sizeof(T)) &&
@@ -367,9 +495,12 @@ void launch_fwd(const LnFwd& a, cudaStream_t s) {
     fwd_kernel<T, 8, 4, 1>(a, s);
   else if (vec && pieces <= 2048)
     fwd_kernel<T, 16, 4, 1>(a, s);
+  else if (a.dim <= 4 * kAnyThreads)
+    fwd_any<T, 4>(a, s);
+  else if (a.dim <= 16 * kAnyThreads)
+    fwd_any<T, 16>(a, s);
   else
-    k_ln_fwd_any<T><<<static_cast<unsigned>(a.rows), kAnyThreads, 0, s>>>(
-        a.dim, static_cast<const T*>(a.x), a.x_ld, a.w, a.b, a.eps, static_cast<T*>(a.y), a.y_ld, a.mean, a.rstd);
+    fwd_any<T, 0>(a, s);
 }
 
 struct LnBwd {
@@ -393,9 +524,16 @@ unsigned bwd_grid(long long rows) {
   return static_cast<unsigned>(rows < most ? rows : most);
 }
 
-template <class T, int kWarps, int kVecs>
+template <class T, int kWarps, int kVecs, int kRows>
 void bwd_kernel(const LnBwd& a, cudaStream_t s) {
-  k_ln_bwd<T, kWarps, kVecs><<<a.grid, 32 * kWarps, 0, s>>>(
+  k_ln_bwd<T, kWarps, kVecs, kRows><<<a.grid, 32 * kWarps, 0, s>>>(
+      a.rows, a.dim, static_cast<const T*>(a.dy), a.dy_ld, static_cast<const T*>(a.x), a.x_ld, a.w, a.mean, a.rstd,
+      static_cast<T*>(a.dx), a.dx_ld, a.part);
+}
+
+template <class T, int kCols>
+void bwd_any(const LnBwd& a, cudaStream_t s) {
+  k_ln_bwd_any<T, kCols><<<a.grid, kAnyThreads, 0, s>>>(
       a.rows, a.dim, static_cast<const T*>(a.dy), a.dy_ld, static_cast<const T*>(a.x), a.x_ld, a.w, a.mean, a.rstd,
       static_cast<T*>(a.dx), a.dx_ld, a.part);
 }
@@ -406,20 +544,27 @@ void launch_bwd(const LnBwd& a, cudaStream_t s) {
                    rows_aligned(a.dy, a.dy_ld, sizeof(T)) && rows_aligned(a.dx, a.dx_ld, sizeof(T)) &&
                    (!a.w || aligned16(a.w));
   const int pieces = a.dim / kLanes<T>;
+  // four rows (two of the longest) in flight per CTA once each CTA has several
+  const bool many = a.rows >= 8ll * a.grid;
+  auto pick = [&](auto one, auto several) { many ? several() : one(); };
   if (vec && pieces <= 64)
-    bwd_kernel<T, 2, 1>(a, s);
+    pick([&] { bwd_kernel<T, 2, 1, 1>(a, s); }, [&] { bwd_kernel<T, 2, 1, 4>(a, s); });
   else if (vec && pieces <= 128)
-    bwd_kernel<T, 4, 1>(a, s);
+    pick([&] { bwd_kernel<T, 4, 1, 1>(a, s); }, [&] { bwd_kernel<T, 4, 1, 4>(a, s); });
   else if (vec && pieces <= 256)
-    bwd_kernel<T, 8, 1>(a, s);
+    pick([&] { bwd_kernel<T, 8, 1, 1>(a, s); }, [&] { bwd_kernel<T, 8, 1, 4>(a, s); });
   else if (vec && pieces <= 512)
-    bwd_kernel<T, 8, 2>(a, s);
+    pick([&] { bwd_kernel<T, 8, 2, 1>(a, s); }, [&] { bwd_kernel<T, 8, 2, 2>(a, s); });
   else if (vec && pieces <= 1024)
-    bwd_kernel<T, 16, 2>(a, s);
+    bwd_kernel<T, 16, 2, 1>(a, s);
+  else if (a.dim <= 4 * kAnyThreads)
+    bwd_any<T, 4>(a, s);
+  else if (a.dim <= 8 * kAnyThreads)
+    bwd_any<T, 8>(a, s);
+  else if (a.dim <= 16 * kAnyThreads)
+    bwd_any<T, 16>(a, s);
   else
-    k_ln_bwd_any<T><<<a.grid, kAnyThreads, 0, s>>>(
-        a.rows, a.dim, static_cast<const T*>(a.dy), a.dy_ld, static_cast<const T*>(a.x), a.x_ld, a.w, a.mean, a.rstd,
-        static_cast<T*>(a.dx), a.dx_ld, a.part);
+    bwd_any<T, 0>(a, s);
 }
 
 pc_status_t check_shape(long long rows, int dim) {
@@ -498,9 +643,17 @@ pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy, long long
     PC_LAUNCH_CHECK();
   }
   if (params) {  // no rows: the sums are zero
-    pc::k_ln_reduce<<<dim3((dim + pc::kReduceCols - 1) / pc::kReduceCols, 2),
-                      dim3(pc::kReduceCols, pc::kReduceRows), 0, stream>>>(
-        static_cast<int>(grid), dim, static_cast<const float*>(ws), dweight, dbias, accumulate);
+    cudaLaunchAttribute attr;  // set up while the rows are still being read
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((dim + pc::kReduceCols - 1) / pc::kReduceCols, 2);
+    cfg.blockDim = dim3(pc::kReduceCols, pc::kReduceRows);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    PC_CUDA(cudaLaunchKernelEx(&cfg, pc::k_ln_reduce, static_cast<int>(grid), dim, static_cast<const float*>(ws),
+                               dweight, dbias, accumulate));
     PC_LAUNCH_CHECK();
   }
   return PC_OK;

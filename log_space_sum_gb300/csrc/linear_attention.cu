@@ -283,29 +283,80 @@ pc_status_t run_tc(const LaArgs& a, int passes, void* ws, cudaStream_t s, bool* 
 
 // ------------------------------------------------------------------- a single token
 // S <- l S + k v^T and o = scale q^T S, in place. Memory-bound: 8 bytes of state per
-// 4 flops. A CTA takes one (b, h): each warp some rows of S, a lane 16 bytes of a row.
+// 4 flops. A CTA takes one (b, h). Rows of whole aligned 16-byte pieces (kVecLanes > 0):
+// kVecLanes lanes share a row of S, a thread keeps kRows rows in flight; otherwise
+// (0) a lane takes one value at a time.
 constexpr int kStepThreads = 256;
-template <class T>
+template <class T, int kVecLanes>
 __global__ void __launch_bounds__(kStepThreads)
     k_la_step(int H, int dk, int dv, const T* __restrict__ q, long long q_b, long long q_h, const T* __restrict__ k,
               long long k_b, long long k_h, const T* __restrict__ v, long long v_b, long long v_h,
               const float* __restrict__ log_decay, float scale, float* __restrict__ state, T* __restrict__ o,
               long long o_b, long long o_h) {
   __shared__ float part[kStepThreads / 32][kMaxHeadDim];
+  __shared__ float qs[kMaxHeadDim], ks[kMaxHeadDim];
   const int b = blockIdx.x / H, h = blockIdx.x % H;
   const float l = decay_pow(log_decay[h], 1);
   const T *qp = q + b * q_b + h * q_h, *kp = k + b * k_b + h * k_h, *vp = v + b * v_b + h * v_h;
   float* S = state + static_cast<long long>(blockIdx.x) * dk * dv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int c = lane; c < dv; c += 32) {
-    const float x = la_load(vp + c);
-    float acc = 0.f;
-    for (int d = warp; d < dk; d += kStepThreads / 32) {
-      const float s = l * S[d * dv + c] + la_load(kp + d) * x;
-      S[d * dv + c] = s;
-      acc += la_load(qp + d) * s;
+  for (int d = threadIdx.x; d < dk; d += kStepThreads) {
+    qs[d] = la_load(qp + d);
+    ks[d] = la_load(kp + d);
+  }
+  if constexpr (kVecLanes > 0) {
+    constexpr int kRows = 8, kGroups = kStepThreads / kVecLanes;  // rows in flight, rows at a time
+    const int c = (threadIdx.x % kVecLanes) * 4, first = threadIdx.x / kVecLanes;
+    const bool in = c < dv;
+    float x[4] = {}, acc[4] = {};
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = la_load(vp + c + i);
     }
-    part[warp][c] = acc;
+    __syncthreads();
+    for (int d0 = first; d0 < dk; d0 += kRows * kGroups) {
+      float4 s[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int d = d0 + i * kGroups;
+        if (in && d < dk) s[i] = __ldcs(reinterpret_cast<const float4*>(S + d * dv + c));
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int d = d0 + i * kGroups;
+        if (in && d < dk) {
+          const float kd = ks[d], qd = qs[d];
+          s[i] = make_float4(l * s[i].x + kd * x[0], l * s[i].y + kd * x[1], l * s[i].z + kd * x[2],
+                             l * s[i].w + kd * x[3]);
+          __stcs(reinterpret_cast<float4*>(S + d * dv + c), s[i]);
+          acc[0] += qd * s[i].x;
+          acc[1] += qd * s[i].y;
+          acc[2] += qd * s[i].z;
+          acc[3] += qd * s[i].w;
+        }
+      }
+    }
+#pragma unroll
+    for (int m = kVecLanes; m < 32; m <<= 1)  // the warp's rows
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], m);
+    if (lane < kVecLanes && in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part[warp][c + i] = acc[i];
+    }
+  } else {
+    __syncthreads();
+    for (int c = lane; c < dv; c += 32) {
+      const float x = la_load(vp + c);
+      float acc = 0.f;
+#pragma unroll 4
+      for (int d = warp; d < dk; d += kStepThreads / 32) {
+        const float s = l * S[d * dv + c] + ks[d] * x;
+        S[d * dv + c] = s;
+        acc += qs[d] * s;
+      }
+      part[warp][c] = acc;
+    }
   }
   __syncthreads();
   for (int c = threadIdx.x; c < dv; c += kStepThreads) {
@@ -314,6 +365,17 @@ __global__ void __launch_bounds__(kStepThreads)
     for (int w = 0; w < kStepThreads / 32; ++w) acc += part[w][c];
     la_store(o + b * o_b + h * o_h + c, acc * scale);
   }
+}
+
+template <class T>
+void launch_step(int B, int H, int dk, int dv, const void* q, const void* k, const void* v, const long long* s,
+                 const float* log_decay, float scale, float* state, void* o, cudaStream_t stream) {
+  auto* kernel = k_la_step<T, 0>;
+  if (dv % 4 == 0 && aligned16(state) && dv <= 128)
+    kernel = dv <= 32 ? k_la_step<T, 8> : dv <= 64 ? k_la_step<T, 16> : k_la_step<T, 32>;
+  kernel<<<static_cast<unsigned>(B) * H, kStepThreads, 0, stream>>>(
+      H, dk, dv, static_cast<const T*>(q), s[0], s[1], static_cast<const T*>(k), s[2], s[3],
+      static_cast<const T*>(v), s[4], s[5], log_decay, scale, state, static_cast<T*>(o), s[6], s[7]);
 }
 
 // ------------------------------------------------------------------------- checks
@@ -461,18 +523,10 @@ pc_status_t pc_linear_attention_step(int B, int H, int Dk, int Dv, const void* q
   PC_TRY(pc::check_tensor("k", k, dtype));
   PC_TRY(pc::check_tensor("v", v, dtype));
   PC_TRY(pc::check_tensor("o", o, dtype));
-  const long long* s = strides;
-  if (dtype == PC_BF16) {
-    using T = __nv_bfloat16;
-    pc::k_la_step<T><<<B * H, pc::kStepThreads, 0, stream>>>(
-        H, Dk, Dv, static_cast<const T*>(q), s[0], s[1], static_cast<const T*>(k), s[2], s[3],
-        static_cast<const T*>(v), s[4], s[5], log_decay, scale, state, static_cast<T*>(o), s[6], s[7]);
-  } else {
-    using T = float;
-    pc::k_la_step<T><<<B * H, pc::kStepThreads, 0, stream>>>(
-        H, Dk, Dv, static_cast<const T*>(q), s[0], s[1], static_cast<const T*>(k), s[2], s[3],
-        static_cast<const T*>(v), s[4], s[5], log_decay, scale, state, static_cast<T*>(o), s[6], s[7]);
-  }
+  if (dtype == PC_BF16)
+    pc::launch_step<__nv_bfloat16>(B, H, Dk, Dv, q, k, v, strides, log_decay, scale, state, o, stream);
+  else
+    pc::launch_step<float>(B, H, Dk, Dv, q, k, v, strides, log_decay, scale, state, o, stream);
   PC_LAUNCH_CHECK();
   return PC_OK;
 }

@@ -42,25 +42,54 @@ __device__ __forceinline__ float block_total(float v, float* red) {
   return s;
 }
 
-// part[g][block]: partial sums of squares, in an order that depends on the size alone.
+// 16 bytes of G: 8 bf16 or 4 float values.
 template <class T>
+constexpr int kPiece = 16 / sizeof(T);
+__device__ __forceinline__ void orth_unpack(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void orth_unpack(const uint4& u, float (&v)[4]) {
+  v[0] = __uint_as_float(u.x);
+  v[1] = __uint_as_float(u.y);
+  v[2] = __uint_as_float(u.z);
+  v[3] = __uint_as_float(u.w);
+}
+
+// part[g][block]: partial sums of squares, in an order that depends on the size alone. G is
+// 16-byte aligned; so is every matrix of a stack whose size is a whole number of pieces
+// (kVec), the others are read value by value.
+template <class T, bool kVec>
 __global__ void __launch_bounds__(kNormThreads) k_orth_squares(long long n, const T* __restrict__ g, float* part) {
   grid_dependents_launch();
   __shared__ float red[kNormThreads / 32];
+  constexpr int L = kVec ? kPiece<T> : 1, kFlight = kVec ? 4 : 8;
   const T* p = g + static_cast<long long>(blockIdx.y) * n;
   const long long stride = static_cast<long long>(gridDim.x) * kNormThreads;
   float s = 0.f;
-  long long i = blockIdx.x * static_cast<long long>(kNormThreads) + threadIdx.x;
-  for (; i + 7 * stride < n; i += 8 * stride) {
-    float v[8];
+  for (long long i = blockIdx.x * static_cast<long long>(kNormThreads) + threadIdx.x; i < n / L;
+       i += kFlight * stride) {
+    float v[kFlight][L];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = orth_value(p + i + k * stride);
+    for (int k = 0; k < kFlight; ++k) {
+      const long long at = i + k * stride;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += v[k] * v[k];
-  }
-  for (; i < n; i += stride) {
-    const float v = orth_value(p + i);
-    s += v * v;
+      for (int e = 0; e < L; ++e) v[k][e] = 0.f;
+      if (at < n / L) {
+        if constexpr (kVec)
+          orth_unpack(reinterpret_cast<const uint4*>(p)[at], v[k]);
+        else
+          v[k][0] = orth_value(p + at);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+#pragma unroll
+      for (int e = 0; e < L; ++e) s += v[k][e] * v[k][e];
   }
   s = block_total(s, red);
   if (threadIdx.x == 0) part[blockIdx.y * kNormBlocks + blockIdx.x] = s;
@@ -89,10 +118,21 @@ __global__ void __launch_bounds__(kNormThreads)
   const int m = blockIdx.z, t = threadIdx.x;
   const T* src = g + static_cast<long long>(m) * rows * cols;
   const int r0 = blockIdx.y * 64, c0 = blockIdx.x * 64;
+  constexpr int L = kPiece<T>, kPerRow = 64 / L;
 #pragma unroll
-  for (int i = t; i < 64 * 64; i += kNormThreads) {
-    const int r = r0 + (i >> 6), c = c0 + (i & 63);
-    tile[i >> 6][i & 63] = r < rows && c < cols ? orth_value(src + static_cast<long long>(r) * cols + c) : 0.f;
+  for (int i = t; i < 64 * kPerRow; i += kNormThreads) {
+    const int rr = i / kPerRow, cc = (i % kPerRow) * L;
+    const int r = r0 + rr, c = c0 + cc;
+    const T* at = src + static_cast<long long>(r) * cols + c;
+    float v[L];
+    if (r < rows && c + L <= cols && (reinterpret_cast<uintptr_t>(at) & 15) == 0) {
+      orth_unpack(*reinterpret_cast<const uint4*>(at), v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < L; ++e) v[e] = r < rows && c + e < cols ? orth_value(at + e) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < L; ++e) tile[rr][cc + e] = v[e];
   }
   grid_dependency_wait();  // the sums of squares
   grid_dependents_launch();
@@ -685,9 +725,13 @@ pc_status_t run_orth(int batch, int rows, int cols, const T* G, int steps, float
   const int M = tall ? cols : rows, N = tall ? rows : cols;
   const OrthPlan p = plan_orth(ws, batch, M, N, kParts);
   const long long n = static_cast<long long>(rows) * cols;
-  const int blocks = static_cast<int>(blocks_of(n, 8 * kNormThreads) < kNormBlocks ? blocks_of(n, 8 * kNormThreads)
-                                                                                   : kNormBlocks);
-  k_orth_squares<T><<<dim3(blocks, batch), kNormThreads, 0, s>>>(n, G, p.part);
+  const bool vec = n % kPiece<T> == 0;
+  const long long want = blocks_of(n, 2 * kNormThreads * (vec ? kPiece<T> : 1));
+  const int blocks = static_cast<int>(want < kNormBlocks ? want : kNormBlocks);
+  if (vec)
+    k_orth_squares<T, true><<<dim3(blocks, batch), kNormThreads, 0, s>>>(n, G, p.part);
+  else
+    k_orth_squares<T, false><<<dim3(blocks, batch), kNormThreads, 0, s>>>(n, G, p.part);
   PC_LAUNCH_CHECK();
   {
     cudaLaunchAttribute attr;
