@@ -247,7 +247,8 @@ pc_status_t run_tc(const LaArgs& a, int passes, void* ws, cudaStream_t s, bool* 
     pc_status_t st = PC_OK;
     if (!tc_output(p, a.T, a.H, a.B) || !tc_map(&m.q, m.q_ext, p.q, p.qs, p.dk, a.T, a.H, a.B, &st) ||
         !tc_map(&m.k, m.k_ext, p.k, p.ks, p.dk, a.T, a.H, a.B, &st) ||
-        !tc_map(&m.v, m.v_ext, p.v, p.vs, p.dv, a.T, a.H, a.B, &st))
+        !tc_map(&m.v, m.v_ext, p.v, p.vs, p.dv, a.T, a.H, a.B, &st) ||
+        !tc_map(&m.o, m.o_ext, p.o, p.os, p.dv, a.T, a.H, a.B, &st))
       return st;
   }
   const long long heads = static_cast<long long>(a.B) * a.H;

@@ -19,6 +19,7 @@
 //                and the columns (of S^T) in two halves
 //   warp 12      TMA: Q, K, V tiles of 128 tokens, two stages (96 KB each at head size 128)
 //   warp 13      MMA issuer
+//   warp 14      TMA store of O, staged in the place of the V tile it was made from
 // The state warps hold 64 floats of S^T beside 32 packed products each: setmaxnreg gives them
 // 168 registers, out of what the others leave of the launch's 4 x 128 (104, 72).
 //
@@ -36,8 +37,8 @@ constexpr int kTcThreads = 16 * 32;
 constexpr int kTcStages = 2;
 
 struct LaMaps {
-  CUtensorMap q, k, v;
-  int q_ext[2], k_ext[2], v_ext[2];  // 1: the map has this head / batch dimension, 0: shared
+  CUtensorMap q, k, v, o;
+  int q_ext[2], k_ext[2], v_ext[2], o_ext[2];  // 1: the map has this head / batch dimension, 0: shared
 };
 
 struct LaTcArgs {
@@ -91,13 +92,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* s_tile = smem + kTcStages * S::kStage;
-  float* pw0 = reinterpret_cast<float*>(smem + S::kFixed);  // l^n at pw[n], n = 0 .. C; 1 below
-  float* pw = pw0 + C;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kFixed + (2 * C + 4) * sizeof(float));
+  float* tables = reinterpret_cast<float*>(smem + S::kFixed);
+  float* pw = tables;                // l^n, n = 0 .. C
+  float* wt = tables + C + 4;        // weights of a full tile's tokens in the state
+  float* near = wt + C;              // c_intra l^(distance) from column j to the block's near edge, j = 0 .. 31
+  float* diag = near + 32 + 32;      // c_intra l^|d| at diag[d], d = -31 .. 31 (column - row)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kFixed + (2 * C + 4 + 128) * sizeof(float));
   uint64_t *qk_full = bars, *v_full = bars + 2, *empty = bars + 4, *sc_full = bars + 6, *oi_full = bars + 7,
            *o_full = bars + 8, *d_full = bars + 9, *p_ready = bars + 10, *sc_read = bars + 11, *o_free = bars + 12,
-           *vh_ready = bars + 13, *vl_ready = bars + 14, *s_ready = bars + 15, *mma_done = bars + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+           *vh_ready = bars + 13, *vl_ready = bars + 14, *s_ready = bars + 15, *mma_done = bars + 16, *o_staged = bars + 17;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
 
   const LaArgs& a = args.a;
   const LaPass& p = a.pass[blockIdx.z];
@@ -124,10 +128,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
     if (seg > final_seg || (n_steps <= 0 && !p.s_out)) return;
   }
 
-  for (int i = threadIdx.x; i < 2 * C + 1; i += kTcThreads) pw0[i] = i < C ? 1.f : decay_pow(g, i - C);
+  {
+    const int i = threadIdx.x;
+    if (i <= C) pw[i] = decay_pow(g, i);
+    if (i < C) wt[i] = p.c_up * decay_pow(g, p.reverse ? i + 1 : C - 1 - i);
+    if (i < 32) near[i] = p.c_intra * decay_pow(g, p.reverse ? i : 31 - i);
+    if (i < 63) diag[i - 31] = p.c_intra * decay_pow(g, i < 31 ? 31 - i : i - 31);
+  }
   if (warp == 0) {
     if (lane == 0) {
-      for (int i = 0; i < 10; ++i) mbar_init(&bars[i], 1);
+      for (int i = 0; i < 10; ++i)
+        if (kStates || (i != 4 && i != 5)) mbar_init(&bars[i], 1);
       mbar_init(p_ready, 4);
       mbar_init(sc_read, 4);
       mbar_init(o_free, 4);
@@ -135,6 +146,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       mbar_init(vl_ready, 8);
       mbar_init(s_ready, 8);
       mbar_init(mma_done, 1);
+      mbar_init(o_staged, 4);
+      if constexpr (!kStates) {  // a stage is free once its products are done and O has left it
+        mbar_init(&empty[0], 2);
+        mbar_init(&empty[1], 2);
+      }
       fence_barrier_init();
     }
     __syncwarp();
@@ -144,7 +160,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int dir = p.reverse ? 1 : -1;  // the direction of time in which exponents grow
   auto stage = [&](int n) { return smem + (n % kTcStages) * S::kStage; };  // Q, then K, then V
 
   if (warp < 4) {
@@ -166,19 +181,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
           if (past || c == quarter) {
             float v[32];
             tmem_ld_32x32(lanes + S::kScore + c * 32, v);
-            if (c == quarter) {  // l^gap at w[j], 1 where the mask gives 0
-              const float* w = pw + (p.reverse ? -lane : lane);
+            if (c == quarter) {
+              const int sign = p.reverse ? 1 : -1;
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
-                const float x = v[j] * (w[j * dir] * p.c_intra);
-                v[j] = (j - lane) * dir >= 0 ? x : 0.f;
+                const float x = v[j] * diag[j - lane];
+                v[j] = (j - lane) * sign >= 0 ? x : 0.f;
               }
             } else {
-              // l^gap = l^(distance to the block's near edge) l^(distance within it)
-              const float edge = pw[p.reverse ? c * 32 - i : i - c * 32 - 31] * p.c_intra;
-              const float* w = pw + (p.reverse ? 0 : 31);
+              // l^gap = l^(from the row to the block's near edge) l^(from there to the column)
+              const float edge = pw[p.reverse ? c * 32 - i : i - c * 32 - 31];
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] *= edge * w[j * dir];
+              for (int j = 0; j < 32; j += 4) {
+                const float4 w = *reinterpret_cast<const float4*>(near + j);
+                mul2(v[j], v[j + 1], edge * w.x, edge * w.y);
+                mul2(v[j + 2], v[j + 3], edge * w.z, edge * w.w);
+              }
             }
 #pragma unroll
             for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
@@ -194,13 +212,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         if (lane == 0) mbar_arrive(sc_read);
         if (!__all_sync(0xffffffffu, mbar_wait(oi_full, ph, status, kErrTimeoutEpilogue))) break;
         tc_fence_after();
-        const float inter = pw[p.reverse ? C - 1 - i : i - tile.pad + 1] * p.c_inter;
+        const float inter = pw[p.reverse ? C - 1 - i : max(i - tile.pad + 1, 0)] * p.c_inter;
 #pragma unroll 1
         for (int c = 0; c < DV; c += 32) {
           float v[32];
           tmem_ld_32x32(lanes + S::kOut + c, v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] *= inter;
+          for (int j = 0; j < 32; j += 2) mul2(v[j], v[j + 1], inter, inter);
           tmem_st_32x32(lanes + S::kOut + c, v);
         }
         tmem_wait_st();
@@ -209,29 +227,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         if (lane == 0) mbar_arrive(p_ready);
         if (!__all_sync(0xffffffffu, mbar_wait(o_full, ph, status, kErrTimeoutEpilogue))) break;
         tc_fence_after();
+        // a whole tile goes through shared memory in rows of 128 swizzled bytes, one that starts
+        // before the sequence (no store may) straight to global memory
         __nv_bfloat16* row = o + (tile.t0 + i) * p.os[1];
+        uint8_t* staged = stage(n) + 2 * S::kQBytes + i * 128;
 #pragma unroll 1
         for (int c = 0; c < DV; c += 32) {
           float v[32];
           tmem_ld_32x32(lanes + S::kOut + c, v);
-          if (i >= tile.pad) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8)
-              if (c + j < p.dv)
-                *reinterpret_cast<uint4*>(row + c + j) =
-                    make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                               pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+          for (int j = 0; j < 32; j += 8) {
+            const uint4 x = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                                       pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+            if (tile.pad == 0)
+              *reinterpret_cast<uint4*>(staged + (c / 64) * C * 128 + (((((c + j) % 64) / 8) ^ (i & 7)) << 4)) = x;
+            else if (i >= tile.pad && c + j < p.dv)
+              *reinterpret_cast<uint4*>(row + c + j) = x;
           }
         }
+        fence_async_shared();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(o_free);
+        if (lane == 0) {
+          mbar_arrive(o_free);
+          mbar_arrive(o_staged);
+        }
       }
     }
   } else if (warp < 12) {
     regs_up<168>();
     // --------------------------------------------------- the state, row r of S^T per thread
-    constexpr int kCols = DK / 2, kToks = C / 2;
+    constexpr int kCols = DK / 2, kToks = C / 2, kUnits = kToks / 16 * 2;
     const int quarter = warp & 3, r = quarter * 32 + lane, part = (warp - 4) >> 2;
     const bool active = quarter * 32 < DV;  // a warp with rows of S^T
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -262,6 +288,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         }
       }
     }
+    // this lane's row of the four 8 x 8 blocks of a unit: blocks 0, 1 the first eight tokens,
+    // 0, 2 the first eight rows of V^T
+    const int v_row = (lane & 7) + (lane & 16) / 2, v_piece = (lane >> 3) & 1;
     auto publish = [&]() {  // S^T in bf16, K-major rows of 128 bytes, swizzled
       if (active) {
 #pragma unroll
@@ -284,36 +313,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
       ok = __all_sync(0xffffffffu, mbar_wait(&v_full[n % kTcStages], (n / kTcStages) & 1, status, kErrTimeoutEpilogue));
       if (!ok) break;
-      uint32_t low[kToks / 2];
+      uint32_t low[kUnits][4];
       if (active) {
-        // column r of V: row t at t * 128 bytes, its 16-byte piece swizzled by t
-        const uint8_t* v = stage(n) + 2 * S::kQBytes + (r / 64) * C * 128 + part * kToks * 128 + (r & 7) * 2;
-        const int piece = (r % 64) / 8;
-        const float* w = p.reverse ? pw + 1 - tile.pad + part * kToks : pw + C - 1 - part * kToks;
+        // Units of 16 tokens x 16 rows of V^T: ldmatrix transposes four 8 x 8 blocks into the
+        // layout of the 16-lane store, a register holding two consecutive tokens of one row.
+        const uint32_t v = smem_addr(stage(n)) + 2 * S::kQBytes + (quarter / 2) * C * 128 + v_row * 128;
+        // a reversed tile's missing rows hold zeros, and its weights count from the first real one
+        const float* w = wt - (p.reverse ? tile.pad : 0) + part * kToks + 2 * (lane & 3);
+        const int first_tok = p.reverse ? tile.pad : 0;
 #pragma unroll
-        for (int t0 = 0; t0 < kToks; t0 += 32) {
-          uint32_t high[16], mid[16];
-#pragma unroll
-          for (int t = 0; t < 32; t += 2) {
-            float x[2];
+        for (int u = 0; u < kUnits; ++u) {
+          const int tok = part * kToks + (u / 2) * 16;  // the unit's first token
+          uint32_t x[4];
+          ldmatrix_x4_trans(v + tok * 128 + (((quarter & 1) * 4 + (u & 1) * 2 + v_piece) ^ (v_row & 7)) * 16, x);
+          float2 ww[2];
+          if (tok >= first_tok) {
+            ww[0] = make_float2(w[(u / 2) * 16], w[(u / 2) * 16 + 1]);
+            ww[1] = make_float2(w[(u / 2) * 16 + 8], w[(u / 2) * 16 + 9]);
+          } else {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const int tt = t0 + t + e;
-              const uint32_t bits = *reinterpret_cast<const uint16_t*>(v + tt * 128 + ((piece ^ (tt & 7)) << 4));
-              x[e] = __uint_as_float(bits << 16) * w[tt * dir];
+              const int t = tok + 8 * e + 2 * (lane & 3);
+              ww[e].x = t >= first_tok ? w[(u / 2) * 16 + 8 * e] : 0.f;
+              ww[e].y = t + 1 >= first_tok ? w[(u / 2) * 16 + 8 * e + 1] : 0.f;
             }
-            const uint32_t hi = pack_bf16x2(x[0], x[1]);
-            x[0] -= __uint_as_float(hi << 16);
-            x[1] -= __uint_as_float(hi & 0xFFFF0000u);
-            const uint32_t mi = pack_bf16x2(x[0], x[1]);
-            x[0] -= __uint_as_float(mi << 16);
-            x[1] -= __uint_as_float(mi & 0xFFFF0000u);
-            high[t / 2] = hi;
-            mid[t / 2] = mi;
-            low[(t0 + t) / 2] = pack_bf16x2(x[0], x[1]);
           }
-          tmem_st_32x16(lanes + S::kHigh + (part * kToks + t0) / 2, high);
-          tmem_st_32x16(lanes + S::kMid + (part * kToks + t0) / 2, mid);
+          uint32_t high[4], mid[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float a0 = __uint_as_float(x[e] << 16), a1 = __uint_as_float(x[e] & 0xFFFF0000u);
+            mul2(a0, a1, ww[e / 2].x, ww[e / 2].y);
+            high[e] = pack_bf16x2(a0, a1);
+            sub2_bf16(a0, a1, high[e]);
+            mid[e] = pack_bf16x2(a0, a1);
+            sub2_bf16(a0, a1, mid[e]);
+            low[u][e] = pack_bf16x2(a0, a1);
+          }
+          const uint32_t at = lanes + (static_cast<uint32_t>((u & 1) * 16) << 16) + tok / 2;
+          tmem_st_16x128_x2(at + S::kHigh, high);
+          tmem_st_16x128_x2(at + S::kMid, mid);
         }
         tmem_wait_st();
       }
@@ -327,12 +365,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       }
       if (active) {
 #pragma unroll
-        for (int t0 = 0; t0 < kToks / 2; t0 += 16) {
-          uint32_t x[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] = low[t0 + e];
-          tmem_st_32x16(lanes + S::kLow + part * (kToks / 2) + t0, x);
-        }
+        for (int u = 0; u < kUnits; ++u)
+          tmem_st_16x128_x2(lanes + (static_cast<uint32_t>((u & 1) * 16) << 16) + S::kLow +
+                                (part * kToks + (u / 2) * 16) / 2,
+                            low[u]);
         tmem_wait_st();
       }
       tc_fence_before();
@@ -348,7 +384,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
           float d[32];
           tmem_ld_32x32(lanes + S::kDelta + part * kCols + c, d);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) s[c + j] = carry * s[c + j] + p.c_up * d[j];
+          for (int j = 0; j < 32; j += 2) fma2(s[c + j], s[c + j + 1], carry, d[j], d[j + 1]);
         }
         tc_fence_before();
       }
@@ -403,68 +439,104 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         mbar_wait(&v_full[n % kTcStages], (n / kTcStages) & 1, status, kErrTimeoutDrain);
       }
     }
-    if (warp == 13 && lane == 0) {
-      // -------------------------------------------------------------- MMA issuer
+    if (!kStates && warp == 14 && lane == 0) {
+      // ------------------------------------------------------------ TMA store of O
+      const LaMaps& m = args.maps[blockIdx.z];
+      for (int n = 0; n < n_steps; ++n) {
+        const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
+        if (!mbar_wait(o_staged, n & 1, status, kErrTimeoutEpilogue)) break;
+        if (tile.pad == 0) {
+#pragma unroll
+          for (int x = 0; x < DV; x += 64)
+            tma_store_4d(&m.o, stage(n) + 2 * S::kQBytes + x * C * 2, x, tile.t0, h * m.o_ext[0], b * m.o_ext[1]);
+          bulk_commit_wait_read();
+        }
+        mbar_arrive(&empty[n % kTcStages]);
+      }
+    }
+    if (warp == 13) {
+      // ----------------- MMA issuer: the whole warp in step (uniform addresses), one lane issues
       constexpr uint32_t idesc_qk = umma_idesc(1, 128, C);
       constexpr uint32_t idesc_qs = umma_idesc(1, 128, DV);
       constexpr uint32_t idesc_pv = umma_idesc(1, 128, DV) | kIdescBMN;
       constexpr uint32_t idesc_up = umma_idesc(1, 128, DK) | kIdescBMN;
+      const bool leader = elect_one();
       auto wait = [&](uint64_t* bar, uint32_t ph) {
-        const bool ok = mbar_wait(bar, ph, status, kErrTimeoutMma);
+        const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, ph, status, kErrTimeoutMma));
         tc_fence_after();
         return ok;
       };
-      const uint32_t s_addr = smem_addr(s_tile);
+      const uint32_t base = smem_addr(smem);
+      const uint64_t s_desc = umma_desc_sw128(base + kTcStages * S::kStage);
       for (int n = 0; n < n_steps; ++n) {
         const int st = n % kTcStages;
         const uint32_t ph = n & 1, sph = (n / kTcStages) & 1;
-        const uint32_t q_addr = smem_addr(stage(n)), k_addr = q_addr + S::kQBytes, v_addr = k_addr + S::kQBytes;
+        const uint32_t q_addr = base + st * S::kStage;
+        const uint64_t q_desc = umma_desc_sw128(q_addr), k_desc = umma_desc_sw128(q_addr + S::kQBytes);
+        const uint64_t k_rows = umma_desc_sw128_mn(q_addr + S::kQBytes, C * 128);
+        const uint64_t v_rows = umma_desc_sw128_mn(q_addr + 2 * S::kQBytes, C * 128);
         auto update = [&](uint32_t a_col, bool fresh) {  // D (+)= A K over the chunk's tokens
 #pragma unroll
           for (int kk = 0; kk < C / 16; ++kk)
-            umma_bf16_ts(tmem + S::kDelta, tmem + a_col + kk * 8, umma_desc_sw128_mn(k_addr + kk * 2048, C * 128),
-                         idesc_up, fresh && kk == 0 ? 0u : 1u);
+            umma_bf16_ts(tmem + S::kDelta, tmem + a_col + kk * 8, k_rows + kk * (2048 >> 4), idesc_up,
+                         fresh && kk == 0 ? 0u : 1u);
         };
         if (!wait(&qk_full[st], sph)) break;
         if constexpr (!kStates) {
           // the score columns hold the last chunk's operands until its products are done
           if (n > 0 && !wait(d_full, ph ^ 1)) break;
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk) {
-            const uint32_t off = (kk / 4) * C * 128 + (kk % 4) * 32;
-            umma_bf16(tmem + S::kScore, umma_desc_sw128(q_addr + off), umma_desc_sw128(k_addr + off), idesc_qk,
-                      kk ? 1u : 0u);
+            for (int kk = 0; kk < DK / 16; ++kk) {
+              const uint32_t off = ((kk / 4) * C * 128 + (kk % 4) * 32) >> 4;
+              umma_bf16(tmem + S::kScore, q_desc + off, k_desc + off, idesc_qk, kk ? 1u : 0u);
+            }
+            umma_commit(sc_full);
           }
-          umma_commit(sc_full);
+          __syncwarp();
           if (!wait(s_ready, ph) || (n > 0 && !wait(o_free, ph ^ 1))) break;
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < DK / 16; ++kk)
-            umma_bf16(tmem + S::kOut, umma_desc_sw128(q_addr + (kk / 4) * C * 128 + (kk % 4) * 32),
-                      umma_desc_sw128(s_addr + (kk / 4) * DV * 128 + (kk % 4) * 32), idesc_qs, kk ? 1u : 0u);
-          umma_commit(oi_full);
+            for (int kk = 0; kk < DK / 16; ++kk)
+              umma_bf16(tmem + S::kOut, q_desc + (((kk / 4) * C * 128 + (kk % 4) * 32) >> 4),
+                        s_desc + (((kk / 4) * DV * 128 + (kk % 4) * 32) >> 4), idesc_qs, kk ? 1u : 0u);
+            umma_commit(oi_full);
+          }
+          __syncwarp();
         }
         if (!wait(vh_ready, ph)) break;
         if constexpr (kStates) {
           if (!wait(vl_ready, ph)) break;
-          update(S::kLow, true);  // the small part first: its sums lose least
-          update(S::kMid, false);
-          update(S::kHigh, false);
+          if (leader) {
+            update(S::kLow, true);  // the small part first: its sums lose least
+            update(S::kMid, false);
+            update(S::kHigh, false);
+          }
         } else {
-          update(S::kMid, true);
-          update(S::kHigh, false);
+          if (leader) {
+            update(S::kMid, true);
+            update(S::kHigh, false);
+          }
+          __syncwarp();
           if (!wait(p_ready, ph) || !wait(&v_full[st], sph)) break;
+          if (leader) {
 #pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk)
-            umma_bf16_ts(tmem + S::kOut, tmem + S::kScore + kk * 8, umma_desc_sw128_mn(v_addr + kk * 2048, C * 128),
-                         idesc_pv, 1u);
-          umma_commit(o_full);
+            for (int kk = 0; kk < C / 16; ++kk)
+              umma_bf16_ts(tmem + S::kOut, tmem + S::kScore + kk * 8, v_rows + kk * (2048 >> 4), idesc_pv, 1u);
+            umma_commit(o_full);
+          }
+          __syncwarp();
           if (!wait(vl_ready, ph)) break;
-          update(S::kLow, false);
+          if (leader) update(S::kLow, false);
         }
-        umma_commit(d_full);
-        umma_commit(&empty[st]);
+        if (leader) {
+          umma_commit(d_full);
+          umma_commit(&empty[st]);
+        }
+        __syncwarp();
       }
-      umma_commit(mma_done);
+      if (leader) umma_commit(mma_done);
+      __syncwarp();
       mbar_wait(mma_done, 0, status, kErrTimeoutDrain);
     }
   }

@@ -155,6 +155,20 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// 4-D tiled store from shared memory; x as for the loads, no coordinate negative; what lies
+// outside the tensor is not written.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int x, int y, int z, int w) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(src))
+               : "memory");
+}
+// Commits this thread's stores and waits until their source may be overwritten.
+__device__ __forceinline__ void bulk_commit_wait_read() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+
 // Orders this thread's shared-memory writes before later accesses by TMA and the tensor core.
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -347,6 +361,31 @@ __device__ __forceinline__ void tmem_st_32x32(uint32_t taddr, const float (&v)[3
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 16 lanes x 8 columns from the registers of an 8 x 8 block layout: thread t writes, for
+// r[0], r[1], r[2], r[3], lane t / 4 (+ 8 for the odd ones) and column t % 4 (+ 4 for the last two).
+__device__ __forceinline__ void tmem_st_16x128_x2(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+// Four 8 x 8 blocks of 16-bit values, transposed: lanes 8m .. 8m + 7 give the addresses of
+// block m's rows; thread t receives, of each block, rows 2 (t % 4) and the next of column t / 4.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Packed float32 pairs (sm_100 family): a += b and a += b + h * k, two lanes per instruction.
@@ -358,6 +397,37 @@ __device__ __forceinline__ void add2(float& a0, float& a1, uint32_t b0, uint32_t
       "mov.b64 {%0, %1}, a;\n\t}"
       : "+f"(a0), "+f"(a1)
       : "r"(b0), "r"(b1));
+}
+// a *= b, a = a * k + b, a -= the bf16 pair b, two lanes per instruction.
+__device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "mul.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void fma2(float& a0, float& a1, float k, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, k;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 b, {%3, %4};\n\t"
+      "mov.b64 k, {%2, %2};\n\t"
+      "fma.rn.f32x2 a, a, k, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(k), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void sub2_bf16(float& a0, float& a1, uint32_t b) {
+  asm("{\n\t.reg .b64 a, b;\n\t.reg .b32 b0, b1;\n\t"
+      "shl.b32 b0, %2, 16;\n\t"
+      "and.b32 b1, %2, 0xFFFF0000;\n\t"
+      "mov.b64 a, {%0, %1};\n\t"
+      "mov.b64 b, {b0, b1};\n\t"
+      "sub.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "r"(b));
 }
 // a += b + (b's exponent and sign bits) * k: b plus half an ulp of b (see half_ulp) for
 // k = 2^-24 (bit pattern 0x33800000), or a multiple of it.
