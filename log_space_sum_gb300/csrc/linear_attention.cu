@@ -195,9 +195,9 @@ bool tc_heads(int dk, int dv, pc_dtype_t dt) {
 int tc_pad(int d) { return d <= 64 ? 64 : 128; }
 
 // Segments of a sequence. One CTA per SM takes a segment; cutting a sequence into S makes
-// the first launch's states cost about 0.6 of a pass's chunks, and each CTA a start of
-// about one and a half chunks (measured at head size 128: 2 us a chunk, 1.2 us of states
-// alone, 3 us from a CTA's launch to its first product), and joining a segment's share 0.3.
+// the first launch's states cost about 0.5 of a pass's chunks, and each CTA a start of
+// about one chunk (measured at head size 128: 3.1 us a chunk, 1.5 us of states alone, 3 us
+// from a CTA's launch to its first product), and joining a segment's share 0.3.
 int tc_segments(long long heads, int T) {
   const int nch = (T + kTcC - 1) / kTcC;
   const long long sms = num_sms();
@@ -206,8 +206,8 @@ int tc_segments(long long heads, int T) {
   for (int s = 1; s <= nch && s <= 64; ++s) {
     const int per = (nch + s - 1) / s;
     if ((nch + per - 1) / per != s) continue;  // the same cut as fewer segments
-    double t = static_cast<double>((heads * s + sms - 1) / sms) * (per + 1.5 + 0.3 * (s - 1));
-    if (s > 1) t += static_cast<double>((heads * (s - 1) + sms - 1) / sms) * (0.6 * per + 1.5);
+    double t = static_cast<double>((heads * s + sms - 1) / sms) * (per + 1.0 + 0.3 * (s - 1));
+    if (s > 1) t += static_cast<double>((heads * (s - 1) + sms - 1) / sms) * (0.5 * per + 1.0);
     if (t < 0.97 * best) {  // a finer cut has to earn its first launch
       best = t;
       at = s;

@@ -9,19 +9,25 @@
 //   update  D  = (V w)^T K        A = V^T times the tokens' weights in tensor memory,
 //                                 B = K (MN-major); S^T <- l^m S^T + D
 //
-// V w is a float32 product: it enters as three bf16 parts (24 bits), so that the state has
-// float32 accuracy; D is summed over one chunk only and added to S in registers with
-// round-to-nearest adds, because the tensor core's accumulator truncates. Scores and the S
+// The weights w are float32, so V w takes four bf16 parts: with w = wh + wm + wl (8 bits each),
+// v wh = p1 + r1 and v wm = p2 + r2 exactly for p = rn(v w), r = fma(v, w, -p), and the parts are
+// p1, r1, p2 and rn(v wl + r2), one packed bf16 instruction each: the state has float32
+// accuracy. D is summed over one chunk only and added to S in registers with round-to-nearest
+// adds, because the tensor core's accumulator truncates. Scores and the S
 // that the queries read are rounded to bf16, once each, below the rounding of O.
 //
-//   warps 0-3    one row of the tile per thread: decay of the scores, O to global memory
-//   warps 4-11   one row of S^T per thread, the eight warps splitting the tokens (of V^T)
-//                and the columns (of S^T) in two halves
-//   warp 12      TMA: Q, K, V tiles of 128 tokens, two stages (96 KB each at head size 128)
-//   warp 13      MMA issuer
-//   warp 14      TMA store of O, staged in the place of the V tile it was made from
-// The state warps hold 64 floats of S^T beside 32 packed products each: setmaxnreg gives them
-// 168 registers, out of what the others leave of the launch's 4 x 128 (104, 72).
+//   warps 0-3    one row of the tile per thread: the decay of the scores and of Q S
+//   warps 4-7    one row of the tile per thread: O, staged in the place of the V tile it was
+//                made from
+//   warps 8-15   one row of S^T per thread: the parts of V^T w, in groups of 32 tokens (kStates:
+//                64; the first four warps the first half of them), then half of S^T's
+//                columns each
+//   warp 16      TMA: Q, K, V tiles of 128 tokens, two stages (96 KB each at head size 128)
+//   warp 17      MMA issuer
+//   warp 18      TMA store of O
+// The state warps hold 64 floats of S^T each: setmaxnreg gives them 128 registers, out of what
+// the others leave of the launch's 5 x 96 (2 x 80, 64; kStates: 168, 2 x 24, 64). A spill would cost more than
+// elsewhere: the tiles leave the L1 cache next to nothing.
 //
 // Segments: with fewer (b, h) than SMs a sequence is cut; a first launch (kStates) leaves
 // each segment's own contribution to the state, and each segment of the second adds up the
@@ -33,7 +39,7 @@
 namespace pc {
 
 constexpr int kTcC = 128;
-constexpr int kTcThreads = 16 * 32;
+constexpr int kTcThreads = 20 * 32;
 constexpr int kTcStages = 2;
 
 struct LaMaps {
@@ -59,12 +65,18 @@ struct TcShape {
   static constexpr uint32_t kBytes = kFixed + kTables + 1024;
   static_assert(kBytes <= 232448, "shared memory per CTA");
   // tensor memory columns
-  static constexpr uint32_t kScore = 0;           // float scores; the decayed ones, packed, in its lower half
-  static constexpr uint32_t kLow = 64;            // third part of V w, once the scores have been read
+  // float scores (128 columns); the decayed ones, packed, then take the first 64
+  static constexpr uint32_t kScore = 0;
   static constexpr uint32_t kOut = 128;
   static constexpr uint32_t kDelta = 256;
-  static constexpr uint32_t kHigh = 384, kMid = 448;
+  // the four parts of V^T w for a group of tokens, half a column each per token; two groups in
+  // turn (kStates: the second in the scores' place)
+  static constexpr uint32_t kParts = 384;
 };
+
+// Ends a batch of loads or stores: the addresses of the next are formed after it (all of
+// a row's at once would not fit the registers beside the state).
+__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
 
 template <int kRegs>
 __device__ __forceinline__ void regs_down() {
@@ -74,6 +86,25 @@ template <int kRegs>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
+
+// Parts wh, wm, wl of the weights of tokens 2i and 2i + 1 of a tile with `pad` missing rows.
+__device__ __forceinline__ void weight_parts(uint32_t* wp, int i, float g, const LaPass& p, int pad) {
+  float w[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int t = 2 * i + e;
+    w[e] = p.c_up * decay_pow(g, p.reverse ? max(t - pad + 1, 0) : kTcC - 1 - t);
+  }
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    const uint32_t x = pack_bf16x2(w[0], w[1]);
+    sub2_bf16(w[0], w[1], x);
+    wp[part * 64 + i] = x;
+  }
+}
+
+// Barrier of the eight state warps.
+__device__ __forceinline__ void state_bar_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
 
 // Tiles' rows along tokens, first coordinate of the tile of `step`, its missing rows.
 struct TcTile {
@@ -94,14 +125,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   uint8_t* s_tile = smem + kTcStages * S::kStage;
   float* tables = reinterpret_cast<float*>(smem + S::kFixed);
   float* pw = tables;                // l^n, n = 0 .. C
-  float* wt = tables + C + 4;        // weights of a full tile's tokens in the state
-  float* near = wt + C;              // c_intra l^(distance) from column j to the block's near edge, j = 0 .. 31
+  uint32_t* wp = reinterpret_cast<uint32_t*>(tables + C + 4);  // [3][64]: bf16 parts of the tokens' weights, by pairs
+  float* near = tables + C + 4 + 192;  // c_intra l^(distance) from column j to the block's near edge, j = 0 .. 31
   float* diag = near + 32 + 32;      // c_intra l^|d| at diag[d], d = -31 .. 31 (column - row)
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kFixed + (2 * C + 4 + 128) * sizeof(float));
-  uint64_t *qk_full = bars, *v_full = bars + 2, *empty = bars + 4, *sc_full = bars + 6, *oi_full = bars + 7,
-           *o_full = bars + 8, *d_full = bars + 9, *p_ready = bars + 10, *sc_read = bars + 11, *o_free = bars + 12,
-           *vh_ready = bars + 13, *vl_ready = bars + 14, *s_ready = bars + 15, *mma_done = bars + 16, *o_staged = bars + 17;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kFixed + (C + 4 + 192 + 128) * sizeof(float));
+  uint64_t *q_full = bars, *v_full = bars + 2, *sc_full = bars + 6, *oi_full = bars + 7,
+           *o_full = bars + 8, *d_full = bars + 9, *p_ready = bars + 10, *o_free = bars + 11, *s_ready = bars + 12,
+           *mma_done = bars + 13, *o_staged = bars + 14, *up_ready = bars + 15, *up_free = bars + 17;
+  uint64_t *q_empty = bars + 19, *k_empty = bars + 21, *v_empty = bars + 4, *k_full = bars + 23;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
 
   const LaArgs& a = args.a;
   const LaPass& p = a.pass[blockIdx.z];
@@ -131,26 +163,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   {
     const int i = threadIdx.x;
     if (i <= C) pw[i] = decay_pow(g, i);
-    if (i < C) wt[i] = p.c_up * decay_pow(g, p.reverse ? i + 1 : C - 1 - i);
+    if (i < C / 2) weight_parts(wp, i, g, p, 0);
     if (i < 32) near[i] = p.c_intra * decay_pow(g, p.reverse ? i : 31 - i);
     if (i < 63) diag[i - 31] = p.c_intra * decay_pow(g, i < 31 ? 31 - i : i - 31);
   }
   if (warp == 0) {
     if (lane == 0) {
-      for (int i = 0; i < 10; ++i)
-        if (kStates || (i != 4 && i != 5)) mbar_init(&bars[i], 1);
-      mbar_init(p_ready, 4);
-      mbar_init(sc_read, 4);
-      mbar_init(o_free, 4);
-      mbar_init(vh_ready, 8);
-      mbar_init(vl_ready, 8);
-      mbar_init(s_ready, 8);
-      mbar_init(mma_done, 1);
-      mbar_init(o_staged, 4);
-      if constexpr (!kStates) {  // a stage is free once its products are done and O has left it
-        mbar_init(&empty[0], 2);
-        mbar_init(&empty[1], 2);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&q_full[i], 1);
+        mbar_init(&k_full[i], 1);
+        mbar_init(&v_full[i], 1);
+        mbar_init(&q_empty[i], 1);
+        mbar_init(&k_empty[i], 1);
+        mbar_init(&v_empty[i], 1);  // its products are done and, where O takes its place, O has left
       }
+      mbar_init(sc_full, 1);
+      mbar_init(oi_full, 1);
+      mbar_init(o_full, 1);
+      mbar_init(d_full, 1);
+      mbar_init(mma_done, 1);
+      mbar_init(p_ready, 4);
+      mbar_init(o_free, 4);
+      mbar_init(o_staged, 4);
+      mbar_init(s_ready, 8);
+      mbar_init(&up_ready[0], 8);
+      mbar_init(&up_ready[1], 8);
+      mbar_init(&up_free[0], 1);
+      mbar_init(&up_free[1], 1);
       fence_barrier_init();
     }
     __syncwarp();
@@ -160,119 +199,134 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  constexpr int kGroup = kStates ? 64 : 32, kGroups = C / kGroup;  // tokens of a group, groups of a tile
+  // parity of the use of buffer grp & 1 by group grp of step n
+  auto use_parity = [&](int n, int grp) { return static_cast<uint32_t>(n * (kGroups / 2) + (grp >> 1)) & 1u; };
+  auto parts = [&](int buf) { return kStates ? (buf ? S::kScore : S::kParts) : S::kParts + buf * 64; };
   auto stage = [&](int n) { return smem + (n % kTcStages) * S::kStage; };  // Q, then K, then V
 
-  if (warp < 4) {
-    regs_down<104>();
+  if (warp < 8) {
+    regs_down<kStates ? 24 : 80>();
     if constexpr (!kStates) {
       // ----------------------------------------------- scores and outputs, row i per thread
       const int quarter = warp & 3, i = quarter * 32 + lane;
       const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + b * p.os[0] + h * p.os[2];
-      for (int n = 0; n < n_steps; ++n) {
-        const uint32_t ph = n & 1;
-        const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
-        if (!__all_sync(0xffffffffu, mbar_wait(sc_full, ph, status, kErrTimeoutEpilogue))) break;
+      auto wait_mma = [&](uint64_t* bar, uint32_t ph) {
+        const bool got = __all_sync(0xffffffffu, mbar_wait(bar, ph, status, kErrTimeoutEpilogue));
         tc_fence_after();
+        return got;
+      };
+      if (warp < 4) {
+        for (int n = 0; n < n_steps; ++n) {
+          const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
+          if (!wait_mma(sc_full, n & 1)) break;
 #pragma unroll 1
-        for (int c = 0; c < C / 32; ++c) {
-          uint32_t packed[16];
-          const bool past = p.reverse ? c > quarter : c < quarter;
-          if (past || c == quarter) {
-            float v[32];
-            tmem_ld_32x32(lanes + S::kScore + c * 32, v);
-            if (c == quarter) {
-              const int sign = p.reverse ? 1 : -1;
+          for (int c = 0; c < C / 32; ++c) {
+            uint32_t packed[16];
+            const bool past = p.reverse ? c > quarter : c < quarter;
+            if (past || c == quarter) {
+              float v[32];
+              tmem_ld_32x32(lanes + S::kScore + c * 32, v);
+              if (c == quarter) {
+                if (p.reverse) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float x = v[j] * diag[j - lane];
-                v[j] = (j - lane) * sign >= 0 ? x : 0.f;
+                  for (int j = 0; j < 32; ++j) v[j] = j >= lane ? v[j] * diag[j - lane] : 0.f;
+                } else {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) v[j] = j <= lane ? v[j] * diag[j - lane] : 0.f;
+                }
+              } else {
+                // l^gap = l^(from the row to the block's near edge) l^(from there to the column)
+                const float edge = pw[p.reverse ? c * 32 - i : i - c * 32 - 31];
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                  const float4 w = *reinterpret_cast<const float4*>(near + j);
+                  mul2(v[j], v[j + 1], w.x, w.y);
+                  mul2(v[j + 2], v[j + 3], w.z, w.w);
+                  mul2(v[j], v[j + 1], edge, edge);
+                  mul2(v[j + 2], v[j + 3], edge, edge);
+                }
               }
+#pragma unroll
+              for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
             } else {
-              // l^gap = l^(from the row to the block's near edge) l^(from there to the column)
-              const float edge = pw[p.reverse ? c * 32 - i : i - c * 32 - 31];
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 w = *reinterpret_cast<const float4*>(near + j);
-                mul2(v[j], v[j + 1], edge * w.x, edge * w.y);
-                mul2(v[j + 2], v[j + 3], edge * w.z, edge * w.w);
-              }
+              for (int j = 0; j < 16; ++j) packed[j] = 0u;
             }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) packed[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) packed[j] = 0u;
+            // columns that this warp has read already
+            tmem_st_32x16(lanes + S::kScore + c * 16, packed);
           }
-          // columns that this warp has read already
-          tmem_st_32x16(lanes + S::kScore + c * 16, packed);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sc_read);
-        if (!__all_sync(0xffffffffu, mbar_wait(oi_full, ph, status, kErrTimeoutEpilogue))) break;
-        tc_fence_after();
-        const float inter = pw[p.reverse ? C - 1 - i : max(i - tile.pad + 1, 0)] * p.c_inter;
+          if (!wait_mma(oi_full, n & 1)) break;
+          const float inter = pw[p.reverse ? C - 1 - i : max(i - tile.pad + 1, 0)] * p.c_inter;
 #pragma unroll 1
-        for (int c = 0; c < DV; c += 32) {
-          float v[32];
-          tmem_ld_32x32(lanes + S::kOut + c, v);
+          for (int c = 0; c < DV; c += 32) {
+            float v[32];
+            tmem_ld_32x32(lanes + S::kOut + c, v);
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) mul2(v[j], v[j + 1], inter, inter);
-          tmem_st_32x32(lanes + S::kOut + c, v);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_ready);
-        if (!__all_sync(0xffffffffu, mbar_wait(o_full, ph, status, kErrTimeoutEpilogue))) break;
-        tc_fence_after();
-        // a whole tile goes through shared memory in rows of 128 swizzled bytes, one that starts
-        // before the sequence (no store may) straight to global memory
-        __nv_bfloat16* row = o + (tile.t0 + i) * p.os[1];
-        uint8_t* staged = stage(n) + 2 * S::kQBytes + i * 128;
-#pragma unroll 1
-        for (int c = 0; c < DV; c += 32) {
-          float v[32];
-          tmem_ld_32x32(lanes + S::kOut + c, v);
-#pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            const uint4 x = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                                       pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
-            if (tile.pad == 0)
-              *reinterpret_cast<uint4*>(staged + (c / 64) * C * 128 + (((((c + j) % 64) / 8) ^ (i & 7)) << 4)) = x;
-            else if (i >= tile.pad && c + j < p.dv)
-              *reinterpret_cast<uint4*>(row + c + j) = x;
+            for (int j = 0; j < 32; j += 2) mul2(v[j], v[j + 1], inter, inter);
+            tmem_st_32x32(lanes + S::kOut + c, v);
           }
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_ready);
         }
-        fence_async_shared();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(o_free);
-          mbar_arrive(o_staged);
+      } else {
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + b * p.os[0] + h * p.os[2];
+        for (int n = 0; n < n_steps; ++n) {
+          const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
+          if (!wait_mma(o_full, n & 1)) break;
+          // a whole tile goes through shared memory in rows of 128 swizzled bytes, one that starts
+          // before the sequence (no store may) straight to global memory
+          __nv_bfloat16* row = o + (tile.t0 + i) * p.os[1];
+          const uint32_t staged = smem_addr(stage(n)) + 2 * S::kQBytes + i * 128 + ((i & 7) << 4);
+#pragma unroll 1
+          for (int c = 0; c < DV; c += 32) {
+            float v[32];
+            tmem_ld_32x32(lanes + S::kOut + c, v);
+            const uint32_t at = (staged + (c / 64) * C * 128) ^ ((c % 64) * 2);
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              const uint4 x = make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                                         pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+              if (tile.pad == 0)
+                st_shared_v4(at ^ (j * 2), x.x, x.y, x.z, x.w);
+              else if (i >= tile.pad && c + j < p.dv)
+                *reinterpret_cast<uint4*>(row + c + j) = x;
+            }
+          }
+          fence_async_shared();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(o_free);
+            mbar_arrive(o_staged);
+          }
         }
       }
     }
-  } else if (warp < 12) {
-    regs_up<168>();
+  } else if (warp < 16) {
+    regs_up<kStates ? 168 : 128>();
     // --------------------------------------------------- the state, row r of S^T per thread
-    constexpr int kCols = DK / 2, kToks = C / 2, kUnits = kToks / 16 * 2;
-    const int quarter = warp & 3, r = quarter * 32 + lane, part = (warp - 4) >> 2;
+    constexpr int kCols = DK / 2;
+    const int quarter = warp & 3, r = quarter * 32 + lane, part = (warp - 8) >> 2;
     const bool active = quarter * 32 < DV;  // a warp with rows of S^T
     const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     float s[kCols];
 #pragma unroll
     for (int c = 0; c < kCols; ++c) s[c] = 0.f;
     if constexpr (!kStates) {
-      const long long size = static_cast<long long>(p.dk) * p.dv;
-      if (p.s_in && r < p.dv) {
-        const float* in = p.s_in + bh * size;
+      // S_0; where there is none the reads go to a valid address and their values are dropped
+      const bool given = p.s_in && r < p.dv;
+      const float* in = !given ? a.log_decay
+                               : p.s_in + bh * static_cast<long long>(p.dk) * p.dv + (p.s_in_transposed ? r * p.dk : r);
+      const int step = !given ? 0 : p.s_in_transposed ? 1 : p.dv;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          const int d = part * kCols + c;
-          if (d < p.dk) s[c] = p.s_in_transposed ? in[static_cast<long long>(r) * p.dk + d] : in[d * p.dv + r];
-        }
+      for (int c = 0; c < kCols; ++c) {
+        const int d = part * kCols + c;
+        const float x = in[min(d, p.dk - 1) * step];
+        s[c] = given && d < p.dk ? x : 0.f;
+        if (c % 16 == 15) keep_order();
       }
       // what the segments before this one add
       const float* ps = args.partial + (static_cast<long long>(blockIdx.z) * a.B * a.H + bh) *
@@ -284,101 +338,111 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         const float carry = decay_pow(g, toks);
         if (active) {
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) s[c] = carry * s[c] + ps[(part * kCols + c) * DV + r];
+          for (int c = 0; c < kCols; ++c) {
+            s[c] = carry * s[c] + ps[(part * kCols + c) * DV + r];
+            if (c % 16 == 15) keep_order();
+          }
         }
       }
     }
     // this lane's row of the four 8 x 8 blocks of a unit: blocks 0, 1 the first eight tokens,
     // 0, 2 the first eight rows of V^T
     const int v_row = (lane & 7) + (lane & 16) / 2, v_piece = (lane >> 3) & 1;
-    auto publish = [&]() {  // S^T in bf16, K-major rows of 128 bytes, swizzled
+    const uint32_t v_off = 2 * S::kQBytes + (quarter / 2) * C * 128 + (part * kGroup / 2 + v_row) * 128 +
+                           ((((quarter & 1) * 4 + v_piece) ^ (v_row & 7)) << 4);
+    // S^T in bf16: K-major rows of 128 bytes, 16-byte pieces swizzled by the row (an exclusive or
+    // with the piece, as the row starts on 128 bytes)
+    const uint32_t s_row = smem_addr(s_tile) + (part * kCols / 64) * DV * 128 + r * 128 +
+                           ((((part * kCols % 64) / 8) ^ (r & 7)) << 4);
+    auto publish = [&]() {
       if (active) {
 #pragma unroll
-        for (int c = 0; c < kCols; c += 8) {
-          const int d = part * kCols + c;
-          uint8_t* dst = s_tile + (d / 64) * DV * 128 + r * 128 + ((((d % 64) / 8) ^ (r & 7)) << 4);
-          *reinterpret_cast<uint4*>(dst) =
-              make_uint4(pack_bf16x2(s[c], s[c + 1]), pack_bf16x2(s[c + 2], s[c + 3]),
-                         pack_bf16x2(s[c + 4], s[c + 5]), pack_bf16x2(s[c + 6], s[c + 7]));
-        }
+        for (int c = 0; c < kCols; c += 8)
+          st_shared_v4(s_row ^ (c * 2), pack_bf16x2(s[c], s[c + 1]), pack_bf16x2(s[c + 2], s[c + 3]),
+                       pack_bf16x2(s[c + 4], s[c + 5]), pack_bf16x2(s[c + 6], s[c + 7]));
       }
       fence_async_shared();
+    };
+    auto publish_done = [&]() {  // S^T may be read, D written
+      tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(s_ready);
     };
     if constexpr (!kStates) publish();
-    bool ok = true;
-    for (int n = 0; n < n_steps; ++n) {
-      const uint32_t ph = n & 1;
-      const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
-      ok = __all_sync(0xffffffffu, mbar_wait(&v_full[n % kTcStages], (n / kTcStages) & 1, status, kErrTimeoutEpilogue));
-      if (!ok) break;
-      uint32_t low[kUnits][4];
+    publish_done();
+    // The parts of V^T w for group `grp` of the tile of step n: this warp's half of its tokens.
+    auto split = [&](int n, int grp) {
+      if (grp == 0) {
+        const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
+        if (!__all_sync(0xffffffffu, mbar_wait(&v_full[n % kTcStages], (n / kTcStages) & 1, status,
+                                               kErrTimeoutEpilogue)))
+          return false;
+        if (p.reverse && tile.pad > 0) {  // (the last tile) its weights count from its first real row
+          state_bar_sync();
+          if (threadIdx.x - 256 < C / 2) weight_parts(wp, threadIdx.x - 256, g, p, tile.pad);
+          state_bar_sync();
+        }
+      }
+      const int buf = grp & 1;
+      if (!__all_sync(0xffffffffu, mbar_wait(&up_free[buf], use_parity(n, grp) ^ 1, status, kErrTimeoutEpilogue)))
+        return false;
+      tc_fence_after();
       if (active) {
-        // Units of 16 tokens x 16 rows of V^T: ldmatrix transposes four 8 x 8 blocks into the
-        // layout of the 16-lane store, a register holding two consecutive tokens of one row.
-        const uint32_t v = smem_addr(stage(n)) + 2 * S::kQBytes + (quarter / 2) * C * 128 + v_row * 128;
-        // a reversed tile's missing rows hold zeros, and its weights count from the first real one
-        const float* w = wt - (p.reverse ? tile.pad : 0) + part * kToks + 2 * (lane & 3);
-        const int first_tok = p.reverse ? tile.pad : 0;
+        const uint32_t v = smem_addr(stage(n)) + v_off + grp * kGroup * 128;
+        const uint32_t* w = wp + (grp * kGroup + part * kGroup / 2) / 2 + (lane & 3);
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-          const int tok = part * kToks + (u / 2) * 16;  // the unit's first token
-          uint32_t x[4];
-          ldmatrix_x4_trans(v + tok * 128 + (((quarter & 1) * 4 + (u & 1) * 2 + v_piece) ^ (v_row & 7)) * 16, x);
-          float2 ww[2];
-          if (tok >= first_tok) {
-            ww[0] = make_float2(w[(u / 2) * 16], w[(u / 2) * 16 + 1]);
-            ww[1] = make_float2(w[(u / 2) * 16 + 8], w[(u / 2) * 16 + 9]);
-          } else {
+        for (int tok = 0; tok < kGroup / 2; tok += 16) {
+          uint32_t ww[3][2];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int t = tok + 8 * e + 2 * (lane & 3);
-              ww[e].x = t >= first_tok ? w[(u / 2) * 16 + 8 * e] : 0.f;
-              ww[e].y = t + 1 >= first_tok ? w[(u / 2) * 16 + 8 * e + 1] : 0.f;
+          for (int e = 0; e < 3; ++e) {
+            ww[e][0] = w[e * 64 + tok / 2];
+            ww[e][1] = w[e * 64 + tok / 2 + 4];
+          }
+          // 16 tokens x 16 rows of V^T at a time: ldmatrix transposes four 8 x 8 blocks into the
+          // layout of the 16-lane store, a register holding two consecutive tokens of one row
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t x[4], p1[4], r1[4], p2[4];
+            ldmatrix_x4_trans((v ^ (u * 32)) + tok * 128, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = e / 2;
+              p1[e] = bf16x2_mul(x[e], ww[0][k]);
+              r1[e] = bf16x2_fms(x[e], ww[0][k], p1[e]);
+              p2[e] = bf16x2_mul(x[e], ww[1][k]);
+              x[e] = bf16x2_fma(x[e], ww[2][k], bf16x2_fms(x[e], ww[1][k], p2[e]));
             }
+            const uint32_t at =
+                lanes + (static_cast<uint32_t>(u * 16) << 16) + parts(buf) + (part * kGroup / 2 + tok) / 2;
+            tmem_st_16x128_x2(at, p1);
+            tmem_st_16x128_x2(at + kGroup / 2, r1);
+            tmem_st_16x128_x2(at + kGroup, p2);
+            tmem_st_16x128_x2(at + 3 * kGroup / 2, x);
           }
-          uint32_t high[4], mid[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a0 = __uint_as_float(x[e] << 16), a1 = __uint_as_float(x[e] & 0xFFFF0000u);
-            mul2(a0, a1, ww[e / 2].x, ww[e / 2].y);
-            high[e] = pack_bf16x2(a0, a1);
-            sub2_bf16(a0, a1, high[e]);
-            mid[e] = pack_bf16x2(a0, a1);
-            sub2_bf16(a0, a1, mid[e]);
-            low[u][e] = pack_bf16x2(a0, a1);
-          }
-          const uint32_t at = lanes + (static_cast<uint32_t>((u & 1) * 16) << 16) + tok / 2;
-          tmem_st_16x128_x2(at + S::kHigh, high);
-          tmem_st_16x128_x2(at + S::kMid, mid);
         }
         tmem_wait_st();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(vh_ready);
-      if constexpr (!kStates) {  // the third part takes the place of scores already read
-        ok = __all_sync(0xffffffffu, mbar_wait(sc_read, ph, status, kErrTimeoutEpilogue));
-        if (!ok) break;
-        tc_fence_after();
-      }
-      if (active) {
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u)
-          tmem_st_16x128_x2(lanes + (static_cast<uint32_t>((u & 1) * 16) << 16) + S::kLow +
-                                (part * kToks + (u / 2) * 16) / 2,
-                            low[u]);
-        tmem_wait_st();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(vl_ready);
-      ok = __all_sync(0xffffffffu, mbar_wait(d_full, ph, status, kErrTimeoutEpilogue));
-      if (!ok) break;
+      if (lane == 0) mbar_arrive(&up_ready[buf]);
+      return true;
+    };
+    auto wait_state = [&](uint64_t* bar, int n) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(bar, n & 1, status, kErrTimeoutEpilogue));
       tc_fence_after();
+      return got;
+    };
+    bool ok = true;
+    for (int n = 0; ok && n < n_steps; ++n) {
+      const bool more = n + 1 < n_steps;
+      if constexpr (kStates)  // the next tile is prepared while this one's products run
+        ok = (n > 0 || (split(0, 0) && split(0, 1))) && (!more || (split(n + 1, 0) && split(n + 1, 1)));
+      else
+        ok = split(n, 0) && split(n, 1) && split(n, 2) && split(n, 3);
+      ok = ok && wait_state(d_full, n);
+      if (!ok) break;
       if (active) {
-        const float carry = pw[C - tile.pad];
+        const float carry = pw[C - tc_tile(first + n, nch, len, p.reverse).pad];
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) {
           float d[32];
@@ -386,10 +450,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
 #pragma unroll
           for (int j = 0; j < 32; j += 2) fma2(s[c + j], s[c + j + 1], carry, d[j], d[j + 1]);
         }
-        tc_fence_before();
       }
-      if constexpr (!kStates) {
-        if (n + 1 < n_steps) publish();
+      if (more) {
+        if constexpr (!kStates) publish();
+        publish_done();
       }
     }
     if (ok) {
@@ -406,40 +470,50 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         for (int c = 0; c < kCols; ++c) {
           const int d = part * kCols + c;
           if (d < p.dk) out[d * p.dv + r] = s[c];
+          if (c % 16 == 15) keep_order();
         }
       }
     }
   } else {
-    regs_down<72>();
-    if (warp == 12 && lane == 0) {
+    regs_down<64>();
+    if (warp == 16 && lane == 0) {
       // ------------------------------------------------------------ TMA producer
       const LaMaps& m = args.maps[blockIdx.z];
-      int issued = 0;
+      int issued[3] = {0, 0, 0};  // tiles of Q, K, V
+      uint64_t* full[3] = {q_full, k_full, v_full};
       for (int n = 0; n < n_steps; ++n) {
         const int st = n % kTcStages;
-        const uint32_t ph = (n / kTcStages) & 1;
-        if (!mbar_wait(&empty[st], ph ^ 1, status, kErrTimeoutProducer)) break;
+        const uint32_t ph = ((n / kTcStages) & 1) ^ 1;
         const int t0 = tc_tile(first + n, nch, len, p.reverse).t0;
         uint8_t* base = stage(n);
-        mbar_arrive_expect_tx(&qk_full[st], kStates ? S::kQBytes : 2 * S::kQBytes);
+        // each tile as soon as its place is free: Q's is after the first two products
+        if constexpr (!kStates) {
+          if (!mbar_wait(&q_empty[st], ph, status, kErrTimeoutProducer)) break;
+          mbar_arrive_expect_tx(&q_full[st], S::kQBytes);
 #pragma unroll
-        for (int x = 0; x < DK; x += 64) {
-          if constexpr (!kStates)
-            tma_load_4d(base + x * C * 2, &m.q, &qk_full[st], x, t0, h * m.q_ext[0], b * m.q_ext[1]);
-          tma_load_4d(base + S::kQBytes + x * C * 2, &m.k, &qk_full[st], x, t0, h * m.k_ext[0], b * m.k_ext[1]);
+          for (int x = 0; x < DK; x += 64)
+            tma_load_4d(base + x * C * 2, &m.q, &q_full[st], x, t0, h * m.q_ext[0], b * m.q_ext[1]);
+          issued[0] = n + 1;
         }
+        if (!mbar_wait(&k_empty[st], ph, status, kErrTimeoutProducer)) break;
+        mbar_arrive_expect_tx(&k_full[st], S::kQBytes);
+#pragma unroll
+        for (int x = 0; x < DK; x += 64)
+          tma_load_4d(base + S::kQBytes + x * C * 2, &m.k, &k_full[st], x, t0, h * m.k_ext[0], b * m.k_ext[1]);
+        issued[1] = n + 1;
+        if (!mbar_wait(&v_empty[st], ph, status, kErrTimeoutProducer)) break;
         mbar_arrive_expect_tx(&v_full[st], S::kVBytes);
 #pragma unroll
         for (int x = 0; x < DV; x += 64)
           tma_load_4d(base + 2 * S::kQBytes + x * C * 2, &m.v, &v_full[st], x, t0, h * m.v_ext[0], b * m.v_ext[1]);
-        issued = n + 1;
+        issued[2] = n + 1;
       }
-      for (int n = issued > kTcStages ? issued - kTcStages : 0; n < issued; ++n) {
-        mbar_wait(&qk_full[n % kTcStages], (n / kTcStages) & 1, status, kErrTimeoutDrain);
-        mbar_wait(&v_full[n % kTcStages], (n / kTcStages) & 1, status, kErrTimeoutDrain);
-      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i)  // every copy lands before the CTA leaves
+        for (int n = max(issued[i] - kTcStages, 0); n < issued[i]; ++n)
+          mbar_wait(&full[i][n % kTcStages], (n / kTcStages) & 1, status, kErrTimeoutDrain);
     }
-    if (!kStates && warp == 14 && lane == 0) {
+    if (!kStates && warp == 18 && lane == 0) {
       // ------------------------------------------------------------ TMA store of O
       const LaMaps& m = args.maps[blockIdx.z];
       for (int n = 0; n < n_steps; ++n) {
@@ -451,10 +525,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
             tma_store_4d(&m.o, stage(n) + 2 * S::kQBytes + x * C * 2, x, tile.t0, h * m.o_ext[0], b * m.o_ext[1]);
           bulk_commit_wait_read();
         }
-        mbar_arrive(&empty[n % kTcStages]);
+        mbar_arrive(&v_empty[n % kTcStages]);
       }
     }
-    if (warp == 13) {
+    if (warp == 17) {
       // ----------------- MMA issuer: the whole warp in step (uniform addresses), one lane issues
       constexpr uint32_t idesc_qk = umma_idesc(1, 128, C);
       constexpr uint32_t idesc_qs = umma_idesc(1, 128, DV);
@@ -475,15 +549,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         const uint64_t q_desc = umma_desc_sw128(q_addr), k_desc = umma_desc_sw128(q_addr + S::kQBytes);
         const uint64_t k_rows = umma_desc_sw128_mn(q_addr + S::kQBytes, C * 128);
         const uint64_t v_rows = umma_desc_sw128_mn(q_addr + 2 * S::kQBytes, C * 128);
-        auto update = [&](uint32_t a_col, bool fresh) {  // D (+)= A K over the chunk's tokens
+        auto update = [&](int grp) {  // D (+)= (V w)^T K over a group of tokens, the small parts first
+          const uint32_t a = tmem + parts(grp & 1);
 #pragma unroll
-          for (int kk = 0; kk < C / 16; ++kk)
-            umma_bf16_ts(tmem + S::kDelta, tmem + a_col + kk * 8, k_rows + kk * (2048 >> 4), idesc_up,
-                         fresh && kk == 0 ? 0u : 1u);
+          for (int part = 3; part >= 0; --part)
+#pragma unroll
+            for (int kk = 0; kk < kGroup / 16; ++kk)
+              umma_bf16_ts(tmem + S::kDelta, a + part * kGroup / 2 + kk * 8,
+                           k_rows + (grp * (kGroup / 16) + kk) * (2048 >> 4), idesc_up,
+                           grp == 0 && part == 3 && kk == 0 ? 0u : 1u);
         };
-        if (!wait(&qk_full[st], sph)) break;
+        auto intra = [&]() {  // O += (P . L) V
+          if (leader) {
+#pragma unroll
+            for (int kk = 0; kk < C / 16; ++kk)
+              umma_bf16_ts(tmem + S::kOut, tmem + S::kScore + kk * 8, v_rows + kk * (2048 >> 4), idesc_pv, 1u);
+            umma_commit(o_full);
+          }
+          __syncwarp();
+        };
+        if ((!kStates && !wait(&q_full[st], sph)) || !wait(&k_full[st], sph)) break;
         if constexpr (!kStates) {
-          // the score columns hold the last chunk's operands until its products are done
+          // the score columns hold the last chunk's operands until their products are done
           if (n > 0 && !wait(d_full, ph ^ 1)) break;
           if (leader) {
 #pragma unroll
@@ -501,39 +588,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
               umma_bf16(tmem + S::kOut, q_desc + (((kk / 4) * C * 128 + (kk % 4) * 32) >> 4),
                         s_desc + (((kk / 4) * DV * 128 + (kk % 4) * 32) >> 4), idesc_qs, kk ? 1u : 0u);
             umma_commit(oi_full);
+            umma_commit(&q_empty[st]);
           }
           __syncwarp();
         }
-        if (!wait(vh_ready, ph)) break;
-        if constexpr (kStates) {
-          if (!wait(vl_ready, ph)) break;
+        if (kStates && !wait(s_ready, ph)) break;
+        bool ok = true;
+#pragma unroll 1
+        for (int grp = 0; ok && grp < kGroups; ++grp) {
+          ok = wait(&up_ready[grp & 1], use_parity(n, grp));
+          if (!ok) break;
           if (leader) {
-            update(S::kLow, true);  // the small part first: its sums lose least
-            update(S::kMid, false);
-            update(S::kHigh, false);
-          }
-        } else {
-          if (leader) {
-            update(S::kMid, true);
-            update(S::kHigh, false);
-          }
-          __syncwarp();
-          if (!wait(p_ready, ph) || !wait(&v_full[st], sph)) break;
-          if (leader) {
-#pragma unroll
-            for (int kk = 0; kk < C / 16; ++kk)
-              umma_bf16_ts(tmem + S::kOut, tmem + S::kScore + kk * 8, v_rows + kk * (2048 >> 4), idesc_pv, 1u);
-            umma_commit(o_full);
+            update(grp);
+            umma_commit(&up_free[grp & 1]);
+            if (grp == kGroups - 1) {
+              umma_commit(d_full);
+              umma_commit(&k_empty[st]);
+              if constexpr (kStates) umma_commit(&v_empty[st]);
+            }
           }
           __syncwarp();
-          if (!wait(vl_ready, ph)) break;
-          if (leader) update(S::kLow, false);
         }
-        if (leader) {
-          umma_commit(d_full);
-          umma_commit(&empty[st]);
+        if (!ok) break;
+        if constexpr (!kStates) {  // last: O then takes the place of the V tile
+          if (!wait(p_ready, ph)) break;
+          intra();
         }
-        __syncwarp();
       }
       if (leader) umma_commit(mma_done);
       __syncwarp();
