@@ -222,15 +222,26 @@ size_t tc_partial_bytes(long long heads, int passes, int segments, int dk, int d
 
 template <int DK, int DV>
 pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s) {
-  using Shape = TcShape<DK, DV>;
-  PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes));
+  constexpr int smem = TcShape<DK, DV, false>::kBytes, states_smem = TcShape<DK, DV, true>::kBytes;
+  PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const unsigned heads = static_cast<unsigned>(t.a.B) * t.a.H;
   if (t.segments > 1) {
-    PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kBytes));
-    k_la_tc<DK, DV, true><<<dim3(heads, t.segments - 1, passes), kTcThreads, Shape::kBytes, s>>>(t);
+    PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, states_smem));
+    k_la_tc<DK, DV, true><<<dim3(heads, t.segments - 1, passes), kTcThreads, states_smem, s>>>(t);
     PC_LAUNCH_CHECK();
   }
-  k_la_tc<DK, DV, false><<<dim3(heads, t.segments, passes), kTcThreads, Shape::kBytes, s>>>(t);
+  // after the states' launch its CTAs start as SMs come free, and wait for the states themselves
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(heads, t.segments, passes);
+  cfg.blockDim = dim3(kTcThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = t.segments > 1 ? 1 : 0;
+  PC_CUDA(cudaLaunchKernelEx(&cfg, k_la_tc<DK, DV, false>, t));
   PC_LAUNCH_CHECK();
   return PC_OK;
 }

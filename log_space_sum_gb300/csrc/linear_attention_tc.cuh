@@ -22,7 +22,8 @@
 //   warps 8-15   one row of S^T per thread: the parts of V^T w, in groups of 32 tokens (kStates:
 //                64; the first four warps the first half of them), then half of S^T's
 //                columns each
-//   warp 16      TMA: Q, K, V tiles of 128 tokens, two stages (96 KB each at head size 128)
+//   warp 16      TMA: Q, K, V tiles of 128 tokens, two stages (96 KB each at head size 128),
+//                kStates three of K and V
 //   warp 17      MMA issuer
 //   warp 18      TMA store of O
 // The state warps hold 64 floats of S^T each: setmaxnreg gives them 128 registers, out of what
@@ -40,7 +41,6 @@ namespace pc {
 
 constexpr int kTcC = 128;
 constexpr int kTcThreads = 20 * 32;
-constexpr int kTcStages = 2;
 
 struct LaMaps {
   CUtensorMap q, k, v, o;
@@ -55,20 +55,22 @@ struct LaTcArgs {
   unsigned* status;
 };
 
-template <int DK, int DV>
+template <int DK, int DV, bool kStates>
 struct TcShape {
   static constexpr uint32_t kQBytes = kTcC * DK * 2, kVBytes = kTcC * DV * 2;
-  static constexpr uint32_t kStage = 2 * kQBytes + kVBytes;
-  static constexpr uint32_t kSBytes = DV * DK * 2;
-  static constexpr uint32_t kFixed = kTcStages * kStage + kSBytes;
-  static constexpr uint32_t kTables = 2048;
-  static constexpr uint32_t kBytes = kFixed + kTables + 1024;
+  static constexpr uint32_t kK = kStates ? 0 : kQBytes, kV = kK + kQBytes;  // tiles' places in a stage
+  static constexpr uint32_t kStage = kV + kVBytes;
+  static constexpr int kStages = kStates ? 3 : 2;
+  static constexpr uint32_t kSBytes = kStates ? 0 : DV * DK * 2;
+  static constexpr uint32_t kFixed = kStages * kStage + kSBytes;
+  static constexpr uint32_t kTables = 2064;  // powers and weights (1808 bytes), barriers
+  static constexpr uint32_t kBytes = kFixed + kTables + 1008;  // alignment: the base is 16-byte aligned
   static_assert(kBytes <= 232448, "shared memory per CTA");
   // tensor memory columns
   // float scores (128 columns); the decayed ones, packed, then take the first 64
   static constexpr uint32_t kScore = 0;
   static constexpr uint32_t kOut = 128;
-  static constexpr uint32_t kDelta = 256;
+  static constexpr uint32_t kDelta = 256;  // kStates: and kOut, in turn
   // the four parts of V^T w for a group of tokens, half a column each per token; two groups in
   // turn (kStates: the second in the scores' place)
   static constexpr uint32_t kParts = 384;
@@ -118,7 +120,8 @@ __device__ __forceinline__ TcTile tc_tile(int step, int nch, int len, int revers
 
 template <int DK, int DV, bool kStates>
 __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__ LaTcArgs args) {
-  using S = TcShape<DK, DV>;
+  using S = TcShape<DK, DV, kStates>;
+  constexpr int kTcStages = S::kStages;
   constexpr int C = kTcC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -129,11 +132,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   float* near = tables + C + 4 + 192;  // c_intra l^(distance) from column j to the block's near edge, j = 0 .. 31
   float* diag = near + 32 + 32;      // c_intra l^|d| at diag[d], d = -31 .. 31 (column - row)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kFixed + (C + 4 + 192 + 128) * sizeof(float));
-  uint64_t *q_full = bars, *v_full = bars + 2, *sc_full = bars + 6, *oi_full = bars + 7,
-           *o_full = bars + 8, *d_full = bars + 9, *p_ready = bars + 10, *o_free = bars + 11, *s_ready = bars + 12,
-           *mma_done = bars + 13, *o_staged = bars + 14, *up_ready = bars + 15, *up_free = bars + 17;
-  uint64_t *q_empty = bars + 19, *k_empty = bars + 21, *v_empty = bars + 4, *k_full = bars + 23;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
+  auto bar = [&](int at) { return bars + at; };
+  uint64_t *q_full = bar(0), *k_full = bar(3), *v_full = bar(6), *q_empty = bar(9), *k_empty = bar(12),
+           *v_empty = bar(15), *up_ready = bar(18), *up_free = bar(20), *sc_full = bar(22), *oi_full = bar(23),
+           *o_full = bar(24), *d_full = bar(25), *p_ready = bar(26), *o_free = bar(27), *s_ready = bar(28),
+           *o_staged = bar(29), *mma_done = bar(30);
+  uint64_t* d_free = bar(22);  // kStates: [2], in the place of sc_full and oi_full
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar(31));
 
   const LaArgs& a = args.a;
   const LaPass& p = a.pass[blockIdx.z];
@@ -147,6 +152,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   if constexpr (kStates) {
     if (seg >= final_seg) return;  // nothing follows: not read
   }
+  if constexpr (kStates) grid_dependents_launch();
   const float g = a.log_decay[h];
   unsigned* status = args.status;
 
@@ -169,7 +175,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   }
   if (warp == 0) {
     if (lane == 0) {
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kTcStages; ++i) {
         mbar_init(&q_full[i], 1);
         mbar_init(&k_full[i], 1);
         mbar_init(&v_full[i], 1);
@@ -177,8 +183,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         mbar_init(&k_empty[i], 1);
         mbar_init(&v_empty[i], 1);  // its products are done and, where O takes its place, O has left
       }
-      mbar_init(sc_full, 1);
-      mbar_init(oi_full, 1);
+      mbar_init(sc_full, kStates ? 8 : 1);
+      mbar_init(oi_full, kStates ? 8 : 1);
       mbar_init(o_full, 1);
       mbar_init(d_full, 1);
       mbar_init(mma_done, 1);
@@ -200,6 +206,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   constexpr int kGroup = kStates ? 64 : 32, kGroups = C / kGroup;  // tokens of a group, groups of a tile
+  auto d_col = [&](int n) { return kStates && (n & 1) ? S::kOut : S::kDelta; };
   // parity of the use of buffer grp & 1 by group grp of step n
   auto use_parity = [&](int n, int grp) { return static_cast<uint32_t>(n * (kGroups / 2) + (grp >> 1)) & 1u; };
   auto parts = [&](int buf) { return kStates ? (buf ? S::kScore : S::kParts) : S::kParts + buf * 64; };
@@ -279,7 +286,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
           // a whole tile goes through shared memory in rows of 128 swizzled bytes, one that starts
           // before the sequence (no store may) straight to global memory
           __nv_bfloat16* row = o + (tile.t0 + i) * p.os[1];
-          const uint32_t staged = smem_addr(stage(n)) + 2 * S::kQBytes + i * 128 + ((i & 7) << 4);
+          const uint32_t staged = smem_addr(stage(n)) + S::kV + i * 128 + ((i & 7) << 4);
 #pragma unroll 1
           for (int c = 0; c < DV; c += 32) {
             float v[32];
@@ -329,6 +336,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         if (c % 16 == 15) keep_order();
       }
       // what the segments before this one add
+      if (seg > 0) grid_dependency_wait();
       const float* ps = args.partial + (static_cast<long long>(blockIdx.z) * a.B * a.H + bh) *
                                            (args.segments - 1) * (DK * DV);
       for (int e = 0; e < seg; ++e, ps += DK * DV) {
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
     // this lane's row of the four 8 x 8 blocks of a unit: blocks 0, 1 the first eight tokens,
     // 0, 2 the first eight rows of V^T
     const int v_row = (lane & 7) + (lane & 16) / 2, v_piece = (lane >> 3) & 1;
-    const uint32_t v_off = 2 * S::kQBytes + (quarter / 2) * C * 128 + (part * kGroup / 2 + v_row) * 128 +
+    const uint32_t v_off = S::kV + (quarter / 2) * C * 128 + (part * kGroup / 2 + v_row) * 128 +
                            ((((quarter & 1) * 4 + v_piece) ^ (v_row & 7)) << 4);
     // S^T in bf16: K-major rows of 128 bytes, 16-byte pieces swizzled by the row (an exclusive or
     // with the piece, as the row starts on 128 bytes)
@@ -363,13 +371,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       }
       fence_async_shared();
     };
-    auto publish_done = [&]() {  // S^T may be read, D written
+    auto arrive = [&](uint64_t* to) {
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(s_ready);
+      if (lane == 0) mbar_arrive(to);
     };
-    if constexpr (!kStates) publish();
-    publish_done();
+    if constexpr (!kStates) {
+      publish();
+      arrive(s_ready);
+    }
     // The parts of V^T w for group `grp` of the tile of step n: this warp's half of its tokens.
     auto split = [&](int n, int grp) {
       if (grp == 0) {
@@ -446,14 +456,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
 #pragma unroll
         for (int c = 0; c < kCols; c += 32) {
           float d[32];
-          tmem_ld_32x32(lanes + S::kDelta + part * kCols + c, d);
+          tmem_ld_32x32(lanes + d_col(n) + part * kCols + c, d);
 #pragma unroll
           for (int j = 0; j < 32; j += 2) fma2(s[c + j], s[c + j + 1], carry, d[j], d[j + 1]);
         }
       }
-      if (more) {
-        if constexpr (!kStates) publish();
-        publish_done();
+      if constexpr (kStates) {
+        arrive(&d_free[n & 1]);  // D may be written again
+      } else if (more) {
+        publish();
+        arrive(s_ready);  // ... and S^T read
       }
     }
     if (ok) {
@@ -499,13 +511,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         mbar_arrive_expect_tx(&k_full[st], S::kQBytes);
 #pragma unroll
         for (int x = 0; x < DK; x += 64)
-          tma_load_4d(base + S::kQBytes + x * C * 2, &m.k, &k_full[st], x, t0, h * m.k_ext[0], b * m.k_ext[1]);
+          tma_load_4d(base + S::kK + x * C * 2, &m.k, &k_full[st], x, t0, h * m.k_ext[0], b * m.k_ext[1]);
         issued[1] = n + 1;
         if (!mbar_wait(&v_empty[st], ph, status, kErrTimeoutProducer)) break;
         mbar_arrive_expect_tx(&v_full[st], S::kVBytes);
 #pragma unroll
         for (int x = 0; x < DV; x += 64)
-          tma_load_4d(base + 2 * S::kQBytes + x * C * 2, &m.v, &v_full[st], x, t0, h * m.v_ext[0], b * m.v_ext[1]);
+          tma_load_4d(base + S::kV + x * C * 2, &m.v, &v_full[st], x, t0, h * m.v_ext[0], b * m.v_ext[1]);
         issued[2] = n + 1;
       }
 #pragma unroll
@@ -522,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         if (tile.pad == 0) {
 #pragma unroll
           for (int x = 0; x < DV; x += 64)
-            tma_store_4d(&m.o, stage(n) + 2 * S::kQBytes + x * C * 2, x, tile.t0, h * m.o_ext[0], b * m.o_ext[1]);
+            tma_store_4d(&m.o, stage(n) + S::kV + x * C * 2, x, tile.t0, h * m.o_ext[0], b * m.o_ext[1]);
           bulk_commit_wait_read();
         }
         mbar_arrive(&v_empty[n % kTcStages]);
@@ -546,16 +558,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         const int st = n % kTcStages;
         const uint32_t ph = n & 1, sph = (n / kTcStages) & 1;
         const uint32_t q_addr = base + st * S::kStage;
-        const uint64_t q_desc = umma_desc_sw128(q_addr), k_desc = umma_desc_sw128(q_addr + S::kQBytes);
-        const uint64_t k_rows = umma_desc_sw128_mn(q_addr + S::kQBytes, C * 128);
-        const uint64_t v_rows = umma_desc_sw128_mn(q_addr + 2 * S::kQBytes, C * 128);
+        const uint64_t q_desc = umma_desc_sw128(q_addr), k_desc = umma_desc_sw128(q_addr + S::kK);
+        const uint64_t k_rows = umma_desc_sw128_mn(q_addr + S::kK, C * 128);
+        const uint64_t v_rows = umma_desc_sw128_mn(q_addr + S::kV, C * 128);
         auto update = [&](int grp) {  // D (+)= (V w)^T K over a group of tokens, the small parts first
           const uint32_t a = tmem + parts(grp & 1);
 #pragma unroll
           for (int part = 3; part >= 0; --part)
 #pragma unroll
             for (int kk = 0; kk < kGroup / 16; ++kk)
-              umma_bf16_ts(tmem + S::kDelta, a + part * kGroup / 2 + kk * 8,
+              umma_bf16_ts(tmem + d_col(n), a + part * kGroup / 2 + kk * 8,
                            k_rows + (grp * (kGroup / 16) + kk) * (2048 >> 4), idesc_up,
                            grp == 0 && part == 3 && kk == 0 ? 0u : 1u);
         };
@@ -592,7 +604,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
           }
           __syncwarp();
         }
-        if (kStates && !wait(s_ready, ph)) break;
+        if (kStates && !wait(&d_free[n & 1], ((n >> 1) & 1) ^ 1)) break;
         bool ok = true;
 #pragma unroll 1
         for (int grp = 0; ok && grp < kGroups; ++grp) {
