@@ -225,9 +225,10 @@ pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s) {
   constexpr int smem = TcShape<DK, DV, false>::kBytes, states_smem = TcShape<DK, DV, true>::kBytes;
   PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   const unsigned heads = static_cast<unsigned>(t.a.B) * t.a.H;
+  t.passes = passes;
   if (t.segments > 1) {
     PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, states_smem));
-    k_la_tc<DK, DV, true><<<dim3(heads, t.segments - 1, passes), kTcThreads, states_smem, s>>>(t);
+    k_la_tc<DK, DV, true><<<dim3(heads * passes, t.segments - 1), kTcThreads, states_smem, s>>>(t);
     PC_LAUNCH_CHECK();
   }
   // after the states' launch its CTAs start as SMs come free, and wait for the states themselves
@@ -235,7 +236,7 @@ pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(heads, t.segments, passes);
+  cfg.gridDim = dim3(heads * passes, t.segments);
   cfg.blockDim = dim3(kTcThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

@@ -51,7 +51,7 @@ struct LaTcArgs {
   LaArgs a;
   LaMaps maps[3];
   float* partial;      // [pass][B*H][segments - 1][DK][DV]
-  int segments, chunks_per_segment;
+  int passes, segments, chunks_per_segment;
   unsigned* status;
 };
 
@@ -141,8 +141,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar(31));
 
   const LaArgs& a = args.a;
-  const LaPass& p = a.pass[blockIdx.z];
-  const int bh = blockIdx.x, b = bh / a.H, h = bh % a.H, seg = blockIdx.y;
+  // the passes of one head run side by side: they read the same tiles, out of L2 but once
+  const int pass = blockIdx.x % args.passes, bh = blockIdx.x / args.passes;
+  const LaPass& p = a.pass[pass];
+  const int b = bh / a.H, h = bh % a.H, seg = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int len = la_length(a, b), nch = (len + C - 1) / C;
   const int first = seg * args.chunks_per_segment;
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       }
       // what the segments before this one add
       if (seg > 0) grid_dependency_wait();
-      const float* ps = args.partial + (static_cast<long long>(blockIdx.z) * a.B * a.H + bh) *
+      const float* ps = args.partial + (static_cast<long long>(pass) * a.B * a.H + bh) *
                                            (args.segments - 1) * (DK * DV);
       for (int e = 0; e < seg; ++e, ps += DK * DV) {
         const int at = e * args.chunks_per_segment;
@@ -470,7 +472,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
     }
     if (ok) {
       if constexpr (kStates) {
-        float* out = args.partial + ((static_cast<long long>(blockIdx.z) * a.B * a.H + bh) * (args.segments - 1) +
+        float* out = args.partial + ((static_cast<long long>(pass) * a.B * a.H + bh) * (args.segments - 1) +
                                      seg) * (DK * DV);
         if (active) {
 #pragma unroll
@@ -490,7 +492,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
     regs_down<64>();
     if (warp == 16 && lane == 0) {
       // ------------------------------------------------------------ TMA producer
-      const LaMaps& m = args.maps[blockIdx.z];
+      const LaMaps& m = args.maps[pass];
       int issued[3] = {0, 0, 0};  // tiles of Q, K, V
       uint64_t* full[3] = {q_full, k_full, v_full};
       for (int n = 0; n < n_steps; ++n) {
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
     }
     if (!kStates && warp == 18 && lane == 0) {
       // ------------------------------------------------------------ TMA store of O
-      const LaMaps& m = args.maps[blockIdx.z];
+      const LaMaps& m = args.maps[pass];
       for (int n = 0; n < n_steps; ++n) {
         const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
         if (!mbar_wait(o_staged, n & 1, status, kErrTimeoutEpilogue)) break;
