@@ -194,42 +194,46 @@ __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uin
   umma_bf16(d, a, b, idesc, acc);  // kind::f16: the instruction descriptor names the type
 }
 
-// 32 consecutive values of a row of an operand, n of them valid.
-template <int kParts>
-__device__ __forceinline__ void load_half_run(const HalfMat& x, size_t at, float (&v)[32], int n) {
-  if (n == 32) {  // ld and the column are multiples of 32
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 w = *reinterpret_cast<const uint4*>(x.ptr + at + 8 * q);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ww[k]));
-        v[8 * q + 2 * k] = f.x;
-        v[8 * q + 2 * k + 1] = f.y;
-      }
-      if constexpr (kParts == 2) {
-        const uint4 l = *reinterpret_cast<const uint4*>(x.ptr + x.lo + at + 8 * q);
-        const uint32_t ll[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&ll[k]));
-          v[8 * q + 2 * k] += f.x;
-          v[8 * q + 2 * k + 1] += f.y;
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      v[i] = i < n ? __half2float(x.ptr[at + i]) : 0.f;
-      if (kParts == 2 && i < n) v[i] += __half2float(x.ptr[x.lo + at + i]);
-    }
-  }
+// 32 consecutive values of a row of an operand. A lane's run is its own row's, so every access
+// of a warp touches 32 rows: 32 bytes at a time halve their number.
+__device__ __forceinline__ void ld_32(const void* p, uint32_t (&r)[16], int at) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[at]), "=r"(r[at + 1]), "=r"(r[at + 2]), "=r"(r[at + 3]), "=r"(r[at + 4]), "=r"(r[at + 5]),
+                 "=r"(r[at + 6]), "=r"(r[at + 7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_32(void* p, const uint32_t (&r)[16], int at) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[at]), "r"(r[at + 1]),
+               "r"(r[at + 2]), "r"(r[at + 3]), "r"(r[at + 4]), "r"(r[at + 5]), "r"(r[at + 6]), "r"(r[at + 7])
+               : "memory");
 }
 
 template <int kParts>
-__device__ __forceinline__ void store_half_run(const HalfMat& x, size_t at, const float (&v)[32], int n) {
+struct HalfRun {
+  uint32_t w[kParts][16];
+  // ld and the column are multiples of 32, so a row's padding is there to be read
+  __device__ __forceinline__ void fetch(const HalfMat& x, size_t at) {
+#pragma unroll
+    for (int part = 0; part < kParts; ++part) {
+      ld_32(x.ptr + part * x.lo + at, w[part], 0);
+      ld_32(x.ptr + part * x.lo + at + 16, w[part], 8);
+    }
+  }
+  __device__ __forceinline__ float2 pair(int i) const {  // values 2i and 2i + 1
+    float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[0][i]));
+    if constexpr (kParts == 2) {
+      const float2 l = __half22float2(*reinterpret_cast<const __half2*>(&w[1][i]));
+      f.x += l.x;
+      f.y += l.y;
+    }
+    return f;
+  }
+};
+
+// Columns past the matrix hold what the accumulator had there: zeros.
+template <int kParts>
+__device__ __forceinline__ void store_half_run(const HalfMat& x, size_t at, const float (&v)[32]) {
   uint32_t hi[16], lo[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
@@ -241,34 +245,33 @@ __device__ __forceinline__ void store_half_run(const HalfMat& x, size_t at, cons
       lo[i] = *reinterpret_cast<const uint32_t*>(&l);
     }
   }
-  if (n == 32) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      *reinterpret_cast<uint4*>(x.ptr + at + 8 * q) = make_uint4(hi[4 * q], hi[4 * q + 1], hi[4 * q + 2], hi[4 * q + 3]);
-      if constexpr (kParts == 2)
-        *reinterpret_cast<uint4*>(x.ptr + x.lo + at + 8 * q) =
-            make_uint4(lo[4 * q], lo[4 * q + 1], lo[4 * q + 2], lo[4 * q + 3]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (i < n) {
-        x.ptr[at + i] = __ushort_as_half(static_cast<unsigned short>(hi[i >> 1] >> (16 * (i & 1))));
-        if constexpr (kParts == 2)
-          x.ptr[x.lo + at + i] = __ushort_as_half(static_cast<unsigned short>(lo[i >> 1] >> (16 * (i & 1))));
-      }
+  st_32(x.ptr + at, hi, 0);
+  st_32(x.ptr + at + 16, hi, 8);
+  if constexpr (kParts == 2) {
+    st_32(x.ptr + x.lo + at, lo, 0);
+    st_32(x.ptr + x.lo + at + 16, lo, 8);
   }
 }
 
 __device__ __forceinline__ void orth_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void orth_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// What the epilogue reads of 32 columns from n of row m: kPoly A, kApply X.
+template <int kParts, int kOp>
+__device__ __forceinline__ void orth_fetch(const OrthArgs& p, int g, int m, int n, HalfRun<kParts>& x) {
+  if constexpr (kOp != kGram) {
+    if (m < p.M && n < p.N)
+      x.fetch(p.prev, static_cast<size_t>(g) * p.prev.rows * p.prev.ld + static_cast<size_t>(m) * p.prev.ld + n);
+  }
+}
+
 // 32 columns from n of row m of D:
 //   kGram   2^12 A = k0 nu^2 D
 //   kPoly   2^10 B = k0 (2^12 A) + k1 D
 //   kApply  X' = k0 nu (k1 Xs + 2^-10 D), to Xs' or to the caller
 template <int kParts, int kOp, class T>
-__device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, int n, bool mirror, float (&v)[32]) {
+__device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, int n, bool mirror, float (&v)[32],
+                                              const HalfRun<kParts>& x) {
   if (m >= p.M || n >= p.N) return;
   const int k = min(32, p.N - n);
   const float nu = p.nu ? p.nu[g] : 1.f;
@@ -278,16 +281,12 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, i
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= f;
   } else {
-    float x[32];
-    load_half_run<kParts>(p.prev, static_cast<size_t>(g) * p.prev.rows * p.prev.ld +
-                                      static_cast<size_t>(m) * p.prev.ld + n, x, k);
-    if constexpr (kOp == kPoly) {
+    const float k0 = kOp == kPoly ? p.k0 : p.k0 * nu * p.k1, k1 = kOp == kPoly ? p.k1 : p.k0 * nu * (1.f / kScaleB);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = p.k0 * x[i] + p.k1 * v[i];
-    } else {
-      const float f = p.k0 * nu;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = f * (p.k1 * x[i] + v[i] * (1.f / kScaleB));
+    for (int i = 0; i < 16; ++i) {
+      const float2 f = x.pair(i);
+      v[2 * i] = k0 * f.x + k1 * v[2 * i];
+      v[2 * i + 1] = k0 * f.y + k1 * v[2 * i + 1];
     }
   }
   if constexpr (kOp == kApply) {
@@ -318,7 +317,7 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, i
       return;
     }
   }
-  store_half_run<kParts>(p.to, at, v, k);
+  store_half_run<kParts>(p.to, at, v);
   if constexpr (kOp != kApply) {
     if (mirror) {  // lanes hold consecutive m: each store covers a run of row n + i
 #pragma unroll
@@ -345,27 +344,28 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, i
 constexpr int kSliceKb = 2;
 constexpr int kOrthThreads = 64 + 8 * 32;
 
-template <int kParts, int BN, int kSplit>
+template <int kParts, int BN, bool kShort>
 struct OrthRing {
-  // split tiles run one after the other in a chain of small launches: two CTAs per SM let
+  // short: a few blocks of K per CTA, in a chain of small launches; two CTAs per SM then let
   // a launch set up while the one before it finishes
-  static constexpr int kFit = ((kSplit > 1 && kParts == 1 ? 113 : 227) * 1024 - 2048) / OrthShape<kParts, BN>::kStage;
+  static constexpr int kFit = ((kShort ? 113 : 227) * 1024 - 2048) / OrthShape<kParts, BN>::kStage;
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr uint32_t kBytes = kStages * OrthShape<kParts, BN>::kStage + 2048;
 };
 
-template <int kParts, int BN, int kSplit, int kOp, class T>
+template <int kParts, int BN, int kSplit, bool kShort, int kOp, class T>
 __global__ void __launch_bounds__(kOrthThreads, 1)
     k_orth_gemm(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__ CUtensorMap a_lo,
                 const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
                 const __grid_constant__ OrthArgs p) {
   using S = OrthShape<kParts, BN>;
-  constexpr int kStages = OrthRing<kParts, BN, kSplit>::kStages;
+  constexpr int kStages = OrthRing<kParts, BN, kShort>::kStages;
   constexpr bool kPairs = kOp != kApply;
   constexpr bool kSliced = kParts == 2;
   constexpr uint32_t kCols = 2 * BN;  // two accumulators
   static_assert(kStages >= 2 && kCols <= 512, "two stages, two accumulators");
-  static_assert(kSplit == 1 || (BN % (32 * kSplit) == 0 && (kSplit - 1) * kBM * (BN / kSplit) * 4 <= kStages * S::kStage),
+  constexpr int kOwn = (BN / 32 + kSplit - 1) / kSplit;  // chunk x of 32 columns belongs to rank x % kSplit
+  static_assert(kSplit == 1 || (kSplit - 1) * kOwn * 32 * kBM * 4 <= kStages * S::kStage,
                 "the ring holds the partial sums of the other CTAs");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -536,14 +536,18 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       tile_at(t, g, m0, n0);
       const bool mirror = kPairs && n0 != m0;
       if constexpr (kSplit == 1 && !kSliced) {
+        HalfRun<kParts> x;
+        orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + part * 32, x);
         ok = wait_unit();
         if (!ok) break;
 #pragma unroll 1
         for (int c = part * 32; c < BN; c += 64) {
+          const HalfRun<kParts> now = x;
+          if (c + 64 < BN) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + c + 64, x);  // under this chunk's work
           float v[32];
           tmem_ld_32x32(lanes + (unit & 1) * BN + c, v);
           if (c + 64 >= BN) release();
-          orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + c, mirror, v);
+          orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + c, mirror, v, now);
         }
       } else {
         float acc[kChunks][32];
@@ -567,20 +571,26 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if constexpr (kSplit == 1) {
           if (ok) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-              orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + (2 * c + part) * 32, mirror, acc[c]);
+            for (int c = 0; c < kChunks; ++c) {
+              HalfRun<kParts> x;
+              orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + (2 * c + part) * 32, x);
+              orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + (2 * c + part) * 32, mirror, acc[c], x);
+            }
           }
         } else {
-          // chunk x belongs to rank x / kOwn; the others' sums land at [source][chunk][column][row]
-          constexpr int kOwn = BN / 32 / kSplit;
+          // the other ranks' sums land at [source][chunk][column][row]
+          HalfRun<kParts> x[kChunks];
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if ((2 * c + part) % kSplit == rank) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + (2 * c + part) * 32, x[c]);
           cluster_sync();  // every ring of the cluster is idle
           auto slot = [&](int src, int own) { return ((src * kOwn + own) * 32 * kBM + row) * 4; };
           if (ok) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-              const int x = 2 * c + part, owner = x / kOwn;
+              const int xc = 2 * c + part, owner = xc % kSplit;
               if (owner == rank) continue;
-              const uint32_t to = cluster_map(smem_addr(smem), owner) + slot(rank - (rank > owner), x % kOwn);
+              const uint32_t to = cluster_map(smem_addr(smem), owner) + slot(rank - (rank > owner), xc / kSplit);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * kBM * 4), "f"(acc[c][i]) : "memory");
@@ -590,15 +600,15 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           if (ok) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
-              const int x = 2 * c + part;
-              if (x / kOwn != rank) continue;
+              const int xc = 2 * c + part;
+              if (xc % kSplit != rank) continue;
 #pragma unroll
               for (int src = 0; src < kSplit - 1; ++src) {
-                const float* from = reinterpret_cast<const float*>(smem + slot(src, x % kOwn));
+                const float* from = reinterpret_cast<const float*>(smem + slot(src, xc / kSplit));
 #pragma unroll
                 for (int i = 0; i < 32; ++i) acc[c][i] += from[i * kBM];
               }
-              orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + x * 32, mirror, acc[c]);
+              orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + xc * 32, mirror, acc[c], x[c]);
             }
           }
         }
@@ -615,16 +625,13 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 // --------------------------------------------------------------------------- launches
 inline unsigned blocks_of(long long a, long long b) { return static_cast<unsigned>((a + b - 1) / b); }
 
-template <int kParts, int BN, int kSplit, int kOp, class T>
+template <int kParts, int BN, int kSplit, bool kShort, int kOp, class T>
 pc_status_t launch_orth(const OrthArgs& p, const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], cudaStream_t s,
-                        long long flops) {
-  constexpr uint32_t smem = OrthRing<kParts, BN, kSplit>::kBytes;
+                        long long tiles, long long flops) {
+  constexpr uint32_t smem = OrthRing<kParts, BN, kShort>::kBytes;
   static_assert(smem <= 232448, "shared memory per CTA");
-  auto* kernel = k_orth_gemm<kParts, BN, kSplit, kOp, T>;
+  auto* kernel = k_orth_gemm<kParts, BN, kSplit, kShort, kOp, T>;
   PC_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
-  const long long tiles =
-      static_cast<long long>(kOp == kApply ? p.tiles_m * static_cast<long long>(p.tiles_n)
-                                           : p.tiles_m * (p.tiles_m + 1ll) / 2) * p.batch;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -646,12 +653,14 @@ pc_status_t launch_orth(const OrthArgs& p, const CUtensorMap (&a)[2], const CUte
   return PC_OK;
 }
 
-// CTAs of a cluster that share a tile: while they all fit the GPU at once and each keeps two
-// blocks of K or more.
+// CTAs of a cluster that share a tile of 128 x 128. A cluster lies within one of the GPU's
+// eight groups of SMs, so at most 8 floor(SMs / 8 / size) clusters run at once; each CTA
+// keeps two blocks of K or more.
 inline int split_of(long long tiles, int num_kb) {
-  int s = 1;
-  while (s < 4 && tiles * s * 2 <= num_sms() && num_kb >= 4 * s) s *= 2;
-  return s;
+  int best = 1;
+  for (int size = 2; size <= 4; ++size)
+    if (tiles <= 8 * (num_sms() / 8 / size) && num_kb >= 2 * size) best = size;
+  return best;
 }
 
 template <int kParts, int kOp, class T>
@@ -662,16 +671,25 @@ pc_status_t run_product(OrthArgs p, const CUtensorMap (&a)[2], const CUtensorMap
   if constexpr (kOp == kApply && kParts == 1) {
     if (wide >= num_sms()) {
       p.tiles_n = static_cast<int>(blocks_of(p.N, 256));
-      return launch_orth<kParts, 256, 1, kOp, T>(p, a, b, s, flops);
+      return launch_orth<kParts, 256, 1, false, kOp, T>(p, a, b, s, wide, flops);
     }
   }
   p.tiles_n = static_cast<int>(blocks_of(p.N, 128));
   const long long tiles = (kOp == kApply ? p.tiles_m * static_cast<long long>(p.tiles_n)
                                          : p.tiles_m * (p.tiles_m + 1ll) / 2) * p.batch;
-  switch (split_of(tiles, p.num_kb)) {
-    case 4: return launch_orth<kParts, 128, 4, kOp, T>(p, a, b, s, flops);
-    case 2: return launch_orth<kParts, 128, 2, kOp, T>(p, a, b, s, flops);
-    default: return launch_orth<kParts, 128, 1, kOp, T>(p, a, b, s, flops);
+  const int split = split_of(tiles, p.num_kb);
+  if (kParts == 1 && p.num_kb <= 6 * split) {
+    switch (split) {
+      case 4: return launch_orth<kParts, 128, 4, kParts == 1, kOp, T>(p, a, b, s, tiles, flops);
+      case 3: return launch_orth<kParts, 128, 3, kParts == 1, kOp, T>(p, a, b, s, tiles, flops);
+      case 2: return launch_orth<kParts, 128, 2, kParts == 1, kOp, T>(p, a, b, s, tiles, flops);
+    }
+  }
+  switch (split) {
+    case 4: return launch_orth<kParts, 128, 4, false, kOp, T>(p, a, b, s, tiles, flops);
+    case 3: return launch_orth<kParts, 128, 3, false, kOp, T>(p, a, b, s, tiles, flops);
+    case 2: return launch_orth<kParts, 128, 2, false, kOp, T>(p, a, b, s, tiles, flops);
+    default: return launch_orth<kParts, 128, 1, false, kOp, T>(p, a, b, s, tiles, flops);
   }
 }
 
@@ -771,7 +789,7 @@ pc_status_t run_orth(int batch, int rows, int cols, const T* G, int steps, float
     gram.to = p.A;
     gram.nu = it == 0 ? p.nu : nullptr;
     gram.k0 = kScaleA * (it == 0 ? 1.f : down * down);
-    PC_TRY((run_product<kParts, kGram, T>(gram, x_rows[i], x_rows[i], s, mm * N)));
+    PC_TRY((run_product<kParts, kGram, float>(gram, x_rows[i], x_rows[i], s, mm * N)));
     OrthArgs poly = q;
     poly.N = M;
     poly.num_kb = static_cast<int>(blocks_of(M, 64));
@@ -779,7 +797,7 @@ pc_status_t run_orth(int batch, int rows, int cols, const T* G, int steps, float
     poly.to = p.Bm;
     poly.k0 = kScaleB / kScaleA * b;
     poly.k1 = kScaleB / (kScaleA * kScaleA) * c;
-    PC_TRY((run_product<kParts, kPoly, T>(poly, ma, ma, s, mm * M)));
+    PC_TRY((run_product<kParts, kPoly, float>(poly, ma, ma, s, mm * M)));
     OrthArgs apply = q;
     apply.N = N;
     apply.num_kb = poly.num_kb;
