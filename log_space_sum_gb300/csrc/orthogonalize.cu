@@ -458,37 +458,39 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       cluster_sync();
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // -------------------------------------------------------------- MMA issuer
-      constexpr uint32_t idesc = umma_idesc(0, kBM, BN) | (kOp == kApply ? kIdescBMN : 0u);  // 0: float16
-      int it = 0, unit = 0;
-      bool ok = true;
-      for (int t = tile0; ok && t < num_tiles; t += tile_step) {
-        for (int kb = kb0; ok && kb < kb1; ++unit) {
-          const int end = kSliced ? min(kb + kSliceKb, kb1) : kb1;
-          const int buf = unit & 1;
-          if (!mbar_wait(&acc_empty[buf], ((unit >> 1) & 1) ^ 1, p.status, kErrTimeoutMma)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem + buf * BN;
-          uint32_t acc = 0;
-          for (; kb < end; ++kb, ++it) {
-            const int s = it % kStages;
-            if (!mbar_wait(&full[s], (it / kStages) & 1, p.status, kErrTimeoutMma)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t a = smem_addr(smem + s * S::kStage), b = a + kParts * S::kA;
+    // ------------------ MMA issuer: the whole warp in step (uniform addresses), one lane issues
+    constexpr uint32_t idesc = umma_idesc(0, kBM, BN) | (kOp == kApply ? kIdescBMN : 0u);  // 0: float16
+    const bool leader = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(bar, parity, p.status, kErrTimeoutMma));
+      tc_fence_after();
+      return got;
+    };
+    const uint32_t ring = smem_addr(smem);
+    int unit = 0, s = 0;
+    uint32_t ph = 0;  // of ring slot s
+    bool ok = true;
+    for (int t = tile0; ok && t < num_tiles; t += tile_step) {
+      for (int kb = kb0; ok && kb < kb1; ++unit) {
+        const int end = kSliced ? min(kb + kSliceKb, kb1) : kb1;
+        const int buf = unit & 1;
+        ok = wait(&acc_empty[buf], ((unit >> 1) & 1) ^ 1);
+        if (!ok) break;
+        const uint32_t d = tmem + buf * BN;
+        uint32_t acc = 0;
+        for (; kb < end; ++kb) {
+          ok = wait(&full[s], ph);
+          if (!ok) break;
+          if (leader) {
+            const uint32_t at = ring + s * S::kStage;
+            const uint64_t a = umma_desc_sw128(at);
+            const uint64_t b = kOp == kApply ? umma_desc_sw128_mn(at + kParts * S::kA, 64 * 128)
+                                             : umma_desc_sw128(at + kParts * S::kA);
+            constexpr uint32_t kBStep = kOp == kApply ? 2048 >> 4 : 32 >> 4;
             auto product = [&](int pa, int pb) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
-                const uint32_t bk = b + pb * S::kB;
-                const uint64_t bd = kOp == kApply ? umma_desc_sw128_mn(bk + kk * 2048, 64 * 128)
-                                                  : umma_desc_sw128(bk + kk * 32);
-                umma_f16(d, umma_desc_sw128(a + pa * S::kA + kk * 32), bd, idesc, acc);
+                umma_f16(d, a + ((pa * S::kA) >> 4) + kk * (32 >> 4), b + ((pb * S::kB) >> 4) + kk * kBStep, idesc, acc);
                 acc = 1;
               }
             };
@@ -499,12 +501,19 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
             product(0, 0);
             umma_commit(&empty[s]);
           }
-          umma_commit(&acc_full[buf]);  // also after a wait that gave up: the epilogue is released
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1;
+          }
         }
+        if (leader) umma_commit(&acc_full[buf]);  // also after a wait that gave up: the epilogue is released
+        __syncwarp();
       }
-      umma_commit(mma_done);
-      mbar_wait(mma_done, 0, p.status, kErrTimeoutDrain);
     }
+    if (leader) umma_commit(mma_done);
+    __syncwarp();
+    mbar_wait(mma_done, 0, p.status, kErrTimeoutDrain);
     if constexpr (kSplit > 1) {
       __syncwarp();
       cluster_sync();
