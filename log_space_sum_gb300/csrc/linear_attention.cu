@@ -28,9 +28,11 @@ __device__ __forceinline__ void la_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void la_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // ------------------------------------------------------------- any type and head size
-// All products in float32 on the CUDA cores. A CTA owns one (b, h) and kDvs columns of v
-// and walks the chunks with its columns of S in shared memory; the scores are formed
-// again for each slice of columns.
+// All products in float32 on the CUDA cores. A CTA owns one (b, h), kDvs columns of v and
+// a segment of the chunks, and walks them with its columns of S in shared memory; the scores
+// are formed again for each slice of columns. A chunk takes about 10 us of latencies on one
+// CTA, so sequences are cut until every SM has several: a first launch (kStates) leaves
+// each segment's own contribution to the state, the second adds up the ones before its own.
 constexpr int kSimtThreads = 256, kSimtC = 32, kSimtDvs = 64;
 constexpr int kMaxHeadDim = 256;
 
@@ -39,10 +41,18 @@ size_t simt_smem(int dk) {
                           size_t(dk) * kSimtDvs + kSimtC + 1);
 }
 
-template <class T>
-__global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant__ LaArgs a) {
+struct LaSimtArgs {
+  LaArgs a;
+  float* partial;  // [pass][B*H][segments - 1][dk][dv], spaced for the largest pass
+  int passes, segments, chunks_per_segment;
+};
+
+template <class T, bool kStates>
+__global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant__ LaSimtArgs args) {
   extern __shared__ float sm[];
-  const LaPass& p = a.pass[blockIdx.z];
+  const LaArgs& a = args.a;
+  const int pass = blockIdx.z % args.passes, seg = blockIdx.z / args.passes;
+  const LaPass& p = a.pass[pass];
   const int c0 = blockIdx.y * kSimtDvs;
   if (c0 >= p.dv) return;
   constexpr int C = kSimtC;
@@ -56,21 +66,31 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
   float* pw = S + dk * kSimtDvs;  // l^0 .. l^C
   const float g = a.log_decay[h];
   if (tid <= C) pw[tid] = decay_pow(g, tid);
-  const long long bh = blockIdx.x;
+  const long long bh = blockIdx.x, size = static_cast<long long>(dk) * p.dv;
+  const int len = la_length(a, b), nch = (len + C - 1) / C;
+  const int first = seg * args.chunks_per_segment, last = min(first + args.chunks_per_segment, nch);
+  const int final_seg = nch > 0 ? (nch - 1) / args.chunks_per_segment : 0;
+  if (kStates ? seg >= final_seg : seg > final_seg && !(seg == args.segments - 1 && len < a.T)) return;
+  float* partial = args.partial + (static_cast<long long>(pass) * a.B * a.H + bh) * (args.segments - 1) * size;
   for (int e = tid; e < dk * kSimtDvs; e += kSimtThreads) {
     const int d = e / kSimtDvs, c = e % kSimtDvs;
     float v = 0.f;
-    if (p.s_in && c < cols)
-      v = p.s_in[bh * dk * p.dv + (p.s_in_transposed ? static_cast<long long>(c0 + c) * dk + d
-                                                     : static_cast<long long>(d) * p.dv + c0 + c)];
+    if (!kStates && c < cols) {
+      const long long at = static_cast<long long>(d) * p.dv + c0 + c;
+      if (p.s_in) v = p.s_in[bh * size + (p.s_in_transposed ? static_cast<long long>(c0 + c) * dk + d : at)];
+      for (int x = 0; x < min(seg, final_seg); ++x) {  // what the segments before this one add
+        int toks = args.chunks_per_segment * C;
+        if (!p.reverse && x == 0) toks -= nch * C - len;
+        v = decay_pow(g, toks) * v + partial[x * size + at];
+      }
+    }
     S[e] = v;
   }
   const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + h * p.qs[2];
   const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + h * p.ks[2];
   const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + h * p.vs[2] + c0;
   T* o = static_cast<T*>(p.o) + b * p.os[0] + h * p.os[2] + c0;
-  const int len = la_length(a, b), nch = (len + C - 1) / C;
-  for (int step = 0; step < nch; ++step) {
+  for (int step = first; step < last; ++step) {
     const int tile = p.reverse ? nch - 1 - step : step;
     const int t0 = len - (nch - tile) * C, pad = max(0, -t0);
     __syncthreads();  // the last chunk's reads are done
@@ -85,41 +105,43 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
       V[e] = i >= pad && c < cols ? la_load(v + (t0 + i) * p.vs[1] + c) : 0.f;
     }
     __syncthreads();
-    const int i = tid >> 3, lane8 = tid & 7;
-    {
-      float acc[C / 8] = {};
-      for (int d = 0; d < dk; ++d) {
-        const float x = Q[i * pitch + d];
-#pragma unroll
-        for (int jj = 0; jj < C / 8; ++jj) acc[jj] += x * K[(lane8 + 8 * jj) * pitch + d];
+    if constexpr (!kStates) {
+      const int i = tid >> 3, lane8 = tid & 7;
+      {
+        float acc[C / 8] = {};
+        for (int d = 0; d < dk; ++d) {
+          const float x = Q[i * pitch + d];
+  #pragma unroll
+          for (int jj = 0; jj < C / 8; ++jj) acc[jj] += x * K[(lane8 + 8 * jj) * pitch + d];
+        }
+  #pragma unroll
+        for (int jj = 0; jj < C / 8; ++jj) {
+          const int j = lane8 + 8 * jj, gap = p.reverse ? j - i : i - j;
+          P[i * (C + 1) + j] = gap >= 0 ? acc[jj] * (pw[gap] * p.c_intra) : 0.f;
+        }
       }
-#pragma unroll
-      for (int jj = 0; jj < C / 8; ++jj) {
-        const int j = lane8 + 8 * jj, gap = p.reverse ? j - i : i - j;
-        P[i * (C + 1) + j] = gap >= 0 ? acc[jj] * (pw[gap] * p.c_intra) : 0.f;
-      }
-    }
-    __syncwarp();  // a warp reads only the rows of P that it wrote
-    const int early = max(i - pad + 1, 0), late = C - 1 - i;
-    {
-      float acc[kSimtDvs / 8] = {};
-      for (int d = 0; d < dk; ++d) {
-        const float x = Q[i * pitch + d];
-#pragma unroll
-        for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] += x * S[d * kSimtDvs + lane8 + 8 * cc];
-      }
-      const float w = pw[p.reverse ? late : early] * p.c_inter;
-#pragma unroll
-      for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] *= w;
-      for (int j = 0; j < C; ++j) {
-        const float x = P[i * (C + 1) + j];
-#pragma unroll
-        for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] += x * V[j * kSimtDvs + lane8 + 8 * cc];
-      }
-      if (i >= pad) {
-#pragma unroll
-        for (int cc = 0; cc < kSimtDvs / 8; ++cc)
-          if (lane8 + 8 * cc < cols) la_store(o + (t0 + i) * p.os[1] + lane8 + 8 * cc, acc[cc]);
+      __syncwarp();  // a warp reads only the rows of P that it wrote
+      const int early = max(i - pad + 1, 0), late = C - 1 - i;
+      {
+        float acc[kSimtDvs / 8] = {};
+        for (int d = 0; d < dk; ++d) {
+          const float x = Q[i * pitch + d];
+  #pragma unroll
+          for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] += x * S[d * kSimtDvs + lane8 + 8 * cc];
+        }
+        const float w = pw[p.reverse ? late : early] * p.c_inter;
+  #pragma unroll
+        for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] *= w;
+        for (int j = 0; j < C; ++j) {
+          const float x = P[i * (C + 1) + j];
+  #pragma unroll
+          for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] += x * V[j * kSimtDvs + lane8 + 8 * cc];
+        }
+        if (i >= pad) {
+  #pragma unroll
+          for (int cc = 0; cc < kSimtDvs / 8; ++cc)
+            if (lane8 + 8 * cc < cols) la_store(o + (t0 + i) * p.os[1] + lane8 + 8 * cc, acc[cc]);
+        }
       }
     }
     __syncthreads();  // every read of S, before its update
@@ -141,27 +163,60 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
     }
   }
   __syncthreads();
-  if (p.s_out)
+  if constexpr (kStates) {
+    for (int e = tid; e < dk * kSimtDvs; e += kSimtThreads) {
+      const int d = e / kSimtDvs, c = e % kSimtDvs;
+      if (c < cols) partial[seg * size + static_cast<long long>(d) * p.dv + c0 + c] = S[e];
+    }
+    return;
+  }
+  if (p.s_out && seg == final_seg)
     for (int e = tid; e < dk * kSimtDvs; e += kSimtThreads) {
       const int d = e / kSimtDvs, c = e % kSimtDvs;
       if (c < cols) p.s_out[bh * dk * p.dv + static_cast<long long>(d) * p.dv + c0 + c] = S[e];
     }
   // rows past the length hold zeros
-  for (long long e = tid; e < static_cast<long long>(a.T - len) * cols; e += kSimtThreads)
-    la_store(o + (len + e / cols) * p.os[1] + e % cols, 0.f);
+  if (seg == args.segments - 1)
+    for (long long e = tid; e < static_cast<long long>(a.T - len) * cols; e += kSimtThreads)
+      la_store(o + (len + e / cols) * p.os[1] + e % cols, 0.f);
+}
+
+// Segments: enough that every SM has four CTAs.
+int simt_segments(long long heads, int T, int dk, int dv) {
+  const int nch = (T + kSimtC - 1) / kSimtC;
+  const int wide = dk > dv ? dk : dv;  // a backward has passes of either order
+  const long long ctas = heads * ((wide + kSimtDvs - 1) / kSimtDvs), want = (4ll * num_sms() + ctas - 1) / ctas;
+  if (nch <= 1 || want <= 1) return 1;
+  const int per = static_cast<int>((nch + want - 1) / want);
+  return (nch + per - 1) / per;
+}
+size_t simt_partial_bytes(long long heads, int segments, int dk, int dv) {
+  return sizeof(float) * static_cast<size_t>(heads) * (segments - 1) * dk * dv;
 }
 
 template <class T>
-pc_status_t launch_simt(const LaArgs& a, int passes, cudaStream_t s) {
+pc_status_t launch_simt(const LaArgs& a, int passes, void* ws, cudaStream_t s) {
   int dk = 0, dv = 0;
   for (int i = 0; i < passes; ++i) {
     dk = a.pass[i].dk > dk ? a.pass[i].dk : dk;
     dv = a.pass[i].dv > dv ? a.pass[i].dv : dv;
   }
-  const size_t smem = simt_smem(dk);
-  PC_CUDA(cudaFuncSetAttribute(k_la_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               static_cast<int>(simt_smem(kMaxHeadDim))));
-  k_la_simt<T><<<dim3(a.B * a.H, (dv + kSimtDvs - 1) / kSimtDvs, passes), kSimtThreads, smem, s>>>(a);
+  const int smem = static_cast<int>(simt_smem(dk)), most = static_cast<int>(simt_smem(kMaxHeadDim));
+  LaSimtArgs t{};
+  t.a = a;
+  t.partial = static_cast<float*>(ws);
+  t.passes = passes;
+  t.segments = simt_segments(static_cast<long long>(a.B) * a.H * passes, a.T, a.pass[0].dk, a.pass[0].dv);
+  const int nch = (a.T + kSimtC - 1) / kSimtC;
+  t.chunks_per_segment = nch > 0 ? (nch + t.segments - 1) / t.segments : 1;
+  const unsigned heads = static_cast<unsigned>(a.B) * a.H, slices = (dv + kSimtDvs - 1) / kSimtDvs;
+  if (t.segments > 1) {
+    PC_CUDA(cudaFuncSetAttribute(k_la_simt<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    k_la_simt<T, true><<<dim3(heads, slices, (t.segments - 1) * passes), kSimtThreads, smem, s>>>(t);
+    PC_LAUNCH_CHECK();
+  }
+  PC_CUDA(cudaFuncSetAttribute(k_la_simt<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+  k_la_simt<T, false><<<dim3(heads, slices, t.segments * passes), kSimtThreads, smem, s>>>(t);
   PC_LAUNCH_CHECK();
   return PC_OK;
 }
@@ -216,8 +271,8 @@ int tc_segments(long long heads, int T) {
   return at;
 }
 
-size_t tc_partial_bytes(long long heads, int passes, int segments, int dk, int dv) {
-  return sizeof(float) * static_cast<size_t>(heads) * passes * (segments - 1) * tc_pad(dk) * tc_pad(dv);
+size_t tc_partial_bytes(long long heads, int segments, int dk, int dv) {
+  return sizeof(float) * static_cast<size_t>(heads) * (segments - 1) * tc_pad(dk) * tc_pad(dv);
 }
 
 template <int DK, int DV>
@@ -280,7 +335,7 @@ pc_status_t run_tc(const LaArgs& a, int passes, void* ws, cudaStream_t s, bool* 
       part.a.pass[j - i] = t.a.pass[j];
       part.maps[j - i] = t.maps[j];
     }
-    part.partial = t.partial + tc_partial_bytes(heads, i, t.segments, dk, dv) / sizeof(float);
+    part.partial = t.partial + tc_partial_bytes(heads * i, t.segments, dk, dv) / sizeof(float);
     if (dk == 64 && dv == 64)
       PC_TRY((launch_tc<64, 64>(part, n - i, s)));
     else if (dk == 64)
@@ -409,11 +464,14 @@ pc_status_t check_tensor(const char* name, const void* p, pc_dtype_t dt) {
   return PC_OK;
 }
 
-// Workspace: the segments' shares of the state.
+// Workspace: the segments' shares of the state, in whichever variant the tensors' alignment
+// will allow.
 size_t la_workspace(int B, int T, int H, int dk, int dv, int passes, pc_dtype_t dt) {
-  const long long heads = static_cast<long long>(B) * H;
-  if (!tc_heads(dk, dv, dt) || T == 0 || heads == 0) return 0;
-  return tc_partial_bytes(heads, passes, tc_segments(heads * passes, T), dk, dv);
+  const long long heads = static_cast<long long>(B) * H * passes;
+  if (T == 0 || heads == 0) return 0;
+  const size_t simt = simt_partial_bytes(heads, simt_segments(heads, T, dk, dv), dk, dv);
+  const size_t tc = tc_heads(dk, dv, dt) ? tc_partial_bytes(heads, tc_segments(heads, T), dk, dv) : 0;
+  return simt > tc ? simt : tc;
 }
 
 pc_status_t run_passes(const LaArgs& a, int passes, pc_dtype_t dt, void* ws, size_t ws_bytes, cudaStream_t s) {
@@ -427,7 +485,7 @@ pc_status_t run_passes(const LaArgs& a, int passes, pc_dtype_t dt, void* ws, siz
     PC_TRY(run_tc(a, passes, ws, s, &done));
     if (done) return PC_OK;
   }
-  return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, passes, s) : launch_simt<float>(a, passes, s);
+  return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, passes, ws, s) : launch_simt<float>(a, passes, ws, s);
 }
 
 LaPass make_pass(const void* q, const long long* qs, const void* k, const long long* ks, const void* v,

@@ -26,7 +26,7 @@ namespace {
 constexpr float kScaleA = 4096.f, kScaleB = 1024.f;
 
 // ------------------------------------------------------------------ norm and operands
-constexpr int kNormThreads = 256, kNormBlocks = 256;
+constexpr int kNormThreads = 256, kNormBlocks = 608;
 
 __device__ __forceinline__ float orth_value(const float* p) { return *p; }
 __device__ __forceinline__ float orth_value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
@@ -107,8 +107,83 @@ __device__ __forceinline__ void half_split(float v, __half* hi, __half* lo) {
   *lo = __float2half_rn(v - __half2float(*hi));
 }
 
-// Xs = 2^e G (or its transpose) over 64 x 64 tiles; nu[g] = 2^-e / (|G|_F + eps). 2^e brings
-// the root mean square of the entries near one, within float16's range for the largest.
+// The whole block's |G|_F^2 from its matrix's partial sums.
+__device__ __forceinline__ float orth_total(int blocks, const float* part, float* red) {
+  float s = 0.f;
+  for (int i = threadIdx.x; i < blocks; i += kNormThreads) s += part[i];
+  return block_total(s, red);
+}
+
+// 2^e for Xs = 2^e G: 2^e |G|_F <= 2^15 and the root mean square near one, exponents only.
+// Zero (or a norm that is not finite): e = 0, and nu = 2^-e / (|G|_F + eps) carries what
+// comes of it.
+__device__ __forceinline__ float orth_scale(int rows, int cols, float total, float eps, float* nu) {
+  const float norm = sqrtf(total) + eps;
+  int e = 0;
+  if (norm > 0.f && norm < 3e38f) {
+    int at;
+    frexpf(norm, &at);  // norm = f 2^at, f in [1/2, 1)
+    const int spread = (32 - __clz(rows) + 32 - __clz(cols)) / 2;  // sqrt(rows cols) within a factor of two
+    e = max(-126, min(min(spread, 15) - at, 126));
+  }
+  *nu = total == 0.f ? 0.f : ldexpf(1.f, -e) / norm;
+  return ldexpf(1.f, e);
+}
+
+// Xs = 2^e G where G is not taller than wide and its rows are whole 16-byte pieces: a stream.
+template <class T, int kParts>
+__global__ void __launch_bounds__(kNormThreads)
+    k_orth_load_rows(int rows, int cols, const T* __restrict__ g, int blocks, const float* part, float eps, HalfMat x,
+                     float* nu) {
+  __shared__ float red[kNormThreads / 32];
+  constexpr int L = kPiece<T>, kFlight = 4;
+  const int m = blockIdx.y, pieces = cols / L;
+  const long long n = static_cast<long long>(rows) * pieces, stride = static_cast<long long>(gridDim.x) * kNormThreads;
+  const T* src = g + static_cast<long long>(m) * rows * cols;
+  __half* dst = x.ptr + static_cast<size_t>(m) * x.rows * x.ld;
+  long long i = blockIdx.x * static_cast<long long>(kNormThreads) + threadIdx.x;
+  uint4 raw[kFlight];
+  auto fetch = [&]() {
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k)
+      if (i + k * stride < n) raw[k] = reinterpret_cast<const uint4*>(src)[i + k * stride];
+  };
+  fetch();
+  grid_dependency_wait();  // the sums of squares
+  grid_dependents_launch();
+  float inv;
+  const float up = orth_scale(rows, cols, orth_total(blocks, part + m * kNormBlocks, red), eps, &inv);
+  if (blockIdx.x == 0 && threadIdx.x == 0) nu[m] = inv;
+  for (; i < n; i += kFlight * stride, fetch()) {
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const long long at = i + k * stride;
+      if (at >= n) break;
+      float v[L];
+      orth_unpack(raw[k], v);
+      uint32_t hi[L / 2], lo[L / 2];
+#pragma unroll
+      for (int e = 0; e < L / 2; ++e) {
+        __half h0, l0, h1, l1;
+        half_split(v[2 * e] * up, &h0, &l0);
+        half_split(v[2 * e + 1] * up, &h1, &l1);
+        const __half2 h = __halves2half2(h0, h1), l = __halves2half2(l0, l1);
+        hi[e] = *reinterpret_cast<const uint32_t*>(&h);
+        lo[e] = *reinterpret_cast<const uint32_t*>(&l);
+      }
+      __half* to = dst + (at / pieces) * x.ld + (at % pieces) * L;
+      if constexpr (L == 8) {
+        *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if constexpr (kParts == 2) *reinterpret_cast<uint4*>(to + x.lo) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      } else {
+        *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+        if constexpr (kParts == 2) *reinterpret_cast<uint2*>(to + x.lo) = make_uint2(lo[0], lo[1]);
+      }
+    }
+  }
+}
+
+// Xs = 2^e G (or its transpose) over 64 x 64 tiles; any shape and alignment.
 template <class T, int kParts>
 __global__ void __launch_bounds__(kNormThreads)
     k_orth_load(int rows, int cols, const T* __restrict__ g, int blocks, const float* part, float eps, int tall,
@@ -136,20 +211,9 @@ __global__ void __launch_bounds__(kNormThreads)
   }
   grid_dependency_wait();  // the sums of squares
   grid_dependents_launch();
-  const float total = block_total(t < blocks ? part[m * kNormBlocks + t] : 0.f, red);
-  const float norm = sqrtf(total) + eps;
-  // 2^e sqrt(total) <= 2^15 and 2^e rms <= 2: exponents only. Zero (or a norm that is not
-  // finite): e = 0, and nu carries what comes of it.
-  int e = 0;
-  if (norm > 0.f && norm < 3e38f) {
-    int at;
-    frexpf(norm, &at);  // norm = f 2^at, f in [1/2, 1)
-    const int spread = (32 - __clz(rows) + 32 - __clz(cols)) / 2;  // sqrt(rows cols) within a factor of two
-    e = min(spread, 15) - at;
-    e = max(-126, min(e, 126));
-  }
-  const float up = ldexpf(1.f, e);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) nu[m] = total == 0.f ? 0.f : ldexpf(1.f, -e) / norm;
+  float inv;
+  const float up = orth_scale(rows, cols, orth_total(blocks, part + m * kNormBlocks, red), eps, &inv);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) nu[m] = inv;
   __half* hi = x.ptr + static_cast<size_t>(m) * x.rows * x.ld;
 #pragma unroll
   for (int i = t; i < 64 * 32; i += kNormThreads) {  // pairs of columns of the operand
@@ -344,22 +408,20 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, i
 constexpr int kSliceKb = 2;
 constexpr int kOrthThreads = 64 + 8 * 32;
 
-template <int kParts, int BN, bool kShort>
+template <int kParts, int BN>
 struct OrthRing {
-  // short: a few blocks of K per CTA, in a chain of small launches; two CTAs per SM then let
-  // a launch set up while the one before it finishes
-  static constexpr int kFit = ((kShort ? 113 : 227) * 1024 - 2048) / OrthShape<kParts, BN>::kStage;
+  static constexpr int kFit = (227 * 1024 - 2048) / OrthShape<kParts, BN>::kStage;
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static constexpr uint32_t kBytes = kStages * OrthShape<kParts, BN>::kStage + 2048;
 };
 
-template <int kParts, int BN, int kSplit, bool kShort, int kOp, class T>
+template <int kParts, int BN, int kSplit, int kOp, class T>
 __global__ void __launch_bounds__(kOrthThreads, 1)
     k_orth_gemm(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__ CUtensorMap a_lo,
                 const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
                 const __grid_constant__ OrthArgs p) {
   using S = OrthShape<kParts, BN>;
-  constexpr int kStages = OrthRing<kParts, BN, kShort>::kStages;
+  constexpr int kStages = OrthRing<kParts, BN>::kStages;
   constexpr bool kPairs = kOp != kApply;
   constexpr bool kSliced = kParts == 2;
   constexpr uint32_t kCols = 2 * BN;  // two accumulators
@@ -540,6 +602,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       if (lane == 0) mbar_arrive(&acc_empty[unit & 1]);
       ++unit;
     };
+    // the other ranks' sums land at [source][chunk][column][row]
+    auto slot = [&](int src, int own) { return ((src * kOwn + own) * 32 * kBM + row) * 4; };
     for (int t = tile0; ok && t < num_tiles; t += tile_step) {
       int g, m0, n0;
       tile_at(t, g, m0, n0);
@@ -557,6 +621,53 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           tmem_ld_32x32(lanes + (unit & 1) * BN + c, v);
           if (c + 64 >= BN) release();
           orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + c, mirror, v, now);
+        }
+      } else if constexpr (kSplit > 1 && !kSliced) {
+        // straight from tensor memory, one chunk of 32 columns at a time
+        static_assert(kChunks == 2, "a warp has the chunks part and part + 2");
+        const bool any = kb1 > kb0;  // a share of no blocks: the accumulator was never written
+        ok = !any || wait_unit();
+        auto load = [&](int xc, float (&v)[32]) {
+          if (any) {
+            tmem_ld_32x32(lanes + (unit & 1) * BN + xc * 32, v);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          }
+        };
+        const int own0 = part % kSplit == rank ? part : (part + 2) % kSplit == rank ? part + 2 : -1;
+        HalfRun<kParts> x;
+        if (own0 >= 0) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + own0 * 32, x);
+        cluster_sync();  // every ring of the cluster is idle
+        if (ok) {
+#pragma unroll 1
+          for (int xc = part; xc < BN / 32; xc += 2) {
+            const int owner = xc % kSplit;
+            if (owner == rank) continue;
+            float v[32];
+            load(xc, v);
+            const uint32_t to = cluster_map(smem_addr(smem), owner) + slot(rank - (rank > owner), xc / kSplit);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + i * kBM * 4), "f"(v[i]) : "memory");
+          }
+        }
+        cluster_sync();  // the others' sums of this CTA's columns have landed
+        if (ok && own0 >= 0) {
+#pragma unroll 1
+          for (int xc = own0; xc < BN / 32; xc += 2) {
+            if (xc % kSplit != rank) continue;
+            if (xc != own0) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + xc * 32, x);
+            float v[32];
+            load(xc, v);
+#pragma unroll
+            for (int src = 0; src < kSplit - 1; ++src) {
+              const float* from = reinterpret_cast<const float*>(smem + slot(src, xc / kSplit));
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] += from[i * kBM];
+            }
+            orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + xc * 32, mirror, v, x);
+          }
         }
       } else {
         float acc[kChunks][32];
@@ -587,13 +698,11 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
             }
           }
         } else {
-          // the other ranks' sums land at [source][chunk][column][row]
           HalfRun<kParts> x[kChunks];
 #pragma unroll
           for (int c = 0; c < kChunks; ++c)
             if ((2 * c + part) % kSplit == rank) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + (2 * c + part) * 32, x[c]);
           cluster_sync();  // every ring of the cluster is idle
-          auto slot = [&](int src, int own) { return ((src * kOwn + own) * 32 * kBM + row) * 4; };
           if (ok) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c) {
@@ -634,12 +743,12 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 // --------------------------------------------------------------------------- launches
 inline unsigned blocks_of(long long a, long long b) { return static_cast<unsigned>((a + b - 1) / b); }
 
-template <int kParts, int BN, int kSplit, bool kShort, int kOp, class T>
+template <int kParts, int BN, int kSplit, int kOp, class T>
 pc_status_t launch_orth(const OrthArgs& p, const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], cudaStream_t s,
                         long long tiles, long long flops) {
-  constexpr uint32_t smem = OrthRing<kParts, BN, kShort>::kBytes;
+  constexpr uint32_t smem = OrthRing<kParts, BN>::kBytes;
   static_assert(smem <= 232448, "shared memory per CTA");
-  auto* kernel = k_orth_gemm<kParts, BN, kSplit, kShort, kOp, T>;
+  auto* kernel = k_orth_gemm<kParts, BN, kSplit, kOp, T>;
   PC_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -663,12 +772,15 @@ pc_status_t launch_orth(const OrthArgs& p, const CUtensorMap (&a)[2], const CUte
 }
 
 // CTAs of a cluster that share a tile of 128 x 128. A cluster lies within one of the GPU's
-// eight groups of SMs, so at most 8 floor(SMs / 8 / size) clusters run at once; each CTA
-// keeps two blocks of K or more.
-inline int split_of(long long tiles, int num_kb) {
+// eight groups of SMs, so at most 8 floor(SMs / 8 / size) clusters run at once. Sharing costs
+// about 1 us (two cluster barriers and the exchange), five blocks of K (measured at 16
+// blocks: 7.4 us a product alone, 7.1 shared by three; at 8: 5.8 against 6.4), so each CTA
+// keeps at least as many; with two parts a block is three products.
+inline int split_of(long long tiles, int num_kb, int parts) {
+  const int blocks = parts == 2 ? 3 * num_kb : num_kb;
   int best = 1;
   for (int size = 2; size <= 4; ++size)
-    if (tiles <= 8 * (num_sms() / 8 / size) && num_kb >= 2 * size) best = size;
+    if (tiles <= 8 * (num_sms() / 8 / size) && blocks >= 5 * size) best = size;
   return best;
 }
 
@@ -680,25 +792,18 @@ pc_status_t run_product(OrthArgs p, const CUtensorMap (&a)[2], const CUtensorMap
   if constexpr (kOp == kApply && kParts == 1) {
     if (wide >= num_sms()) {
       p.tiles_n = static_cast<int>(blocks_of(p.N, 256));
-      return launch_orth<kParts, 256, 1, false, kOp, T>(p, a, b, s, wide, flops);
+      return launch_orth<kParts, 256, 1, kOp, T>(p, a, b, s, wide, flops);
     }
   }
   p.tiles_n = static_cast<int>(blocks_of(p.N, 128));
   const long long tiles = (kOp == kApply ? p.tiles_m * static_cast<long long>(p.tiles_n)
                                          : p.tiles_m * (p.tiles_m + 1ll) / 2) * p.batch;
-  const int split = split_of(tiles, p.num_kb);
-  if (kParts == 1 && p.num_kb <= 6 * split) {
-    switch (split) {
-      case 4: return launch_orth<kParts, 128, 4, kParts == 1, kOp, T>(p, a, b, s, tiles, flops);
-      case 3: return launch_orth<kParts, 128, 3, kParts == 1, kOp, T>(p, a, b, s, tiles, flops);
-      case 2: return launch_orth<kParts, 128, 2, kParts == 1, kOp, T>(p, a, b, s, tiles, flops);
-    }
-  }
+  const int split = split_of(tiles, p.num_kb, kParts);
   switch (split) {
-    case 4: return launch_orth<kParts, 128, 4, false, kOp, T>(p, a, b, s, tiles, flops);
-    case 3: return launch_orth<kParts, 128, 3, false, kOp, T>(p, a, b, s, tiles, flops);
-    case 2: return launch_orth<kParts, 128, 2, false, kOp, T>(p, a, b, s, tiles, flops);
-    default: return launch_orth<kParts, 128, 1, false, kOp, T>(p, a, b, s, tiles, flops);
+    case 4: return launch_orth<kParts, 128, 4, kOp, T>(p, a, b, s, tiles, flops);
+    case 3: return launch_orth<kParts, 128, 3, kOp, T>(p, a, b, s, tiles, flops);
+    case 2: return launch_orth<kParts, 128, 2, kOp, T>(p, a, b, s, tiles, flops);
+    default: return launch_orth<kParts, 128, 1, kOp, T>(p, a, b, s, tiles, flops);
   }
 }
 
@@ -765,13 +870,20 @@ pc_status_t run_orth(int batch, int rows, int cols, const T* G, int steps, float
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks_of(cols, 64), blocks_of(rows, 64), batch);
     cfg.blockDim = dim3(kNormThreads);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    PC_CUDA(cudaLaunchKernelEx(&cfg, k_orth_load<T, kParts>, rows, cols, G, blocks, static_cast<const float*>(p.part),
-                               eps, tall, p.X[0], p.nu));
+    if (!tall && cols % kPiece<T> == 0) {
+      const long long want_load = blocks_of(n / kPiece<T>, 4 * kNormThreads), most = 4ll * num_sms();
+      cfg.gridDim = dim3(static_cast<unsigned>(want_load < most ? want_load : most), batch);
+      PC_CUDA(cudaLaunchKernelEx(&cfg, k_orth_load_rows<T, kParts>, rows, cols, G, blocks,
+                                 static_cast<const float*>(p.part), eps, p.X[0], p.nu));
+    } else {
+      cfg.gridDim = dim3(blocks_of(cols, 64), blocks_of(rows, 64), batch);
+      PC_CUDA(cudaLaunchKernelEx(&cfg, k_orth_load<T, kParts>, rows, cols, G, blocks,
+                                 static_cast<const float*>(p.part), eps, tall, p.X[0], p.nu));
+    }
     PC_LAUNCH_CHECK();
   }
   CUtensorMap x_rows[2][2], x_cols[2][2], ma[2], mb[2];  // X as K-major rows, and as rows along K
