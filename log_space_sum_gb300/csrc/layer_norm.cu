@@ -82,7 +82,10 @@ __device__ __forceinline__ float2 row_sum(float a, float b, float2* red) {
 
 // ------------------------------------------------------------------------ forward
 // kWarps = 1: a warp per row, kRows rows per CTA; kWarps > 1: a CTA per row. A thread
-// holds kVecs 16-byte pieces of its row (piece i at (i * threads + t)).
+// holds kVecs 16-byte pieces of its row (piece i at (i * threads + t)). A CTA per row and no
+// loop over rows: CTAs that stay and fetch ahead were slower (32768 rows of 4096 bf16 values:
+// 109 us against 101, of 1024: 34 against 29), and so were more threads per row (128 us with
+// 256 threads, 177 with 512).
 template <class T, int kWarps, int kVecs, int kRows>
 __global__ void __launch_bounds__(32 * kWarps * kRows)
     k_ln_fwd(long long rows, int dim, const T* __restrict__ x, long long x_ld, const float* __restrict__ w,
@@ -213,10 +216,10 @@ __global__ void __launch_bounds__(kAnyThreads)
 // ----------------------------------------------------------------------- backward
 // A CTA walks groups of kRows rows; a thread keeps its columns' sums of dy z and dy in
 // registers over all of them and writes them once, as one row of the partial sums
-// part[2][gridDim.x][dim] (k_ln_reduce adds those rows in a fixed order). All loads of
-// a group are in flight together and one barrier serves its rows' sums.
-template <class T, int kWarps, int kVecs, int kRows>
-__global__ void __launch_bounds__(32 * kWarps)
+// part[2][gridDim.x][dim] (k_ln_reduce adds those rows in a fixed order). One barrier serves
+// the group's sums, and the next group's loads are on their way meanwhile.
+template <class T, int kWarps, int kVecs, int kRows, int kCtas>
+__global__ void __launch_bounds__(32 * kWarps, kCtas)
     k_ln_bwd(long long rows, int dim, const T* __restrict__ dy, long long dy_ld, const T* __restrict__ x,
              long long x_ld, const float* __restrict__ w, const float* __restrict__ mean,
              const float* __restrict__ rstd, T* __restrict__ dx, long long dx_ld, float* __restrict__ part) {
@@ -236,24 +239,28 @@ __global__ void __launch_bounds__(32 * kWarps)
     if (w && c < dim) load_params<L>(w, c, wv[i]);
   }
   int flip = 0;
-  for (long long r0 = static_cast<long long>(blockIdx.x) * kRows; r0 < rows;
-       r0 += static_cast<long long>(gridDim.x) * kRows, flip ^= 1) {
-    uint4 rx[kRows][kVecs], rd[kRows][kVecs];
-    float m[kRows], rs[kRows];
+  uint4 rx[kRows][kVecs], rd[kRows][kVecs], nx[kRows][kVecs], nd[kRows][kVecs];
+  auto fetch = [&](uint4 (&tx)[kRows][kVecs], uint4 (&td)[kRows][kVecs], long long r0) {
 #pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const long long r = r0 + k;
+    for (int k = 0; k < kRows; ++k)
 #pragma unroll
       for (int i = 0; i < kVecs; ++i) {
         const int c = (i * kThreads + t) * L;
-        rx[k][i] = rd[k][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (c < dim && r < rows) {
-          rx[k][i] = __ldcs(reinterpret_cast<const uint4*>(x + r * x_ld + c));
-          rd[k][i] = __ldcs(reinterpret_cast<const uint4*>(dy + r * dy_ld + c));
-        }
+        const bool in = c < dim && r0 + k < rows;
+        tx[k][i] = in ? __ldcs(reinterpret_cast<const uint4*>(x + (r0 + k) * x_ld + c)) : make_uint4(0u, 0u, 0u, 0u);
+        td[k][i] = in ? __ldcs(reinterpret_cast<const uint4*>(dy + (r0 + k) * dy_ld + c)) : make_uint4(0u, 0u, 0u, 0u);
       }
-      m[k] = r < rows ? mean[r] : 0.f;
-      rs[k] = r < rows ? rstd[r] : 0.f;
+  };
+  const long long stride = static_cast<long long>(gridDim.x) * kRows;
+  long long r0 = static_cast<long long>(blockIdx.x) * kRows;
+  fetch(rx, rd, r0);
+  for (; r0 < rows; r0 += stride, flip ^= 1) {
+    fetch(nx, nd, r0 + stride);
+    float m[kRows], rs[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      m[k] = r0 + k < rows ? mean[r0 + k] : 0.f;
+      rs[k] = r0 + k < rows ? rstd[r0 + k] : 0.f;
     }
     float sg[kRows], sz[kRows];
 #pragma unroll
@@ -308,6 +315,13 @@ __global__ void __launch_bounds__(32 * kWarps)
         }
       }
     }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        rx[k][i] = nx[k][i];
+        rd[k][i] = nd[k][i];
+      }
   }
   if (part) {
 #pragma unroll
@@ -490,7 +504,7 @@ void launch_fwd(const LnFwd& a, cudaStream_t s) {
   else if (vec && pieces <= 256)
     fwd_kernel<T, 4, 2, 1>(a, s);
   else if (vec && pieces <= 512)
-    fwd_kernel<T, 4, 4, 1>(a, s);
+    fwd_kernel<T, 2, 8, 1>(a, s);
   else if (vec && pieces <= 1024)
     fwd_kernel<T, 8, 4, 1>(a, s);
   else if (vec && pieces <= 2048)
@@ -517,46 +531,47 @@ struct LnBwd {
   unsigned grid;
 };
 
-// CTAs of the backward: enough to fill the GPU, few enough that the partial sums stay
-// small beside the rows. (The same for every variant: the workspace query uses it.)
+// CTAs of the backward at most, the rows of partial sums that the workspace holds.
 unsigned bwd_grid(long long rows) {
-  const long long most = 4ll * num_sms();
+  const long long most = 6ll * num_sms();
   return static_cast<unsigned>(rows < most ? rows : most);
 }
 
-template <class T, int kWarps, int kVecs, int kRows>
-void bwd_kernel(const LnBwd& a, cudaStream_t s) {
-  k_ln_bwd<T, kWarps, kVecs, kRows><<<a.grid, 32 * kWarps, 0, s>>>(
+template <class T, int kWarps, int kVecs, int kRows, int kCtas>
+void bwd_kernel(LnBwd& a, cudaStream_t s) {
+  const long long want = (a.rows + kRows - 1) / kRows, most = static_cast<long long>(kCtas) * num_sms();
+  a.grid = static_cast<unsigned>(want < most ? want : most);
+  k_ln_bwd<T, kWarps, kVecs, kRows, kCtas><<<a.grid, 32 * kWarps, 0, s>>>(
       a.rows, a.dim, static_cast<const T*>(a.dy), a.dy_ld, static_cast<const T*>(a.x), a.x_ld, a.w, a.mean, a.rstd,
       static_cast<T*>(a.dx), a.dx_ld, a.part);
 }
 
 template <class T, int kCols>
-void bwd_any(const LnBwd& a, cudaStream_t s) {
+void bwd_any(LnBwd& a, cudaStream_t s) {
   k_ln_bwd_any<T, kCols><<<a.grid, kAnyThreads, 0, s>>>(
       a.rows, a.dim, static_cast<const T*>(a.dy), a.dy_ld, static_cast<const T*>(a.x), a.x_ld, a.w, a.mean, a.rstd,
       static_cast<T*>(a.dx), a.dx_ld, a.part);
 }
 
 template <class T>
-void launch_bwd(const LnBwd& a, cudaStream_t s) {
+void launch_bwd(LnBwd& a, cudaStream_t s) {
   const bool vec = a.dim % kLanes<T> == 0 && rows_aligned(a.x, a.x_ld, sizeof(T)) &&
                    rows_aligned(a.dy, a.dy_ld, sizeof(T)) && rows_aligned(a.dx, a.dx_ld, sizeof(T)) &&
                    (!a.w || aligned16(a.w));
   const int pieces = a.dim / kLanes<T>;
-  // four rows (two of the longest) in flight per CTA once each CTA has several
-  const bool many = a.rows >= 8ll * a.grid;
-  auto pick = [&](auto one, auto several) { many ? several() : one(); };
+  // CTAs of 768 threads per SM (512 for long rows) leave the registers for a group in hand
+  // and one on its way; two rows a group while there are rows for that
+  const bool many = a.rows >= 16ll * num_sms();
   if (vec && pieces <= 64)
-    pick([&] { bwd_kernel<T, 2, 1, 1>(a, s); }, [&] { bwd_kernel<T, 2, 1, 4>(a, s); });
+    many ? bwd_kernel<T, 2, 1, 2, 6>(a, s) : bwd_kernel<T, 2, 1, 1, 6>(a, s);
   else if (vec && pieces <= 128)
-    pick([&] { bwd_kernel<T, 4, 1, 1>(a, s); }, [&] { bwd_kernel<T, 4, 1, 4>(a, s); });
+    many ? bwd_kernel<T, 4, 1, 2, 6>(a, s) : bwd_kernel<T, 4, 1, 1, 6>(a, s);
   else if (vec && pieces <= 256)
-    pick([&] { bwd_kernel<T, 8, 1, 1>(a, s); }, [&] { bwd_kernel<T, 8, 1, 4>(a, s); });
+    many ? bwd_kernel<T, 8, 1, 2, 3>(a, s) : bwd_kernel<T, 8, 1, 1, 3>(a, s);
   else if (vec && pieces <= 512)
-    pick([&] { bwd_kernel<T, 8, 2, 1>(a, s); }, [&] { bwd_kernel<T, 8, 2, 2>(a, s); });
+    bwd_kernel<T, 8, 2, 1, 2>(a, s);
   else if (vec && pieces <= 1024)
-    bwd_kernel<T, 16, 2, 1>(a, s);
+    bwd_kernel<T, 16, 2, 1, 1>(a, s);
   else if (a.dim <= 4 * kAnyThreads)
     bwd_any<T, 4>(a, s);
   else if (a.dim <= 8 * kAnyThreads)
@@ -627,20 +642,21 @@ pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy, long long
     PC_TRY(pc::check_rows("dx", dx, dx_ld, rows, dim, dtype));
     PC_CHECK(mean && rstd, PC_ERR_NULL, "mean and rstd must not be NULL");
   }
-  const unsigned grid = pc::bwd_grid(rows);
+  unsigned grid = pc::bwd_grid(rows);  // of the launch at most
   if (params && rows > 0) {
     PC_CHECK(ws && ws_bytes >= 2 * sizeof(float) * static_cast<size_t>(grid) * dim, PC_ERR_WORKSPACE,
              "workspace of %zu bytes is too small", ws_bytes);
     PC_CHECK(pc::aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
   }
   if (rows > 0) {
-    const pc::LnBwd a{rows, dim, dy, dy_ld, x, x_ld, weight, mean, rstd, dx, dx_ld,
+    pc::LnBwd a{rows, dim, dy, dy_ld, x, x_ld, weight, mean, rstd, dx, dx_ld,
                       params ? static_cast<float*>(ws) : nullptr, grid};
     if (dtype == PC_BF16)
       pc::launch_bwd<__nv_bfloat16>(a, stream);
     else
       pc::launch_bwd<float>(a, stream);
     PC_LAUNCH_CHECK();
+    grid = a.grid;
   }
   if (params) {  // no rows: the sums are zero
     cudaLaunchAttribute attr;  // set up while the rows are still being read
