@@ -28,17 +28,36 @@ __device__ __forceinline__ void la_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void la_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // ------------------------------------------------------------- any type and head size
-// All products in float32 on the CUDA cores. A CTA owns one (b, h), kDvs columns of v and
-// a segment of the chunks, and walks them with its columns of S in shared memory; the scores
-// are formed again for each slice of columns. A chunk takes about 10 us of latencies on one
-// CTA, so sequences are cut until every SM has several: a first launch (kStates) leaves
-// each segment's own contribution to the state, the second adds up the ones before its own.
+// All products in float32 on the CUDA cores. A CTA owns one (b, h), kSimtDvs columns of v
+// and a segment of the chunks, and walks them with its columns of S in shared memory; the
+// scores are formed again for each slice of columns. A thread's outputs are tiles of 2 x 2
+// scores, 2 x 4 of O and 4 x 4 of S, fed by 16-byte shared loads (one value at a time the
+// loads bound the kernel). A chunk is a few us of latencies on one CTA, so sequences are cut
+// until every SM has several: a first launch (kStates) leaves each segment's own
+// contribution to the state, the second adds up the ones before its own.
 constexpr int kSimtThreads = 256, kSimtC = 32, kSimtDvs = 64;
 constexpr int kMaxHeadDim = 256;
 
+// Floats between rows of Q and K: whole 16-byte pieces, an odd number of them (eight lanes'
+// rows then lie in different banks).
+__host__ __device__ inline int simt_pitch(int dk) { return 4 * (((dk + 3) / 4) | 1); }
+constexpr int kSimtPPitch = kSimtC + 4;
+
 size_t simt_smem(int dk) {
-  return sizeof(float) * (2 * size_t(kSimtC) * (dk + 1) + size_t(kSimtC) * kSimtDvs + size_t(kSimtC) * (kSimtC + 1) +
-                          size_t(dk) * kSimtDvs + kSimtC + 1);
+  const size_t wide = (dk + 3) / 4 * 4;
+  return sizeof(float) * (2 * size_t(kSimtC) * simt_pitch(dk) + 2 * size_t(kSimtC) * kSimtDvs +
+                          size_t(kSimtC) * kSimtPPitch + wide * kSimtDvs + kSimtC + 1);
+}
+
+__device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ void fma4(float4& a, float k, const float4& v) {
+  a.x += k * v.x;
+  a.y += k * v.y;
+  a.z += k * v.z;
+  a.w += k * v.w;
+}
+__device__ __forceinline__ float dot4(const float4& a, const float4& b, float c) {
+  return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w + c;
 }
 
 struct LaSimtArgs {
@@ -49,21 +68,24 @@ struct LaSimtArgs {
 
 template <class T, bool kStates>
 __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant__ LaSimtArgs args) {
-  extern __shared__ float sm[];
+  extern __shared__ __align__(16) float sm[];
+  if constexpr (kStates) grid_dependents_launch();
   const LaArgs& a = args.a;
   const int pass = blockIdx.z % args.passes, seg = blockIdx.z / args.passes;
   const LaPass& p = a.pass[pass];
   const int c0 = blockIdx.y * kSimtDvs;
   if (c0 >= p.dv) return;
   constexpr int C = kSimtC;
-  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, dk = p.dk, pitch = dk + 1, tid = threadIdx.x;
+  const int b = blockIdx.x / a.H, h = blockIdx.x % a.H, dk = p.dk, pitch = simt_pitch(dk), tid = threadIdx.x;
+  const int wide = (dk + 3) / 4 * 4, warp = tid >> 5, lane = tid & 31;
   const int cols = min(kSimtDvs, p.dv - c0);
   float* Q = sm;
   float* K = Q + C * pitch;
   float* V = K + C * pitch;
-  float* P = V + C * kSimtDvs;
-  float* S = P + C * (C + 1);
-  float* pw = S + dk * kSimtDvs;  // l^0 .. l^C
+  float* Vw = V + C * kSimtDvs;  // V times the tokens' weights in the state
+  float* P = Vw + C * kSimtDvs;
+  float* S = P + C * kSimtPPitch;
+  float* pw = S + wide * kSimtDvs;  // l^0 .. l^C
   const float g = a.log_decay[h];
   if (tid <= C) pw[tid] = decay_pow(g, tid);
   const long long bh = blockIdx.x, size = static_cast<long long>(dk) * p.dv;
@@ -72,17 +94,19 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
   const int final_seg = nch > 0 ? (nch - 1) / args.chunks_per_segment : 0;
   if (kStates ? seg >= final_seg : seg > final_seg && !(seg == args.segments - 1 && len < a.T)) return;
   float* partial = args.partial + (static_cast<long long>(pass) * a.B * a.H + bh) * (args.segments - 1) * size;
-  for (int e = tid; e < dk * kSimtDvs; e += kSimtThreads) {
+  // decay over a segment before this one; a forward's first one may lack tokens
+  const float over = decay_pow(g, args.chunks_per_segment * C);
+  if (!kStates && seg > 0) grid_dependency_wait();  // the states
+  const float over0 = p.reverse ? over : decay_pow(g, args.chunks_per_segment * C - (nch * C - len));
+  for (int e = tid; e < wide * kSimtDvs; e += kSimtThreads) {
     const int d = e / kSimtDvs, c = e % kSimtDvs;
     float v = 0.f;
-    if (!kStates && c < cols) {
+    if (!kStates && c < cols && d < dk) {
       const long long at = static_cast<long long>(d) * p.dv + c0 + c;
       if (p.s_in) v = p.s_in[bh * size + (p.s_in_transposed ? static_cast<long long>(c0 + c) * dk + d : at)];
-      for (int x = 0; x < min(seg, final_seg); ++x) {  // what the segments before this one add
-        int toks = args.chunks_per_segment * C;
-        if (!p.reverse && x == 0) toks -= nch * C - len;
-        v = decay_pow(g, toks) * v + partial[x * size + at];
-      }
+#pragma unroll 4
+      for (int x = 0; x < min(seg, final_seg); ++x)  // what the segments before this one add
+        v = (x == 0 ? over0 : over) * v + partial[x * size + at];
     }
     S[e] = v;
   }
@@ -94,72 +118,90 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
     const int tile = p.reverse ? nch - 1 - step : step;
     const int t0 = len - (nch - tile) * C, pad = max(0, -t0);
     __syncthreads();  // the last chunk's reads are done
-    for (int e = tid; e < C * dk; e += kSimtThreads) {
-      const int i = e / dk, d = e % dk;
+#pragma unroll
+    for (int r = 0; r < C / 8; ++r) {
+      const int i = warp + 8 * r;
       const bool in = i >= pad;
-      Q[i * pitch + d] = in ? la_load(q + (t0 + i) * p.qs[1] + d) : 0.f;
-      K[i * pitch + d] = in ? la_load(k + (t0 + i) * p.ks[1] + d) : 0.f;
-    }
-    for (int e = tid; e < C * kSimtDvs; e += kSimtThreads) {
-      const int i = e / kSimtDvs, c = e % kSimtDvs;
-      V[e] = i >= pad && c < cols ? la_load(v + (t0 + i) * p.vs[1] + c) : 0.f;
+      for (int d = lane; d < wide; d += 32) {
+        const bool there = in && d < dk;
+        if (!kStates) Q[i * pitch + d] = there ? la_load(q + (t0 + i) * p.qs[1] + d) : 0.f;
+        K[i * pitch + d] = there ? la_load(k + (t0 + i) * p.ks[1] + d) : 0.f;
+      }
+      const float w = pw[p.reverse ? max(i - pad + 1, 0) : C - 1 - i] * p.c_up;
+#pragma unroll
+      for (int c = lane; c < kSimtDvs; c += 32) {
+        const float x = in && c < cols ? la_load(v + (t0 + i) * p.vs[1] + c) : 0.f;
+        V[i * kSimtDvs + c] = x;
+        Vw[i * kSimtDvs + c] = x * w;
+      }
     }
     __syncthreads();
+    const int pair = 2 * (tid >> 4), col = tid & 15;  // rows pair, pair + 1; columns 4 col .. of O and S
     if constexpr (!kStates) {
-      const int i = tid >> 3, lane8 = tid & 7;
-      {
-        float acc[C / 8] = {};
-        for (int d = 0; d < dk; ++d) {
-          const float x = Q[i * pitch + d];
-  #pragma unroll
-          for (int jj = 0; jj < C / 8; ++jj) acc[jj] += x * K[(lane8 + 8 * jj) * pitch + d];
-        }
-  #pragma unroll
-        for (int jj = 0; jj < C / 8; ++jj) {
-          const int j = lane8 + 8 * jj, gap = p.reverse ? j - i : i - j;
-          P[i * (C + 1) + j] = gap >= 0 ? acc[jj] * (pw[gap] * p.c_intra) : 0.f;
-        }
+      float score[2][2] = {};
+      for (int d = 0; d < wide; d += 4) {
+        const float4 q0 = ld4(Q + pair * pitch + d), q1 = ld4(Q + (pair + 1) * pitch + d);
+        const float4 k0 = ld4(K + col * pitch + d), k1 = ld4(K + (col + 16) * pitch + d);
+        score[0][0] = dot4(q0, k0, score[0][0]);
+        score[0][1] = dot4(q0, k1, score[0][1]);
+        score[1][0] = dot4(q1, k0, score[1][0]);
+        score[1][1] = dot4(q1, k1, score[1][1]);
       }
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int i = pair + r, j = col + 16 * x, gap = p.reverse ? j - i : i - j;
+          P[i * kSimtPPitch + j] = gap >= 0 ? score[r][x] * (pw[gap] * p.c_intra) : 0.f;
+        }
       __syncwarp();  // a warp reads only the rows of P that it wrote
-      const int early = max(i - pad + 1, 0), late = C - 1 - i;
-      {
-        float acc[kSimtDvs / 8] = {};
-        for (int d = 0; d < dk; ++d) {
-          const float x = Q[i * pitch + d];
-  #pragma unroll
-          for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] += x * S[d * kSimtDvs + lane8 + 8 * cc];
+      float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+      auto add = [&](const float* a, int pitch_a, const float* x) {  // four terms of both rows
+        const float4 f0 = ld4(a), f1 = ld4(a + pitch_a);
+        const float a0[4] = {f0.x, f0.y, f0.z, f0.w}, a1[4] = {f1.x, f1.y, f1.z, f1.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 y = ld4(x + e * kSimtDvs + 4 * col);
+          fma4(acc[0], a0[e], y);
+          fma4(acc[1], a1[e], y);
         }
-        const float w = pw[p.reverse ? late : early] * p.c_inter;
-  #pragma unroll
-        for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] *= w;
-        for (int j = 0; j < C; ++j) {
-          const float x = P[i * (C + 1) + j];
-  #pragma unroll
-          for (int cc = 0; cc < kSimtDvs / 8; ++cc) acc[cc] += x * V[j * kSimtDvs + lane8 + 8 * cc];
-        }
-        if (i >= pad) {
-  #pragma unroll
-          for (int cc = 0; cc < kSimtDvs / 8; ++cc)
-            if (lane8 + 8 * cc < cols) la_store(o + (t0 + i) * p.os[1] + lane8 + 8 * cc, acc[cc]);
-        }
+      };
+      for (int d = 0; d < wide; d += 4) add(Q + pair * pitch + d, pitch, S + d * kSimtDvs);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int i = pair + r;
+        const float w = pw[p.reverse ? C - 1 - i : max(i - pad + 1, 0)] * p.c_inter;
+        acc[r] = make_float4(acc[r].x * w, acc[r].y * w, acc[r].z * w, acc[r].w * w);
       }
+      for (int j = 0; j < C; j += 4) add(P + pair * kSimtPPitch + j, kSimtPPitch, V + j * kSimtDvs);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int i = pair + r;
+        const float x[4] = {acc[r].x, acc[r].y, acc[r].z, acc[r].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i >= pad && 4 * col + e < cols) la_store(o + (t0 + i) * p.os[1] + 4 * col + e, x[e]);
+      }
+      __syncthreads();  // every read of S, before its update
     }
-    __syncthreads();  // every read of S, before its update
-    {
-      const int c = tid % kSimtDvs;
-      float vr[C];
+    const float carry = pw[C - pad];
+    for (int d = 4 * (tid >> 4); d < wide; d += 4 * (kSimtThreads / 16)) {
+      float4 acc[4];
 #pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 x = ld4(S + (d + e) * kSimtDvs + 4 * col);
+        acc[e] = make_float4(carry * x.x, carry * x.y, carry * x.z, carry * x.w);
+      }
+#pragma unroll 4
       for (int j = 0; j < C; ++j) {
-        const int up = p.reverse ? max(j - pad + 1, 0) : C - 1 - j;
-        vr[j] = V[j * kSimtDvs + c] * (pw[up] * p.c_up);
+        const float4 x = ld4(K + j * pitch + d), y = ld4(Vw + j * kSimtDvs + 4 * col);
+        fma4(acc[0], x.x, y);
+        fma4(acc[1], x.y, y);
+        fma4(acc[2], x.z, y);
+        fma4(acc[3], x.w, y);
       }
-      const float carry = pw[C - pad];
-      for (int d = tid / kSimtDvs; d < dk; d += kSimtThreads / kSimtDvs) {
-        float acc = 0.f;
 #pragma unroll
-        for (int j = 0; j < C; ++j) acc += K[j * pitch + d] * vr[j];
-        S[d * kSimtDvs + c] = carry * S[d * kSimtDvs + c] + acc;
-      }
+      for (int e = 0; e < 4; ++e) *reinterpret_cast<float4*>(S + (d + e) * kSimtDvs + 4 * col) = acc[e];
     }
   }
   __syncthreads();
@@ -194,6 +236,26 @@ size_t simt_partial_bytes(long long heads, int segments, int dk, int dv) {
   return sizeof(float) * static_cast<size_t>(heads) * (segments - 1) * dk * dv;
 }
 
+// Launches a pass, after its states' launch (`dependent`) as its programmatic dependent: CTAs
+// start as SMs come free and wait for the states themselves.
+template <class Args>
+pc_status_t launch_after(void (*kernel)(Args), dim3 grid, int threads, int smem, cudaStream_t s, bool dependent,
+                         const Args& args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  PC_CUDA(cudaLaunchKernelEx(&cfg, kernel, args));
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
 template <class T>
 pc_status_t launch_simt(const LaArgs& a, int passes, void* ws, cudaStream_t s) {
   int dk = 0, dv = 0;
@@ -216,8 +278,8 @@ pc_status_t launch_simt(const LaArgs& a, int passes, void* ws, cudaStream_t s) {
     PC_LAUNCH_CHECK();
   }
   PC_CUDA(cudaFuncSetAttribute(k_la_simt<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
-  k_la_simt<T, false><<<dim3(heads, slices, t.segments * passes), kSimtThreads, smem, s>>>(t);
-  PC_LAUNCH_CHECK();
+  PC_TRY(launch_after(k_la_simt<T, false>, dim3(heads, slices, t.segments * passes), kSimtThreads, smem, s,
+                      t.segments > 1, t));
   return PC_OK;
 }
 
@@ -286,20 +348,7 @@ pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s) {
     k_la_tc<DK, DV, true><<<dim3(heads * passes, t.segments - 1), kTcThreads, states_smem, s>>>(t);
     PC_LAUNCH_CHECK();
   }
-  // after the states' launch its CTAs start as SMs come free, and wait for the states themselves
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(heads * passes, t.segments);
-  cfg.blockDim = dim3(kTcThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = t.segments > 1 ? 1 : 0;
-  PC_CUDA(cudaLaunchKernelEx(&cfg, k_la_tc<DK, DV, false>, t));
-  PC_LAUNCH_CHECK();
-  return PC_OK;
+  return launch_after(k_la_tc<DK, DV, false>, dim3(heads * passes, t.segments), kTcThreads, smem, s, t.segments > 1, t);
 }
 
 // Runs the passes on the tensor cores; *done = false (and nothing launched) where a tensor's
