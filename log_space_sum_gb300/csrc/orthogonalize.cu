@@ -15,6 +15,15 @@
 // 2^-s Xs, 2^s ~ sqrt(N) (a row of X then has entries of about one), A as 2^12 A, B as
 // 2^10 B. The first Xs is G times a power of two alone (exact for bf16 G); the rest of
 // the norm, nu, enters with the first products in float32.
+//
+// Very wide matrices take several steps on the M x M matrix alone: with P = a I + B, X' = P X has
+// X' X'^T = P A P, everything commutes, and
+//
+//   T = A P = a A + A B,   A <- T P = a T + T B,   Q <- Q P = a Q + Q B   (Q = P at first)
+//
+// are symmetric products of M x M matrices; X <- Q X at the end. An error of A in the direction
+// of a small singular value grows by a^2 a step (2e4 over four), so A, B, T and Q are kept in two
+// parts here; X itself is then rounded once in all, and bf16 G not at all.
 #include <cuda_fp16.h>
 
 #include "pc_gemm.cuh"
@@ -23,7 +32,7 @@
 namespace pc {
 namespace {
 
-constexpr float kScaleA = 4096.f, kScaleB = 1024.f;
+constexpr float kScaleA = 4096.f, kScaleB = 1024.f, kScaleQ = 64.f;
 
 // ------------------------------------------------------------------ norm and operands
 constexpr int kNormThreads = 256, kNormBlocks = 608;
@@ -237,10 +246,14 @@ enum OrthOp : int { kGram = 0, kPoly = 1, kApply = 2 };
 
 struct OrthArgs {
   int tiles_m, tiles_n, batch;  // kGram, kPoly: tiles_m = tiles_n, pairs m <= n only
+  int b_groups;                 // matrix g of the first operand meets g mod b_groups of the second
   int num_kb;
   int M, N;                     // valid rows and columns of the result
-  HalfMat prev;                 // kPoly: A; kApply: X
+  HalfMat prev;                 // added k0 times: kPoly: A; kApply: X (none where the matrix holds a I)
   HalfMat to;                   // the result, in operand form
+  int symmetric;                // kPoly in two parts: exactly
+  HalfMat also;                 // kPoly: 2^6 (a I + B) goes here, or NULL
+  float diag;                   // 2^6 a
   const float* nu;              // first step: the norm's factor, else NULL
   float k0, k1;                 // see the epilogue
   void* out;                    // last kApply: the caller's matrix, else NULL
@@ -248,10 +261,10 @@ struct OrthArgs {
   unsigned* status;
 };
 
-template <int kParts, int BN>
+template <int kPa, int kPb, int BN>
 struct OrthShape {
   static constexpr uint32_t kA = kBM * 128, kB = BN * 128;  // one part's 64 values of K
-  static constexpr uint32_t kStage = kParts * (kA + kB);
+  static constexpr uint32_t kStage = kPa * kA + kPb * kB;
 };
 
 __device__ __forceinline__ void umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -321,9 +334,9 @@ __device__ __forceinline__ void orth_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void orth_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // What the epilogue reads of 32 columns from n of row m: kPoly A, kApply X.
-template <int kParts, int kOp>
+template <int kParts, bool kPrev>
 __device__ __forceinline__ void orth_fetch(const OrthArgs& p, int g, int m, int n, HalfRun<kParts>& x) {
-  if constexpr (kOp != kGram) {
+  if constexpr (kPrev) {
     if (m < p.M && n < p.N)
       x.fetch(p.prev, static_cast<size_t>(g) * p.prev.rows * p.prev.ld + static_cast<size_t>(m) * p.prev.ld + n);
   }
@@ -333,15 +346,19 @@ __device__ __forceinline__ void orth_fetch(const OrthArgs& p, int g, int m, int 
 //   kGram   2^12 A = k0 nu^2 D
 //   kPoly   2^10 B = k0 (2^12 A) + k1 D
 //   kApply  X' = k0 nu (k1 Xs + 2^-10 D), to Xs' or to the caller
-template <int kParts, int kOp, class T>
+template <int kParts, int kOp, bool kPrev, class T>
 __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, int n, bool mirror, float (&v)[32],
-                                              const HalfRun<kParts>& x) {
+                                              const HalfRun<kParts>& x, float* square) {
   if (m >= p.M || n >= p.N) return;
   const int k = min(32, p.N - n);
   const float nu = p.nu ? p.nu[g] : 1.f;
   const size_t base = static_cast<size_t>(g) * p.to.rows * p.to.ld, at = base + static_cast<size_t>(m) * p.to.ld + n;
   if constexpr (kOp == kGram) {
     const float f = p.k0 * nu * nu;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= f;
+  } else if constexpr (!kPrev) {
+    const float f = p.k0 * nu;
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= f;
   } else {
@@ -381,18 +398,48 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, i
       return;
     }
   }
-  store_half_run<kParts>(p.to, at, v);
-  if constexpr (kOp != kApply) {
-    if (mirror) {  // lanes hold consecutive m: each store covers a run of row n + i
+  // Steps on the Gram matrix mirror the diagonal's tiles too, its squares of 32 x 32 by way of
+  // shared memory (two-byte stores along the rows took 6 us): what little A and B do not
+  // commute by would otherwise leave an antisymmetric part, which grows by a^2 a step.
+  const int above = n - (m & ~31);
+  if (kOp == kPoly && kParts == 2 && p.symmetric) {
+    if (above < 0) return;  // its mirror image is written
+    if (above == 0) {
+      const int lane = m & 31, rows = p.M - m + lane;
+      const unsigned lanes = rows < 32 ? (1u << rows) - 1 : 0xffffffffu;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) square[lane * 33 + i] = v[i];
+      __syncwarp(lanes);
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (i < k) {
-          const size_t to = base + static_cast<size_t>(n + i) * p.to.ld + m;
-          __half hi, lo;
-          half_split(v[i], &hi, &lo);
-          p.to.ptr[to] = hi;
-          if constexpr (kParts == 2) p.to.ptr[p.to.lo + to] = lo;
-        }
+        if (i < lane) v[i] = square[i * 33 + lane];
+      __syncwarp(lanes);
+    } else {
+      mirror = true;
+    }
+  }
+  auto store = [&](const HalfMat& x) {
+    store_half_run<kParts>(x, at, v);
+    if constexpr (kOp != kApply) {
+      if (mirror) {  // lanes hold consecutive m: each store covers a run of row n + i
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (i < k) {
+            const size_t to = base + static_cast<size_t>(n + i) * x.ld + m;
+            __half hi, lo;
+            half_split(v[i], &hi, &lo);
+            x.ptr[to] = hi;
+            if constexpr (kParts == 2) x.ptr[x.lo + to] = lo;
+          }
+      }
+    }
+  };
+  store(p.to);
+  if constexpr (kOp == kPoly && kParts == 2) {
+    if (p.also.ptr) {  // rows and columns as p.to
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = v[i] * (kScaleQ / kScaleB) + (n + i == m ? p.diag : 0.f);
+      store(p.also);
     }
   }
 }
@@ -403,27 +450,32 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, i
 // with kSplit = 1 the CTAs are persistent and the accumulator alternates between two
 // buffers, so that one tile's epilogue runs under the next one's products.
 //   warp 0 TMA, warp 1 MMA, warps 2-9 epilogue (two per lane quarter)
-// Two parts (hi + lo): three products a step, in slices of kSliceKb blocks of K that are
-// added up in registers, because the accumulator truncates.
+// Two parts (hi + lo): three products a step. A result in two parts is formed in slices of
+// kSliceKb blocks of K that are added up in registers, because the accumulator truncates.
 constexpr int kSliceKb = 2;
 constexpr int kOrthThreads = 64 + 8 * 32;
+constexpr int kSquare = 32 * 33;
 
-template <int kParts, int BN>
+template <int kPa, int kPb, int BN>
 struct OrthRing {
-  static constexpr int kFit = (227 * 1024 - 2048) / OrthShape<kParts, BN>::kStage;
+  static constexpr int kFit = (227 * 1024 - 2048) / OrthShape<kPa, kPb, BN>::kStage;
   static constexpr int kStages = kFit < 6 ? kFit : 6;
-  static constexpr uint32_t kBytes = kStages * OrthShape<kParts, BN>::kStage + 2048;
+  // base to 1024 bytes, barriers, and a square for each epilogue warp (two-part results)
+  static constexpr uint32_t kBytes = kStages * OrthShape<kPa, kPb, BN>::kStage + 2048 +
+                                     (kPa == 2 && kPb == 2 ? 8 * kSquare * 4 : 0);
 };
 
-template <int kParts, int BN, int kSplit, int kOp, class T>
+// kPa, kPb: parts of the operands; kParts: of the result and what is added to it.
+template <int kPa, int kPb, int kParts, int BN, int kSplit, int kOp, class T>
 __global__ void __launch_bounds__(kOrthThreads, 1)
     k_orth_gemm(const __grid_constant__ CUtensorMap a_hi, const __grid_constant__ CUtensorMap a_lo,
                 const __grid_constant__ CUtensorMap b_hi, const __grid_constant__ CUtensorMap b_lo,
                 const __grid_constant__ OrthArgs p) {
-  using S = OrthShape<kParts, BN>;
-  constexpr int kStages = OrthRing<kParts, BN>::kStages;
+  using S = OrthShape<kPa, kPb, BN>;
+  constexpr int kStages = OrthRing<kPa, kPb, BN>::kStages;
   constexpr bool kPairs = kOp != kApply;
   constexpr bool kSliced = kParts == 2;
+  constexpr bool kPrev = kOp == kPoly || (kOp == kApply && kPa == kPb);
   constexpr uint32_t kCols = 2 * BN;  // two accumulators
   static_assert(kStages >= 2 && kCols <= 512, "two stages, two accumulators");
   constexpr int kOwn = (BN / 32 + kSplit - 1) / kSplit;  // chunk x of 32 columns belongs to rank x % kSplit
@@ -496,16 +548,18 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           mbar_arrive_expect_tx(&full[s], S::kStage);
           uint8_t* base = smem + s * S::kStage;
 #pragma unroll
-          for (int part = 0; part < kParts; ++part) {
-            const CUtensorMap* am = part ? &a_lo : &a_hi;
+          for (int part = 0; part < kPa; ++part)
+            tma_load_3d(base + part * S::kA, part ? &a_lo : &a_hi, &full[s], kb * 64, m0, g);
+          const int gb = g < p.b_groups ? g : g - p.b_groups;
+#pragma unroll
+          for (int part = 0; part < kPb; ++part) {
             const CUtensorMap* bm = part ? &b_lo : &b_hi;
-            tma_load_3d(base + part * S::kA, am, &full[s], kb * 64, m0, g);
-            uint8_t* bt = base + kParts * S::kA + part * S::kB;
+            uint8_t* bt = base + kPa * S::kA + part * S::kB;
             if constexpr (kOp == kApply) {
 #pragma unroll
-              for (int c = 0; c < BN; c += 64) tma_load_3d(bt + c * 128, bm, &full[s], n0 + c, kb * 64, g);
+              for (int c = 0; c < BN; c += 64) tma_load_3d(bt + c * 128, bm, &full[s], n0 + c, kb * 64, gb);
             } else {
-              tma_load_3d(bt, bm, &full[s], kb * 64, n0, g);
+              tma_load_3d(bt, bm, &full[s], kb * 64, n0, gb);
             }
           }
           issued = it + 1;
@@ -546,8 +600,8 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           if (leader) {
             const uint32_t at = ring + s * S::kStage;
             const uint64_t a = umma_desc_sw128(at);
-            const uint64_t b = kOp == kApply ? umma_desc_sw128_mn(at + kParts * S::kA, 64 * 128)
-                                             : umma_desc_sw128(at + kParts * S::kA);
+            const uint64_t b = kOp == kApply ? umma_desc_sw128_mn(at + kPa * S::kA, 64 * 128)
+                                             : umma_desc_sw128(at + kPa * S::kA);
             constexpr uint32_t kBStep = kOp == kApply ? 2048 >> 4 : 32 >> 4;
             auto product = [&](int pa, int pb) {
 #pragma unroll
@@ -556,10 +610,9 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
                 acc = 1;
               }
             };
-            if constexpr (kParts == 2) {  // the small products first
-              product(1, 0);
-              product(0, 1);
-            }
+            // the small products first
+            if constexpr (kPa == 2) product(1, 0);
+            if constexpr (kPb == 2) product(0, 1);
             product(0, 0);
             umma_commit(&empty[s]);
           }
@@ -603,6 +656,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       ++unit;
     };
     // the other ranks' sums land at [source][chunk][column][row]
+    float* square = reinterpret_cast<float*>(smem + kStages * S::kStage + 1024) + (warp - 2) * kSquare;
     auto slot = [&](int src, int own) { return ((src * kOwn + own) * 32 * kBM + row) * 4; };
     for (int t = tile0; ok && t < num_tiles; t += tile_step) {
       int g, m0, n0;
@@ -610,17 +664,17 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       const bool mirror = kPairs && n0 != m0;
       if constexpr (kSplit == 1 && !kSliced) {
         HalfRun<kParts> x;
-        orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + part * 32, x);
+        orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + part * 32, x);
         ok = wait_unit();
         if (!ok) break;
 #pragma unroll 1
         for (int c = part * 32; c < BN; c += 64) {
           const HalfRun<kParts> now = x;
-          if (c + 64 < BN) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + c + 64, x);  // under this chunk's work
+          if (c + 64 < BN) orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + c + 64, x);  // under this chunk's work
           float v[32];
           tmem_ld_32x32(lanes + (unit & 1) * BN + c, v);
           if (c + 64 >= BN) release();
-          orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + c, mirror, v, now);
+          orth_epilogue<kParts, kOp, kPrev, T>(p, g, m0 + row, n0 + c, mirror, v, now, square);
         }
       } else if constexpr (kSplit > 1 && !kSliced) {
         // straight from tensor memory, one chunk of 32 columns at a time
@@ -637,7 +691,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         };
         const int own0 = part % kSplit == rank ? part : (part + 2) % kSplit == rank ? part + 2 : -1;
         HalfRun<kParts> x;
-        if (own0 >= 0) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + own0 * 32, x);
+        if (own0 >= 0) orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + own0 * 32, x);
         cluster_sync();  // every ring of the cluster is idle
         if (ok) {
 #pragma unroll 1
@@ -657,7 +711,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll 1
           for (int xc = own0; xc < BN / 32; xc += 2) {
             if (xc % kSplit != rank) continue;
-            if (xc != own0) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + xc * 32, x);
+            if (xc != own0) orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + xc * 32, x);
             float v[32];
             load(xc, v);
 #pragma unroll
@@ -666,10 +720,15 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] += from[i * kBM];
             }
-            orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + xc * 32, mirror, v, x);
+            orth_epilogue<kParts, kOp, kPrev, T>(p, g, m0 + row, n0 + xc * 32, mirror, v, x, square);
           }
         }
       } else {
+        HalfRun<kParts> x[kChunks];  // fetched under the products
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+          if (kSplit == 1 || (2 * c + part) % kSplit == rank)
+            orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + (2 * c + part) * 32, x[c]);
         float acc[kChunks][32];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -691,17 +750,10 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         if constexpr (kSplit == 1) {
           if (ok) {
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-              HalfRun<kParts> x;
-              orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + (2 * c + part) * 32, x);
-              orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + (2 * c + part) * 32, mirror, acc[c], x);
-            }
+            for (int c = 0; c < kChunks; ++c)
+              orth_epilogue<kParts, kOp, kPrev, T>(p, g, m0 + row, n0 + (2 * c + part) * 32, mirror, acc[c], x[c], square);
           }
         } else {
-          HalfRun<kParts> x[kChunks];
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            if ((2 * c + part) % kSplit == rank) orth_fetch<kParts, kOp>(p, g, m0 + row, n0 + (2 * c + part) * 32, x[c]);
           cluster_sync();  // every ring of the cluster is idle
           if (ok) {
 #pragma unroll
@@ -726,7 +778,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) acc[c][i] += from[i * kBM];
               }
-              orth_epilogue<kParts, kOp, T>(p, g, m0 + row, n0 + xc * 32, mirror, acc[c], x[c]);
+              orth_epilogue<kParts, kOp, kPrev, T>(p, g, m0 + row, n0 + xc * 32, mirror, acc[c], x[c], square);
             }
           }
         }
@@ -743,12 +795,12 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 // --------------------------------------------------------------------------- launches
 inline unsigned blocks_of(long long a, long long b) { return static_cast<unsigned>((a + b - 1) / b); }
 
-template <int kParts, int BN, int kSplit, int kOp, class T>
+template <int kPa, int kPb, int kParts, int BN, int kSplit, int kOp, class T>
 pc_status_t launch_orth(const OrthArgs& p, const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], cudaStream_t s,
                         long long tiles, long long flops) {
-  constexpr uint32_t smem = OrthRing<kParts, BN>::kBytes;
+  constexpr uint32_t smem = OrthRing<kPa, kPb, BN>::kBytes;
   static_assert(smem <= 232448, "shared memory per CTA");
-  auto* kernel = k_orth_gemm<kParts, BN, kSplit, kOp, T>;
+  auto* kernel = k_orth_gemm<kPa, kPb, kParts, BN, kSplit, kOp, T>;
   PC_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -776,62 +828,81 @@ pc_status_t launch_orth(const OrthArgs& p, const CUtensorMap (&a)[2], const CUte
 // about 1 us (two cluster barriers and the exchange), five blocks of K (measured at 16
 // blocks: 7.4 us a product alone, 7.1 shared by three; at 8: 5.8 against 6.4), so each CTA
 // keeps at least as many; with two parts a block is three products.
-inline int split_of(long long tiles, int num_kb, int parts) {
-  const int blocks = parts == 2 ? 3 * num_kb : num_kb;
+inline int split_of(long long tiles, int num_kb, int products) {
   int best = 1;
   for (int size = 2; size <= 4; ++size)
-    if (tiles <= 8 * (num_sms() / 8 / size) && blocks >= 5 * size) best = size;
+    if (tiles <= 8 * (num_sms() / 8 / size) && products * num_kb >= 5 * size) best = size;
   return best;
 }
 
-template <int kParts, int kOp, class T>
+template <int kPa, int kPb, int kParts, int kOp, class T>
 pc_status_t run_product(OrthArgs p, const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], cudaStream_t s,
                         long long flops) {
   p.tiles_m = static_cast<int>(blocks_of(p.M, kBM));
   const long long wide = static_cast<long long>(p.tiles_m) * blocks_of(p.N, 256) * p.batch;
-  if constexpr (kOp == kApply && kParts == 1) {
-    if (wide >= num_sms()) {
+  if constexpr (kOp == kApply && kPb == 1) {
+    if (wide >= num_sms() || kPa == 2) {  // by_gram's matrices have the tiles
       p.tiles_n = static_cast<int>(blocks_of(p.N, 256));
-      return launch_orth<kParts, 256, 1, kOp, T>(p, a, b, s, wide, flops);
+      return launch_orth<kPa, kPb, kParts, 256, 1, kOp, T>(p, a, b, s, wide, flops);
     }
   }
-  p.tiles_n = static_cast<int>(blocks_of(p.N, 128));
-  const long long tiles = (kOp == kApply ? p.tiles_m * static_cast<long long>(p.tiles_n)
-                                         : p.tiles_m * (p.tiles_m + 1ll) / 2) * p.batch;
-  const int split = split_of(tiles, p.num_kb, kParts);
-  switch (split) {
-    case 4: return launch_orth<kParts, 128, 4, kOp, T>(p, a, b, s, tiles, flops);
-    case 3: return launch_orth<kParts, 128, 3, kOp, T>(p, a, b, s, tiles, flops);
-    case 2: return launch_orth<kParts, 128, 2, kOp, T>(p, a, b, s, tiles, flops);
-    default: return launch_orth<kParts, 128, 1, kOp, T>(p, a, b, s, tiles, flops);
+  if constexpr (kPa == kPb) {
+    p.tiles_n = static_cast<int>(blocks_of(p.N, 128));
+    const long long tiles = (kOp == kApply ? p.tiles_m * static_cast<long long>(p.tiles_n)
+                                           : p.tiles_m * (p.tiles_m + 1ll) / 2) * p.batch;
+    const int split = split_of(tiles, p.num_kb, kPa == 2 ? 3 : 1);
+    switch (split) {
+      case 4: return launch_orth<kPa, kPb, kParts, 128, 4, kOp, T>(p, a, b, s, tiles, flops);
+      case 3: return launch_orth<kPa, kPb, kParts, 128, 3, kOp, T>(p, a, b, s, tiles, flops);
+      case 2: return launch_orth<kPa, kPb, kParts, 128, 2, kOp, T>(p, a, b, s, tiles, flops);
+      default: return launch_orth<kPa, kPb, kParts, 128, 1, kOp, T>(p, a, b, s, tiles, flops);
+    }
   }
+  return PC_OK;
+}
+
+// Whether steps are taken on the Gram matrix (see the top). Five steps of it are 14 products of
+// M x M matrices in two parts, about 12 us each up to M = 1024, for 4/5 of the gram and 7/10 of
+// the apply products. Measured (us, X at every step against this): 512 x 8192 159, 165;
+// 1024 x 2048 142, 206; 1024 x 8192 233, 234; 1024 x 16384 345, 277; 2048 x 8192 507, 595;
+// 2048 x 16384 862, 715.
+inline bool by_gram(long long batch, long long M, long long N, int parts) {
+  M = round_up(M, kBM);
+  return parts == 1 && N >= 8 * M && static_cast<double>(batch) * M * M * N >= 1.2e10;
 }
 
 struct OrthPlan {
   HalfMat X[2], A, Bm;
+  HalfMat slots;  // by_gram: five stacks of M x M matrices in two parts, Bm likewise
   float *part, *nu;
   size_t bytes;
 };
 
 OrthPlan plan_orth(void* ws, int batch, int M, int N, int parts) {
   Carver c(ws);
-  OrthPlan p;
-  auto mat = [&](int rows, int cols) {
+  OrthPlan p{};
+  auto mat = [&](int rows, int cols, int of, int stacks) {
     HalfMat m;
     m.rows = rows;
     m.cols = cols;
     m.ld = round_up(cols, 64);
-    const size_t n = static_cast<size_t>(batch) * rows * m.ld;
-    m.lo = parts == 2 ? n : 0;
-    m.ptr = static_cast<__half*>(c.take(n * parts * sizeof(__half)));
+    const size_t n = static_cast<size_t>(batch) * stacks * rows * m.ld;
+    m.lo = of == 2 ? n : 0;
+    m.ptr = static_cast<__half*>(c.take(n * of * sizeof(__half)));
     return m;
   };
   p.part = static_cast<float*>(c.take(sizeof(float) * kNormBlocks * batch));
   p.nu = static_cast<float*>(c.take(sizeof(float) * batch));
-  p.X[0] = mat(M, N);
-  p.X[1] = mat(M, N);
-  p.A = mat(M, M);
-  p.Bm = mat(M, M);
+  p.X[0] = mat(M, N, parts, 1);
+  p.X[1] = mat(M, N, parts, 1);
+  if (by_gram(batch, M, N, parts)) {
+    p.slots = mat(M, M, 2, 5);
+    p.Bm = mat(M, M, 2, 1);
+    p.A = p.slots;
+  } else {
+    p.A = mat(M, M, parts, 1);
+    p.Bm = mat(M, M, parts, 1);
+  }
   p.bytes = c.used;
   return p;
 }
@@ -846,6 +917,119 @@ pc_status_t half_maps(CUtensorMap (&map)[2], const HalfMat& x, int batch, int bo
     o.ld = x.ld;
     o.groups = batch;
     PC_TRY(encode_operand_map(&map[part], o, kPrecF16Ops, box_rows, 0));
+  }
+  return PC_OK;
+}
+
+// Steps that are taken on one Gram matrix: Q, a product of polynomials whose largest value on
+// the singular values is `growth`, has to fit float16 beside its scale.
+inline int gram_steps(float a, float b, float c) {
+  auto at = [&](float x) { return fabsf(a + x * (b + x * c)); };  // x: squared singular value, up to 1.5^2
+  float growth = fmaxf(at(0.f), at(2.25f));
+  if (c != 0.f && -b / (2.f * c) > 0.f && -b / (2.f * c) < 2.25f) growth = fmaxf(growth, at(-b / (2.f * c)));
+  int n = 1;
+  for (float g = growth * growth; g <= 512.f && n < 16; g *= growth) ++n;
+  return n;
+}
+
+template <int kParts, class T>
+pc_status_t iterate(const OrthPlan& p, int batch, int M, int N, int steps, float a, float b, float c, int tall, T* out,
+                    cudaStream_t s) {
+  CUtensorMap x_rows[2][2], x_cols[2][2], ma[2], mb[2];  // X as K-major rows, and as rows along K
+  for (int i = 0; i < 2; ++i) {
+    PC_TRY(half_maps(x_rows[i], p.X[i], batch, kBM));
+    PC_TRY(half_maps(x_cols[i], p.X[i], batch, 64));
+  }
+  PC_TRY(half_maps(ma, p.A, batch, kBM));
+  PC_TRY(half_maps(mb, p.Bm, batch, kBM));
+  int bits = 0;  // 2^s ~ sqrt(N)
+  while ((4ll << (2 * bits)) <= N) ++bits;
+  const float up = static_cast<float>(1 << bits), down = 1.f / up;
+  const long long mm = static_cast<long long>(batch) * M * M;
+  const int m_kb = static_cast<int>(blocks_of(M, 64));
+  OrthArgs square{};  // an M x M result
+  square.batch = square.b_groups = batch;
+  square.M = square.N = M;
+  square.num_kb = m_kb;
+  square.status = device_status_word();
+  const int most = p.slots.ptr ? gram_steps(a, b, c) : 1;
+  for (int it = 0, i = 0; it < steps; i ^= 1) {
+    const int count = steps - it < most ? steps - it : most;
+    const bool last = it + count == steps;
+    OrthArgs gram = square;
+    gram.num_kb = static_cast<int>(blocks_of(N, 64));
+    gram.nu = it == 0 ? p.nu : nullptr;
+    gram.k0 = kScaleA * (it == 0 ? 1.f : down * down);
+    OrthArgs poly = square;
+    poly.k0 = kScaleB / kScaleA * b;
+    poly.k1 = kScaleB / (kScaleA * kScaleA) * c;
+    OrthArgs apply = square;
+    apply.N = N;
+    apply.prev = p.X[i];
+    apply.to = p.X[i ^ 1];
+    apply.nu = gram.nu;
+    apply.k0 = (it == 0 ? 1.f : down) * (last ? 1.f : up);
+    apply.k1 = a;
+    apply.out = last ? out : nullptr;
+    apply.tall = tall;
+    it += count;
+    if (count == 1) {
+      gram.to = poly.prev = p.A;
+      poly.to = p.Bm;
+      PC_TRY((run_product<kParts, kParts, kParts, kGram, float>(gram, x_rows[i], x_rows[i], s, mm * N)));
+      PC_TRY((run_product<kParts, kParts, kParts, kPoly, float>(poly, ma, ma, s, mm * M)));
+      PC_TRY((run_product<kParts, kParts, kParts, kApply, T>(apply, mb, x_cols[i], s, 2 * mm * N)));
+      continue;
+    }
+    if constexpr (kParts == 1) {
+      // the slots hold A in 2, Q in 1 or 3, T in 4 or 0, so that (Q, A) or (A, Q) and the
+      // pair that takes their products with P lie side by side
+      CUtensorMap at[5][2];
+      HalfMat slot[5];
+      for (int k = 0; k < 5; ++k) {
+        slot[k] = p.slots;
+        slot[k].ptr += static_cast<size_t>(k) * batch * M * p.slots.ld;
+        PC_TRY(half_maps(at[k], slot[k], k == 1 || k == 2 ? 2 * batch : batch, kBM));
+      }
+      gram.to = poly.prev = slot[2];
+      PC_TRY((run_product<1, 1, 2, kGram, float>(gram, x_rows[i], x_rows[i], s, mm * N)));
+      poly.symmetric = 1;
+      int q = 1;
+      for (int k = 0; k < count; ++k) {
+        poly.to = p.Bm;
+        poly.also = k == 0 ? slot[q] : HalfMat{};
+        poly.diag = kScaleQ * a;
+        PC_TRY((run_product<2, 2, 2, kPoly, float>(poly, at[2], at[2], s, mm * M)));
+        // products with P: a times the operand and the operand times B
+        auto times = [&](int from, int to, int stacks) {
+          OrthArgs t = square;
+          t.batch = stacks * batch;
+          t.prev = slot[from];
+          t.to = slot[to];
+          t.symmetric = 1;
+          t.k0 = a;
+          t.k1 = 1.f / kScaleB;
+          return run_product<2, 2, 2, kPoly, float>(t, at[from], mb, s, stacks * mm * M);
+        };
+        if (k + 1 == count) {
+          if (k > 0) {
+            PC_TRY(times(q, 4 - q, 1));
+            q = 4 - q;
+          }
+          break;
+        }
+        const int t = k == 0 || q == 1 ? 4 : 0;
+        if (k == 0) {
+          PC_TRY(times(2, t, 1));
+        } else {
+          PC_TRY(times(q == 1 ? 1 : 2, q == 1 ? 3 : 0, 2));
+          q = 4 - q;
+        }
+        PC_TRY(times(t, 2, 1));
+      }
+      apply.k0 *= 1.f / kScaleQ;
+      PC_TRY((run_product<2, 1, 1, kApply, T>(apply, at[q], x_cols[i], s, 4 * mm * N)));
+    }
   }
   return PC_OK;
 }
@@ -886,52 +1070,7 @@ pc_status_t run_orth(int batch, int rows, int cols, const T* G, int steps, float
     }
     PC_LAUNCH_CHECK();
   }
-  CUtensorMap x_rows[2][2], x_cols[2][2], ma[2], mb[2];  // X as K-major rows, and as rows along K
-  for (int i = 0; i < 2; ++i) {
-    PC_TRY(half_maps(x_rows[i], p.X[i], batch, kBM));
-    PC_TRY(half_maps(x_cols[i], p.X[i], batch, 64));
-  }
-  PC_TRY(half_maps(ma, p.A, batch, kBM));
-  PC_TRY(half_maps(mb, p.Bm, batch, kBM));
-  int bits = 0;  // 2^s ~ sqrt(N)
-  while ((4ll << (2 * bits)) <= N) ++bits;
-  const float up = static_cast<float>(1 << bits), down = 1.f / up;
-  const long long mm = static_cast<long long>(batch) * M * M;
-  OrthArgs q{};
-  q.batch = batch;
-  q.M = M;
-  q.status = device_status_word();
-  for (int it = 0; it < steps; ++it) {
-    const int i = it & 1;
-    const bool last = it + 1 == steps;
-    OrthArgs gram = q;
-    gram.N = M;
-    gram.num_kb = static_cast<int>(blocks_of(N, 64));
-    gram.to = p.A;
-    gram.nu = it == 0 ? p.nu : nullptr;
-    gram.k0 = kScaleA * (it == 0 ? 1.f : down * down);
-    PC_TRY((run_product<kParts, kGram, float>(gram, x_rows[i], x_rows[i], s, mm * N)));
-    OrthArgs poly = q;
-    poly.N = M;
-    poly.num_kb = static_cast<int>(blocks_of(M, 64));
-    poly.prev = p.A;
-    poly.to = p.Bm;
-    poly.k0 = kScaleB / kScaleA * b;
-    poly.k1 = kScaleB / (kScaleA * kScaleA) * c;
-    PC_TRY((run_product<kParts, kPoly, float>(poly, ma, ma, s, mm * M)));
-    OrthArgs apply = q;
-    apply.N = N;
-    apply.num_kb = poly.num_kb;
-    apply.prev = p.X[i];
-    apply.to = p.X[i ^ 1];
-    apply.nu = gram.nu;
-    apply.k0 = (it == 0 ? 1.f : down) * (last ? 1.f : up);
-    apply.k1 = a;
-    apply.out = last ? out : nullptr;
-    apply.tall = tall;
-    PC_TRY((run_product<kParts, kApply, T>(apply, mb, x_cols[i], s, 2 * mm * N)));
-  }
-  return PC_OK;
+  return iterate<kParts, T>(p, batch, M, N, steps, a, b, c, tall, out, s);
 }
 
 pc_status_t check_orth(int batch, int rows, int cols, int steps, pc_precision_t prec, pc_dtype_t dtype) {

@@ -139,3 +139,61 @@ def test_refusals():
         pc.orthogonalize(g, steps=0)
     with pytest.raises(pc.PCError, match="PC_ERR_ALIGNMENT"):
         pc.orthogonalize(_draw((65,), "fp32", 8)[1:].view(8, 8))
+
+
+def _exact(G, coefficients=(3.4445, -4.7750, 2.0315), steps=5):
+    """The formula in float64 on the device (the matrices are large)."""
+    a, b, c = coefficients
+    X = G.double().mT if G.shape[-2] > G.shape[-1] else G.double()
+    X = X / (X.norm(dim=(-1, -2), keepdim=True) + 1e-7)
+    for _ in range(steps):
+        A = X @ X.mT
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return X.mT if G.shape[-2] > G.shape[-1] else X
+
+
+@pytest.mark.parametrize("shape", [(1024, 16384), (16500, 1000), (3, 520, 16001)])
+def test_very_wide(shape):
+    """Steps on the Gram matrix in two parts. A G of 8 bits is exact in float16, so what is left
+    is 2^-22 an operand and the accumulator's truncation, at most 2^-24 for each of the N / 16
+    additions, 6e-5 of A (3e-5 of X); with the slope of five steps on singular values that are
+    all alike (their errors carry over as they are): 2e-4 allowed."""
+    G = _draw(shape, "bf16", 11)
+    want = _exact(G)
+    norm = want.norm(dim=(-1, -2))
+    X = pc.orthogonalize(G.float())
+    assert ((X.double() - want).norm(dim=(-1, -2)) <= 2e-4 * norm).all()
+    X = pc.orthogonalize(G)
+    assert X.dtype == torch.bfloat16
+    assert ((X.double() - want).norm(dim=(-1, -2)) <= (2e-4 + 1.7e-3) * norm).all()
+    G = _draw(shape, "fp32", 12)  # rounded to 11 bits
+    want = _exact(G)
+    assert ((pc.orthogonalize(G).double() - want).norm(dim=(-1, -2)) <= 2e-3 * norm).all()
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 7, 11])
+def test_very_wide_steps(steps):
+    """One step, several on one Gram matrix, and more than one of those; X is rounded in between."""
+    G = _draw((512, 46000), "bf16", 13).float()
+    want = _exact(G, steps=steps)
+    X = pc.orthogonalize(G, steps=steps)
+    assert (X.double() - want).norm() <= 2e-3 * want.norm()
+    coefficients = (1.5, -0.5, 0.0)
+    want = _exact(G, coefficients, steps)
+    X = pc.orthogonalize(G, steps=steps, coefficients=coefficients)
+    assert (X.double() - want).norm() <= 2e-3 * want.norm()
+
+
+def test_very_wide_uneven():
+    """Directions of very different size: the noise of two-part operands, 485 times 2e-7 of the
+    matrix, and 2e4 times 2e-7 of A's in the slope of B's share, absolute."""
+    g = _draw((512, 46000), "bf16", 14, 1.0).float()
+    one = torch.outer(g[:, 0], g[0]).bfloat16().float()
+    for G in (one, one + 1e-3 * g.sign(), torch.cat([1e3 * g[:1], g[1:]])):
+        G = G.bfloat16().float()
+        want = _exact(G)
+        assert (pc.orthogonalize(G).double() - want).norm() <= 2e-3 * want.norm() + 485 * 2e-7 + 2e4 * 2e-7 * 4.775
+    G = g.clone()
+    G[3, 5] = float("inf")
+    assert not torch.isfinite(pc.orthogonalize(G)).any()
+    assert not pc.orthogonalize(torch.zeros_like(g)).any()
