@@ -254,6 +254,10 @@ struct OrthArgs {
   int symmetric;                // kPoly in two parts: exactly
   HalfMat also;                 // kPoly: 2^6 (a I + B) goes here, or NULL
   float diag;                   // 2^6 a
+  // One part: what rounding took off the diagonal of 2^10 B [group][M]. B is near a multiple of
+  // the identity where the singular values are alike, and its diagonal's errors then are too:
+  // without them the whole update's error falls from 1.9e-3 to 1.1e-3 (400 x 8192).
+  float* off;
   const float* nu;              // first step: the norm's factor, else NULL
   float k0, k1;                 // see the epilogue
   void* out;                    // last kApply: the caller's matrix, else NULL
@@ -289,6 +293,7 @@ __device__ __forceinline__ void st_32(void* p, const uint32_t (&r)[16], int at) 
 template <int kParts>
 struct HalfRun {
   uint32_t w[kParts][16];
+  float off;
   // ld and the column are multiples of 32, so a row's padding is there to be read
   __device__ __forceinline__ void fetch(const HalfMat& x, size_t at) {
 #pragma unroll
@@ -334,18 +339,20 @@ __device__ __forceinline__ void orth_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void orth_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
 // What the epilogue reads of 32 columns from n of row m: kPoly A, kApply X.
-template <int kParts, bool kPrev>
+template <int kParts, int kOp, bool kPrev>
 __device__ __forceinline__ void orth_fetch(const OrthArgs& p, int g, int m, int n, HalfRun<kParts>& x) {
   if constexpr (kPrev) {
-    if (m < p.M && n < p.N)
+    if (m < p.M && n < p.N) {
       x.fetch(p.prev, static_cast<size_t>(g) * p.prev.rows * p.prev.ld + static_cast<size_t>(m) * p.prev.ld + n);
+      if constexpr (kOp == kApply && kParts == 1) x.off = p.off[static_cast<size_t>(g) * p.M + m];
+    }
   }
 }
 
 // 32 columns from n of row m of D:
 //   kGram   2^12 A = k0 nu^2 D
 //   kPoly   2^10 B = k0 (2^12 A) + k1 D
-//   kApply  X' = k0 nu (k1 Xs + 2^-10 D), to Xs' or to the caller
+//   kApply  X' = k0 nu ((k1 + 2^-10 off) Xs + 2^-10 D), to Xs' or to the caller
 template <int kParts, int kOp, bool kPrev, class T>
 __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, int n, bool mirror, float (&v)[32],
                                               const HalfRun<kParts>& x, float* square) {
@@ -362,7 +369,8 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, i
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= f;
   } else {
-    const float k0 = kOp == kPoly ? p.k0 : p.k0 * nu * p.k1, k1 = kOp == kPoly ? p.k1 : p.k0 * nu * (1.f / kScaleB);
+    const float a = kOp == kApply && kParts == 1 ? p.k1 + x.off * (1.f / kScaleB) : p.k1;
+    const float k0 = kOp == kPoly ? p.k0 : p.k0 * nu * a, k1 = kOp == kPoly ? p.k1 : p.k0 * nu * (1.f / kScaleB);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float2 f = x.pair(i);
@@ -416,6 +424,15 @@ __device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, i
       __syncwarp(lanes);
     } else {
       mirror = true;
+    }
+  }
+  if constexpr (kOp == kPoly && kParts == 1) {
+    if (above == 0) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (n + i == m) d = v[i];
+      p.off[static_cast<size_t>(g) * p.M + m] = d - __half2float(__float2half_rn(d));
     }
   }
   auto store = [&](const HalfMat& x) {
@@ -664,13 +681,13 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       const bool mirror = kPairs && n0 != m0;
       if constexpr (kSplit == 1 && !kSliced) {
         HalfRun<kParts> x;
-        orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + part * 32, x);
+        orth_fetch<kParts, kOp, kPrev>(p, g, m0 + row, n0 + part * 32, x);
         ok = wait_unit();
         if (!ok) break;
 #pragma unroll 1
         for (int c = part * 32; c < BN; c += 64) {
           const HalfRun<kParts> now = x;
-          if (c + 64 < BN) orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + c + 64, x);  // under this chunk's work
+          if (c + 64 < BN) orth_fetch<kParts, kOp, kPrev>(p, g, m0 + row, n0 + c + 64, x);  // under this chunk's work
           float v[32];
           tmem_ld_32x32(lanes + (unit & 1) * BN + c, v);
           if (c + 64 >= BN) release();
@@ -691,7 +708,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
         };
         const int own0 = part % kSplit == rank ? part : (part + 2) % kSplit == rank ? part + 2 : -1;
         HalfRun<kParts> x;
-        if (own0 >= 0) orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + own0 * 32, x);
+        if (own0 >= 0) orth_fetch<kParts, kOp, kPrev>(p, g, m0 + row, n0 + own0 * 32, x);
         cluster_sync();  // every ring of the cluster is idle
         if (ok) {
 #pragma unroll 1
@@ -711,7 +728,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll 1
           for (int xc = own0; xc < BN / 32; xc += 2) {
             if (xc % kSplit != rank) continue;
-            if (xc != own0) orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + xc * 32, x);
+            if (xc != own0) orth_fetch<kParts, kOp, kPrev>(p, g, m0 + row, n0 + xc * 32, x);
             float v[32];
             load(xc, v);
 #pragma unroll
@@ -728,7 +745,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
           if (kSplit == 1 || (2 * c + part) % kSplit == rank)
-            orth_fetch<kParts, kPrev>(p, g, m0 + row, n0 + (2 * c + part) * 32, x[c]);
+            orth_fetch<kParts, kOp, kPrev>(p, g, m0 + row, n0 + (2 * c + part) * 32, x[c]);
         float acc[kChunks][32];
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
@@ -874,7 +891,7 @@ inline bool by_gram(long long batch, long long M, long long N, int parts) {
 struct OrthPlan {
   HalfMat X[2], A, Bm;
   HalfMat slots;  // by_gram: five stacks of M x M matrices in two parts, Bm likewise
-  float *part, *nu;
+  float *part, *nu, *off;
   size_t bytes;
 };
 
@@ -893,6 +910,7 @@ OrthPlan plan_orth(void* ws, int batch, int M, int N, int parts) {
   };
   p.part = static_cast<float*>(c.take(sizeof(float) * kNormBlocks * batch));
   p.nu = static_cast<float*>(c.take(sizeof(float) * batch));
+  p.off = static_cast<float*>(c.take(sizeof(float) * batch * M));
   p.X[0] = mat(M, N, parts, 1);
   p.X[1] = mat(M, N, parts, 1);
   if (by_gram(batch, M, N, parts)) {
@@ -976,6 +994,7 @@ pc_status_t iterate(const OrthPlan& p, int batch, int M, int N, int steps, float
     if (count == 1) {
       gram.to = poly.prev = p.A;
       poly.to = p.Bm;
+      poly.off = apply.off = p.off;
       PC_TRY((run_product<kParts, kParts, kParts, kGram, float>(gram, x_rows[i], x_rows[i], s, mm * N)));
       PC_TRY((run_product<kParts, kParts, kParts, kPoly, float>(poly, ma, ma, s, mm * M)));
       PC_TRY((run_product<kParts, kParts, kParts, kApply, T>(apply, mb, x_cols[i], s, 2 * mm * N)));
