@@ -174,3 +174,37 @@ def test_refusals():
         pc.layer_norm_fwd(x, w, b, eps=-1.0)
     with pytest.raises(ValueError, match="collapse"):
         pc.layer_norm_fwd(torch.empty(4, 6, 64, device="cuda")[:, :3], w, b)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("rows,dim,ld,first", [(1, 3, 11, 5), (9, 13, 13, 0), (17, 65, 77, 3), (40, 511, 640, 1), (300, 257, 263, 6),
+                                               (2500, 1031, 1033, 7), (1300, 1537, 1537, 0), (50, 4091, 4097, 2),
+                                               (20, 8190, 8191, 4), (9000, 100, 101, 1)])
+def test_rows_that_start_and_end_inside_a_piece(rows, dim, ld, first, dtype):
+    """Rows ld values apart from an odd place: the values around them are NaN in the inputs and
+    stay as they are in the outputs. Outputs placed as the inputs, and one value further."""
+    x, dy, w, b = _draw(rows, dim, dtype, rows + dim)
+
+    def inside(t, shift=0, fill=float("nan")):
+        flat = torch.full((first + shift + rows * ld + 16,), fill, dtype=t.dtype, device="cuda")
+        view = flat[first + shift:first + shift + rows * ld].view(rows, ld)[:, :dim]
+        if t is not None:
+            view.copy_(t)
+        return flat, view
+
+    xv, dv = inside(x)[1], inside(dy)[1]
+    results = []
+    for shift in (0, 1):
+        flat, out = inside(torch.zeros_like(x), shift, 7.0)
+        got = pc.layer_norm_fwd(xv, w, b, out=out)
+        _check_fwd(x, w, b, got, dtype)
+        flat2, dx = inside(torch.zeros_like(x), shift, 7.0)
+        grads = pc.layer_norm_bwd(dv, xv, w, got[1], got[2], dx=dx)
+        _check_bwd(x, dy, w, got[1], got[2], grads, dtype)
+        for f, view in ((flat, out), (flat2, dx)):
+            view.fill_(7.0)
+            assert (f == 7.0).all()
+        results.append(got[1:])
+    again = pc.layer_norm_bwd(dv, xv, w, *results[0])
+    more = pc.layer_norm_bwd(dv, xv, w, *results[0])
+    assert all(torch.equal(p, q) for p, q in zip(again, more))
