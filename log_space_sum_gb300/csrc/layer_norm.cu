@@ -8,7 +8,8 @@
 // Memory-bound: x (and dy) are read once and y (dx) written once, about ten flops per
 // element. A row lives in the registers of one warp or one CTA between its load and its
 // store, so the variance is that of the centred values (no cancellation) at no extra
-// traffic. Statistics, sums and the weight's gradients are float32 throughout; the only
+// traffic. Measured, bf16: forward 32768 x 4096 99 us (5.4 TB/s), gradient 32768 x 1024 38 us on the
+// GPU (34 and 5.9 TB/s without the weight's sums). Statistics, sums and the weight's gradients are float32 throughout; the only
 // rounding to bf16 is that of y and dx.
 #include "pc_device.cuh"
 #include "pc_host.h"
@@ -89,15 +90,18 @@ template <class T>
 __device__ __forceinline__ int row_shift(const T* row) {  // values of the first piece before the row
   return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
 }
-template <bool kEdges, int L>
-__device__ __forceinline__ void only_inside(int c, int dim, float (&v)[L]) {
-  if constexpr (kEdges) {
-    if (c < 0 || c + L > dim) {
+// Bits of a piece from column c that are the row's.
+template <class T>
+__device__ __forceinline__ uint4 piece_mask(int c, int dim) {
+  constexpr int kWord = 4 / sizeof(T);
+  uint32_t m[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int j = 0; j < L; ++j)
-        if (c + j < 0 || c + j >= dim) v[j] = 0.f;
-    }
-  }
+  for (int j = 0; j < kLanes<T>; ++j)
+    if (c + j >= 0 && c + j < dim) m[j / kWord] |= (kWord == 2 ? 0xFFFFu : 0xFFFFFFFFu) << (j % kWord * 16);
+  return make_uint4(m[0], m[1], m[2], m[3]);
+}
+__device__ __forceinline__ uint4 masked(const uint4& v, const uint4& m) {
+  return make_uint4(v.x & m.x, v.y & m.y, v.z & m.z, v.w & m.w);
 }
 template <bool kEdges, int L>
 __device__ __forceinline__ void params_at(const float* p, int c, int dim, float (&v)[L]) {
@@ -194,7 +198,7 @@ __global__ void __launch_bounds__(32 * kWarps * kRows)
 
 // The forward of rows with edges: a CTA walks rows gridDim.x (a multiple of kLanes<T>) apart,
 // one at a time with the next on its way, its parameters in registers (a CTA for each row would
-// read them a value at a time: 55 us for 16384 rows of 1537 bf16 values against 30).
+// read them a value at a time: 55 us for 16384 rows of 1537 bf16 values against 28).
 template <class T, int kWarps, int kVecs, int kCtas>
 __global__ void __launch_bounds__(32 * kWarps, kCtas)
     k_ln_fwd_edges(long long rows, int dim, const T* __restrict__ x, long long x_ld, const float* __restrict__ w,
@@ -202,6 +206,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas)
                    float* __restrict__ mean, float* __restrict__ rstd) {
   constexpr int L = kLanes<T>, kThreads = 32 * kWarps;
   __shared__ float2 red[2][kWarps];
+  __shared__ uint4 inside[kVecs][kThreads];
   const int t = threadIdx.x;
   const int shift = row_shift(x + blockIdx.x * x_ld);
   float wv[kVecs][L], bv[kVecs][L];
@@ -215,6 +220,7 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas)
     }
     if (w && c < dim) params_at<true, L>(w, c, dim, wv[i]);
     if (b && c < dim) params_at<true, L>(b, c, dim, bv[i]);
+    inside[i][t] = piece_mask<T>(c, dim);  // read by this thread alone
   }
   uint4 raw[kVecs], next[kVecs];
   auto fetch = [&](long long r) {
@@ -227,14 +233,13 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas)
   fetch(blockIdx.x);
   for (long long r = blockIdx.x; r < rows; r += gridDim.x) {
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) raw[i] = next[i];
+    for (int i = 0; i < kVecs; ++i) raw[i] = masked(next[i], inside[i][t]);
     fetch(r + gridDim.x);
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       float v[L];
       unpack(raw[i], v);
-      only_inside<true>((i * kThreads + t) * L - shift, dim, v);
 #pragma unroll
       for (int j = 0; j < L; ++j) s += v[j];
     }
@@ -245,12 +250,13 @@ __global__ void __launch_bounds__(32 * kWarps, kCtas)
       const int c = (i * kThreads + t) * L - shift;
       float v[L];
       unpack(raw[i], v);
+      if (c >= 0 && c + L <= dim) {
 #pragma unroll
-      for (int j = 0; j < L; ++j) v[j] -= m;
-      only_inside<true>(c, dim, v);
-      if (c < dim) {
+        for (int j = 0; j < L; ++j) s += (v[j] - m) * (v[j] - m);
+      } else {
 #pragma unroll
-        for (int j = 0; j < L; ++j) s += v[j] * v[j];
+        for (int j = 0; j < L; ++j)
+          if (c + j >= 0 && c + j < dim) s += (v[j] - m) * (v[j] - m);
       }
     }
     const float rs = 1.f / sqrtf(row_sum<kWarps>(s, 0.f, red[1]).x / dim + eps);
@@ -348,6 +354,7 @@ __global__ void __launch_bounds__(32 * kWarps * kGroups, kCtas)
   __shared__ float2 red[2][kGroups][kWarps];
   constexpr int kPitch = kThreads + 4;  // of value j of every thread's piece
   __shared__ float sums[kGroups > 1 ? 2 : 1][kGroups > 1 ? kPitch * kVecs * L : 1];
+  __shared__ uint4 inside[kEdges ? kVecs : 1][kEdges ? kThreads : 1];  // the same for every group
   const int group = threadIdx.x / kThreads, t = threadIdx.x % kThreads;
   const long long first = blockIdx.x + static_cast<long long>(group) * gridDim.x;  // a CTA's shifts are alike
   const long long stride = static_cast<long long>(gridDim.x) * kGroups;
@@ -362,7 +369,9 @@ __global__ void __launch_bounds__(32 * kWarps * kGroups, kCtas)
       wv[i][j] = 1.f;
     }
     if (w && c < dim) params_at<kEdges, L>(w, c, dim, wv[i]);
+    if (kEdges && group == 0) inside[i][t] = piece_mask<T>(c, dim);
   }
+  if constexpr (kEdges) __syncthreads();
   int flip = 0;
   uint4 rx[kVecs], rd[kVecs], nx[kVecs], nd[kVecs];
   auto fetch = [&](long long r) {
@@ -378,8 +387,14 @@ __global__ void __launch_bounds__(32 * kWarps * kGroups, kCtas)
   for (long long r = first; r < rows; r += stride, flip ^= 1) {
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
-      rx[i] = nx[i];
-      rd[i] = nd[i];
+      if constexpr (kEdges) {
+        const uint4 m = inside[i][t];
+        rx[i] = masked(nx[i], m);
+        rd[i] = masked(nd[i], m);
+      } else {
+        rx[i] = nx[i];
+        rd[i] = nd[i];
+      }
     }
     fetch(r + stride);
     const float m = mean[r], rs = rstd[r];
@@ -389,8 +404,6 @@ __global__ void __launch_bounds__(32 * kWarps * kGroups, kCtas)
       float xv[L], dv[L];
       unpack(rx[i], xv);
       unpack(rd[i], dv);
-      only_inside<kEdges>((i * kThreads + t) * L - shift, dim, xv);
-      only_inside<kEdges>((i * kThreads + t) * L - shift, dim, dv);
 #pragma unroll
       for (int j = 0; j < L; ++j) {  // past dim: dy = 0 adds nothing
         const float z = (xv[j] - m) * rs, g = dv[j] * wv[i][j];
@@ -720,17 +733,18 @@ template <class T, bool kEdges>
 void bwd_pieces(LnBwd& a, int pieces, cudaStream_t s) {
   // Two pieces a thread and 512 threads an SM: few warps a row make its sums cheap, and a row on
   // its way for each group covers the latency. 32768 rows of 1024 bf16 values: 38 us; with one
-  // piece a thread 43, with two rows at a time 49, with four pieces a thread 67 (spills); without
-  // the groups (one row of partial sums each) 42. Rows with edges of up to 256 pieces are faster
-  // without (16384 rows of 1537: 46 us against 59).
+  // piece a thread 44, with two rows at a time 49, with four pieces a thread 76 (spills); without
+  // the groups (one row of partial sums each) 42. One CTA an SM has fewer rows of partial sums
+  // still, and from 129 pieces on gains by it (16384 rows of 2048: 38 us against 39); below, the
+  // groups in turn cost more (32768 rows of 512: 20.5 against 19).
   if (pieces <= 64)
     bwd_kernel<T, 1, 2, 8, 2, kEdges>(a, s);
   else if (pieces <= 128)
     bwd_kernel<T, 2, 2, 4, 2, kEdges>(a, s);
   else if (pieces <= 256)
-    bwd_kernel<T, 4, 2, kEdges ? 1 : 2, kEdges ? 4 : 2, kEdges>(a, s);
+    bwd_kernel<T, 4, 2, 4, 1, kEdges>(a, s);
   else if (pieces <= 512)
-    bwd_kernel<T, 8, 2, 1, 2, kEdges>(a, s);
+    bwd_kernel<T, 8, 2, 2, 1, kEdges>(a, s);
   else
     bwd_kernel<T, 16, 2, 1, 1, kEdges>(a, s);
 }
