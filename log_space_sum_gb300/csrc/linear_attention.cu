@@ -96,20 +96,37 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
   float* partial = args.partial + (static_cast<long long>(pass) * a.B * a.H + bh) * (args.segments - 1) * size;
   // decay over a segment before this one; a forward's first one may lack tokens
   const float over = decay_pow(g, args.chunks_per_segment * C);
-  if (!kStates && seg > 0) grid_dependency_wait();  // the states
   const float over0 = p.reverse ? over : decay_pow(g, args.chunks_per_segment * C - (nch * C - len));
-  for (int e = tid; e < wide * kSimtDvs; e += kSimtThreads) {
-    const int d = e / kSimtDvs, c = e % kSimtDvs;
-    float v = 0.f;
-    if (!kStates && c < cols && d < dk) {
-      const long long at = static_cast<long long>(d) * p.dv + c0 + c;
-      if (p.s_in) v = p.s_in[bh * size + (p.s_in_transposed ? static_cast<long long>(c0 + c) * dk + d : at)];
-#pragma unroll 4
-      for (int x = 0; x < min(seg, final_seg); ++x)  // what the segments before this one add
-        v = (x == 0 ? over0 : over) * v + partial[x * size + at];
+  auto load_state = [&]() {  // S before this segment, many loads in flight
+    constexpr int kAtOnce = 8;
+    const int before = kStates ? 0 : min(seg, final_seg);
+    if (before > 0) grid_dependency_wait();
+    for (int e0 = tid; e0 < wide * kSimtDvs; e0 += kAtOnce * kSimtThreads) {
+      const int c = e0 % kSimtDvs, d0 = e0 / kSimtDvs;  // the others are kSimtThreads / kSimtDvs rows apart
+      float v[kAtOnce];
+      bool in[kAtOnce];
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x) {
+        const int d = d0 + x * (kSimtThreads / kSimtDvs);
+        in[x] = !kStates && c < cols && d < dk;
+        v[x] = in[x] && p.s_in ? p.s_in[bh * size + (p.s_in_transposed ? static_cast<long long>(c0 + c) * dk + d
+                                                                       : static_cast<long long>(d) * p.dv + c0 + c)]
+                               : 0.f;
+      }
+#pragma unroll 2
+      for (int y = 0; y < before; ++y) {  // what the segments before this one add
+        const float* ps = partial + y * size + static_cast<long long>(d0) * p.dv + c0 + c;
+        const float carry = y == 0 ? over0 : over;
+#pragma unroll
+        for (int x = 0; x < kAtOnce; ++x)
+          if (in[x]) v[x] = carry * v[x] + ps[x * (kSimtThreads / kSimtDvs) * p.dv];
+      }
+#pragma unroll
+      for (int x = 0; x < kAtOnce; ++x)
+        if (d0 + x * (kSimtThreads / kSimtDvs) < wide) S[e0 + x * kSimtThreads] = v[x];
     }
-    S[e] = v;
-  }
+  };
+  if (kStates || first >= last) load_state();
   const T* q = static_cast<const T*>(p.q) + b * p.qs[0] + h * p.qs[2];
   const T* k = static_cast<const T*>(p.k) + b * p.ks[0] + h * p.ks[2];
   const T* v = static_cast<const T*>(p.v) + b * p.vs[0] + h * p.vs[2] + c0;
@@ -154,7 +171,12 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
           const int i = pair + r, j = col + 16 * x, gap = p.reverse ? j - i : i - j;
           P[i * kSimtPPitch + j] = gap >= 0 ? score[r][x] * (pw[gap] * p.c_intra) : 0.f;
         }
-      __syncwarp();  // a warp reads only the rows of P that it wrote
+      if (step == first) {  // the states may have been on their way until now
+        load_state();
+        __syncthreads();
+      } else {
+        __syncwarp();  // a warp reads only the rows of P that it wrote
+      }
       float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
       auto add = [&](const float* a, int pitch_a, const float* x) {  // four terms of both rows
         const float4 f0 = ld4(a), f1 = ld4(a + pitch_a);
