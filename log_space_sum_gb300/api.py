@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import struct
 
 import torch
 
@@ -516,8 +517,10 @@ def layer_norm_bwd(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None,
 
 
 def _strides(*tensors):
-    flat = [s for t in tensors for s in t.stride()[:-1]]
-    return (C.c_longlong * len(flat))(*flat)
+    flat = ()
+    for t in tensors:
+        flat += t.stride()[:-1]
+    return struct.pack(f"{len(flat)}q", *flat)
 
 
 def _attention_inputs(q, k, v, log_decay, state, lengths, lead):

@@ -295,11 +295,11 @@ pc_status_t launch_simt(const LaArgs& a, int passes, void* ws, cudaStream_t s) {
   t.chunks_per_segment = nch > 0 ? (nch + t.segments - 1) / t.segments : 1;
   const unsigned heads = static_cast<unsigned>(a.B) * a.H, slices = (dv + kSimtDvs - 1) / kSimtDvs;
   if (t.segments > 1) {
-    PC_CUDA(cudaFuncSetAttribute(k_la_simt<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+    PC_TRY((allow_smem<k_la_simt<T, true>>(most)));
     k_la_simt<T, true><<<dim3(heads, slices, (t.segments - 1) * passes), kSimtThreads, smem, s>>>(t);
     PC_LAUNCH_CHECK();
   }
-  PC_CUDA(cudaFuncSetAttribute(k_la_simt<T, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
+  PC_TRY((allow_smem<k_la_simt<T, false>>(most)));
   PC_TRY(launch_after(k_la_simt<T, false>, dim3(heads, slices, t.segments * passes), kSimtThreads, smem, s,
                       t.segments > 1, t));
   return PC_OK;
@@ -362,11 +362,11 @@ size_t tc_partial_bytes(long long heads, int segments, int dk, int dv) {
 template <int DK, int DV>
 pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s) {
   constexpr int smem = TcShape<DK, DV, false>::kBytes, states_smem = TcShape<DK, DV, true>::kBytes;
-  PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  PC_TRY((allow_smem<k_la_tc<DK, DV, false>>(smem)));
   const unsigned heads = static_cast<unsigned>(t.a.B) * t.a.H;
   t.passes = passes;
   if (t.segments > 1) {
-    PC_CUDA(cudaFuncSetAttribute(k_la_tc<DK, DV, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, states_smem));
+    PC_TRY((allow_smem<k_la_tc<DK, DV, true>>(states_smem)));
     k_la_tc<DK, DV, true><<<dim3(heads * passes, t.segments - 1), kTcThreads, states_smem, s>>>(t);
     PC_LAUNCH_CHECK();
   }

@@ -817,8 +817,8 @@ pc_status_t launch_orth(const OrthArgs& p, const CUtensorMap (&a)[2], const CUte
                         long long tiles, long long flops) {
   constexpr uint32_t smem = OrthRing<kPa, kPb, BN>::kBytes;
   static_assert(smem <= 232448, "shared memory per CTA");
-  auto* kernel = k_orth_gemm<kPa, kPb, kParts, BN, kSplit, kOp, T>;
-  PC_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)));
+  constexpr auto kernel = k_orth_gemm<kPa, kPb, kParts, BN, kSplit, kOp, T>;
+  PC_TRY(allow_smem<kernel>(static_cast<int>(smem)));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include <cstdarg>
 #include <cstddef>
 #include <cstdint>
@@ -101,6 +103,21 @@ inline pc_status_t check_dtype(pc_dtype_t t) {
 inline int dtype_bytes(pc_dtype_t t) { return t == PC_BF16 ? 2 : 4; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Allows a kernel `bytes` of dynamic shared memory: always the same number, so once for each
+// device (0.4 us a launch otherwise: 58 us against 51 for the host's part of an orthogonalised
+// update).
+template <auto kKernel>
+pc_status_t allow_smem(int bytes) {
+  static std::atomic<unsigned long long> done{0};
+  int device = 0;
+  PC_CUDA(cudaGetDevice(&device));
+  const unsigned long long bit = device < 64 ? 1ull << device : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return PC_OK;
+  PC_CUDA(cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return PC_OK;
+}
 
 inline long long round_up(long long v, long long m) { return (v + m - 1) / m * m; }
 
