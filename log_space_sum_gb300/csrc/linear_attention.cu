@@ -335,7 +335,7 @@ int tc_pad(int d) { return d <= 64 ? 64 : 128; }
 
 // Segments of a sequence. One CTA per SM takes a segment; cutting a sequence into S makes
 // the first launch's states cost about 0.5 of a pass's chunks, and each CTA a start of
-// about one chunk (measured at head size 128: 3.1 us a chunk, 1.5 us of states alone, 3 us
+// about one chunk (measured at head size 128: 3.1 us a chunk, 1.7 us of states alone, 3 us
 // from a CTA's launch to its first product), and joining a segment's share 0.3.
 int tc_segments(long long heads, int T) {
   const int nch = (T + kTcC - 1) / kTcC;

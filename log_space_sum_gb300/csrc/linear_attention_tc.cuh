@@ -30,6 +30,10 @@
 // the others leave of the launch's 5 x 96 (2 x 80, 64; kStates: 168, 2 x 24, 64). A spill would cost more than
 // elsewhere: the tiles leave the L1 cache next to nothing.
 //
+// A chunk of 128 tokens at head size 128 takes 3.1 us (5800 cycles), 4600 cycles of them MMAs: a
+// gradient of 8 x 2048 tokens, 16 heads, 167 us (384 CTAs in 2.5 waves), 1 x 32771 tokens forward
+// 152 us (DRAM at 5.2 TB/s in the pass itself).
+//
 // Segments: with fewer (b, h) than SMs a sequence is cut; a first launch (kStates) leaves
 // each segment's own contribution to the state, and each segment of the second adds up the
 // ones before it.
