@@ -497,7 +497,8 @@ PCSUM_API pc_status_t pc_linear_attention_step(int B, int H, int Dk, int Dv, con
  * where rows > cols); out [rows][cols] (elements) = X. a s + b s^3 + c s^5 acts on the
  * singular values. |G|_F^2 is summed in float32; a matrix of zeros gives zeros.
  * Precision: PC_PREC_AUTO and PC_PREC_TF32 form every product from operands of 11
- * significant bits, PC_PREC_FP32 from operands of 22 (hi + lo); float32 accumulation.
+ * significant bits (matrices at least eight times as wide as high may take several steps
+ * on A alone, in 22), PC_PREC_FP32 from operands of 22 (hi + lo); float32 accumulation.
  * out may be G. G and out are 16-byte aligned. Errors: PC_ERR_UNKNOWN_PRECISION,
  * PC_ERR_UNSUPPORTED, PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_ALIGNMENT, PC_ERR_WORKSPACE.
  * Workspace: pc_orthogonalize_workspace bytes, 16-byte aligned. */
