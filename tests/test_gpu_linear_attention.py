@@ -183,6 +183,17 @@ def test_long_sequence_state_and_segments():
     _check(q, k, v, do, decay, S, dS, "bf16")
 
 
+@pytest.mark.parametrize("lengths", [None, [1500, 1499, 700, 1]])
+def test_two_uneven_segments(lengths):
+    """Heads for half the SMs: a long first segment beside its states' launch and a short one
+    after it, in order of time (forward) and against it (in the gradient's passes where fewer
+    heads leave the same room)."""
+    q, k, v, do, decay, S, dS = _draw(4, 1500, 16, 64, 128, "bf16", 17)
+    _check(q, k, v, do, decay, S, dS, "bf16", lengths=lengths)
+    q, k, v, do, decay, S, dS = _draw(4, 1500, 6, 128, 128, "bf16", 18)
+    _check(q, k, v, do, decay, S, dS, "bf16", lengths=lengths)
+
+
 def test_repeats_streams_and_wide_offsets():
     q, k, v, do, decay, S, dS = _draw(2, 500, 4, 128, 128, "bf16", 17)
     first = pc.linear_attention_bwd(q, k, v, decay, do, state=S, dstate=dS)
