@@ -899,8 +899,10 @@ struct OrthPlan {
   size_t bytes;
 };
 
+// The workspace is 16-byte aligned, the operands' 32-byte accesses want more: its first
+// 256-byte boundary is where the plan begins.
 OrthPlan plan_orth(void* ws, int batch, int M, int N, int parts) {
-  Carver c(ws);
+  Carver c(reinterpret_cast<void*>(round_up(reinterpret_cast<intptr_t>(ws), 256)));
   OrthPlan p{};
   auto mat = [&](int rows, int cols, int of, int stacks) {
     HalfMat m;
@@ -925,7 +927,7 @@ OrthPlan plan_orth(void* ws, int batch, int M, int N, int parts) {
     p.A = mat(M, M, parts, 1);
     p.Bm = mat(M, M, parts, 1);
   }
-  p.bytes = c.used;
+  p.bytes = c.used + 256 - 16;  // what the boundary may cost
   return p;
 }
 
