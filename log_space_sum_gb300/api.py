@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes as C
 import functools
 import struct
+import threading
 
 import torch
 
@@ -21,7 +22,7 @@ from . import _native as N
 
 PRECISIONS = {"auto": 0, "tf32": 1, "fp32": 2}
 
-_ws_cache: dict = {}
+_local = threading.local()  # .workspaces: {(device, stream): buffer}, of this host thread
 
 
 def precision_code(precision) -> int:
@@ -70,12 +71,22 @@ def _stream(device) -> int:
 
 
 def workspace(nbytes: int, device) -> torch.Tensor:
-    """Scratch buffer of at least nbytes, cached per (device, stream)."""
+    """Scratch buffer of at least nbytes, cached per (host thread, device, stream): the calls
+    that share one run one after the other. Two threads' launches on one stream may alternate,
+    so each has its own. A call that is being captured takes one from the graph's own memory,
+    which lasts as long as the graph and is no other call's: a cached one may be replaced
+    before a replay, and replays are not ordered with the calls of the stream captured on."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    try:
+        cache = _local.workspaces
+    except AttributeError:
+        cache = _local.workspaces = {}
     key = (device, _stream(device))
-    ws = _ws_cache.get(key)
+    ws = cache.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+        cache[key] = ws
     return ws
 
 

@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_la_simt(const __grid_constant_
   if (seg == args.segments - 1)
     for (long long e = tid; e < static_cast<long long>(a.T - len) * cols; e += kSimtThreads)
       la_store(o + (len + e / cols) * p.os[1] + e % cols, 0.f);
+  la_end_after_states();
 }
 
 // Segments: enough that every SM has four CTAs.

@@ -33,4 +33,10 @@ __device__ __forceinline__ int la_length(const LaArgs& a, int b) {
   return a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
 }
 
+// A pass ends after the launch of its states, whether or not a segment read them: a later
+// dependent launch (of another host thread's call, between this one's) waits for the pass alone.
+__device__ __forceinline__ void la_end_after_states() {
+  if ((blockIdx.x | blockIdx.y | blockIdx.z) == 0) grid_dependency_wait();
+}
+
 }  // namespace pc

@@ -169,7 +169,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
     for (long long e = static_cast<long long>(seg) * kTcThreads + threadIdx.x; e < n;
          e += static_cast<long long>(args.segments) * kTcThreads)
       *reinterpret_cast<uint4*>(o + (len + e / pieces) * p.os[1] + (e % pieces) * 8) = make_uint4(0u, 0u, 0u, 0u);
-    if (seg > final_seg || (n_steps <= 0 && !p.s_out)) return;
+    if (seg > final_seg || (n_steps <= 0 && !p.s_out)) {
+      la_end_after_states();
+      return;
+    }
   }
 
   {
@@ -644,6 +647,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  if constexpr (!kStates) la_end_after_states();
 }
 
 }  // namespace pc
