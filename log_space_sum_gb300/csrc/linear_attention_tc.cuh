@@ -142,6 +142,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
            *o_full = bar(24), *d_full = bar(25), *p_ready = bar(26), *o_free = bar(27), *s_ready = bar(28),
            *o_staged = bar(29), *mma_done = bar(30);
   uint64_t* d_free = bar(22);  // kStates: [2], in the place of sc_full and oi_full
+  // Of chunk n. kStates: the state warps announce a chunk's operands before they look at the last
+  // one's D, so two of these phases can end before a delayed warp looks at the first: two
+  // barriers in turn (the other in the place of o_full), of which d_free holds back the next use.
+  auto d_done = [&](int n) { return kStates && (n & 1) ? o_full : d_full; };
+  auto d_parity = [&](int n) { return static_cast<uint32_t>(kStates ? n >> 1 : n) & 1u; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar(31));
 
   const LaArgs& a = args.a;
@@ -446,8 +451,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       if (lane == 0) mbar_arrive(&up_ready[buf]);
       return true;
     };
-    auto wait_state = [&](uint64_t* bar, int n) {
-      const bool got = __all_sync(0xffffffffu, mbar_wait(bar, n & 1, status, kErrTimeoutEpilogue));
+    auto wait_state = [&](int n) {
+      const bool got = __all_sync(0xffffffffu, mbar_wait(d_done(n), d_parity(n), status, kErrTimeoutEpilogue));
       tc_fence_after();
       return got;
     };
@@ -458,7 +463,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         ok = (n > 0 || (split(0, 0) && split(0, 1))) && (!more || (split(n + 1, 0) && split(n + 1, 1)));
       else
         ok = split(n, 0) && split(n, 1) && split(n, 2) && split(n, 3);
-      ok = ok && wait_state(d_full, n);
+      ok = ok && wait_state(n);
       if (!ok) break;
       if (active) {
         const float carry = pw[C - tc_tile(first + n, nch, len, p.reverse).pad];
@@ -623,7 +628,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
             update(grp);
             umma_commit(&up_free[grp & 1]);
             if (grp == kGroups - 1) {
-              umma_commit(d_full);
+              umma_commit(d_done(n));
               umma_commit(&k_empty[st]);
               if constexpr (kStates) umma_commit(&v_empty[st]);
             }
