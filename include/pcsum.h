@@ -104,8 +104,9 @@ PCSUM_API unsigned long long pc_launch_count(void);
 PCSUM_API pc_status_t pc_device_status(pc_stream_t stream);
 
 /* Limit, in nanoseconds, of the first waits of the tensor-core contraction kernel on the
- * current device (a free ring slot, a filled slot, a free or complete accumulator);
- * 0 restores the default of 2 s. A kernel whose wait runs out records PC_ERR_TIMEOUT
+ * current device (a free ring slot, a filled slot, a free or complete accumulator); in the
+ * kernels of linear attention and of the orthogonalised update, of the waits for a complete
+ * accumulator (where one is formed in slices, none). 0 restores the default of 2 s. A kernel whose wait runs out records PC_ERR_TIMEOUT
  * for pc_device_status, skips the rest of its tile and exits cleanly: waits for work it
  * has already issued (copies landing, MMAs completing before tensor memory is freed)
  * always keep the default limit, so no copy or MMA is left in flight. The limit is a

@@ -109,9 +109,6 @@ __device__ __forceinline__ void weight_parts(uint32_t* wp, int i, float g, const
   }
 }
 
-// Barrier of the eight state warps.
-__device__ __forceinline__ void state_bar_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
-
 // Tiles' rows along tokens, first coordinate of the tile of `step`, its missing rows.
 struct TcTile {
   int t0, pad;
@@ -135,6 +132,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   uint32_t* wp = reinterpret_cast<uint32_t*>(tables + C + 4);  // [3][64]: bf16 parts of the tokens' weights, by pairs
   float* near = tables + C + 4 + 192;  // c_intra l^(distance) from column j to the block's near edge, j = 0 .. 31
   float* diag = near + 32 + 32;      // c_intra l^|d| at diag[d], d = -31 .. 31 (column - row)
+  uint64_t* spare = reinterpret_cast<uint64_t*>(near + 96);
+  auto* limit = reinterpret_cast<unsigned long long*>(spare);  // first_wait_limit
+  uint64_t *w_free = spare + 1, *w_ready = spare + 2;          // of a padded tile's weights
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kFixed + (C + 4 + 192 + 128) * sizeof(float));
   auto bar = [&](int at) { return bars + at; };
   uint64_t *q_full = bar(0), *k_full = bar(3), *v_full = bar(6), *q_empty = bar(9), *k_empty = bar(12),
@@ -186,6 +186,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
     if (i < C / 2) weight_parts(wp, i, g, p, 0);
     if (i < 32) near[i] = p.c_intra * decay_pow(g, p.reverse ? i : 31 - i);
     if (i < 63) diag[i - 31] = p.c_intra * decay_pow(g, i < 31 ? 31 - i : i - 31);
+    if (i == kTcThreads - 1) *limit = first_wait_limit(status);
   }
   if (warp == 0) {
     if (lane == 0) {
@@ -210,6 +211,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       mbar_init(&up_ready[1], 8);
       mbar_init(&up_free[0], 1);
       mbar_init(&up_free[1], 1);
+      mbar_init(w_free, 8);
+      mbar_init(w_ready, 8);
       fence_barrier_init();
     }
     __syncwarp();
@@ -225,6 +228,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
   auto use_parity = [&](int n, int grp) { return static_cast<uint32_t>(n * (kGroups / 2) + (grp >> 1)) & 1u; };
   auto parts = [&](int buf) { return kStates ? (buf ? S::kScore : S::kParts) : S::kParts + buf * 64; };
   auto stage = [&](int n) { return smem + (n % kTcStages) * S::kStage; };  // Q, then K, then V
+  // Which waits run out is each warp's own finding: no role waits for another at a barrier without a
+  // limit before the CTA's last. The limit that the host may set holds for the waits for products:
+  // the roles that they starve run into the default (read by the issuer, it took 8 us of 149 at
+  // 1 x 32771 tokens; by every state warp's wait, 3).
+  auto wait_products = [&](uint64_t* bar, uint32_t parity) {
+    const bool got = __all_sync(0xffffffffu, mbar_wait(bar, parity, status, kErrTimeoutEpilogue, *limit));
+    tc_fence_after();
+    return got;
+  };
 
   if (warp < 8) {
     regs_down<kStates ? 24 : 80>();
@@ -232,15 +244,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       // ----------------------------------------------- scores and outputs, row i per thread
       const int quarter = warp & 3, i = quarter * 32 + lane;
       const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      auto wait_mma = [&](uint64_t* bar, uint32_t ph) {
-        const bool got = __all_sync(0xffffffffu, mbar_wait(bar, ph, status, kErrTimeoutEpilogue));
-        tc_fence_after();
-        return got;
-      };
       if (warp < 4) {
         for (int n = 0; n < n_steps; ++n) {
           const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
-          if (!wait_mma(sc_full, n & 1)) break;
+          if (!wait_products(sc_full, n & 1)) break;
 #pragma unroll 1
           for (int c = 0; c < C / 32; ++c) {
             uint32_t packed[16];
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
             // columns that this warp has read already
             tmem_st_32x16(lanes + S::kScore + c * 16, packed);
           }
-          if (!wait_mma(oi_full, n & 1)) break;
+          if (!wait_products(oi_full, n & 1)) break;
           const float inter = pw[p.reverse ? C - 1 - i : max(i - tile.pad + 1, 0)] * p.c_inter;
 #pragma unroll 1
           for (int c = 0; c < DV; c += 32) {
@@ -292,11 +299,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
           __syncwarp();
           if (lane == 0) mbar_arrive(p_ready);
         }
+        tmem_wait_st();  // after a wait that ran out
       } else {
         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + b * p.os[0] + h * p.os[2];
         for (int n = 0; n < n_steps; ++n) {
           const TcTile tile = tc_tile(first + n, nch, len, p.reverse);
-          if (!wait_mma(o_full, n & 1)) break;
+          if (!wait_products(o_full, n & 1)) break;
           // a whole tile goes through shared memory in rows of 128 swizzled bytes, one that starts
           // before the sequence (no store may) straight to global memory
           __nv_bfloat16* row = o + (tile.t0 + i) * p.os[1];
@@ -402,9 +410,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
                                                kErrTimeoutEpilogue)))
           return false;
         if (p.reverse && tile.pad > 0) {  // (the last tile) its weights count from its first real row
-          state_bar_sync();
+          auto meet = [&](uint64_t* bar) {  // the eight state warps
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            return __all_sync(0xffffffffu, mbar_wait(bar, 0, status, kErrTimeoutEpilogue)) != 0;
+          };
+          if (!meet(w_free)) return false;
           if (threadIdx.x - 256 < C / 2) weight_parts(wp, threadIdx.x - 256, g, p, tile.pad);
-          state_bar_sync();
+          if (!meet(w_ready)) return false;
         }
       }
       const int buf = grp & 1;
@@ -451,11 +464,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
       if (lane == 0) mbar_arrive(&up_ready[buf]);
       return true;
     };
-    auto wait_state = [&](int n) {
-      const bool got = __all_sync(0xffffffffu, mbar_wait(d_done(n), d_parity(n), status, kErrTimeoutEpilogue));
-      tc_fence_after();
-      return got;
-    };
     bool ok = true;
     for (int n = 0; ok && n < n_steps; ++n) {
       const bool more = n + 1 < n_steps;
@@ -463,7 +471,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         ok = (n > 0 || (split(0, 0) && split(0, 1))) && (!more || (split(n + 1, 0) && split(n + 1, 1)));
       else
         ok = split(n, 0) && split(n, 1) && split(n, 2) && split(n, 3);
-      ok = ok && wait_state(n);
+      ok = ok && wait_products(d_done(n), d_parity(n));
       if (!ok) break;
       if (active) {
         const float carry = pw[C - tc_tile(first + n, nch, len, p.reverse).pad];
