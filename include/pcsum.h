@@ -460,8 +460,9 @@ PCSUM_API pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy,
  * that the queries read are rounded to bf16 there, the state itself is carried in
  * float32 from products of full precision; otherwise all arithmetic is float32. Equal
  * inputs give equal bits.
- * Errors: PC_ERR_UNSUPPORTED (element type, head sizes above 256, state_out == state),
- * PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_ALIGNMENT, PC_ERR_WORKSPACE. Workspace:
+ * o and state_out may not overlap an input: parts of a call read and write side by side.
+ * Errors: PC_ERR_UNSUPPORTED (element type, head sizes above 256, an output that is an input
+ * itself), PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_ALIGNMENT, PC_ERR_WORKSPACE. Workspace:
  * pc_linear_attention_workspace bytes (may be 0), 16-byte aligned. */
 PCSUM_API pc_status_t pc_linear_attention_workspace(int B, int T, int H, int Dk, int Dv, int with_backward,
                                                     pc_dtype_t dtype, size_t* bytes);
@@ -475,8 +476,10 @@ PCSUM_API pc_status_t pc_linear_attention_fwd(int B, int T, int H, int Dk, int D
 /* Its gradients (the decay is a constant of the model), given do and, optionally, the
  * gradient dstate_out of S_n (NULL: zeros):
  *   dq, dk, dv (elements), rows past a sequence's length zero
- *   dstate [B][H][Dk][Dv]          gradient of S_0, NULL: not wanted; may not be dstate_out
+ *   dstate [B][H][Dk][Dv]          gradient of S_0, NULL: not wanted
  *   strides (HOST)                 as above, in the order q, k, v, do, dq, dk, dv
+ * dq, dk, dv and dstate may overlap neither an input (state and dstate_out among them) nor one
+ * another; one that is another argument itself is PC_ERR_UNSUPPORTED.
  * The states are computed again from q, k, v: the forward keeps nothing. */
 PCSUM_API pc_status_t pc_linear_attention_bwd(int B, int T, int H, int Dk, int Dv, const void* q, const void* k,
                                               const void* v, const void* d_o, const long long* strides,

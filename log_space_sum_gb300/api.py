@@ -566,7 +566,7 @@ def linear_attention_fwd(q, k, v, log_decay, scale=1.0, state=None, lengths=None
     S_t. q, k [B,T,H,Dk], v [B,T,H,Dv] float32 or bfloat16, any strides with the last
     dimension contiguous; log_decay [H] <= 0, ``state`` [B,H,Dk,Dv] float32 (None: zeros),
     ``lengths`` [B] int32 (None: T). Returns (o [B,T,H,Dv], state after each sequence's
-    last token)."""
+    last token). Outputs that are passed in may not overlap an input."""
     dev, dt, H, Dk, Dv = _attention_inputs(q, k, v, log_decay, state, lengths, 2)
     B, T = q.shape[:2]
     out = _given(out, "out", v.shape, dt, dev)
@@ -587,7 +587,8 @@ def linear_attention_bwd(q, k, v, log_decay, do, scale=1.0, state=None, dstate=N
     """Gradients of linear_attention_fwd (pc_linear_attention_bwd) from ``do`` [B,T,H,Dv]
     and, optionally, ``dstate`` [B,H,Dk,Dv], the gradient of the state it returned. Returns
     a dict with dq, dk, dv and dstate, the gradient of its initial state. dq, dk, dv may be
-    passed in with any strides (slices of one projection's gradient)."""
+    passed in with any strides (slices of one projection's gradient); they and
+    ``dstate_in``, where dstate is to lie, may not overlap an input or one another."""
     dev, dt, H, Dk, Dv = _attention_inputs(q, k, v, log_decay, state, lengths, 2)
     B, T = q.shape[:2]
     _shaped(_elements(do, "do", dt, dev), "do", v.shape)

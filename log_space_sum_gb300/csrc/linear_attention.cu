@@ -552,6 +552,12 @@ pc_status_t check_tensor(const char* name, const void* p, pc_dtype_t dt) {
   return PC_OK;
 }
 
+// An output may not lie where an input does: CTAs of one call read and write side by side.
+pc_status_t check_apart(const char* out_name, const void* out, const char* in_name, const void* in) {
+  PC_CHECK(out != in, PC_ERR_UNSUPPORTED, "%s may not be %s itself", out_name, in_name);
+  return PC_OK;
+}
+
 // Workspace: the segments' shares of the state, in whichever variant the tensors' alignment
 // will allow.
 size_t la_workspace(int B, int T, int H, int dk, int dv, int passes, pc_dtype_t dt) {
@@ -630,8 +636,11 @@ pc_status_t pc_linear_attention_fwd(int B, int T, int H, int Dk, int Dv, const v
     PC_TRY(pc::check_tensor("k", k, dtype));
     PC_TRY(pc::check_tensor("v", v, dtype));
     PC_TRY(pc::check_tensor("o", o, dtype));
+    PC_TRY(pc::check_apart("o", o, "q", q));
+    PC_TRY(pc::check_apart("o", o, "k", k));
+    PC_TRY(pc::check_apart("o", o, "v", v));
   }
-  PC_CHECK(!state || state != state_out, PC_ERR_UNSUPPORTED, "state_out may not be state itself");
+  if (state) PC_TRY(pc::check_apart("state_out", state_out, "state", state));
   pc::LaArgs a{};
   a.B = B;
   a.T = T;
@@ -656,8 +665,13 @@ pc_status_t pc_linear_attention_bwd(int B, int T, int H, int Dk, int Dv, const v
     const char* names[7] = {"q", "k", "v", "do", "dq", "dk", "dv"};
     const void* all[7] = {q, k, v, d_o, dq, dk, dv};
     for (int i = 0; i < 7; ++i) PC_TRY(pc::check_tensor(names[i], all[i], dtype));
+    for (int i = 4; i < 7; ++i)
+      for (int j = 0; j < i; ++j) PC_TRY(pc::check_apart(names[i], all[i], names[j], all[j]));
   }
-  PC_CHECK(!dstate_out || dstate_out != dstate, PC_ERR_UNSUPPORTED, "dstate may not be dstate_out itself");
+  if (dstate) {
+    PC_TRY(pc::check_apart("dstate", dstate, "dstate_out", dstate_out));
+    PC_TRY(pc::check_apart("dstate", dstate, "state", state));
+  }
   const long long *qs = strides, *ks = strides + 3, *vs = strides + 6, *gs = strides + 9;
   pc::LaArgs a{};
   a.B = B;

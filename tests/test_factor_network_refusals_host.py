@@ -1,0 +1,60 @@
+"""Refusals of the factor network's entry points beyond their types and shapes: before anything is
+launched (no GPU)."""
+import ctypes as C
+
+import pytest
+
+from log_space_sum_gb300 import _native as N
+from log_space_sum_gb300 import build as B
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return N.load()
+
+
+def _places(n):
+    """n pointers, all different and 16-byte aligned."""
+    return [C.c_void_p(0x10000 * (i + 1)) for i in range(n)]
+
+
+def _strides(tensors, H=4, D=64, T=8):
+    return (C.c_longlong * (3 * tensors))(*([T * H * D, H * D, D] * tensors))
+
+
+def _forward(lib, q, k, v, o, state=None, state_out=None, strides=None):
+    return N.STATUS[lib.pc_linear_attention_fwd(2, 8, 4, 64, 64, q, k, v, strides or _strides(4), C.c_void_p(0x8000), 1.0,
+                                                state, None, o, state_out, 0, C.c_void_p(0x4000), 0, None)]
+
+
+def _backward(lib, tensors, state=None, dstate_out=None, dstate=None, strides=None):
+    q, k, v, do, dq, dk, dv = tensors
+    return N.STATUS[lib.pc_linear_attention_bwd(2, 8, 4, 64, 64, q, k, v, do, strides or _strides(7), C.c_void_p(0x8000),
+                                                1.0, state, dstate_out, None, dq, dk, dv, dstate, 0,
+                                                C.c_void_p(0x4000), 0, None)]
+
+
+def test_attention_outputs_that_are_inputs(lib):
+    q, k, v, o, s = _places(5)
+    for same in (q, k, v):
+        assert _forward(lib, q, k, v, same) == "PC_ERR_UNSUPPORTED"
+        assert b"o may not be" in lib.pc_last_error()
+    assert _forward(lib, q, k, v, o, s, s) == "PC_ERR_UNSUPPORTED"
+
+
+def test_attention_gradients_that_are_inputs_or_one_another(lib):
+    t = _places(7)
+    for i in range(4, 7):
+        for j in range(i):
+            same = list(t)
+            same[i] = t[j]
+            assert _backward(lib, same) == "PC_ERR_UNSUPPORTED", (i, j)
+            assert b"may not be" in lib.pc_last_error()
+
+
+def test_attention_state_gradient_in_the_state(lib):
+    t, (s, ds) = _places(7), (C.c_void_p(0x900000), C.c_void_p(0x980000))
+    assert _backward(lib, t, state=s, dstate_out=ds, dstate=s) == "PC_ERR_UNSUPPORTED"
+    assert b"dstate may not be state" in lib.pc_last_error()
+    assert _backward(lib, t, state=s, dstate_out=ds, dstate=ds) == "PC_ERR_UNSUPPORTED"
