@@ -450,7 +450,8 @@ PCSUM_API pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy,
  *   S_t = l S_{t-1} + k_t v_t^T,   o_t = scale q_t^T S_t,   t = 1 .. n,  S_0 = state
  *   q, k (elements) [B][T][H][Dk], v, o (elements) [B][T][H][Dv]
  *   strides (HOST)                 (batch, token, head) strides in elements, in the order
- *                                  q, k, v, o; the innermost dimension is contiguous
+ *                                  q, k, v, o; the innermost dimension is contiguous; an
+ *                                  input's may be 0 (shared by heads, say), an output's not
  *   log_decay [H]                  <= 0; -inf: only the current token counts
  *   state [B][H][Dk][Dv]           S_0, NULL: zeros
  *   state_out [B][H][Dk][Dv]       S_n, NULL: not wanted; may not be `state`

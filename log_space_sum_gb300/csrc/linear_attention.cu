@@ -558,6 +558,13 @@ pc_status_t check_apart(const char* out_name, const void* out, const char* in_na
   return PC_OK;
 }
 
+// An output's elements may not share memory, as a stride of zero makes them.
+pc_status_t check_stored_once(const char* name, const long long* strides, const int* dims, int n) {
+  for (int i = 0; i < n; ++i)
+    PC_CHECK(dims[i] <= 1 || strides[i] != 0, PC_ERR_SHAPE, "%s: stride 0 along a dimension of %d", name, dims[i]);
+  return PC_OK;
+}
+
 // Workspace: the segments' shares of the state, in whichever variant the tensors' alignment
 // will allow.
 size_t la_workspace(int B, int T, int H, int dk, int dv, int passes, pc_dtype_t dt) {
@@ -639,6 +646,8 @@ pc_status_t pc_linear_attention_fwd(int B, int T, int H, int Dk, int Dv, const v
     PC_TRY(pc::check_apart("o", o, "q", q));
     PC_TRY(pc::check_apart("o", o, "k", k));
     PC_TRY(pc::check_apart("o", o, "v", v));
+    const int dims[3] = {B, T, H};
+    PC_TRY(pc::check_stored_once("o", strides + 9, dims, 3));
   }
   if (state) PC_TRY(pc::check_apart("state_out", state_out, "state", state));
   pc::LaArgs a{};
@@ -667,6 +676,8 @@ pc_status_t pc_linear_attention_bwd(int B, int T, int H, int Dk, int Dv, const v
     for (int i = 0; i < 7; ++i) PC_TRY(pc::check_tensor(names[i], all[i], dtype));
     for (int i = 4; i < 7; ++i)
       for (int j = 0; j < i; ++j) PC_TRY(pc::check_apart(names[i], all[i], names[j], all[j]));
+    const int dims[3] = {B, T, H};
+    for (int i = 4; i < 7; ++i) PC_TRY(pc::check_stored_once(names[i], strides + 3 * i, dims, 3));
   }
   if (dstate) {
     PC_TRY(pc::check_apart("dstate", dstate, "dstate_out", dstate_out));
@@ -696,6 +707,8 @@ pc_status_t pc_linear_attention_step(int B, int H, int Dk, int Dv, const void* q
   PC_TRY(pc::check_tensor("k", k, dtype));
   PC_TRY(pc::check_tensor("v", v, dtype));
   PC_TRY(pc::check_tensor("o", o, dtype));
+  const int dims[2] = {B, H};
+  PC_TRY(pc::check_stored_once("o", strides + 6, dims, 2));
   if (dtype == PC_BF16)
     pc::launch_step<__nv_bfloat16>(B, H, Dk, Dv, q, k, v, strides, log_decay, scale, state, o, stream);
   else

@@ -58,3 +58,24 @@ def test_attention_state_gradient_in_the_state(lib):
     assert _backward(lib, t, state=s, dstate_out=ds, dstate=s) == "PC_ERR_UNSUPPORTED"
     assert b"dstate may not be state" in lib.pc_last_error()
     assert _backward(lib, t, state=s, dstate_out=ds, dstate=ds) == "PC_ERR_UNSUPPORTED"
+
+
+def test_attention_outputs_whose_elements_share_memory(lib):
+    """An input may be shared by heads or sequences (stride 0); an output would be written by several
+    parts at once."""
+    q, k, v, o = _places(4)
+    for dim in range(3):
+        st = _strides(4)
+        st[9 + dim] = 0
+        assert _forward(lib, q, k, v, o, strides=st) == "PC_ERR_SHAPE"
+        assert b"o: stride 0" in lib.pc_last_error()
+        for tensor in range(4, 7):
+            st = _strides(7)
+            st[3 * tensor + dim] = 0
+            assert _backward(lib, _places(7), strides=st) == "PC_ERR_SHAPE"
+            assert b"stride 0" in lib.pc_last_error()
+    for dim in range(2):
+        st = (C.c_longlong * 8)(*([256, 64] * 4))
+        st[6 + dim] = 0
+        got = lib.pc_linear_attention_step(2, 4, 64, 64, q, k, v, st, C.c_void_p(0x8000), 1.0, C.c_void_p(0x9000), o, 0, None)
+        assert N.STATUS[got] == "PC_ERR_SHAPE"
