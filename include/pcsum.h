@@ -500,7 +500,9 @@ PCSUM_API pc_status_t pc_linear_attention_step(int B, int H, int Dk, int Dv, con
 /* Orthogonalised update of `batch` matrices G [rows][cols] (elements): X_0 = G / (|G|_F +
  * eps), then `steps` times A = X X^T, X <- a X + (b A + c A A) X (of the transposed matrix
  * where rows > cols); out [rows][cols] (elements) = X. a s + b s^3 + c s^5 acts on the
- * singular values. |G|_F^2 is summed in float32; a matrix of zeros gives zeros.
+ * singular values. |G|_F^2 is summed in float32: a matrix of zeros, or of values whose squares
+ * vanish there (below 1e-23), gives zeros; squares that overflow give what is not finite.
+ * The significant bits below hold at any |G|_F / eps.
  * Precision: PC_PREC_AUTO and PC_PREC_TF32 form every product from operands of 11
  * significant bits (matrices at least eight times as wide as high may take several steps
  * on A alone, in 22), PC_PREC_FP32 from operands of 22 (hi + lo); float32 accumulation.

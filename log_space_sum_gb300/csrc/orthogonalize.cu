@@ -14,7 +14,8 @@
 // Power-of-two factors keep every operand in float16's range: X is stored as Xs with X =
 // 2^-s Xs, 2^s ~ sqrt(N) (a row of X then has entries of about one), A as 2^12 A, B as
 // 2^10 B. The first Xs is G times a power of two alone (exact for bf16 G); the rest of
-// the norm, nu, enters with the first products in float32.
+// the norm, nu, enters with the first products in float32. Where |G|_F is small beside eps, so is
+// X, and it grows by a step: its matrix then has a further power of two for each step (orth_scales).
 //
 // Very wide matrices take several steps on the M x M matrix alone: with P = a I + B, X' = P X has
 // X' X'^T = P A P, everything commutes, and
@@ -131,7 +132,7 @@ __device__ __forceinline__ float orth_total(int blocks, const float* part, float
 // Zero (or a norm that is not finite): e = 0, and nu = 2^-e / (|G|_F + eps) carries what
 // comes of it.
 __device__ __forceinline__ float orth_scale(int rows, int cols, float total, float eps, float* nu) {
-  const float norm = sqrtf(total) + eps;
+  const float norm = sqrtf(total);
   int e = 0;
   if (norm > 0.f && norm < 3e38f) {
     int at;
@@ -139,15 +140,37 @@ __device__ __forceinline__ float orth_scale(int rows, int cols, float total, flo
     const int spread = (32 - __clz(rows) + 32 - __clz(cols)) / 2;  // sqrt(rows cols) within a factor of two
     e = max(-126, min(min(spread, 15) - at, 126));
   }
-  *nu = total == 0.f ? 0.f : ldexpf(1.f, -e) / norm;
+  *nu = total == 0.f ? 0.f : ldexpf(1.f, -e) / (norm + eps);
   return ldexpf(1.f, e);
+}
+
+// What a matrix's X before each step is held by: X_0 = x Xs, and X_k = 2^-s x Xs with x = 1 / y a power of
+// two, from the bound u of |X_k|_F that the polynomial gives: y u <= 1 where u < 1/2, else y = 1.
+// scales[step][batch].
+struct OrthSteps {
+  int steps, batch;
+  float a, b, c;
+  float2* scales;
+};
+constexpr int kMaxSteps = 100;
+__device__ __forceinline__ void orth_scales(const OrthSteps& p, int m, float total, float eps, float nu) {
+  p.scales[m] = make_float2(nu, 1.f);
+  float u = sqrtf(total) / (sqrtf(total) + eps);
+  for (int k = 1; k < p.steps; ++k) {
+    const float u2 = u * u;
+    u = fminf(u * (fabsf(p.a) + u2 * (fabsf(p.b) + u2 * fabsf(p.c))), 2.f);
+    int t = 0;
+    if (u > 0.f && u < 0.5f) frexpf(u, &t);  // u = f 2^t, f in [1/2, 1)
+    t = max(t, -126);
+    p.scales[static_cast<size_t>(k) * p.batch + m] = make_float2(ldexpf(1.f, t), ldexpf(1.f, -t));
+  }
 }
 
 // Xs = 2^e G where G is not taller than wide and its rows are whole 16-byte pieces: a stream.
 template <class T, int kParts>
 __global__ void __launch_bounds__(kNormThreads)
     k_orth_load_rows(int rows, int cols, const T* __restrict__ g, int blocks, const float* part, float eps, HalfMat x,
-                     float* nu) {
+                     const OrthSteps steps) {
   __shared__ float red[kNormThreads / 32];
   constexpr int L = kPiece<T>, kFlight = 4;
   const int m = blockIdx.y, pieces = cols / L;
@@ -165,8 +188,8 @@ __global__ void __launch_bounds__(kNormThreads)
   grid_dependency_wait();  // the sums of squares
   grid_dependents_launch();
   float inv;
-  const float up = orth_scale(rows, cols, orth_total(blocks, part + m * kNormBlocks, red), eps, &inv);
-  if (blockIdx.x == 0 && threadIdx.x == 0) nu[m] = inv;
+  const float total = orth_total(blocks, part + m * kNormBlocks, red), up = orth_scale(rows, cols, total, eps, &inv);
+  if (blockIdx.x == 0 && threadIdx.x == 0) orth_scales(steps, m, total, eps, inv);
   for (; i < n; i += kFlight * stride, fetch()) {
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
@@ -200,7 +223,7 @@ __global__ void __launch_bounds__(kNormThreads)
 template <class T, int kParts>
 __global__ void __launch_bounds__(kNormThreads)
     k_orth_load(int rows, int cols, const T* __restrict__ g, int blocks, const float* part, float eps, int tall,
-                HalfMat x, float* nu) {
+                HalfMat x, const OrthSteps steps) {
   __shared__ float red[kNormThreads / 32];
   __shared__ float tile[64][65];
   const int m = blockIdx.z, t = threadIdx.x;
@@ -225,8 +248,8 @@ __global__ void __launch_bounds__(kNormThreads)
   grid_dependency_wait();  // the sums of squares
   grid_dependents_launch();
   float inv;
-  const float up = orth_scale(rows, cols, orth_total(blocks, part + m * kNormBlocks, red), eps, &inv);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) nu[m] = inv;
+  const float total = orth_total(blocks, part + m * kNormBlocks, red), up = orth_scale(rows, cols, total, eps, &inv);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && t == 0) orth_scales(steps, m, total, eps, inv);
   __half* hi = x.ptr + static_cast<size_t>(m) * x.rows * x.ld;
 #pragma unroll
   for (int i = t; i < 64 * 32; i += kNormThreads) {  // pairs of columns of the operand
@@ -262,7 +285,7 @@ struct OrthArgs {
   // the identity where the singular values are alike, and its diagonal's errors then are too:
   // without them the whole update's error falls from 1.9e-3 to 1.1e-3 (400 x 8192).
   float* off;
-  const float* nu;              // first step: the norm's factor, else NULL
+  const float2 *scale, *next;   // orth_scales of X (kGram, kApply) and of X' (NULL: the caller's)
   float k0, k1;                 // see the epilogue
   void* out;                    // last kApply: the caller's matrix, else NULL
   int tall;
@@ -342,6 +365,15 @@ __device__ __forceinline__ void store_half_run(const HalfMat& x, size_t at, cons
 __device__ __forceinline__ void orth_store(float* p, float v) { *p = v; }
 __device__ __forceinline__ void orth_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
+// The matrix's scales in one: X = nu Xs, times the power of two of Xs'. Read before the products are
+// waited for (beside X's values it took 3 us of the 120 at 1024 x 1024).
+template <int kOp>
+__device__ __forceinline__ float orth_nu(const OrthArgs& p, int g) {
+  if constexpr (kOp == kPoly) return 1.f;
+  const float nu = p.scale[g].x;
+  return kOp == kApply && p.next ? nu * p.next[g].y : nu;
+}
+
 // What the epilogue reads of 32 columns from n of row m: kPoly A, kApply X.
 template <int kParts, int kOp, bool kPrev>
 __device__ __forceinline__ void orth_fetch(const OrthArgs& p, int g, int m, int n, HalfRun<kParts>& x) {
@@ -357,12 +389,12 @@ __device__ __forceinline__ void orth_fetch(const OrthArgs& p, int g, int m, int 
 //   kGram   2^12 A = k0 nu^2 D
 //   kPoly   2^10 B = k0 (2^12 A) + k1 D
 //   kApply  X' = k0 nu ((k1 + 2^-10 off) Xs + 2^-10 D), to Xs' or to the caller
+// (nu with the power of two of Xs')
 template <int kParts, int kOp, bool kPrev, class T>
-__device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, int m, int n, bool mirror, float (&v)[32],
-                                              const HalfRun<kParts>& x, float* square) {
+__device__ __forceinline__ void orth_epilogue(const OrthArgs& p, int g, float nu, int m, int n, bool mirror,
+                                              float (&v)[32], const HalfRun<kParts>& x, float* square) {
   if (m >= p.M || n >= p.N) return;
   const int k = min(32, p.N - n);
-  const float nu = p.nu ? p.nu[g] : 1.f;
   const size_t base = static_cast<size_t>(g) * p.to.rows * p.to.ld, at = base + static_cast<size_t>(m) * p.to.ld + n;
   if constexpr (kOp == kGram) {
     const float f = p.k0 * nu * nu;
@@ -686,6 +718,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
       int g, m0, n0;
       tile_at(t, g, m0, n0);
       const bool mirror = kPairs && n0 != m0;
+      const float nu = orth_nu<kOp>(p, g);
       if constexpr (kSplit == 1 && !kSliced) {
         HalfRun<kParts> x;
         orth_fetch<kParts, kOp, kPrev>(p, g, m0 + row, n0 + part * 32, x);
@@ -698,7 +731,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           float v[32];
           tmem_ld_32x32(lanes + (unit & 1) * BN + c, v);
           if (c + 64 >= BN) release();
-          orth_epilogue<kParts, kOp, kPrev, T>(p, g, m0 + row, n0 + c, mirror, v, now, square);
+          orth_epilogue<kParts, kOp, kPrev, T>(p, g, nu, m0 + row, n0 + c, mirror, v, now, square);
         }
       } else if constexpr (kSplit > 1 && !kSliced) {
         // straight from tensor memory, one chunk of 32 columns at a time
@@ -744,7 +777,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) v[i] += from[i * kBM];
             }
-            orth_epilogue<kParts, kOp, kPrev, T>(p, g, m0 + row, n0 + xc * 32, mirror, v, x, square);
+            orth_epilogue<kParts, kOp, kPrev, T>(p, g, nu, m0 + row, n0 + xc * 32, mirror, v, x, square);
           }
         }
       } else {
@@ -775,7 +808,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
           if (ok) {
 #pragma unroll
             for (int c = 0; c < kChunks; ++c)
-              orth_epilogue<kParts, kOp, kPrev, T>(p, g, m0 + row, n0 + (2 * c + part) * 32, mirror, acc[c], x[c], square);
+              orth_epilogue<kParts, kOp, kPrev, T>(p, g, nu, m0 + row, n0 + (2 * c + part) * 32, mirror, acc[c], x[c], square);
           }
         } else {
           cluster_sync();  // every ring of the cluster is idle
@@ -802,7 +835,7 @@ __global__ void __launch_bounds__(kOrthThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) acc[c][i] += from[i * kBM];
               }
-              orth_epilogue<kParts, kOp, kPrev, T>(p, g, m0 + row, n0 + xc * 32, mirror, acc[c], x[c], square);
+              orth_epilogue<kParts, kOp, kPrev, T>(p, g, nu, m0 + row, n0 + xc * 32, mirror, acc[c], x[c], square);
             }
           }
         }
@@ -898,7 +931,8 @@ inline bool by_gram(long long batch, long long M, long long N, int parts) {
 struct OrthPlan {
   HalfMat X[2], A, Bm;
   HalfMat slots;  // by_gram: five stacks of M x M matrices in two parts, Bm likewise
-  float *part, *nu, *off;
+  float *part, *off;
+  float2* scales;
   size_t bytes;
 };
 
@@ -918,7 +952,7 @@ OrthPlan plan_orth(void* ws, int batch, int M, int N, int parts) {
     return m;
   };
   p.part = static_cast<float*>(c.take(sizeof(float) * kNormBlocks * batch));
-  p.nu = static_cast<float*>(c.take(sizeof(float) * batch));
+  p.scales = static_cast<float2*>(c.take(sizeof(float2) * batch * kMaxSteps));
   p.off = static_cast<float*>(c.take(sizeof(float) * batch * M));
   p.X[0] = mat(M, N, parts, 1);
   p.X[1] = mat(M, N, parts, 1);
@@ -985,7 +1019,7 @@ pc_status_t iterate(const OrthPlan& p, int batch, int M, int N, int steps, float
     const bool last = it + count == steps;
     OrthArgs gram = square;
     gram.num_kb = static_cast<int>(blocks_of(N, 64));
-    gram.nu = it == 0 ? p.nu : nullptr;
+    gram.scale = p.scales + static_cast<size_t>(it) * batch;
     gram.k0 = kScaleA * (it == 0 ? 1.f : down * down);
     OrthArgs poly = square;
     poly.k0 = kScaleB / kScaleA * b;
@@ -994,7 +1028,8 @@ pc_status_t iterate(const OrthPlan& p, int batch, int M, int N, int steps, float
     apply.N = N;
     apply.prev = p.X[i];
     apply.to = p.X[i ^ 1];
-    apply.nu = gram.nu;
+    apply.scale = gram.scale;
+    apply.next = last ? nullptr : gram.scale + static_cast<size_t>(count) * batch;
     apply.k0 = (it == 0 ? 1.f : down) * (last ? 1.f : up);
     apply.k1 = a;
     apply.out = last ? out : nullptr;
@@ -1086,15 +1121,16 @@ pc_status_t run_orth(int batch, int rows, int cols, const T* G, int steps, float
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    const OrthSteps scaled{steps, batch, a, b, c, p.scales};
     if (!tall && cols % kPiece<T> == 0) {
       const long long want_load = blocks_of(n / kPiece<T>, 4 * kNormThreads), most = 4ll * num_sms();
       cfg.gridDim = dim3(static_cast<unsigned>(want_load < most ? want_load : most), batch);
       PC_CUDA(cudaLaunchKernelEx(&cfg, k_orth_load_rows<T, kParts>, rows, cols, G, blocks,
-                                 static_cast<const float*>(p.part), eps, p.X[0], p.nu));
+                                 static_cast<const float*>(p.part), eps, p.X[0], scaled));
     } else {
       cfg.gridDim = dim3(blocks_of(cols, 64), blocks_of(rows, 64), batch);
       PC_CUDA(cudaLaunchKernelEx(&cfg, k_orth_load<T, kParts>, rows, cols, G, blocks,
-                                 static_cast<const float*>(p.part), eps, tall, p.X[0], p.nu));
+                                 static_cast<const float*>(p.part), eps, tall, p.X[0], scaled));
     }
     PC_LAUNCH_CHECK();
   }
@@ -1109,7 +1145,7 @@ pc_status_t check_orth(int batch, int rows, int cols, int steps, pc_precision_t 
   PC_CHECK(rows <= (1 << 20) && cols <= (1 << 20), PC_ERR_SHAPE, "rows and columns up to 2^20 (got %d, %d)", rows, cols);
   const long long tiles = static_cast<long long>(blocks_of(rows, kBM)) * blocks_of(cols, kBM) * batch;
   PC_CHECK(tiles < (1ll << 29), PC_ERR_SHAPE, "batch * rows * cols too large (%d matrices of %d x %d)", batch, rows, cols);
-  PC_CHECK(steps >= 1 && steps <= 100, PC_ERR_SHAPE, "steps must be in [1, 100] (got %d)", steps);
+  PC_CHECK(steps >= 1 && steps <= kMaxSteps, PC_ERR_SHAPE, "steps must be in [1, %d] (got %d)", kMaxSteps, steps);
   return PC_OK;
 }
 
