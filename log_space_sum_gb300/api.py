@@ -66,6 +66,8 @@ def _ptr(t):
 
 def _stream(device) -> int:
     # the handle alone: torch.cuda.current_stream would build a Stream object for each call
+    if not isinstance(device, torch.device) or device.type != "cuda":
+        return torch.cuda.current_stream(device).cuda_stream  # an index, a name, or its error
     index = device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
