@@ -464,7 +464,8 @@ PCSUM_API pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy,
  * o and state_out may not overlap an input: parts of a call read and write side by side.
  * Errors: PC_ERR_UNSUPPORTED (element type, head sizes above 256, an output that is an input
  * itself), PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_ALIGNMENT, PC_ERR_WORKSPACE. Workspace:
- * pc_linear_attention_workspace bytes (may be 0), 16-byte aligned. */
+ * pc_linear_attention_workspace bytes (may be 0; with_backward != 0: for either direction),
+ * 16-byte aligned. */
 PCSUM_API pc_status_t pc_linear_attention_workspace(int B, int T, int H, int Dk, int Dv, int with_backward,
                                                     pc_dtype_t dtype, size_t* bytes);
 

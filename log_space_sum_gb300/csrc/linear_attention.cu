@@ -626,7 +626,11 @@ pc_status_t pc_linear_attention_workspace(int B, int T, int H, int Dk, int Dv, i
   pc::clear_error();
   PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
   PC_TRY(pc::check_la(B, T, H, Dk, Dv, dtype));
-  *bytes = pc::la_workspace(B, T, H, Dk, Dv, with_backward ? 3 : 1, dtype);
+  *bytes = pc::la_workspace(B, T, H, Dk, Dv, 1, dtype);
+  if (with_backward) {  // three times the heads may be cut less
+    const size_t back = pc::la_workspace(B, T, H, Dk, Dv, 3, dtype);
+    if (back > *bytes) *bytes = back;
+  }
   return PC_OK;
 }
 

@@ -79,3 +79,16 @@ def test_attention_outputs_whose_elements_share_memory(lib):
         st[6 + dim] = 0
         got = lib.pc_linear_attention_step(2, 4, 64, 64, q, k, v, st, C.c_void_p(0x8000), 1.0, C.c_void_p(0x9000), o, 0, None)
         assert N.STATUS[got] == "PC_ERR_SHAPE"
+
+
+def test_attention_workspace_with_backward_serves_both_directions(lib):
+    """The gradient's passes are three times the heads and may be cut into fewer segments."""
+    def size(shape, back, dtype):
+        nb = C.c_size_t(0)
+        assert lib.pc_linear_attention_workspace(*shape, back, dtype, C.byref(nb)) == 0
+        return nb.value
+
+    for dtype in (0, 1):
+        for shape in [(1, 1500, 5, 128, 128)] + [(B, T, H, dk, dv) for B in (1, 2, 4) for T in (33, 333, 1500, 4000, 20000)
+                                                 for H in (1, 3, 5, 16) for dk, dv in ((64, 64), (128, 64), (40, 56))]:
+            assert size(shape, 1, dtype) >= size(shape, 0, dtype), (shape, dtype)
