@@ -120,7 +120,9 @@ PCSUM_API pc_status_t pc_set_wait_limit_ns(unsigned long long ns);
  * pc_profile_start(capacity) and pc_profile_stop, every contraction the library
  * launches records a CUDA event pair on its stream (at most `capacity` records), except
  * the HMM's chain contractions: each chain of T-1 consecutive launches of one kind is
- * one record (events between them would break their programmatic overlap).
+ * one record (events between them would break their programmatic overlap), and so is a call
+ * of linear attention over whole sequences (its products are those of the recurrence over T
+ * tokens of each sequence: two in the forward, five in the gradient).
  * pc_profile_stop synchronises the device, then writes for each record i
  * (i < *count <= capacity): ms[i] = elapsed device time, kind[i] = which contraction
  * (PC_KIND_*), flops[i] = the algorithmic flops of its launches, 2*M*N*K each (each
@@ -136,7 +138,8 @@ typedef enum {
   PC_KIND_HMM_FWD = 3, PC_KIND_HMM_ELEM = 4, PC_KIND_HMM_PARAM = 5,
   PC_KIND_HCLT_FWD = 6, PC_KIND_HCLT_ELEM = 7, PC_KIND_HCLT_PARAM = 8,
   PC_KIND_LOWRANK_FWD = 9, PC_KIND_LOWRANK_BWD = 10, PC_KIND_EM_MSTEP = 11,
-  PC_KIND_HMM_MEM = 12, PC_KIND_HCLT_MEM = 13, PC_KIND_ORTHOGONALIZE = 14
+  PC_KIND_HMM_MEM = 12, PC_KIND_HCLT_MEM = 13, PC_KIND_ORTHOGONALIZE = 14,
+  PC_KIND_LINEAR_ATTENTION = 15
 } pc_kind_t;
 PCSUM_API pc_status_t pc_profile_start(int capacity);
 PCSUM_API pc_status_t pc_profile_stop(int* count, float* ms, int* kind, long long* flops,

@@ -23,7 +23,7 @@ KINDS = {
     0: "layer_fwd", 1: "layer_elem", 2: "layer_param", 3: "hmm_fwd", 4: "hmm_elem",
     5: "hmm_param", 6: "hclt_fwd", 7: "hclt_elem", 8: "hclt_param", 9: "lowrank_fwd",
     10: "lowrank_bwd", 11: "em_mstep", 12: "hmm_mem", 13: "hclt_mem",
-    14: "orthogonalize",
+    14: "orthogonalize", 15: "linear_attention",
 }
 # kinds whose flops field holds algorithmic bytes
 MEMORY_KINDS = {"em_mstep", "hmm_mem", "hclt_mem"}

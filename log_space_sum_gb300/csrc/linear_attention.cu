@@ -280,7 +280,7 @@ pc_status_t launch_after(void (*kernel)(Args), dim3 grid, int threads, int smem,
 }
 
 template <class T>
-pc_status_t launch_simt(const LaArgs& a, int passes, void* ws, cudaStream_t s) {
+pc_status_t launch_simt(const LaArgs& a, int passes, void* ws, cudaStream_t s, int* launches) {
   int dk = 0, dv = 0;
   for (int i = 0; i < passes; ++i) {
     dk = a.pass[i].dk > dk ? a.pass[i].dk : dk;
@@ -299,10 +299,12 @@ pc_status_t launch_simt(const LaArgs& a, int passes, void* ws, cudaStream_t s) {
     PC_TRY((allow_smem<k_la_simt<T, true>>(most)));
     k_la_simt<T, true><<<dim3(heads, slices, (t.segments - 1) * passes), kSimtThreads, smem, s>>>(t);
     PC_LAUNCH_CHECK();
+    ++*launches;
   }
   PC_TRY((allow_smem<k_la_simt<T, false>>(most)));
   PC_TRY(launch_after(k_la_simt<T, false>, dim3(heads, slices, t.segments * passes), kSimtThreads, smem, s,
                       t.segments > 1, t));
+  ++*launches;
   return PC_OK;
 }
 
@@ -377,7 +379,7 @@ size_t tc_partial_bytes(long long heads, int segments, int dk, int dv) {
 }
 
 template <int DK, int DV>
-pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s) {
+pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s, int* launches) {
   constexpr int smem = TcShape<DK, DV, false>::kBytes, states_smem = TcShape<DK, DV, true>::kBytes;
   PC_TRY((allow_smem<k_la_tc<DK, DV, false>>(smem)));
   const unsigned heads = static_cast<unsigned>(t.a.B) * t.a.H;
@@ -386,13 +388,15 @@ pc_status_t launch_tc(LaTcArgs& t, int passes, cudaStream_t s) {
     PC_TRY((allow_smem<k_la_tc<DK, DV, true>>(states_smem)));
     k_la_tc<DK, DV, true><<<dim3(heads * passes, t.segments - 1), kTcThreads, states_smem, s>>>(t);
     PC_LAUNCH_CHECK();
+    ++*launches;
   }
+  ++*launches;
   return launch_after(k_la_tc<DK, DV, false>, dim3(heads * passes, t.segments), kTcThreads, smem, s, t.segments > 1, t);
 }
 
 // Runs the passes on the tensor cores; *done = false (and nothing launched) where a tensor's
 // alignment does not allow it.
-pc_status_t run_tc(const LaArgs& a, int passes, void* ws, cudaStream_t s, bool* done) {
+pc_status_t run_tc(const LaArgs& a, int passes, void* ws, cudaStream_t s, int* launches, bool* done) {
   *done = false;
   LaTcArgs t{};
   t.a = a;
@@ -425,13 +429,13 @@ pc_status_t run_tc(const LaArgs& a, int passes, void* ws, cudaStream_t s, bool* 
     }
     part.partial = t.partial + tc_partial_bytes(heads * i, t.segments, dk, dv) / sizeof(float);
     if (dk == 64 && dv == 64)
-      PC_TRY((launch_tc<64, 64>(part, n - i, s)));
+      PC_TRY((launch_tc<64, 64>(part, n - i, s, launches)));
     else if (dk == 64)
-      PC_TRY((launch_tc<64, 128>(part, n - i, s)));
+      PC_TRY((launch_tc<64, 128>(part, n - i, s, launches)));
     else if (dv == 64)
-      PC_TRY((launch_tc<128, 64>(part, n - i, s)));
+      PC_TRY((launch_tc<128, 64>(part, n - i, s, launches)));
     else
-      PC_TRY((launch_tc<128, 128>(part, n - i, s)));
+      PC_TRY((launch_tc<128, 128>(part, n - i, s, launches)));
     i = n;
   }
   return PC_OK;
@@ -581,12 +585,15 @@ pc_status_t run_passes(const LaArgs& a, int passes, pc_dtype_t dt, void* ws, siz
   PC_CHECK(need == 0 || (ws && ws_bytes >= need), PC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes,
            need);
   PC_CHECK(need == 0 || aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  ProfileGroup record(s, PC_KIND_LINEAR_ATTENTION,
+                      static_cast<long long>(a.B) * a.T * a.H * (passes == 1 ? 4 : 10) * p.dk * p.dv);
   if (a.T > 0 && tc_heads(p.dk, p.dv, dt)) {
     bool done = false;
-    PC_TRY(run_tc(a, passes, ws, s, &done));
+    PC_TRY(run_tc(a, passes, ws, s, &record.launches, &done));
     if (done) return PC_OK;
   }
-  return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, passes, ws, s) : launch_simt<float>(a, passes, ws, s);
+  return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, passes, ws, s, &record.launches)
+                       : launch_simt<float>(a, passes, ws, s, &record.launches);
 }
 
 LaPass make_pass(const void* q, const long long* qs, const void* k, const long long* ks, const void* v,

@@ -59,6 +59,20 @@ struct ProfileScope {
   ProfileScope& operator=(const ProfileScope&) = delete;
 };
 
+// One profiler record around several launches (events between them would break their
+// programmatic overlap); the launches are counted as they go.
+struct ProfileGroup {
+  int slot;
+  cudaStream_t s;
+  int kind, launches = 0;
+  long long flops;
+  ProfileGroup(cudaStream_t s_, int kind_, long long flops_)
+      : slot(profile_group_begin(s_)), s(s_), kind(kind_), flops(flops_) {}
+  ~ProfileGroup() { profile_group_end(slot, s, kind, flops, launches); }
+  ProfileGroup(const ProfileGroup&) = delete;
+  ProfileGroup& operator=(const ProfileGroup&) = delete;
+};
+
 #define PC_CHECK(cond, st, ...)                 \
   do {                                          \
     if (!(cond)) return ::pc::set_error(st, __VA_ARGS__); \
