@@ -483,6 +483,7 @@ PCSUM_API pc_status_t pc_linear_attention_fwd(int B, int T, int H, int Dk, int D
  *   dq, dk, dv (elements), rows past a sequence's length zero
  *   dstate [B][H][Dk][Dv]          gradient of S_0, NULL: not wanted
  *   strides (HOST)                 as above, in the order q, k, v, do, dq, dk, dv
+ * B * H < 2^31 / 3 for bf16 elements of head sizes for the tensor cores.
  * dq, dk, dv and dstate may overlap neither an input (state and dstate_out among them) nor one
  * another; one that is another argument itself is PC_ERR_UNSUPPORTED.
  * The states are computed again from q, k, v: the forward keeps nothing. */

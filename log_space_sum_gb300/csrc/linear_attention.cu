@@ -588,6 +588,8 @@ pc_status_t run_passes(const LaArgs& a, int passes, pc_dtype_t dt, void* ws, siz
   ProfileGroup record(s, PC_KIND_LINEAR_ATTENTION,
                       static_cast<long long>(a.B) * a.T * a.H * (passes == 1 ? 4 : 10) * p.dk * p.dv);
   if (a.T > 0 && tc_heads(p.dk, p.dv, dt)) {
+    PC_CHECK(static_cast<long long>(a.B) * a.H * passes < (1ll << 31), PC_ERR_SHAPE,
+             "%d passes of B * H = %lld heads: fewer than 2^31 in all wanted", passes, static_cast<long long>(a.B) * a.H);
     bool done = false;
     PC_TRY(run_tc(a, passes, ws, s, &record.launches, &done));
     if (done) return PC_OK;

@@ -92,3 +92,12 @@ def test_attention_workspace_with_backward_serves_both_directions(lib):
         for shape in [(1, 1500, 5, 128, 128)] + [(B, T, H, dk, dv) for B in (1, 2, 4) for T in (33, 333, 1500, 4000, 20000)
                                                  for H in (1, 3, 5, 16) for dk, dv in ((64, 64), (128, 64), (40, 56))]:
             assert size(shape, 1, dtype) >= size(shape, 0, dtype), (shape, dtype)
+
+
+def test_attention_gradient_of_too_many_heads(lib):
+    """A gradient on the tensor cores launches a column of CTAs for each head of each of three passes."""
+    t = _places(7)
+    st = _strides(7, H=1 << 15, D=8, T=1)
+    got = lib.pc_linear_attention_bwd(1 << 15, 1, 1 << 15, 8, 8, *t[:4], st, C.c_void_p(0x8000), 1.0, None, None, None, *t[4:],
+                                      None, 1, None, 0, None)
+    assert N.STATUS[got] == "PC_ERR_SHAPE" and b"fewer than 2^31" in lib.pc_last_error()
