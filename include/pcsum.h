@@ -424,7 +424,7 @@ PCSUM_API pc_status_t pc_em_normalize(int G, int M, int N, const float* F, const
 
 /* Layer norm of `rows` rows of `dim` elements, row r at r * ld:
  *   mean = avg(x), rstd = (avg((x - mean)^2) + eps)^(-1/2), y = (x - mean) rstd weight + bias
- *   x, y (elements)                row strides x_ld, y_ld >= dim; y may be x
+ *   x, y (elements)                row strides x_ld, y_ld >= dim; y may be x, at the same stride
  *   weight, bias [dim]             NULL: 1, 0
  *   mean, rstd [rows]              outputs, each may be NULL; the backward reads them
  * rows may be 0. Errors: PC_ERR_UNSUPPORTED (element type), PC_ERR_SHAPE, PC_ERR_NULL,
@@ -435,7 +435,8 @@ PCSUM_API pc_status_t pc_layer_norm_fwd(long long rows, int dim, const void* x, 
                                         float* rstd, pc_dtype_t dtype, pc_stream_t stream);
 
 /* Its gradient from the forward's statistics, z = (x - mean) rstd, g = dy weight:
- *   dx = rstd (g - avg(g) - z avg(g z))       (elements, row stride dx_ld; dx may be dy)
+ *   dx = rstd (g - avg(g) - z avg(g z))       (elements, row stride dx_ld; dx may be dy or x, at
+ *                                               the same stride)
  *   dweight [dim] = sum_r dy z,  dbias [dim] = sum_r dy
  * dweight and dbias may be NULL; with accumulate != 0 they are added to. The row sums are
  * taken in a fixed order: equal inputs give equal bits. Workspace (needed with dweight or

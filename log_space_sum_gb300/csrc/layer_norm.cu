@@ -785,6 +785,15 @@ pc_status_t check_rows(const char* name, const void* p, long long ld, long long 
   return PC_OK;
 }
 
+// In place a row is written where it was read: at another stride it would lie on other rows, which
+// other CTAs have yet to read.
+pc_status_t check_in_place(const char* out_name, const void* out, long long out_ld, const char* in_name, const void* in,
+                           long long in_ld, long long rows) {
+  PC_CHECK(out != in || rows <= 1 || out_ld == in_ld, PC_ERR_SHAPE, "%s is %s with another row stride (%lld, %lld)",
+           out_name, in_name, out_ld, in_ld);
+  return PC_OK;
+}
+
 }  // namespace
 }  // namespace pc
 
@@ -800,6 +809,7 @@ pc_status_t pc_layer_norm_fwd(long long rows, int dim, const void* x, long long 
   if (rows == 0) return PC_OK;
   PC_TRY(pc::check_rows("x", x, x_ld, rows, dim, dtype));
   PC_TRY(pc::check_rows("y", y, y_ld, rows, dim, dtype));
+  PC_TRY(pc::check_in_place("y", y, y_ld, "x", x, x_ld, rows));
   const pc::LnFwd a{rows, dim, x, x_ld, weight, bias, eps, y, y_ld, mean, rstd};
   if (dtype == PC_BF16)
     pc::launch_fwd<__nv_bfloat16>(a, stream);
@@ -829,6 +839,8 @@ pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy, long long
     PC_TRY(pc::check_rows("dy", dy, dy_ld, rows, dim, dtype));
     PC_TRY(pc::check_rows("x", x, x_ld, rows, dim, dtype));
     PC_TRY(pc::check_rows("dx", dx, dx_ld, rows, dim, dtype));
+    PC_TRY(pc::check_in_place("dx", dx, dx_ld, "dy", dy, dy_ld, rows));
+    PC_TRY(pc::check_in_place("dx", dx, dx_ld, "x", x, x_ld, rows));
     PC_CHECK(mean && rstd, PC_ERR_NULL, "mean and rstd must not be NULL");
   }
   unsigned grid = pc::bwd_grid(rows);  // of the launch at most

@@ -101,3 +101,15 @@ def test_attention_gradient_of_too_many_heads(lib):
     got = lib.pc_linear_attention_bwd(1 << 15, 1, 1 << 15, 8, 8, *t[:4], st, C.c_void_p(0x8000), 1.0, None, None, None, *t[4:],
                                       None, 1, None, 0, None)
     assert N.STATUS[got] == "PC_ERR_SHAPE" and b"fewer than 2^31" in lib.pc_last_error()
+
+
+def test_layer_norm_in_place_at_another_stride(lib):
+    x, dy, m, s, ws = _places(5)
+    fwd = lambda y, ld, rows=4: N.STATUS[lib.pc_layer_norm_fwd(rows, 8, x, 16, None, None, 1e-5, y, ld, None, None, 0, None)]  # noqa: E731
+    assert fwd(x, 8) == "PC_ERR_SHAPE" and b"another row stride" in lib.pc_last_error()
+
+    def bwd(dx, ld):
+        return N.STATUS[lib.pc_layer_norm_bwd(4, 8, dy, 8, x, 16, None, m, s, dx, ld, None, None, 0, 0, ws, 1 << 20, None)]
+
+    assert bwd(dy, 16) == "PC_ERR_SHAPE" and b"another row stride" in lib.pc_last_error()
+    assert bwd(x, 8) == "PC_ERR_SHAPE" and b"another row stride" in lib.pc_last_error()

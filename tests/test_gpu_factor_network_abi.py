@@ -54,3 +54,20 @@ def test_orthogonalize_workspace_aligned_to_16_bytes(shape, precision, dtype):
         pc.device_status()
         assert torch.equal(out, want), shift
         assert ws.untouched_around(), shift
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,dim,first", [(700, 1024, 0), (900, 513, 3), (60, 4097, 1), (30, 9000, 0)])
+def test_layer_norm_gradient_in_the_place_of_its_inputs(rows, dim, first, dtype):
+    """dx over dy and over x: the bits of a dx of its own at the same place in a 16-byte piece (at
+    another, the rows are taken value by value and summed in another order)."""
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    place = lambda: r(rows * dim + 8).to(dtype)[first:first + rows * dim].view(rows, dim)  # noqa: E731
+    x, dy, w = place(), place(), r(dim)
+    _, mean, rstd = pc.layer_norm_fwd(x, w)
+    want = pc.layer_norm_bwd(dy, x, w, mean, rstd, dx=place())
+    for over in (0, 1):
+        a, b = place().copy_(x), place().copy_(dy)
+        got = pc.layer_norm_bwd(b, a, w, mean, rstd, dx=(b, a)[over])
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
