@@ -465,6 +465,8 @@ PCSUM_API pc_status_t pc_layer_norm_bwd(long long rows, int dim, const void* dy,
  * that the queries read are rounded to bf16 there, the state itself is carried in
  * float32 from products of full precision; otherwise all arithmetic is float32. Equal
  * inputs give equal bits.
+ * What is not finite in a token reaches the outputs of the tokens after it, and may reach those
+ * of up to 127 tokens before it: tiles of tokens are multiplied whole.
  * o and state_out may not overlap an input: parts of a call read and write side by side.
  * Errors: PC_ERR_UNSUPPORTED (element type, head sizes above 256, an output that is an input
  * itself), PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_ALIGNMENT, PC_ERR_WORKSPACE. Workspace:
@@ -487,7 +489,8 @@ PCSUM_API pc_status_t pc_linear_attention_fwd(int B, int T, int H, int Dk, int D
  * B * H < 2^31 / 3 for bf16 elements of head sizes for the tensor cores.
  * dq, dk, dv and dstate may overlap neither an input (state and dstate_out among them) nor one
  * another; one that is another argument itself is PC_ERR_UNSUPPORTED.
- * The states are computed again from q, k, v: the forward keeps nothing. */
+ * The states are computed again from q, k, v: the forward keeps nothing. What is not finite in a
+ * token reaches, beside the gradients that it enters, those of up to 127 tokens on either side. */
 PCSUM_API pc_status_t pc_linear_attention_bwd(int B, int T, int H, int Dk, int Dv, const void* q, const void* k,
                                               const void* v, const void* d_o, const long long* strides,
                                               const float* log_decay, float scale, const float* state,
@@ -512,6 +515,11 @@ PCSUM_API pc_status_t pc_linear_attention_step(int B, int H, int Dk, int Dv, con
  * Precision: PC_PREC_AUTO and PC_PREC_TF32 form every product from operands of 11
  * significant bits (matrices at least eight times as wide as high may take several steps
  * on A alone, in 22), PC_PREC_FP32 from operands of 22 (hi + lo); float32 accumulation.
+ * Rounding fills the directions that G lacks with singular values of an operand's relative
+ * error, and the iteration raises every small one by up to |a| a step: by 485 in five steps of
+ * 3.4445, so that a G of low rank may come out 0.1 off (of |X_0|_F = 1) in 11 bits and 1e-4 in
+ * 22. Operands are float16 with fixed factors: singular values s of X past 4, or |b s^2 + c s^4| past
+ * 64, overflow and give what is not finite (3.4445, -4.7750, 2.0315 stay below 1.3 and 3).
  * out may be G. G and out are 16-byte aligned. Errors: PC_ERR_UNKNOWN_PRECISION,
  * PC_ERR_UNSUPPORTED, PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_ALIGNMENT, PC_ERR_WORKSPACE.
  * Workspace: pc_orthogonalize_workspace bytes, 16-byte aligned. */

@@ -625,7 +625,9 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, out=None):
 def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, precision="auto", out=None):
     """Orthogonalised update of a matrix or a stack of them (pc_orthogonalize): G [..., R,
     C] float32 or bfloat16, contiguous; ``steps`` Newton-Schulz products X <- a X + (b A +
-    c A A) X, A = X X^T, from X = G / (|G|_F + eps). Returns X in G's shape and type."""
+    c A A) X, A = X X^T, from X = G / (|G|_F + eps). Returns X in G's shape and type.
+    Operands have 11 significant bits with "auto" and "tf32", float32 G too: "fp32" (22 bits) for
+    matrices of low rank, whose missing directions rounding fills and the iteration raises."""
     prec = precision_code(precision)
     _elements(G, "G")
     dev = G.device

@@ -8,7 +8,7 @@
 // Memory-bound: x (and dy) are read once and y (dx) written once, about ten flops per
 // element. A row lives in the registers of one warp or one CTA between its load and its
 // store, so the variance is that of the centred values (no cancellation) at no extra
-// traffic. Measured, bf16: forward 32768 x 4096 99 us (5.4 TB/s), gradient 32768 x 1024 38 us on the
+// traffic. Measured, bf16: forward 32768 x 4096 98 us (5.5 TB/s), gradient 32768 x 1024 37 us on the
 // GPU (34 and 5.9 TB/s without the weight's sums). Statistics, sums and the weight's gradients are float32 throughout; the only
 // rounding to bf16 is that of y and dx.
 #include "pc_device.cuh"
@@ -127,9 +127,9 @@ __device__ __forceinline__ void store_piece(T* row, int c, int dim, const float 
 // ------------------------------------------------------------------------ forward
 // kWarps = 1: a warp per row, kRows rows per CTA; kWarps > 1: a CTA per row. A thread
 // holds kVecs 16-byte pieces of its row (piece i at (i * threads + t)). A CTA per row and no
-// loop over rows: CTAs that stay and fetch ahead were slower (32768 rows of 4096 bf16 values:
-// 109 us against 101, of 1024: 34 against 29), and so were more threads per row (128 us with
-// 256 threads, 177 with 512).
+// loop over rows: CTAs that stay and fetch ahead (as below for rows with edges) were slower (32768 rows
+// of 4096 bf16 values: 98.7 us against 96.8, float32 230 against 152; of 1024 bf16: 27.5 against
+// 26.2), and so were more threads per row (128 us with 256 threads, 177 with 512).
 template <class T, int kWarps, int kVecs, int kRows>
 __global__ void __launch_bounds__(32 * kWarps * kRows)
     k_ln_fwd(long long rows, int dim, const T* __restrict__ x, long long x_ld, const float* __restrict__ w,

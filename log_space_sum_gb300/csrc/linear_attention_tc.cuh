@@ -31,8 +31,8 @@
 // elsewhere: the tiles leave the L1 cache next to nothing.
 //
 // A chunk of 128 tokens at head size 128 takes 3.1 us (5800 cycles), 4600 cycles of them MMAs: a
-// gradient of 8 x 2048 tokens, 16 heads, 167 us (384 CTAs in 2.5 waves), 1 x 32771 tokens forward
-// 152 us (DRAM at 5.2 TB/s in the pass itself).
+// gradient of 8 x 2048 tokens, 16 heads, 163 us on the GPU (384 CTAs in 2.5 waves), 1 x 32771 tokens
+// forward 150 us (DRAM at 5.2 TB/s in the pass itself); call after call from Python 167 and 153 to 163.
 //
 // Segments: with fewer (b, h) than SMs a sequence is cut; a first launch (kStates) leaves
 // each segment's own contribution to the state, and each segment of the second adds up the
@@ -604,7 +604,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_la_tc(const __grid_constant__
         };
         if ((!kStates && !wait(&q_full[st], sph)) || !wait(&k_full[st], sph)) break;
         if constexpr (!kStates) {
-          // the score columns hold the last chunk's operands until their products are done
+          // The score columns still hold the last chunk's decayed scores, the operands of O's products
+          // that were issued just now: these scores may be issued behind them because one thread's
+          // MMAs run in the order of their issue. The wait holds the issue back until the last
+          // update has ended; it guards nothing.
           if (n > 0 && !wait(d_full, ph ^ 1)) break;
           if (leader) {
 #pragma unroll

@@ -26,9 +26,9 @@
 // of a small singular value grows by a^2 a step (2e4 over four), so A, B, T and Q are kept in two
 // parts here; X itself is then rounded once in all, and bf16 G not at all.
 //
-// Measured, five steps, bf16: 1024 x 1024 130 us (15 dependent products of 8 us: 2.1 from launch to
-// launch, 2.7 of cluster exchange, 1.0 of products), 1024 x 16384 278 us (14 M x M products in two parts of
-// 12 us, gram 25, last product 50: 1.37 PF/s); float32, 6 of 770 x 333: 161 us.
+// Measured, five steps, bf16: 1024 x 1024 129 us (15 dependent products of 8 us: 2.1 from launch to
+// launch, 2.7 of cluster exchange, 1.0 of products), 1024 x 16384 275 us (14 M x M products in two parts of
+// 12 us, gram 25, last product 49: 1.40 PF/s); float32, 6 of 770 x 333: 162 us.
 #include <cuda_fp16.h>
 
 #include "pc_gemm.cuh"
