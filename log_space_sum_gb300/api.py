@@ -75,8 +75,8 @@ def _stream(device) -> int:
 def workspace(nbytes: int, device) -> torch.Tensor:
     """Scratch buffer of at least nbytes, cached per (host thread, device, stream): the calls
     that share one run one after the other. Two threads' launches on one stream may alternate,
-    so each has its own. A call that is being captured takes one from the graph's own memory,
-    which lasts as long as the graph and is no other call's: a cached one may be replaced
+    so each has its own. A call that is being captured (torch.cuda.graph) takes one from the graph's
+    own memory, which lasts as long as the graph and is no other call's: a cached one may be replaced
     before a replay, and replays are not ordered with the calls of the stream captured on."""
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
