@@ -63,11 +63,17 @@ typedef enum {
 } pc_precision_t;
 
 /* Element type of the activations and matrices of the factor network's operators
- * (layer norm, linear attention, orthogonalised updates). */
+ * (layer norm, attention, orthogonalised updates, ...). */
 typedef enum {
   PC_F32 = 0, /* float32 */
   PC_BF16 = 1 /* bfloat16 */
 } pc_dtype_t;
+
+/* Which features of a head a rotation by position takes as pairs, of R in all. */
+typedef enum {
+  PC_ROTARY_HALF = 0,       /* i and R / 2 + i */
+  PC_ROTARY_INTERLEAVED = 1 /* 2i and 2i + 1 */
+} pc_rotary_t;
 
 typedef enum {
   PC_OK = 0,
@@ -79,7 +85,8 @@ typedef enum {
   PC_ERR_UNSUPPORTED = 6,       /* a valid request outside the library's limits */
   PC_ERR_CUDA = 7,              /* a CUDA call failed (launch or device query) */
   PC_ERR_TIMEOUT = 8,           /* a device-side wait ran out (see pc_device_status) */
-  PC_ERR_RANGE = 9              /* an HMM sample left the exactly-scaled range (see pc_hmm_fwd_bwd) */
+  PC_ERR_RANGE = 9              /* an HMM sample left the exactly-scaled range (see pc_hmm_fwd_bwd), or a
+                                   paged cache's table or slot lay outside it */
 } pc_status_t;
 
 /* Library version string, e.g. "pcsum 0.1 sm_103a". Static storage. */
@@ -99,8 +106,8 @@ PCSUM_API unsigned long long pc_launch_count(void);
 /* Synchronises `stream`, then reads and clears the device status word of the current
  * device. Returns PC_OK; PC_ERR_TIMEOUT if a kernel gave up a bounded wait since the last
  * read; else PC_ERR_RANGE if an HMM call flagged a sample whose values left the range its
- * per-layer scaling keeps exact (that sample's LL is NaN and it passed no flow); or
- * PC_ERR_CUDA. Diagnostic; not for the hot path. */
+ * per-layer scaling keeps exact (that sample's LL is NaN and it passed no flow), or if an
+ * operator of the paged cache passed over a page or slot outside the cache; or PC_ERR_CUDA. Diagnostic; not for the hot path. */
 PCSUM_API pc_status_t pc_device_status(pc_stream_t stream);
 
 /* Limit, in nanoseconds, of the first waits of the tensor-core contraction kernel on the
@@ -528,6 +535,120 @@ PCSUM_API pc_status_t pc_orthogonalize_workspace(int batch, int rows, int cols, 
 PCSUM_API pc_status_t pc_orthogonalize(int batch, int rows, int cols, const void* G, int steps, float a, float b,
                                        float c, float eps, void* out, pc_dtype_t dtype, pc_precision_t prec, void* ws,
                                        size_t ws_bytes, pc_stream_t stream);
+
+/* Norms of queries and keys for each head and their rotation by position, in one pass over
+ * `tokens` tokens of Hq and Hk heads of `dim` features (either number of heads may be 0):
+ *   u = x (avg(x^2) + eps)^(-1/2) weight          norm != 0; weight NULL: 1
+ *   u = x                                         norm == 0 (eps and the weights are not read)
+ *   y_a = amplitude (u_a cos f - u_b sin f), y_b = amplitude (u_b cos f + u_a sin f)
+ *                                                 for pair i of the first `rotary` features, (a, b) by
+ *                                                 `layout`, f = positions[t] frequencies[i]; y = u elsewhere
+ *   q, q_out (elements) [tokens][Hq][dim], k, k_out [tokens][Hk][dim]
+ *   strides (HOST)                (token, head) strides in elements, in the order q, k, q_out, k_out; the
+ *                                 innermost dimension is contiguous; an output's are not 0
+ *   q_weight, k_weight [dim]      float32
+ *   positions [tokens]            int32, any; frequencies [rotary / 2] float32, finite, radians a position
+ * Angles are exact to 2^-32 of a turn at any position. An output may be its own input, at the same
+ * strides. tokens may be 0. Errors: PC_ERR_UNSUPPORTED (element type, layout, dim above 256), PC_ERR_SHAPE
+ * (rotary odd or above dim, ...), PC_ERR_NULL, PC_ERR_ALIGNMENT. */
+PCSUM_API pc_status_t pc_qk_norm_rotary_fwd(long long tokens, int Hq, int Hk, int dim, int rotary, const void* q,
+                                            const void* k, const long long* strides, const float* q_weight,
+                                            const float* k_weight, const int32_t* positions, const float* frequencies,
+                                            float eps, float amplitude, pc_rotary_t layout, int norm, void* q_out,
+                                            void* k_out, pc_dtype_t dtype, pc_stream_t stream);
+
+/* Its gradients from those of its outputs and from its inputs (which are not read without a norm): dq, dk
+ * (elements), dq_weight, dk_weight [dim] float32 (each may be NULL; sums over all rows, of the heads too; with
+ * accumulate != 0 they are added to; not written without a norm).
+ *   strides (HOST)                (token, head), in the order dq_out, dk_out, q, k, dq, dk
+ * The sums are taken in a fixed order: equal inputs give equal bits. dq may be dq_out or q, and dk likewise, at
+ * the same strides. Workspace: pc_qk_norm_rotary_bwd_workspace bytes (0 without a norm), 16-byte aligned. */
+PCSUM_API pc_status_t pc_qk_norm_rotary_bwd_workspace(long long tokens, int Hq, int Hk, int dim, int norm, size_t* bytes);
+
+PCSUM_API pc_status_t pc_qk_norm_rotary_bwd(long long tokens, int Hq, int Hk, int dim, int rotary, const void* dq_out,
+                                            const void* dk_out, const void* q, const void* k, const long long* strides,
+                                            const float* q_weight, const float* k_weight, const int32_t* positions,
+                                            const float* frequencies, float eps, float amplitude, pc_rotary_t layout,
+                                            int norm, void* dq, void* dk, float* dq_weight, float* dk_weight,
+                                            int accumulate, pc_dtype_t dtype, void* ws, size_t ws_bytes,
+                                            pc_stream_t stream);
+
+/* Causal softmax attention over B packed sequences: the tokens starts[b] .. starts[b + 1] - 1 of T
+ * are sequence b (starts [B + 1] int32, ascending from 0; NULL: B sequences of T / B tokens). H heads of
+ * queries read Hk heads of keys and values, H / Hk (a whole number) each:
+ *   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i . k_j - lse_i),  j <= i of the same sequence,
+ *   lse_i = log sum_j exp(scale q_i . k_j)
+ *   q, o (elements) [T][H][D], k, v (elements) [T][Hk][D]
+ *   strides (HOST)                (token, head) strides in elements, in the order q, k, v, o; the innermost
+ *                                 dimension is contiguous; an input's may be 0, an output's not
+ *   lse [H][T] float32            may be NULL; the gradient reads it
+ * Rows of o and lse that belong to no sequence are left as they were, and what the tokens of one sequence
+ * hold never reaches another's outputs. B and T may be 0, and so may a sequence's length. Statistics and sums
+ * are float32. bf16 elements of head sizes that are multiples of 8 up to 128, in 16-byte aligned rows, take the
+ * tensor cores: probabilities are rounded to bf16 there before they meet the values; otherwise all
+ * arithmetic is float32. Equal inputs give equal bits. What is not finite in a value reaches the rows that see it, and may
+ * reach rows up to 127 tokens before it: tiles are multiplied whole.
+ * o may not overlap an input. Errors: PC_ERR_UNSUPPORTED (element type, D above 256, o an input itself), PC_ERR_SHAPE,
+ * PC_ERR_NULL, PC_ERR_ALIGNMENT. */
+PCSUM_API pc_status_t pc_attention_fwd(int B, int T, int H, int Hk, int D, const void* q, const void* k, const void* v,
+                                       const long long* strides, const int32_t* starts, float scale, void* o, float* lse,
+                                       pc_dtype_t dtype, pc_stream_t stream);
+
+/* Its gradients from do, the forward's o and its lse:
+ *   dv_j = sum_i p_ij do_i,  ds_ij = p_ij (do_i . v_j - do_i . o_i),
+ *   dq_i = scale sum_j ds_ij k_j,  dk_j = scale sum_i ds_ij q_i      (sums over a group's heads in dk, dv)
+ *   strides (HOST)                (token, head), in the order q, k, v, o, do, dq, dk, dv
+ * Rows of no sequence are left as they were. dq, dk, dv may overlap neither an input nor one another. No sum is
+ * left to atomics: equal inputs give equal bits. On the tensor cores p and ds are rounded to bf16 before
+ * their products. Workspace: pc_attention_bwd_workspace bytes, 16-byte aligned. */
+PCSUM_API pc_status_t pc_attention_bwd_workspace(int B, int T, int H, int Hk, int D, pc_dtype_t dtype, size_t* bytes);
+
+PCSUM_API pc_status_t pc_attention_bwd(int B, int T, int H, int Hk, int D, const void* q, const void* k, const void* v,
+                                       const void* o, const void* d_o, const long long* strides, const int32_t* starts,
+                                       float scale, const float* lse, void* dq, void* dk, void* dv, pc_dtype_t dtype,
+                                       void* ws, size_t ws_bytes, pc_stream_t stream);
+
+/* Attention of new tokens over a paged cache that holds them already: sequence b has lengths[b] tokens in
+ * all, of which the last starts[b + 1] - starts[b] are the rows of q (starts as above; NULL: T / B each);
+ * the token at position p lies in slot p % page_size of page tables[b][p / page_size] and sees the positions
+ * up to its own. A row before position 0 (more rows than tokens) sees nothing: o = 0, lse = -inf.
+ *   q, o (elements) [T][H][D]
+ *   k_pages, v_pages (elements) [pages][page_size][Hk][D]
+ *   strides (HOST)                q (token, head), k_pages (page, slot, head), v_pages (page, slot, head), o (token, head)
+ *   tables [B][width], lengths [B] int32
+ * Slots behind a sequence's length are not read into any output. A position whose table entry is missing (past
+ * `width`) or outside the pages counts as masked, and PC_ERR_RANGE is left for pc_device_status. Precision and overlap as
+ * above; pages may be shared by sequences. Workspace: pc_paged_attention_workspace bytes (may be 0), 16-byte aligned. */
+PCSUM_API pc_status_t pc_paged_attention_workspace(int B, int T, int H, int Hk, int D, int pages, int page_size, int width,
+                                                   pc_dtype_t dtype, size_t* bytes);
+
+PCSUM_API pc_status_t pc_paged_attention(int B, int T, int H, int Hk, int D, int pages, int page_size, int width,
+                                         const void* q, const void* k_pages, const void* v_pages, const long long* strides,
+                                         const int32_t* tables, const int32_t* lengths, const int32_t* starts, float scale,
+                                         void* o, float* lse, pc_dtype_t dtype, void* ws, size_t ws_bytes,
+                                         pc_stream_t stream);
+
+/* A step's bookkeeping of a paged cache: request b holds cached[b] tokens and adds added[b] (both int32, values
+ * below 0 count as 0). Pages that it lacks are taken from free_list[0 .. free_pages) in the order of the requests.
+ *   tables [B][width]             in and out: entries of pages that a request already holds are kept, those that it takes
+ *                                 are written (-1 where the list has run out)
+ *   starts [B + 1], lengths [B]   running sums of added; cached + added
+ *   positions, slots [tokens]     (int32, int64) of the new tokens, packed by request: slot = page * page_size + place in the
+ *                                 page, or -1: no page, past the table's width, or behind the last request's tokens
+ *   taken [1]                     pages that all requests need, also where that is more than free_pages
+ * B up to 16384. Totals of tokens and pages below 2^31. Errors: PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_UNSUPPORTED. */
+PCSUM_API pc_status_t pc_paged_plan(int B, int width, int page_size, int free_pages, int tokens, const int32_t* cached,
+                                    const int32_t* added, const int32_t* free_list, int32_t* tables, int32_t* starts,
+                                    int32_t* lengths, int32_t* positions, long long* slots, int32_t* taken,
+                                    pc_stream_t stream);
+
+/* Writes the keys and values of `tokens` tokens into the slots of a paged cache; a slot below 0 is passed over, one
+ * past the cache too, with PC_ERR_RANGE left for pc_device_status. Of tokens with one slot any may stay.
+ *   k, v (elements) [tokens][heads][dim]; k_pages, v_pages (elements) [pages][page_size][heads][dim]
+ *   strides (HOST)                k (token, head), v (token, head), k_pages (page, slot, head), v_pages (page, slot, head) */
+PCSUM_API pc_status_t pc_paged_write(long long tokens, int heads, int dim, int pages, int page_size, const void* k,
+                                     const void* v, const long long* strides, const long long* slots, void* k_pages,
+                                     void* v_pages, pc_dtype_t dtype, pc_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -8,6 +8,8 @@ passes PyTorch device memory and streams to it. Build the library with
 from ._native import PCError, declared_symbols, load  # noqa: F401
 from .api import (  # noqa: F401
     PRECISIONS,
+    attention_bwd,
+    attention_fwd,
     device_status,
     em_normalize,
     hclt_fwd_bwd,
@@ -24,8 +26,14 @@ from .api import (  # noqa: F401
     lowrank_sum_exp_bwd,
     lowrank_sum_exp_fwd,
     orthogonalize,
+    paged_attention,
+    paged_plan,
+    paged_write,
     precision_code,
     profile_start,
+    qk_norm_rotary_bwd,
+    qk_norm_rotary_fwd,
+    rotary_frequencies,
     set_wait_limit_ns,
     profile_stop,
     sum_layer_bwd,

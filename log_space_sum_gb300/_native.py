@@ -72,6 +72,17 @@ SIGNATURES = {
                                 _sz, _p],
     "pc_linear_attention_step": [_i, _i, _i, _i, _p, _p, _p, _p, _p, _f, _p, _p, _i, _p],
     "pc_orthogonalize_workspace": [_i, _i, _i, _i, _p],
+    "pc_qk_norm_rotary_fwd": [_ll, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _f, _f, _i, _i, _p, _p, _i, _p],
+    "pc_qk_norm_rotary_bwd_workspace": [_ll, _i, _i, _i, _i, _p],
+    "pc_qk_norm_rotary_bwd": [_ll, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _f, _f, _i, _i, _p, _p, _p, _p, _i,
+                              _i, _p, _sz, _p],
+    "pc_attention_fwd": [_i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _f, _p, _p, _i, _p],
+    "pc_attention_bwd_workspace": [_i, _i, _i, _i, _i, _i, _p],
+    "pc_attention_bwd": [_i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _f, _p, _p, _p, _p, _i, _p, _sz, _p],
+    "pc_paged_attention_workspace": [_i, _i, _i, _i, _i, _i, _i, _i, _i, _p],
+    "pc_paged_attention": [_i, _i, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _f, _p, _p, _i, _p, _sz, _p],
+    "pc_paged_plan": [_i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p],
+    "pc_paged_write": [_ll, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _i, _p],
     "pc_orthogonalize": [_i, _i, _i, _p, _i, _f, _f, _f, _f, _p, _i, _i, _p, _sz, _p],
 }
 _STR = {"pc_version", "pc_status_string", "pc_last_error"}

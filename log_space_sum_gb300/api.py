@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes as C
 import functools
+import math
 import struct
 import threading
 
@@ -620,6 +621,258 @@ def linear_attention_step(q, k, v, log_decay, state, scale=1.0, out=None):
     N.call("pc_linear_attention_step", q.shape[0], H, Dk, Dv, _ptr(q), _ptr(k), _ptr(v), _strides(q, k, v, out),
            _ptr(log_decay), scale, _ptr(state), _ptr(out), DTYPES[dt], _stream(dev))
     return out
+
+
+# Causal softmax attention and what stands around it: the norms and rotation of its queries and keys, its paged
+# cache. Tokens are packed: the leading dimension runs over the tokens of all sequences.
+ROTARY_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _on(device, name, *args):
+    """Calls an entry point with ``device`` current: the library launches on the current one."""
+    if device.index == torch.cuda.current_device():
+        return N.call(name, *args, _stream(device))
+    with torch.cuda.device(device):
+        return N.call(name, *args, _stream(device))
+
+
+def _heads(t, name, dtype=None, device=None):
+    _elements(t, name, dtype, device)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions (tokens, heads, features), got {t.dim()}")
+    return t
+
+
+def _int32(t, name, shape, device):
+    return _shaped(_check(t, name, dtype=torch.int32, device=device), name, shape)
+
+
+def rotary_frequencies(rotary, base=10000.0, factor=1.0, method="linear", original=None, slow=1.0, fast=32.0, device="cuda"):
+    """Frequencies of a rotation by position over ``rotary`` features (float32 [rotary / 2], radians a
+    position: base^(-2i/rotary)) and its amplitude, for contexts ``factor`` times as long as the model was
+    trained on: "linear" divides every frequency by the factor; "base" raises the base so that the
+    slowest pair alone is slowed by it; "bands" slows the pairs that turn less than ``slow`` times over the
+    ``original`` context by the factor, keeps those that turn more than ``fast`` times, goes linearly from one to the
+    other between them, and returns the amplitude 1 + 0.1 log(factor) (the others': 1)."""
+    if rotary < 2 or rotary % 2:
+        raise ValueError(f"rotary must be even and positive, got {rotary}")
+    if factor < 1 or base <= 0:
+        raise ValueError("factor must be at least one and base positive")
+    i = torch.arange(0, rotary, 2, dtype=torch.float64)
+    amplitude = 1.0
+    if method == "base" and rotary > 2:
+        base = base * factor ** (rotary / (rotary - 2))
+    f = base ** (-i / rotary)
+    if method == "linear" or (method == "base" and rotary == 2):
+        f = f / factor
+    elif method == "bands":
+        if original is None or not slow < fast:
+            raise ValueError("bands needs the original context's length and slow < fast")
+        turns = original * f / (2 * math.pi)
+        kept = ((turns - slow) / (fast - slow)).clamp(0, 1)
+        f = f * kept + f / factor * (1 - kept)
+        amplitude = 1 + 0.1 * math.log(factor)
+    elif method != "base":
+        raise ValueError(f"unknown method {method!r}; valid ones are 'linear', 'base' and 'bands'")
+    return f.float().to(device), amplitude
+
+
+def _rotary_inputs(q, k, positions, frequencies, q_weight, k_weight, layout, norm):
+    _heads(q, "q")
+    dev, dt = q.device, q.dtype
+    _heads(k, "k", dt, dev)
+    T, _, D = q.shape
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected ({T}, heads, {D})")
+    if layout not in ROTARY_LAYOUTS:
+        raise ValueError(f"unknown layout {layout!r}; valid ones are 'half' and 'interleaved'")
+    if not norm and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights need norm=True")
+    _param(q_weight, "q_weight", D, dev)
+    _param(k_weight, "k_weight", D, dev)
+    rotary = 0
+    if frequencies is not None:
+        _check(frequencies, "frequencies", device=dev)
+        if frequencies.dim() != 1:
+            raise ValueError("frequencies must have one dimension")
+        rotary = 2 * frequencies.shape[0]
+        if positions is None:
+            raise ValueError("frequencies need positions")
+        _int32(positions, "positions", (T,), dev)
+    return dev, dt, T, D, rotary
+
+
+def qk_norm_rotary_fwd(q, k, positions=None, frequencies=None, q_weight=None, k_weight=None, eps=1e-6, layout="half",
+                       amplitude=1.0, norm=True, q_out=None, k_out=None):
+    """Norms of queries and keys for each head and their rotation by position, in one pass
+    (pc_qk_norm_rotary_fwd): q [T,H,D], k [T,Hk,D] float32 or bfloat16, any strides with the last dimension
+    contiguous; u = x (mean x^2 + eps)^-1/2 weight (weights [D] float32 or None; ``norm`` False: u = x), then the first 2 F
+    features are turned by positions [T] int32 times frequencies [F] float32 (None: no rotation; see
+    rotary_frequencies), times ``amplitude``, as pairs (i, F + i) ("half") or (2i, 2i + 1) ("interleaved").
+    Returns (q_out, k_out), which may be passed in, q and k themselves too."""
+    dev, dt, T, D, rotary = _rotary_inputs(q, k, positions, frequencies, q_weight, k_weight, layout, norm)
+    q_out, k_out = _given(q_out, "q_out", q.shape, dt, dev), _given(k_out, "k_out", k.shape, dt, dev)
+    _on(dev, "pc_qk_norm_rotary_fwd", T, q.shape[1], k.shape[1], D, rotary, _ptr(q), _ptr(k), _strides(q, k, q_out, k_out),
+        _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(frequencies), eps, amplitude, ROTARY_LAYOUTS[layout],
+        int(bool(norm)), _ptr(q_out), _ptr(k_out), DTYPES[dt])
+    return q_out, k_out
+
+
+def qk_norm_rotary_bwd(dq_out, dk_out, q, k, positions=None, frequencies=None, q_weight=None, k_weight=None, eps=1e-6,
+                       layout="half", amplitude=1.0, norm=True, dq=None, dk=None, dq_weight=None, dk_weight=None,
+                       accumulate=False):
+    """Gradients of qk_norm_rotary_fwd (pc_qk_norm_rotary_bwd) from those of its outputs and from its
+    inputs: a dict with dq, dk (in the inputs' type) and dq_weight, dk_weight [D] (float32 sums over tokens and
+    heads, added to the given tensors with ``accumulate``; None without a norm)."""
+    dev, dt, T, D, rotary = _rotary_inputs(q, k, positions, frequencies, q_weight, k_weight, layout, norm)
+    _shaped(_heads(dq_out, "dq_out", dt, dev), "dq_out", q.shape)
+    _shaped(_heads(dk_out, "dk_out", dt, dev), "dk_out", k.shape)
+    if accumulate and norm and (dq_weight is None or dk_weight is None):
+        raise ValueError("accumulate needs dq_weight and dk_weight to add to")
+    dq, dk = _given(dq, "dq", q.shape, dt, dev), _given(dk, "dk", k.shape, dt, dev)
+    ws, nb = None, 0
+    if norm:
+        dq_weight, dk_weight = (torch.empty(D, dtype=torch.float32, device=dev) if t is None else _param(t, n, D, dev)
+                                for t, n in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")))
+        ws = workspace(_query("pc_qk_norm_rotary_bwd_workspace", T, q.shape[1], k.shape[1], D, 1), dev)
+        nb = ws.numel()
+    else:
+        dq_weight = dk_weight = None
+    _on(dev, "pc_qk_norm_rotary_bwd", T, q.shape[1], k.shape[1], D, rotary, _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k),
+        _strides(dq_out, dk_out, q, k, dq, dk), _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(frequencies), eps,
+        amplitude, ROTARY_LAYOUTS[layout], int(bool(norm)), _ptr(dq), _ptr(dk), _ptr(dq_weight), _ptr(dk_weight),
+        int(bool(accumulate)), DTYPES[dt], _ptr(ws), nb)
+    return dict(dq=dq, dk=dk, dq_weight=dq_weight, dk_weight=dk_weight)
+
+
+def _packed_inputs(q, k, v, starts, scale):
+    _heads(q, "q")
+    dev, dt = q.device, q.dtype
+    T, H, D = q.shape
+    _heads(k, "k", dt, dev)
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected ({T}, heads, {D})")
+    _shaped(_heads(v, "v", dt, dev), "v", k.shape)
+    B = 1
+    if starts is not None:
+        _check(starts, "starts", dtype=torch.int32, device=dev)
+        if starts.dim() != 1 or starts.shape[0] < 1:
+            raise ValueError("starts must have one dimension and one element at least")
+        B = starts.shape[0] - 1
+    return dev, dt, B, T, H, k.shape[1], D, (D ** -0.5 if scale is None and D else scale)
+
+
+def attention_fwd(q, k, v, starts=None, scale=None, out=None, lse=None):
+    """Causal softmax attention over packed sequences (pc_attention_fwd): q [T,H,D], k, v [T,Hk,D] float32
+    or bfloat16, any strides with the last dimension contiguous, H a multiple of Hk; ``starts`` [B+1]
+    int32, the sequences' first tokens and their end (None: one sequence); ``scale`` of the scores, D^-1/2 unless given.
+    Returns (o [T,H,D], lse [H,T] float32, the logarithms of the rows' sums, which attention_bwd reads).
+    Rows of no sequence are left as they were in tensors that are passed in."""
+    dev, dt, B, T, H, Hk, D, scale = _packed_inputs(q, k, v, starts, scale)
+    out = _given(out, "out", q.shape, dt, dev)
+    lse = torch.empty(H, T, dtype=torch.float32, device=dev) if lse is None else _shaped(
+        _check(lse, "lse", device=dev), "lse", (H, T))
+    _on(dev, "pc_attention_fwd", B, T, H, Hk, D, _ptr(q), _ptr(k), _ptr(v), _strides(q, k, v, out), _ptr(starts), scale,
+        _ptr(out), _ptr(lse), DTYPES[dt])
+    return out, lse
+
+
+def attention_bwd(q, k, v, o, lse, do, starts=None, scale=None, dq=None, dk=None, dv=None):
+    """Gradients of attention_fwd (pc_attention_bwd) from its outputs o and lse and from ``do`` [T,H,D]: a dict
+    with dq, dk, dv, which may be passed in with any strides (slices of one projection's gradient); they may
+    not overlap an input or one another."""
+    dev, dt, B, T, H, Hk, D, scale = _packed_inputs(q, k, v, starts, scale)
+    _shaped(_heads(o, "o", dt, dev), "o", q.shape)
+    _shaped(_heads(do, "do", dt, dev), "do", q.shape)
+    _shaped(_check(lse, "lse", device=dev), "lse", (H, T))
+    dq, dk, dv = (_given(t, n, like.shape, dt, dev) for t, n, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v)))
+    code = DTYPES[dt]
+    ws = workspace(_query("pc_attention_bwd_workspace", B, T, H, Hk, D, code), dev)
+    _on(dev, "pc_attention_bwd", B, T, H, Hk, D, _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(do),
+        _strides(q, k, v, o, do, dq, dk, dv), _ptr(starts), scale, _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), code, _ptr(ws),
+        ws.numel())
+    return dict(dq=dq, dk=dk, dv=dv)
+
+
+def _pages(k_pages, v_pages, dtype, device):
+    _elements(k_pages, "k_pages", dtype, device)
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages must have 4 dimensions (pages, page size, heads, features), got {k_pages.dim()}")
+    return _shaped(_elements(v_pages, "v_pages", dtype, device), "v_pages", k_pages.shape)
+
+
+def paged_attention(q, k_pages, v_pages, tables, lengths, starts=None, scale=None, out=None, lse=None):
+    """Causal softmax attention of new tokens over a paged cache that holds them already
+    (pc_paged_attention): q [T,H,D], the new tokens packed by ``starts`` [B+1] int32 (None: T / B each);
+    k_pages, v_pages [P,page,Hk,D], any strides with the last dimension contiguous; tables [B,W] int32, lengths [B] int32,
+    the sequences' tokens with the new ones. Returns o [T,H,D]; the rows' log sums go to ``lse`` [H,T] where it
+    is given. A table entry outside the pages counts as masked and is reported by device_status()."""
+    _heads(q, "q")
+    dev, dt = q.device, q.dtype
+    T, H, D = q.shape
+    _pages(k_pages, v_pages, dt, dev)
+    P, page, Hk = k_pages.shape[:3]
+    if k_pages.shape[3] != D:
+        raise ValueError(f"k_pages has head size {k_pages.shape[3]}, expected {D}")
+    _check(lengths, "lengths", dtype=torch.int32, device=dev)
+    if lengths.dim() != 1:
+        raise ValueError("lengths must have one dimension")
+    B = lengths.shape[0]
+    _check(tables, "tables", dtype=torch.int32, device=dev)
+    if tables.dim() != 2 or tables.shape[0] != B:
+        raise ValueError(f"tables has shape {tuple(tables.shape)}, expected ({B}, pages of a sequence)")
+    if starts is not None:
+        _int32(starts, "starts", (B + 1,), dev)
+    out = _given(out, "out", q.shape, dt, dev)
+    if lse is not None:
+        _shaped(_check(lse, "lse", device=dev), "lse", (H, T))
+    code, W = DTYPES[dt], tables.shape[1]
+    ws = workspace(_query("pc_paged_attention_workspace", B, T, H, Hk, D, P, page, W, code), dev)
+    _on(dev, "pc_paged_attention", B, T, H, Hk, D, P, page, W, _ptr(q), _ptr(k_pages), _ptr(v_pages),
+        _strides(q, k_pages, v_pages, out), _ptr(tables), _ptr(lengths), _ptr(starts), D ** -0.5 if scale is None else scale,
+        _ptr(out), _ptr(lse), code, _ptr(ws), ws.numel())
+    return out
+
+
+def paged_plan(cached, added, tables, free, page_size, tokens):
+    """A step's bookkeeping of a paged cache (pc_paged_plan): requests that hold ``cached`` [B] tokens and add
+    ``added`` [B] (int32) take the pages that they lack from ``free`` [F] int32, in order; their entries are
+    written into ``tables`` [B,W] int32. Returns a dict with starts [B+1], lengths [B], positions
+    [tokens] (int32), slots [tokens] (int64, -1 where a token has no place) and taken [1] int32, the pages that
+    were needed: more than F where ``free`` was too short. ``tokens`` is the sum of ``added``, which the host knows."""
+    _check(cached, "cached", dtype=torch.int32)
+    dev = cached.device
+    if cached.dim() != 1:
+        raise ValueError("cached must have one dimension")
+    B = cached.shape[0]
+    _int32(added, "added", (B,), dev)
+    _check(tables, "tables", dtype=torch.int32, device=dev)
+    if tables.dim() != 2 or tables.shape[0] != B:
+        raise ValueError(f"tables has shape {tuple(tables.shape)}, expected ({B}, pages of a request)")
+    _check(free, "free", dtype=torch.int32, device=dev)
+    if free.dim() != 1:
+        raise ValueError("free must have one dimension")
+    new = lambda *shape, dtype=torch.int32: torch.empty(*shape, dtype=dtype, device=dev)  # noqa: E731
+    starts, lengths, positions, taken = new(B + 1), new(B), new(tokens), new(1)
+    slots = new(tokens, dtype=torch.int64)
+    _on(dev, "pc_paged_plan", B, tables.shape[1], page_size, free.shape[0], tokens, _ptr(cached), _ptr(added), _ptr(free),
+        _ptr(tables), _ptr(starts), _ptr(lengths), _ptr(positions), _ptr(slots), _ptr(taken))
+    return dict(starts=starts, lengths=lengths, positions=positions, slots=slots, taken=taken)
+
+
+def paged_write(k, v, k_pages, v_pages, slots):
+    """Writes keys and values [T,Hk,D] into the slots [T] int64 of a paged cache k_pages, v_pages [P,page,Hk,D]
+    (pc_paged_write); a slot of -1 is passed over."""
+    _heads(k, "k")
+    dev, dt = k.device, k.dtype
+    T, Hk, D = k.shape
+    _shaped(_heads(v, "v", dt, dev), "v", k.shape)
+    _pages(k_pages, v_pages, dt, dev)
+    P, page = k_pages.shape[:2]
+    _shaped(k_pages, "k_pages", (P, page, Hk, D))
+    _shaped(_check(slots, "slots", dtype=torch.int64, device=dev), "slots", (T,))
+    _on(dev, "pc_paged_write", T, Hk, D, P, page, _ptr(k), _ptr(v), _strides(k, v, k_pages, v_pages), _ptr(slots),
+        _ptr(k_pages), _ptr(v_pages), DTYPES[dt])
 
 
 def orthogonalize(G, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7, precision="auto", out=None):

@@ -256,6 +256,8 @@ pc_status_t pc_device_status(pc_stream_t stream) {
     PC_CUDA(cudaMemcpy(word, &zero, sizeof(zero), cudaMemcpyHostToDevice));
     if (v & pc::kErrTimeoutBits)
       return pc::set_error(PC_ERR_TIMEOUT, "a kernel gave up a bounded wait (status bits 0x%x)", v);
+    if (!(v & pc::kErrRange))
+      return pc::set_error(PC_ERR_RANGE, "a page or slot outside the paged cache was passed over (status bits 0x%x)", v);
     return pc::set_error(PC_ERR_RANGE,
                          "an HMM sample left the range its per-layer scaling keeps exact: its ll is NaN and it "
                          "passed no flow (status bits 0x%x)", v);

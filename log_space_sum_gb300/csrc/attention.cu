@@ -1,0 +1,382 @@
+// Causal softmax attention: packed prompts (forward and gradient) and new tokens over a paged cache.
+//
+//   s_ij = scale q_i . k_j over the keys j that row i sees, p = softmax(s), o_i = sum_j p_ij v_j,
+//   lse_i = log sum_j exp(s_ij)
+//   delta_i = do_i . o_i,  ds = p (do v^T - delta),  dq = scale ds k,  dk = scale ds^T q,  dv = p^T do
+//
+// One pass over the keys with each row's running maximum and sum: neither scores nor probabilities are
+// stored. The gradient forms the probabilities again from lse, in two kernels (dk and dv by tiles of keys,
+// dq by tiles of rows): seven products instead of five, but no sum is left to atomics, whose order
+// would change the bits, and the heads of a group add up in the tile of their keys.
+#include <climits>
+
+#include "attention_simt.cuh"
+#include "pc_host.h"
+
+namespace pc {
+namespace {
+
+constexpr int kMaxHeadDim = 256;
+constexpr int kMaxSplits = 64;
+
+// Joins the ranges' outputs: a warp a row. Rows of no sequence are left as they were.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_join(const __grid_constant__ AttnArgs a) {
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5), rows = static_cast<long long>(a.T) * a.H;
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const int t = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H);
+  if (a.starts && (t < a.starts[0] || t >= a.starts[a.B])) return;
+  float m[kMaxSplits / 32], l[kMaxSplits / 32], top = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 32; ++i) {
+    const int s = lane + 32 * i;
+    const float2 v = s < a.splits ? a.part_ml[s * rows + row] : make_float2(-INFINITY, 0.f);
+    m[i] = v.x;
+    l[i] = v.y;
+    top = fmaxf(top, v.x);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxSplits / 32; ++i) {
+    l[i] = l[i] == 0.f ? 0.f : l[i] * exp2f(m[i] - base);
+    sum += l[i];
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const float by = sum == 0.f ? 0.f : 1.f / sum;
+  T* o = static_cast<T*>(a.o) + t * a.os[0] + h * a.os[1];
+  float acc[kMaxHeadDim / 32] = {};
+  for (int s = 0; s < a.splits; ++s) {
+    float w = 0.f;
+#pragma unroll
+    for (int i = 0; i < kMaxSplits / 32; ++i)
+      if (s / 32 == i) w = __shfl_sync(0xffffffffu, l[i], s & 31);
+    if (w == 0.f) continue;  // (uniform)
+    const float* p = a.part_o + (s * rows + row) * a.D;
+#pragma unroll
+    for (int i = 0; i < kMaxHeadDim / 32; ++i)
+      if (lane + 32 * i < a.D) acc[i] += w * p[lane + 32 * i];
+  }
+#pragma unroll
+  for (int i = 0; i < kMaxHeadDim / 32; ++i)
+    if (lane + 32 * i < a.D) attn_store(o + lane + 32 * i, acc[i] * by);
+  if (a.lse && lane == 0) a.lse[static_cast<long long>(h) * a.T + t] = (top + log2f(sum)) * kLn2;
+}
+
+// Heads of a row tile: the largest divisor of the group up to 16.
+int pack_of(int group) {
+  int p = group < 16 ? group : 16;
+  while (group % p) --p;
+  return p;
+}
+
+// Tiles of `per` tokens that all sequences have at most.
+long long tiles_of(const AttnArgs& a, int per) {
+  if (!a.starts) return static_cast<long long>(a.B) * ((a.T / a.B + per - 1) / per);
+  return a.T / per + (a.B < a.T ? a.B : a.T);
+}
+
+constexpr int simt_dim(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+constexpr int simt_bt(int DP) { return DP == 256 ? 32 : 64; }
+
+// Ranges of the keys on the CUDA cores: enough CTAs for two on each SM, none with fewer than four tiles.
+int simt_splits(const AttnArgs& a) {
+  if (!a.page) return 1;
+  const int bt = simt_bt(simt_dim(a.D));
+  const long long ctas = tiles_of(a, bt / a.pack) * (a.H / a.pack);
+  const long long most = static_cast<long long>(a.width) * a.page / (4 * bt), want = 2ll * num_sms() / (ctas ? ctas : 1);
+  long long s = want < most ? want : most;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+size_t part_bytes(const AttnArgs& a, int splits) {
+  return splits <= 1 ? 0 : static_cast<size_t>(splits) * a.T * a.H * (a.D + 2) * sizeof(float) + 256;
+}
+
+void carve_parts(AttnArgs& a, int splits, void* ws) {
+  a.splits = splits;
+  if (splits <= 1) return;
+  Carver c(ws);
+  a.part_ml = static_cast<float2*>(c.take(static_cast<size_t>(splits) * a.T * a.H * sizeof(float2)));
+  a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(splits) * a.T * a.H);
+}
+
+template <class T, int DP>
+pc_status_t launch_simt_dim(const AttnArgs& a, cudaStream_t s) {
+  constexpr int BT = simt_bt(DP);
+  using S = SimtTile<DP, BT>;
+  constexpr int smem = (3 * S::kRows + S::kScores) * 4;
+  const long long tiles = tiles_of(a, BT / a.pack);
+  PC_CHECK(tiles < INT_MAX, PC_ERR_SHAPE, "%lld tiles of rows: fewer than 2^31 wanted", tiles);
+  PC_TRY((allow_smem<k_attn_simt<T, DP, BT>>(smem)));
+  k_attn_simt<T, DP, BT><<<dim3(static_cast<unsigned>(tiles), a.H / a.pack, a.splits), kSimtThreads, smem, s>>>(a);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+template <class T>
+pc_status_t launch_join(const AttnArgs& a, cudaStream_t s) {
+  const long long ctas = (static_cast<long long>(a.T) * a.H + 7) / 8;
+  PC_CHECK(ctas < INT_MAX, PC_ERR_SHAPE, "T * H = %lld rows: fewer than 2^34 wanted", static_cast<long long>(a.T) * a.H);
+  k_attn_join<T><<<static_cast<unsigned>(ctas), 256, 0, s>>>(a);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+template <class T>
+pc_status_t launch_simt(AttnArgs& a, void* ws, cudaStream_t s, int* launches) {
+  carve_parts(a, simt_splits(a), ws);
+  const int dp = simt_dim(a.D);
+  PC_TRY((dp == 64 ? launch_simt_dim<T, 64>(a, s) : dp == 128 ? launch_simt_dim<T, 128>(a, s) : launch_simt_dim<T, 256>(a, s)));
+  ++*launches;
+  if (a.splits > 1) {
+    PC_TRY(launch_join<T>(a, s));
+    ++*launches;
+  }
+  return PC_OK;
+}
+
+template <class T, int DP>
+pc_status_t launch_simt_bwd_dim(const AttnBwdArgs& b, cudaStream_t s) {
+  const AttnArgs& a = b.a;
+  constexpr int BT = simt_bt(DP);
+  using S = SimtTile<DP, BT>;
+  constexpr int smem = (4 * S::kRows + 2 * S::kScores) * 4, smem_dq = (4 * S::kRows + S::kScores) * 4;
+  const long long keys = tiles_of(a, BT), rows = tiles_of(a, BT / a.pack);
+  PC_CHECK(keys < INT_MAX && rows < INT_MAX, PC_ERR_SHAPE, "%lld tiles of rows: fewer than 2^31 wanted", rows);
+  PC_TRY((allow_smem<k_attn_simt_dkdv<T, DP, BT>>(smem)));
+  PC_TRY((allow_smem<k_attn_simt_dq<T, DP, BT>>(smem_dq)));
+  k_attn_simt_dkdv<T, DP, BT><<<dim3(static_cast<unsigned>(keys), a.Hk), kSimtThreads, smem, s>>>(b);
+  PC_LAUNCH_CHECK();
+  k_attn_simt_dq<T, DP, BT><<<dim3(static_cast<unsigned>(rows), a.H / a.pack), kSimtThreads, smem_dq, s>>>(b);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+template <class T>
+pc_status_t launch_bwd(const AttnBwdArgs& b, cudaStream_t s, int* launches) {
+  const AttnArgs& a = b.a;
+  const long long ctas = (static_cast<long long>(a.T) * a.H + 7) / 8;
+  PC_CHECK(ctas < INT_MAX, PC_ERR_SHAPE, "T * H = %lld rows: fewer than 2^34 wanted", static_cast<long long>(a.T) * a.H);
+  k_attn_delta<T><<<static_cast<unsigned>(ctas), 256, 0, s>>>(b);
+  PC_LAUNCH_CHECK();
+  *launches += 3;
+  const int dp = simt_dim(a.D);
+  return dp == 64    ? launch_simt_bwd_dim<T, 64>(b, s)
+         : dp == 128 ? launch_simt_bwd_dim<T, 128>(b, s)
+                     : launch_simt_bwd_dim<T, 256>(b, s);
+}
+
+// ------------------------------------------------------------------------- checks
+pc_status_t check_attn(int B, int T, int H, int Hk, int D, pc_dtype_t dt) {
+  PC_TRY(check_dtype(dt));
+  PC_CHECK(B >= 0 && T >= 0 && B < (1 << 30) && T < (1 << 30), PC_ERR_SHAPE, "B and T must be in [0, 2^30) (got %d, %d)", B, T);
+  PC_CHECK(H >= 1 && Hk >= 1 && H % Hk == 0 && H <= 65535, PC_ERR_SHAPE,
+           "heads must be in [1, 65535] and a multiple of the keys' heads (got %d, %d)", H, Hk);
+  PC_CHECK(D >= 1, PC_ERR_SHAPE, "head size must be >= 1 (got %d)", D);
+  PC_CHECK(D <= kMaxHeadDim, PC_ERR_UNSUPPORTED, "head sizes up to %d (got %d)", kMaxHeadDim, D);
+  return PC_OK;
+}
+
+pc_status_t check_tensor(const char* name, const void* p, pc_dtype_t dt) {
+  PC_CHECK(p, PC_ERR_NULL, "%s must not be NULL", name);
+  PC_CHECK(reinterpret_cast<uintptr_t>(p) % dtype_bytes(dt) == 0, PC_ERR_ALIGNMENT, "%s is not aligned to its type", name);
+  return PC_OK;
+}
+
+// An output's elements may not share memory.
+pc_status_t check_out(const char* name, const long long* strides, int tokens, int heads) {
+  PC_CHECK((tokens <= 1 || strides[0] != 0) && (heads <= 1 || strides[1] != 0), PC_ERR_SHAPE, "%s: stride 0", name);
+  return PC_OK;
+}
+
+pc_status_t check_even(int B, int T, const int32_t* starts) {
+  PC_CHECK(starts || (B > 0 && T % B == 0), PC_ERR_SHAPE, "without starts, T = %d must be a multiple of B = %d", T, B);
+  return PC_OK;
+}
+
+AttnArgs make_args(int B, int T, int H, int Hk, int D, float scale, const int32_t* starts) {
+  AttnArgs a{};
+  a.B = B;
+  a.T = T;
+  a.H = H;
+  a.Hk = Hk;
+  a.group = H / Hk;
+  a.pack = pack_of(a.group);
+  a.D = D;
+  a.scale = scale;
+  a.starts = starts;
+  a.splits = 1;
+  return a;
+}
+
+// The planners look at sizes alone; a workspace is sized for sequences of any lengths.
+const int32_t* some_starts() { return reinterpret_cast<const int32_t*>(uintptr_t(4)); }
+
+size_t paged_bytes(const AttnArgs& a) { return part_bytes(a, simt_splits(a)); }
+
+}  // namespace
+}  // namespace pc
+
+extern "C" {
+
+pc_status_t pc_attention_bwd_workspace(int B, int T, int H, int Hk, int D, pc_dtype_t dtype, size_t* bytes) {
+  pc::clear_error();
+  PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
+  PC_TRY(pc::check_attn(B, T, H, Hk, D, dtype));
+  *bytes = static_cast<size_t>(T) * H * sizeof(float);
+  return PC_OK;
+}
+
+pc_status_t pc_attention_fwd(int B, int T, int H, int Hk, int D, const void* q, const void* k, const void* v,
+                             const long long* strides, const int32_t* starts, float scale, void* o, float* lse,
+                             pc_dtype_t dtype, cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_attn(B, T, H, Hk, D, dtype));
+  if (B == 0 || T == 0) return PC_OK;
+  PC_CHECK(strides, PC_ERR_NULL, "strides must not be NULL");
+  PC_TRY(pc::check_even(B, T, starts));
+  const char* names[4] = {"q", "k", "v", "o"};
+  const void* all[4] = {q, k, v, o};
+  for (int i = 0; i < 4; ++i) PC_TRY(pc::check_tensor(names[i], all[i], dtype));
+  for (int i = 0; i < 3; ++i) PC_CHECK(o != all[i], PC_ERR_UNSUPPORTED, "o may not be %s itself", names[i]);
+  PC_TRY(pc::check_out("o", strides + 6, T, H));
+  pc::AttnArgs a = pc::make_args(B, T, H, Hk, D, scale, starts);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  for (int i = 0; i < 2; ++i) {
+    a.qs[i] = strides[i];
+    a.ks[1 + i] = strides[2 + i];
+    a.vs[1 + i] = strides[4 + i];
+    a.os[i] = strides[6 + i];
+  }
+  a.status = pc::device_status_word();
+  int launches = 0;
+  return dtype == PC_BF16 ? pc::launch_simt<__nv_bfloat16>(a, nullptr, stream, &launches)
+                          : pc::launch_simt<float>(a, nullptr, stream, &launches);
+}
+
+pc_status_t pc_attention_bwd(int B, int T, int H, int Hk, int D, const void* q, const void* k, const void* v, const void* o,
+                             const void* d_o, const long long* strides, const int32_t* starts, float scale, const float* lse,
+                             void* dq, void* dk, void* dv, pc_dtype_t dtype, void* ws, size_t ws_bytes,
+                             cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_attn(B, T, H, Hk, D, dtype));
+  if (B == 0 || T == 0) return PC_OK;
+  PC_CHECK(strides && lse, PC_ERR_NULL, "strides and lse must not be NULL");
+  PC_TRY(pc::check_even(B, T, starts));
+  const char* names[8] = {"q", "k", "v", "o", "do", "dq", "dk", "dv"};
+  const void* all[8] = {q, k, v, o, d_o, dq, dk, dv};
+  for (int i = 0; i < 8; ++i) PC_TRY(pc::check_tensor(names[i], all[i], dtype));
+  for (int i = 5; i < 8; ++i)
+    for (int j = 0; j < i; ++j) PC_CHECK(all[i] != all[j], PC_ERR_UNSUPPORTED, "%s may not be %s itself", names[i], names[j]);
+  for (int i = 5; i < 8; ++i) PC_TRY(pc::check_out(names[i], strides + 2 * i, T, i == 5 ? H : Hk));
+  const size_t need = static_cast<size_t>(T) * H * sizeof(float);
+  PC_CHECK(ws && ws_bytes >= need, PC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  PC_CHECK(pc::aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  pc::AttnBwdArgs b{};
+  b.a = pc::make_args(B, T, H, Hk, D, scale, starts);
+  b.a.q = q;
+  b.a.k = k;
+  b.a.v = v;
+  b.a.o = const_cast<void*>(o);
+  b.a.status = pc::device_status_word();
+  b.d_o = d_o;
+  b.lse = lse;
+  b.delta = static_cast<float*>(ws);
+  b.dq = dq;
+  b.dk = dk;
+  b.dv = dv;
+  for (int i = 0; i < 2; ++i) {
+    b.a.qs[i] = strides[i];
+    b.a.ks[1 + i] = strides[2 + i];
+    b.a.vs[1 + i] = strides[4 + i];
+    b.a.os[i] = strides[6 + i];
+    b.gs[i] = strides[8 + i];
+    b.dqs[i] = strides[10 + i];
+    b.dks[i] = strides[12 + i];
+    b.dvs[i] = strides[14 + i];
+  }
+  int launches = 0;
+  return dtype == PC_BF16 ? pc::launch_bwd<__nv_bfloat16>(b, stream, &launches) : pc::launch_bwd<float>(b, stream, &launches);
+}
+
+pc_status_t pc_paged_attention_workspace(int B, int T, int H, int Hk, int D, int pages, int page_size, int width,
+                                         pc_dtype_t dtype, size_t* bytes) {
+  pc::clear_error();
+  PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
+  PC_TRY(pc::check_attn(B, T, H, Hk, D, dtype));
+  PC_CHECK(pages >= 0 && page_size >= 1 && width >= 0 && static_cast<long long>(width) * page_size < (1ll << 30), PC_ERR_SHAPE,
+           "pages, width >= 0, page_size >= 1 and width * page_size < 2^30 wanted (got %d, %d, %d)", pages, width, page_size);
+  *bytes = 0;
+  if (B == 0 || T == 0) return PC_OK;
+  for (int even = 0; even < 2; ++even) {
+    if (even && T % B) continue;
+    pc::AttnArgs a = pc::make_args(B, T, H, Hk, D, 1.f, even ? nullptr : pc::some_starts());
+    a.page = page_size;
+    a.width = width;
+    a.pages = pages;
+    const size_t n = pc::paged_bytes(a);
+    if (n > *bytes) *bytes = n;
+  }
+  return PC_OK;
+}
+
+pc_status_t pc_paged_attention(int B, int T, int H, int Hk, int D, int pages, int page_size, int width, const void* q,
+                               const void* k_pages, const void* v_pages, const long long* strides, const int32_t* tables,
+                               const int32_t* lengths, const int32_t* starts, float scale, void* o, float* lse,
+                               pc_dtype_t dtype, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_attn(B, T, H, Hk, D, dtype));
+  PC_CHECK(pages >= 0 && page_size >= 1 && width >= 0 && static_cast<long long>(width) * page_size < (1ll << 30), PC_ERR_SHAPE,
+           "pages, width >= 0, page_size >= 1 and width * page_size < 2^30 wanted (got %d, %d, %d)", pages, width, page_size);
+  if (B == 0 || T == 0) return PC_OK;
+  PC_CHECK(strides && lengths, PC_ERR_NULL, "strides and lengths must not be NULL");
+  PC_CHECK(width == 0 || tables, PC_ERR_NULL, "tables must not be NULL");
+  PC_TRY(pc::check_even(B, T, starts));
+  PC_TRY(pc::check_tensor("q", q, dtype));
+  PC_TRY(pc::check_tensor("o", o, dtype));
+  if (pages > 0) {
+    PC_TRY(pc::check_tensor("k_pages", k_pages, dtype));
+    PC_TRY(pc::check_tensor("v_pages", v_pages, dtype));
+  }
+  PC_CHECK(o != q && o != k_pages && o != v_pages, PC_ERR_UNSUPPORTED, "o may not be an input itself");
+  PC_TRY(pc::check_out("o", strides + 8, T, H));
+  pc::AttnArgs a = pc::make_args(B, T, H, Hk, D, scale, starts);
+  a.q = q;
+  a.k = k_pages;
+  a.v = v_pages;
+  a.o = o;
+  a.lse = lse;
+  for (int i = 0; i < 2; ++i) {
+    a.qs[i] = strides[i];
+    a.os[i] = strides[8 + i];
+  }
+  for (int i = 0; i < 3; ++i) {
+    a.ks[i] = strides[2 + i];
+    a.vs[i] = strides[5 + i];
+  }
+  a.tables = tables;
+  a.lengths = lengths;
+  a.page = page_size;
+  a.pages = pages;
+  a.width = width;
+  const size_t need = pc::paged_bytes(a);
+  PC_CHECK(need == 0 || (ws && ws_bytes >= need), PC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  PC_CHECK(need == 0 || pc::aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  a.status = pc::device_status_word();
+  PC_CHECK(a.status, PC_ERR_CUDA, "device status word unavailable");
+  int launches = 0;
+  return dtype == PC_BF16 ? pc::launch_simt<__nv_bfloat16>(a, ws, stream, &launches)
+                          : pc::launch_simt<float>(a, ws, stream, &launches);
+}
+
+}  // extern "C"

@@ -1,0 +1,103 @@
+// What the kernels of softmax attention share: their arguments, where sequences, rows and cached
+// tokens lie.
+//
+// Rows. The heads of a group read the same keys: a kernel's row is one token and one of `pack` heads
+// of a group, row r of a tile being token r / pack and head r % pack, so that a tile of keys and values
+// is read once for all of them and a single token fills more of a tile. pack is the largest divisor of
+// the group up to 16.
+#pragma once
+
+#include "pc_device.cuh"
+
+namespace pc {
+
+struct AttnArgs {
+  const void *q, *k, *v;
+  void* o;
+  long long qs[2], os[2];  // (token, head) strides
+  long long ks[3], vs[3];  // packed: (-, token, head); paged: (page, slot, head)
+  const int32_t* starts;   // [B + 1]; NULL: the tokens are split evenly over the sequences
+  const int32_t* lengths;  // paged: [B], tokens of each sequence with the new ones
+  const int32_t* tables;   // paged: [B][width]
+  int B, T, H, Hk, group, pack, D;
+  int width, page, pages;  // paged, else page = 0
+  float scale;
+  float* lse;              // [H][T], may be NULL
+  // keys cut into `splits` ranges: each leaves its own normalised output, the rows' running maxima (log2) and sums
+  int splits;
+  float* part_o;           // [splits][T * H][D]
+  float2* part_ml;         // [splits][T * H]
+  unsigned* status;
+};
+
+// Tokens of a sequence: rows [start, start + n) of q and o; keys 0 .. ctx - 1; the token i sees the
+// keys 0 .. ctx - n + i. Values outside what the tensors hold are taken to their ends.
+struct AttnSeq {
+  int start, n, ctx;
+};
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int b) {
+  AttnSeq s;
+  if (a.starts) {
+    s.start = min(max(a.starts[b], 0), a.T);
+    s.n = min(max(a.starts[b + 1], s.start), a.T) - s.start;
+  } else {
+    s.n = a.T / a.B;
+    s.start = b * s.n;
+  }
+  s.ctx = a.page ? max(a.lengths[b], 0) : s.n;
+  return s;
+}
+
+// The tile `tile` of `per` tokens out of all sequences' tiles, one sequence after the other: its sequence and
+// place, or b = -1 past the last. The whole warp takes part.
+struct AttnTile {
+  int b, at;
+};
+__device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, int tile, int per) {
+  const int lane = threadIdx.x & 31;
+  if (!a.starts) {
+    const int each = (a.T / a.B + per - 1) / per;
+    if (each == 0 || tile >= a.B * each) return {-1, 0};
+    return {tile / each, tile % each};
+  }
+  int base = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const int b = b0 + lane;
+    int n = 0;
+    if (b < a.B) n = (attn_seq(a, b).n + per - 1) / per;
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, d);
+      if (lane >= d) sum += x;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, base + sum > tile);
+    if (here) {
+      const int l = __ffs(here) - 1;
+      return {b0 + l, tile - base - __shfl_sync(0xffffffffu, sum - n, l)};
+    }
+    base += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return {-1, 0};
+}
+
+// Row of cached token j of sequence b in the pages, or -1 where the table has no page for it (flagged).
+__device__ __forceinline__ long long paged_row(const AttnArgs& a, int b, int j, const long long* strides) {
+  const int col = j / a.page;
+  int id = -1;
+  if (col < a.width) id = a.tables[static_cast<long long>(b) * a.width + col];
+  if (id < 0 || id >= a.pages) {
+    atomicOr(a.status, kErrPage);
+    return -1;
+  }
+  return id * strides[0] + (j - col * a.page) * strides[1];
+}
+
+__device__ __forceinline__ float attn_load(const float* p) { return *p; }
+__device__ __forceinline__ float attn_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void attn_store(float* p, float v) { *p = v; }
+__device__ __forceinline__ void attn_store(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.69314718055994531f;
+
+}  // namespace pc

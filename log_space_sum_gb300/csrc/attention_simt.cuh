@@ -1,0 +1,429 @@
+// Softmax attention on the CUDA cores: float32 elements, and whatever the tensor-core kernels do not
+// take (head sizes, strides and alignments of their own). Tiles of BT rows by BT keys in shared memory as
+// float32, 256 threads, each an M x M block of the scores (M = BT / 16): row ty M + i, key tx + 16 j, so
+// that one half-warp holds whole rows and the softmax needs shuffles only. Products and statistics are
+// float32 throughout.
+#pragma once
+
+#include "attention.cuh"
+
+namespace pc {
+
+constexpr int kSimtThreads = 256;
+
+template <int DP, int BT>
+struct SimtTile {
+  static constexpr int M = BT / 16, C = DP / 64, Ld = DP + 4, Lp = BT + 4;
+  static constexpr int kRows = BT * Ld, kScores = BT * Lp;  // floats
+};
+
+// BT rows of D elements (zeros behind D); row(r) is its first element's address or NULL for zeros.
+template <class T, int DP, int BT, class F>
+__device__ __forceinline__ void simt_load(float* dst, int D, F row) {
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < BT; r += kSimtThreads / 32) {
+    const T* p = row(r);
+#pragma unroll
+    for (int d = lane; d < DP; d += 32) dst[r * (DP + 4) + d] = p && d < D ? attn_load(p + d) : 0.f;
+  }
+}
+
+// acc[i][j] = A[ty M + i] . B[tx + 16 j]
+template <int DP, int BT>
+__device__ __forceinline__ void simt_dot(const float* A, const float* B, float (&acc)[BT / 16][BT / 16]) {
+  using S = SimtTile<DP, BT>;
+  constexpr int M = S::M;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+#pragma unroll
+    for (int j = 0; j < M; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < DP; d += 4) {
+    float4 x[M], y[M];
+#pragma unroll
+    for (int i = 0; i < M; ++i) x[i] = *reinterpret_cast<const float4*>(A + (ty * M + i) * S::Ld + d);
+#pragma unroll
+    for (int j = 0; j < M; ++j) y[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * S::Ld + d);
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int j = 0; j < M; ++j) {
+        acc[i][j] += x[i].x * y[j].x;
+        acc[i][j] += x[i].y * y[j].y;
+        acc[i][j] += x[i].z * y[j].z;
+        acc[i][j] += x[i].w * y[j].w;
+      }
+  }
+}
+
+// acc[i][c] += sum_j P[ty M + i][j] X[j][tx 4 + 64 c ..]
+template <int DP, int BT>
+__device__ __forceinline__ void simt_rows(const float* P, const float* X, float (&acc)[BT / 16][DP / 64][4]) {
+  using S = SimtTile<DP, BT>;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll 2
+  for (int j = 0; j < BT; j += 4) {
+    float p[S::M][4];
+#pragma unroll
+    for (int i = 0; i < S::M; ++i) {
+      const float4 v = *reinterpret_cast<const float4*>(P + (ty * S::M + i) * S::Lp + j);
+      p[i][0] = v.x, p[i][1] = v.y, p[i][2] = v.z, p[i][3] = v.w;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int c = 0; c < S::C; ++c) {
+        const float4 x = *reinterpret_cast<const float4*>(X + (j + e) * S::Ld + tx * 4 + 64 * c);
+#pragma unroll
+        for (int i = 0; i < S::M; ++i) {
+          acc[i][c][0] += p[i][e] * x.x;
+          acc[i][c][1] += p[i][e] * x.y;
+          acc[i][c][2] += p[i][e] * x.z;
+          acc[i][c][3] += p[i][e] * x.w;
+        }
+      }
+  }
+}
+
+// acc[i][c] += sum_r P[r][ty M + i] X[r][tx 4 + 64 c ..]
+template <int DP, int BT>
+__device__ __forceinline__ void simt_cols(const float* P, const float* X, float (&acc)[BT / 16][DP / 64][4]) {
+  using S = SimtTile<DP, BT>;
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll 4
+  for (int r = 0; r < BT; ++r) {
+    float p[S::M];
+#pragma unroll
+    for (int i = 0; i < S::M; ++i) p[i] = P[r * S::Lp + ty * S::M + i];
+#pragma unroll
+    for (int c = 0; c < S::C; ++c) {
+      const float4 x = *reinterpret_cast<const float4*>(X + r * S::Ld + tx * 4 + 64 * c);
+#pragma unroll
+      for (int i = 0; i < S::M; ++i) {
+        acc[i][c][0] += p[i] * x.x;
+        acc[i][c][1] += p[i] * x.y;
+        acc[i][c][2] += p[i] * x.z;
+        acc[i][c][3] += p[i] * x.w;
+      }
+    }
+  }
+}
+
+template <int N, int C>
+__device__ __forceinline__ void simt_zero(float (&acc)[N][C][4]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[i][c][e] = 0.f;
+}
+
+template <class T, int DP>
+__device__ __forceinline__ void simt_store(T* row, int D, const float (&acc)[DP / 64][4], float by) {
+  const int tx = threadIdx.x & 15;
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int d = tx * 4 + 64 * c + e;
+      if (d < D) attn_store(row + d, acc[c][e] * by);
+    }
+}
+
+// Sum and maximum over the 16 lanes that hold a row.
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+__device__ __forceinline__ float row_max(float v) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+// Forward: one tile of rows against the keys of one split, with the running maximum and sum of a softmax.
+template <class T, int DP, int BT>
+__global__ void __launch_bounds__(kSimtThreads) k_attn_simt(const __grid_constant__ AttnArgs a) {
+  using S = SimtTile<DP, BT>;
+  constexpr int M = S::M;
+  extern __shared__ float simt_smem[];
+  float *Q = simt_smem, *K = Q + S::kRows, *V = K + S::kRows, *P = V + S::kRows;
+  const int per = BT / a.pack, hp = blockIdx.y, hk = hp * a.pack / a.group, split = blockIdx.z;
+  const AttnTile tile = attn_tile(a, blockIdx.x, per);
+  if (tile.b < 0) return;
+  const AttnSeq s = attn_seq(a, tile.b);
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int t0 = tile.at * per, before = s.ctx - s.n;  // the tile's tokens, keys before the sequence's rows
+  auto token = [&](int r) { return t0 + r / a.pack; };
+  auto there = [&](int r) { return r < per * a.pack && token(r) < s.n; };
+  simt_load<T, DP, BT>(Q, a.D, [&](int r) -> const T* {
+    return there(r) ? static_cast<const T*>(a.q) + (s.start + token(r)) * a.qs[0] + (hp * a.pack + r % a.pack) * a.qs[1]
+                    : nullptr;
+  });
+  int last[M];  // last key that a row sees
+  float m[M], l[M], acc[M][S::C][4];
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    last[i] = there(ty * M + i) ? before + token(ty * M + i) : -1;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+  }
+  simt_zero(acc);
+  const int keys = max(before + min(t0 + per, s.n), 0), tiles = (keys + BT - 1) / BT;
+  const int j_first = static_cast<int>(static_cast<long long>(tiles) * split / a.splits);
+  const int j_last = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / a.splits);
+  const float k2 = a.scale * kLog2e;
+  for (int jt = j_first; jt < j_last; ++jt) {
+    const int j0 = jt * BT;
+    __syncthreads();
+    auto key_row = [&](const void* base, const long long* strides, int r) -> const T* {
+      if (j0 + r >= keys) return nullptr;
+      long long at = hk * strides[2];
+      if (a.page) {
+        const long long row = paged_row(a, tile.b, j0 + r, strides);
+        if (row < 0) return nullptr;
+        at += row;
+      } else {
+        at += (s.start + j0 + r) * strides[1];
+      }
+      return static_cast<const T*>(base) + at;
+    };
+    simt_load<T, DP, BT>(K, a.D, [&](int r) { return key_row(a.k, a.ks, r); });
+    simt_load<T, DP, BT>(V, a.D, [&](int r) { return key_row(a.v, a.vs, r); });
+    __syncthreads();
+    float p[M][M];
+    simt_dot<DP, BT>(Q, K, p);
+    bool held[M];  // a key that the table has no page for counts for nothing
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const int key = j0 + tx + 16 * j;
+      held[j] = key < keys;
+      if (a.page && held[j]) {
+        const int col = key / a.page;
+        const int id = col < a.width ? a.tables[static_cast<long long>(tile.b) * a.width + col] : -1;
+        held[j] = id >= 0 && id < a.pages;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < M; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < M; ++j) {
+        p[i][j] = held[j] && j0 + tx + 16 * j <= last[i] ? p[i][j] * k2 : -INFINITY;
+        top = fmaxf(top, p[i][j]);
+      }
+      top = fmaxf(m[i], row_max(top));
+      const float base = top == -INFINITY ? 0.f : top, keep = exp2f(m[i] - base);
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < M; ++j) {
+        p[i][j] = exp2f(p[i][j] - base);
+        sum += p[i][j];
+        P[(ty * M + i) * S::Lp + tx + 16 * j] = p[i][j];
+      }
+      l[i] = l[i] * keep + row_sum(sum);
+      m[i] = top;
+#pragma unroll
+      for (int c = 0; c < S::C; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][c][e] *= keep;
+    }
+    __syncwarp();
+    simt_rows<DP, BT>(P, V, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const int r = ty * M + i;
+    if (!there(r)) continue;
+    const int h = hp * a.pack + r % a.pack;
+    const long long t = s.start + token(r);
+    // (a sum that is not a number stays one)
+    const float by = l[i] == 0.f ? 0.f : 1.f / l[i];
+    if (a.splits == 1) {
+      simt_store<T, DP>(static_cast<T*>(a.o) + t * a.os[0] + h * a.os[1], a.D, acc[i], by);
+      if (a.lse && tx == 0) a.lse[static_cast<long long>(h) * a.T + t] = (m[i] + log2f(l[i])) * kLn2;
+    } else {
+      const long long row = static_cast<long long>(split) * a.T * a.H + t * a.H + h;
+      simt_store<float, DP>(a.part_o + row * a.D, a.D, acc[i], by);
+      if (tx == 0) a.part_ml[row] = make_float2(m[i], l[i]);
+    }
+  }
+}
+
+struct AttnBwdArgs {
+  AttnArgs a;  // q, k, v and their strides; o is the forward's
+  const void* d_o;
+  long long gs[2];
+  const float* lse;  // [H][T]
+  float* delta;      // [H][T]: sum over a row of do o
+  void *dq, *dk, *dv;
+  long long dqs[2], dks[2], dvs[2];
+};
+
+// delta = the row sums of do o: a warp a row.
+template <class T>
+__global__ void __launch_bounds__(256) k_attn_delta(const __grid_constant__ AttnBwdArgs b) {
+  const AttnArgs& a = b.a;
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<long long>(a.T) * a.H) return;
+  const int t = static_cast<int>(row / a.H), h = static_cast<int>(row % a.H), lane = threadIdx.x & 31;
+  const T* o = static_cast<const T*>(a.o) + t * a.os[0] + h * a.os[1];
+  const T* g = static_cast<const T*>(b.d_o) + t * b.gs[0] + h * b.gs[1];
+  float v = 0.f;
+  for (int d = lane; d < a.D; d += 32) v += attn_load(o + d) * attn_load(g + d);
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if (lane == 0) b.delta[static_cast<long long>(h) * a.T + t] = v;
+}
+
+// p = exp(s - lse) and ds = p (do v^T - delta) of one tile; rows with last[i] = -1 and keys that a row
+// does not see give zeros.
+template <int DP, int BT>
+__device__ __forceinline__ void simt_ds(const float* Q, const float* K, const float* G, const float* V, float k2, int j0,
+                                        const int (&last)[BT / 16], const float (&lse2)[BT / 16],
+                                        const float (&delta)[BT / 16], float (&p)[BT / 16][BT / 16],
+                                        float (&ds)[BT / 16][BT / 16]) {
+  constexpr int M = BT / 16;
+  const int tx = threadIdx.x & 15;
+  simt_dot<DP, BT>(Q, K, p);
+  simt_dot<DP, BT>(G, V, ds);
+#pragma unroll
+  for (int i = 0; i < M; ++i)
+#pragma unroll
+    for (int j = 0; j < M; ++j) {
+      const bool seen = j0 + tx + 16 * j <= last[i];
+      p[i][j] = seen ? exp2f(p[i][j] * k2 - lse2[i]) : 0.f;
+      ds[i][j] = seen ? p[i][j] * (ds[i][j] - delta[i]) : 0.f;
+    }
+}
+
+// dk and dv of one tile of keys: all rows of the group's heads from its first token on.
+template <class T, int DP, int BT>
+__global__ void __launch_bounds__(kSimtThreads) k_attn_simt_dkdv(const __grid_constant__ AttnBwdArgs b) {
+  using S = SimtTile<DP, BT>;
+  constexpr int M = S::M;
+  const AttnArgs& a = b.a;
+  extern __shared__ float simt_smem[];
+  float *Q = simt_smem, *G = Q + S::kRows, *K = G + S::kRows, *V = K + S::kRows, *P = V + S::kRows, *D = P + S::kScores;
+  const int per = BT / a.pack, hk = blockIdx.y;
+  const AttnTile tile = attn_tile(a, blockIdx.x, BT);
+  if (tile.b < 0) return;
+  const AttnSeq s = attn_seq(a, tile.b);
+  const int ty = threadIdx.x >> 4, j0 = tile.at * BT;
+  auto key_row = [&](const void* base, const long long* strides, int r) -> const T* {
+    return j0 + r < s.n ? static_cast<const T*>(base) + (s.start + j0 + r) * strides[1] + hk * strides[2] : nullptr;
+  };
+  simt_load<T, DP, BT>(K, a.D, [&](int r) { return key_row(a.k, a.ks, r); });
+  simt_load<T, DP, BT>(V, a.D, [&](int r) { return key_row(a.v, a.vs, r); });
+  float dk[M][S::C][4], dv[M][S::C][4];
+  simt_zero(dk);
+  simt_zero(dv);
+  for (int hp = hk * (a.group / a.pack); hp < (hk + 1) * (a.group / a.pack); ++hp)
+    for (int t0 = j0 / per * per; t0 < s.n; t0 += per) {
+      auto there = [&](int r) { return r < per * a.pack && t0 + r / a.pack < s.n; };
+      auto head = [&](int r) { return hp * a.pack + r % a.pack; };
+      __syncthreads();
+      simt_load<T, DP, BT>(Q, a.D, [&](int r) -> const T* {
+        return there(r) ? static_cast<const T*>(a.q) + (s.start + t0 + r / a.pack) * a.qs[0] + head(r) * a.qs[1] : nullptr;
+      });
+      simt_load<T, DP, BT>(G, a.D, [&](int r) -> const T* {
+        return there(r) ? static_cast<const T*>(b.d_o) + (s.start + t0 + r / a.pack) * b.gs[0] + head(r) * b.gs[1] : nullptr;
+      });
+      __syncthreads();
+      int last[M];
+      float lse2[M], delta[M], p[M][M], ds[M][M];
+#pragma unroll
+      for (int i = 0; i < M; ++i) {
+        const int r = ty * M + i;
+        const bool on = there(r);
+        const long long at = on ? static_cast<long long>(head(r)) * a.T + s.start + t0 + r / a.pack : 0;
+        last[i] = on ? t0 + r / a.pack : -1;
+        lse2[i] = on ? b.lse[at] * kLog2e : 0.f;
+        delta[i] = on ? b.delta[at] : 0.f;
+      }
+      simt_ds<DP, BT>(Q, K, G, V, a.scale * kLog2e, j0, last, lse2, delta, p, ds);
+      const int tx = threadIdx.x & 15;
+#pragma unroll
+      for (int i = 0; i < M; ++i)
+#pragma unroll
+        for (int j = 0; j < M; ++j) {
+          P[(ty * M + i) * S::Lp + tx + 16 * j] = p[i][j];
+          D[(ty * M + i) * S::Lp + tx + 16 * j] = ds[i][j];
+        }
+      __syncthreads();
+      simt_cols<DP, BT>(P, G, dv);
+      simt_cols<DP, BT>(D, Q, dk);
+    }
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const int j = j0 + ty * M + i;
+    if (j >= s.n) continue;
+    simt_store<T, DP>(static_cast<T*>(b.dk) + (s.start + j) * b.dks[0] + hk * b.dks[1], a.D, dk[i], a.scale);
+    simt_store<T, DP>(static_cast<T*>(b.dv) + (s.start + j) * b.dvs[0] + hk * b.dvs[1], a.D, dv[i], 1.f);
+  }
+}
+
+// dq of one tile of rows.
+template <class T, int DP, int BT>
+__global__ void __launch_bounds__(kSimtThreads) k_attn_simt_dq(const __grid_constant__ AttnBwdArgs b) {
+  using S = SimtTile<DP, BT>;
+  constexpr int M = S::M;
+  const AttnArgs& a = b.a;
+  extern __shared__ float simt_smem[];
+  float *Q = simt_smem, *G = Q + S::kRows, *K = G + S::kRows, *V = K + S::kRows, *D = V + S::kRows;
+  const int per = BT / a.pack, hp = blockIdx.y, hk = hp * a.pack / a.group;
+  const AttnTile tile = attn_tile(a, blockIdx.x, per);
+  if (tile.b < 0) return;
+  const AttnSeq s = attn_seq(a, tile.b);
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15, t0 = tile.at * per;
+  auto there = [&](int r) { return r < per * a.pack && t0 + r / a.pack < s.n; };
+  auto head = [&](int r) { return hp * a.pack + r % a.pack; };
+  simt_load<T, DP, BT>(Q, a.D, [&](int r) -> const T* {
+    return there(r) ? static_cast<const T*>(a.q) + (s.start + t0 + r / a.pack) * a.qs[0] + head(r) * a.qs[1] : nullptr;
+  });
+  simt_load<T, DP, BT>(G, a.D, [&](int r) -> const T* {
+    return there(r) ? static_cast<const T*>(b.d_o) + (s.start + t0 + r / a.pack) * b.gs[0] + head(r) * b.gs[1] : nullptr;
+  });
+  int last[M];
+  float lse2[M], delta[M], dq[M][S::C][4];
+  simt_zero(dq);
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const int r = ty * M + i;
+    const bool on = there(r);
+    const long long at = on ? static_cast<long long>(head(r)) * a.T + s.start + t0 + r / a.pack : 0;
+    last[i] = on ? t0 + r / a.pack : -1;
+    lse2[i] = on ? b.lse[at] * kLog2e : 0.f;
+    delta[i] = on ? b.delta[at] : 0.f;
+  }
+  const int keys = min(t0 + per, s.n);
+  for (int j0 = 0; j0 < keys; j0 += BT) {
+    __syncthreads();
+    auto key_row = [&](const void* base, const long long* strides, int r) -> const T* {
+      return j0 + r < keys ? static_cast<const T*>(base) + (s.start + j0 + r) * strides[1] + hk * strides[2] : nullptr;
+    };
+    simt_load<T, DP, BT>(K, a.D, [&](int r) { return key_row(a.k, a.ks, r); });
+    simt_load<T, DP, BT>(V, a.D, [&](int r) { return key_row(a.v, a.vs, r); });
+    __syncthreads();
+    float p[M][M], ds[M][M];
+    simt_ds<DP, BT>(Q, K, G, V, a.scale * kLog2e, j0, last, lse2, delta, p, ds);
+#pragma unroll
+    for (int i = 0; i < M; ++i)
+#pragma unroll
+      for (int j = 0; j < M; ++j) D[(ty * M + i) * S::Lp + tx + 16 * j] = ds[i][j];
+    __syncwarp();
+    simt_rows<DP, BT>(D, K, dq);
+  }
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    const int r = ty * M + i;
+    if (there(r))
+      simt_store<T, DP>(static_cast<T*>(b.dq) + (s.start + t0 + r / a.pack) * b.dqs[0] + head(r) * b.dqs[1], a.D, dq[i],
+                        a.scale);
+  }
+}
+
+}  // namespace pc

@@ -1,0 +1,248 @@
+// The bookkeeping of a paged cache, on the GPU: block tables, slots and positions of a step's new
+// tokens from the requests' lengths, and the writes of their keys and values into the pages.
+//
+// Request b holds cached[b] tokens in ceil(cached / page) pages and adds added[b]; the pages that
+// it lacks are taken from `free` in the order of the requests:
+//   first[b] = sum over earlier requests of ceil((cached + added) / page) - ceil(cached / page)
+//   page of position p = tables[b][p / page], or free[first[b] + p / page - ceil(cached / page)]
+//   slot = page * page size + p % page size
+// The plan is latency: every CTA adds up all the requests by itself (two numbers each, a scan of
+// 1024 at a time), so that none waits for another, and then takes its share of the tokens and of
+// the tables' new entries by bisection. The writes are bandwidth: one 16-byte piece a thread and turn.
+#include "pc_device.cuh"
+#include "pc_host.h"
+
+namespace pc {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxRequests = 16384;  // starts and first in shared memory: 128 KB
+
+// Exclusive sums over the CTA of one pair a thread; returns the totals too.
+__device__ __forceinline__ void scan_pairs(int (&v)[2], int (&total)[2]) {
+  __shared__ int sums[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int own[2] = {v[0], v[1]};
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int x = __shfl_up_sync(0xffffffffu, v[i], d);
+      if (lane >= d) v[i] += x;
+    }
+  }
+  if (lane == 31) {
+    sums[0][warp] = v[0];
+    sums[1][warp] = v[1];
+  }
+  __syncthreads();
+  if (warp < 2) {
+    int x = sums[warp][lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, d);
+      if (lane >= d) x += y;
+    }
+    sums[warp][lane] = x;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[i] += (warp ? sums[i][warp - 1] : 0) - own[i];
+    total[i] = sums[i][31];
+  }
+  __syncthreads();
+}
+
+// The last index i of at[0 .. n) (ascending) with at[i] <= x.
+__device__ __forceinline__ int last_at_most(const int* at, int n, int x) {
+  int lo = 0, hi = n;  // at[lo] <= x < at[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+struct PlanArgs {
+  int B, width, page, free_pages, tokens;
+  const int32_t *cached, *added, *free_list;
+  int32_t *tables, *starts, *lengths, *positions, *taken;
+  long long* slots;
+};
+
+__global__ void __launch_bounds__(kPlanThreads) k_paged_plan(const __grid_constant__ PlanArgs a) {
+  extern __shared__ int shared[];
+  int *starts = shared, *first = shared + a.B;
+  int base[2] = {0, 0};
+  for (int at = 0; at < a.B; at += kPlanThreads) {
+    const int b = at + threadIdx.x;
+    int v[2] = {0, 0}, total[2];
+    int held = 0, add = 0;
+    if (b < a.B) {
+      held = max(a.cached[b], 0);
+      add = max(a.added[b], 0);
+      v[0] = add;
+      v[1] = static_cast<int>((static_cast<long long>(held) + add + a.page - 1) / a.page -
+                              (static_cast<long long>(held) + a.page - 1) / a.page);
+    }
+    scan_pairs(v, total);
+    if (b < a.B) {
+      starts[b] = base[0] + v[0];
+      first[b] = base[1] + v[1];
+      if (blockIdx.x == 0) {
+        a.starts[b] = starts[b];
+        a.lengths[b] = held + add;
+      }
+    }
+    base[0] += total[0];
+    base[1] += total[1];
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    a.starts[a.B] = base[0];
+    *a.taken = base[1];
+  }
+  const int stride = gridDim.x * kPlanThreads, at = blockIdx.x * kPlanThreads + threadIdx.x;
+  for (long long t = at; t < a.tokens; t += stride) {
+    int position = 0;
+    long long slot = -1;
+    if (t < base[0]) {
+      const int b = last_at_most(starts, a.B, static_cast<int>(t));
+      const int held = max(a.cached[b], 0), have = static_cast<int>((static_cast<long long>(held) + a.page - 1) / a.page);
+      position = held + static_cast<int>(t) - starts[b];
+      const int col = position / a.page;
+      int page = -1;
+      // (unsigned: sums that overflow pass no bound)
+      if (static_cast<unsigned>(col) < static_cast<unsigned>(a.width)) {
+        const unsigned fresh = static_cast<unsigned>(first[b]) + static_cast<unsigned>(col - have);
+        if (col < have) page = a.tables[static_cast<long long>(b) * a.width + col];
+        else if (fresh < static_cast<unsigned>(a.free_pages)) page = a.free_list[fresh];
+      }
+      if (page >= 0) slot = static_cast<long long>(page) * a.page + position % a.page;
+    }
+    a.positions[t] = position;
+    a.slots[t] = slot;
+  }
+  // entries that no token above reads: they lie past the pages held
+  for (long long i = at; i < base[1]; i += stride) {
+    const int b = last_at_most(first, a.B, static_cast<int>(i));
+    const int held = max(a.cached[b], 0);
+    const long long col = (static_cast<long long>(held) + a.page - 1) / a.page + i - first[b];
+    if (col >= 0 && col < a.width) a.tables[static_cast<long long>(b) * a.width + col] = i < a.free_pages ? a.free_list[i] : -1;
+  }
+}
+
+struct WriteArgs {
+  const void* x[2];
+  void* pages[2];
+  long long xs[2][2], ps[2][3];  // (token, head) and (page, slot, head) strides
+  const long long* slots;
+  long long tokens, capacity;
+  int heads, dim, page;
+  unsigned* status;
+};
+
+// P: the type of one access, E elements.
+template <class P, int E>
+__global__ void __launch_bounds__(256) k_paged_write(const __grid_constant__ WriteArgs a) {
+  const int n = blockIdx.y, pieces = a.dim / E, per_token = a.heads * pieces;
+  const long long all = a.tokens * per_token;
+  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < all; i += static_cast<long long>(gridDim.x) * 256) {
+    const long long t = i / per_token;
+    const int rest = static_cast<int>(i - t * per_token), h = rest / pieces, d = (rest - h * pieces);
+    const long long slot = a.slots[t];
+    if (slot < 0) continue;  // no place
+    if (slot >= a.capacity) {
+      if (rest == 0) atomicOr(a.status, kErrPage);
+      continue;
+    }
+    const P* from = static_cast<const P*>(a.x[n]) + (t * a.xs[n][0] + h * a.xs[n][1]) / E + d;
+    P* to = static_cast<P*>(a.pages[n]) + (slot / a.page * a.ps[n][0] + slot % a.page * a.ps[n][1] + h * a.ps[n][2]) / E + d;
+    *to = *from;
+  }
+}
+
+template <class P, int E>
+pc_status_t launch_write(const WriteArgs& a, cudaStream_t s) {
+  const long long all = a.tokens * a.heads * (a.dim / E);
+  long long ctas = (all + 255) / 256;
+  if (ctas > 16ll * num_sms()) ctas = 16ll * num_sms();
+  k_paged_write<P, E><<<dim3(static_cast<unsigned>(ctas), 2), 256, 0, s>>>(a);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+}  // namespace
+}  // namespace pc
+
+extern "C" {
+
+pc_status_t pc_paged_plan(int B, int width, int page_size, int free_pages, int tokens, const int32_t* cached,
+                          const int32_t* added, const int32_t* free_list, int32_t* tables, int32_t* starts, int32_t* lengths,
+                          int32_t* positions, long long* slots, int32_t* taken, cudaStream_t stream) {
+  pc::clear_error();
+  PC_CHECK(B >= 0 && width >= 0 && free_pages >= 0 && tokens >= 0, PC_ERR_SHAPE,
+           "B, width, free_pages and tokens must be >= 0 (got %d, %d, %d, %d)", B, width, free_pages, tokens);
+  PC_CHECK(B <= pc::kMaxRequests, PC_ERR_UNSUPPORTED, "up to %d requests (got %d)", pc::kMaxRequests, B);
+  PC_CHECK(page_size >= 1, PC_ERR_SHAPE, "page_size must be >= 1 (got %d)", page_size);
+  PC_CHECK(starts && taken, PC_ERR_NULL, "starts and taken must not be NULL");
+  PC_CHECK(B == 0 || (cached && added && lengths), PC_ERR_NULL, "cached, added and lengths must not be NULL");
+  PC_CHECK(B == 0 || width == 0 || tables, PC_ERR_NULL, "tables must not be NULL");
+  PC_CHECK(free_pages == 0 || free_list, PC_ERR_NULL, "free must not be NULL");
+  PC_CHECK(tokens == 0 || (positions && slots), PC_ERR_NULL, "positions and slots must not be NULL");
+  pc::PlanArgs a{B, width, page_size, free_pages, tokens, cached, added, free_list, tables, starts, lengths, positions,
+                 taken, slots};
+  PC_TRY(pc::allow_smem<pc::k_paged_plan>(pc::kMaxRequests * 2 * static_cast<int>(sizeof(int))));
+  int ctas = (tokens + pc::kPlanThreads - 1) / pc::kPlanThreads;
+  if (ctas < 1) ctas = 1;
+  if (ctas > pc::num_sms()) ctas = pc::num_sms();
+  pc::k_paged_plan<<<ctas, pc::kPlanThreads, B * 2 * sizeof(int), stream>>>(a);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+pc_status_t pc_paged_write(long long tokens, int heads, int dim, int pages, int page_size, const void* k, const void* v,
+                           const long long* strides, const long long* slots, void* k_pages, void* v_pages, pc_dtype_t dtype,
+                           cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_dtype(dtype));
+  PC_CHECK(tokens >= 0 && tokens < (1ll << 31) && heads >= 1 && dim >= 1 && pages >= 0 && page_size >= 1, PC_ERR_SHAPE,
+           "tokens in [0, 2^31), pages >= 0, heads, dim and page_size >= 1 wanted (got %lld, %d, %d, %d, %d)", tokens, pages,
+           heads, dim, page_size);
+  PC_CHECK(static_cast<long long>(heads) * dim < (1ll << 31), PC_ERR_SHAPE, "heads * dim must be < 2^31");
+  if (tokens == 0) return PC_OK;
+  PC_CHECK(k && v && strides && slots, PC_ERR_NULL, "k, v, strides and slots must not be NULL");
+  PC_CHECK(pages == 0 || (k_pages && v_pages), PC_ERR_NULL, "k_pages and v_pages must not be NULL");
+  PC_CHECK(k_pages == nullptr || k_pages != v_pages, PC_ERR_UNSUPPORTED, "k_pages may not be v_pages itself");
+  pc::WriteArgs a{};
+  const void* x[2] = {k, v};
+  void* p[2] = {k_pages, v_pages};
+  const int es = pc::dtype_bytes(dtype);
+  long long common = dim;  // what a 16-byte piece has to divide
+  for (int n = 0; n < 2; ++n) {
+    PC_CHECK(reinterpret_cast<uintptr_t>(x[n]) % es == 0 && reinterpret_cast<uintptr_t>(p[n]) % es == 0, PC_ERR_ALIGNMENT,
+             "keys, values and pages must be aligned to their type");
+    a.x[n] = x[n];
+    a.pages[n] = p[n];
+    common |= static_cast<long long>((reinterpret_cast<uintptr_t>(x[n]) | reinterpret_cast<uintptr_t>(p[n])) / es);
+    for (int i = 0; i < 2; ++i) common |= a.xs[n][i] = strides[2 * n + i];
+    for (int i = 0; i < 3; ++i) common |= a.ps[n][i] = strides[4 + 3 * n + i];
+    PC_CHECK((pages <= 1 || a.ps[n][0] != 0) && (page_size <= 1 || a.ps[n][1] != 0) && (heads <= 1 || a.ps[n][2] != 0),
+             PC_ERR_SHAPE, "pages: stride 0");
+  }
+  a.slots = slots;
+  a.tokens = tokens;
+  a.capacity = static_cast<long long>(pages) * page_size;
+  a.heads = heads;
+  a.dim = dim;
+  a.page = page_size;
+  a.status = pc::device_status_word();
+  PC_CHECK(a.status, PC_ERR_CUDA, "device status word unavailable");
+  const bool whole = common % (16 / es) == 0;
+  if (whole) return es == 2 ? pc::launch_write<uint4, 8>(a, stream) : pc::launch_write<uint4, 4>(a, stream);
+  return es == 2 ? pc::launch_write<uint16_t, 1>(a, stream) : pc::launch_write<uint32_t, 1>(a, stream);
+}
+
+}  // extern "C"

@@ -14,7 +14,7 @@ namespace pc {
 // ----------------------------------------------------------------- device status
 // Bits of the device status word a kernel sets when it gives up a bounded wait.
 enum : unsigned { kErrTimeoutProducer = 1u, kErrTimeoutMma = 2u, kErrTimeoutEpilogue = 4u,
-                  kErrTimeoutDrain = 8u, kErrRange = 16u };
+                  kErrTimeoutDrain = 8u, kErrRange = 16u, kErrPage = 32u };
 constexpr unsigned kErrTimeoutBits = 15u;
 
 // 2 s of wall time: three orders of magnitude above the longest legitimate wait here

@@ -1,0 +1,567 @@
+// Norms of queries and keys for each head and their rotation by position, in one pass, and its
+// gradient.
+//
+//   forward   z = x rstd,  rstd = (avg(x^2) + eps)^(-1/2),  u = z w,
+//             (y_a, y_b) = (u_a cos - u_b sin, u_b cos + u_a sin) for the R / 2 pairs (a, b),
+//             y = u elsewhere; the angle of pair i at position p is p f_i
+//   backward  g = the pairs of dy turned back,  dw = sum over rows of g z,
+//             h = g w,  dx = rstd (h - z avg(h z))
+//
+// Memory-bound: a row (one head of one token) is read once and written once. A row lies in the
+// registers of L = 1 .. 32 lanes, two pieces of V elements a lane: V pairs, whether a pair lies
+// side by side or half a rotation apart, so that no element changes lanes. Angles are reduced in
+// fixed point: f_i / 2 pi as a 64-bit fraction of a turn, whose product with the position wraps to
+// the turn's fraction by itself, exact to 2^-32 of a turn at any int32 position (a float32 angle
+// is off by 0.004 radians at position 131072). They are formed once for all the heads of a token that
+// a warp takes. Norms, sums, rotations and the weights' gradients are float32; the only rounding to
+// bf16 is that of y and dx.
+#include "pc_device.cuh"
+#include "pc_host.h"
+
+namespace pc {
+namespace {
+
+constexpr int kMaxDim = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+template <class T, int V>
+struct Piece;  // V elements in one access
+template <>
+struct Piece<__nv_bfloat16, 8> { using type = uint4; };
+template <>
+struct Piece<__nv_bfloat16, 4> { using type = uint2; };
+template <>
+struct Piece<__nv_bfloat16, 2> { using type = uint32_t; };
+template <>
+struct Piece<__nv_bfloat16, 1> { using type = uint16_t; };
+template <>
+struct Piece<float, 4> { using type = uint4; };
+template <>
+struct Piece<float, 2> { using type = uint2; };
+template <>
+struct Piece<float, 1> { using type = uint32_t; };
+
+template <class T, int V>
+__device__ __forceinline__ void get(const T* p, float (&v)[V]) {
+  typename Piece<T, V>::type u = *reinterpret_cast<const typename Piece<T, V>::type*>(p);
+  const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = static_cast<float>(e[i]);
+}
+template <class T, int V>
+__device__ __forceinline__ void put(T* p, const float (&v)[V]) {
+  typename Piece<T, V>::type u;
+  T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+  for (int i = 0; i < V; ++i) e[i] = static_cast<T>(v[i]);
+  *reinterpret_cast<typename Piece<T, V>::type*>(p) = u;
+}
+
+struct RotArgs {
+  const void *x[2], *dy[2];  // queries, keys
+  void* y[2];                // outputs: y, or dx
+  const float* weight[2];
+  long long xs[2][2], gs[2][2], ys[2][2];  // (token, head) strides
+  const int32_t* positions;
+  const float* frequencies;
+  float* partial;  // backward: [CTA][2][dim]
+  long long tokens;
+  int heads[2], dim, rotary, interleaved, norm, lanes_log2;
+  int groups[2];         // warps' steps over a token's heads: 32 / L rows each
+  int steps, chunks;     // steps of a warp, and how many warps share a token
+  float eps, amplitude, sign;
+};
+
+// f / 2 pi as a fraction of a turn in 64 bits: the float's 24-bit significand times 2^96 / 2 pi,
+// shifted into place.
+__device__ __forceinline__ unsigned long long turn_step(float f) {
+  const uint32_t bits = __float_as_uint(f);
+  const int e = static_cast<int>((bits >> 23) & 0xff);
+  const unsigned long long m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);
+  const int shift = 32 - ((e ? e : 1) - 150);  // value = m 2^(e - 150)
+  if (shift >= 120 || shift < 0) return 0ull;  // below 2^-24 of a turn at any position; above 2^55, or not finite
+  // 2^96 / 2 pi = hi 2^64 + lo
+  const unsigned __int128 lo = static_cast<unsigned __int128>(m) * 0x9391054A7F09D5F4ull;
+  const unsigned __int128 p = lo + (static_cast<unsigned __int128>(m * 0x28BE60DBull) << 64);
+  const unsigned long long s = static_cast<unsigned long long>(p >> shift);
+  return bits >> 31 ? 0ull - s : s;
+}
+
+// cos and sin of the angle of `turns` / 2^64 turns.
+template <class T>
+__device__ __forceinline__ void turn_cos_sin(unsigned long long turns, float& c, float& s) {
+  const float t = static_cast<float>(static_cast<int32_t>(turns >> 32)) * 4.656612873077393e-10f;  // half turns, [-1, 1]
+  if constexpr (sizeof(T) == 2) {
+    // the reduced angle's hardware sine and cosine: off by 2^-20 or so, far below bf16's 2^-9
+    c = __cosf(t * 3.14159265358979f);
+    s = __sinf(t * 3.14159265358979f);
+  } else {
+    sincospif(t, &s, &c);
+  }
+}
+
+// Lane's place in a row: where its slot's two pieces lie and whether they are there.
+template <int V>
+__device__ __forceinline__ void slot_places(const RotArgs& a, int slot, int (&at)[2], bool (&has)[2]) {
+  const int half = a.rotary / 2;
+  if (a.interleaved || slot * V >= half) {
+    const int base = a.interleaved ? slot * 2 * V : a.rotary + 2 * (slot * V - half);
+    at[0] = base;
+    at[1] = base + V;
+  } else {
+    at[0] = slot * V;
+    at[1] = half + slot * V;
+  }
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    has[e] = at[e] < a.dim;
+    if (!has[e]) at[e] = 0;
+  }
+}
+// Index of the frequency of the slot's pair i; past R / 2: none.
+template <int V>
+__device__ __forceinline__ int pair_index(const RotArgs& a, int slot, int i) {
+  return slot * V + i;
+}
+
+template <int V>
+__device__ __forceinline__ void turn(bool interleaved, float (&u)[2][V], const float (&c)[V], const float (&s)[V]) {
+  if (V > 1 && interleaved) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {  // pair i: elements 2i, 2i + 1 of the 2V
+      float& p = u[(2 * i) / V][(2 * i) % V];
+      float& q = u[(2 * i + 1) / V][(2 * i + 1) % V];
+      const float x = p, y = q;
+      p = x * c[i] - y * s[i];
+      q = y * c[i] + x * s[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const float x = u[0][i], y = u[1][i];
+      u[0][i] = x * c[i] - y * s[i];
+      u[1][i] = y * c[i] + x * s[i];
+    }
+  }
+}
+
+template <int N>
+__device__ __forceinline__ void lane_sum(float (&v)[N], int lanes_log2) {
+  for (int w = 0; w < lanes_log2; ++w) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1 << w);
+  }
+}
+
+// A warp takes one token's heads, `steps` groups of 32 / L rows (fewer for the last chunk); with
+// kBack the warps of a CTA walk tokens, and sum the weights' gradients.
+template <class T, int V, int K, bool kBack>
+__global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) k_qk_norm_rotary(const __grid_constant__ RotArgs a) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int L = 1 << a.lanes_log2, row = lane >> a.lanes_log2, rows = 32 >> a.lanes_log2;
+  int at[K][2];
+  bool has[K][2];
+  unsigned long long step[K][V];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int slot = (lane & (L - 1)) + k * L;
+    slot_places<V>(a, slot, at[k], has[k]);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int p = pair_index<V>(a, slot, i);
+      step[k][i] = p < a.rotary / 2 ? turn_step(a.frequencies[p]) : 0ull;
+    }
+  }
+  float w[2][K][2][V];
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[n][k][e][i] = a.weight[n] && has[k][e] ? __ldg(a.weight[n] + at[k][e] + i) : 1.f;
+  float dw[kBack ? 2 : 1][kBack ? K : 1][2][V];
+  if constexpr (kBack) {
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < V; ++i) dw[n][k][e][i] = 0.f;
+  }
+  const long long units = a.tokens * a.chunks, all = static_cast<long long>(gridDim.x) * kWarps;
+  for (long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp; unit < units; unit += all) {
+    const long long t = unit / a.chunks;
+    const int first = static_cast<int>(unit % a.chunks) * a.steps;
+    const int last = min(first + a.steps, a.groups[0] + a.groups[1]);
+    const unsigned long long pos = a.rotary ? static_cast<unsigned long long>(static_cast<long long>(a.positions[t])) : 0ull;
+    float c[K][V], s[K][V];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        turn_cos_sin<T>(pos * step[k][i], c[k][i], s[k][i]);
+        const bool turned = pair_index<V>(a, (lane & (L - 1)) + k * L, i) < a.rotary / 2;
+        c[k][i] = turned ? c[k][i] * a.amplitude : 1.f;
+        s[k][i] = turned ? s[k][i] * a.amplitude * a.sign : 0.f;
+      }
+    auto side = [&](const int n, int from, int to) {  // queries, then keys
+      if (from >= to) return;
+      const T* x = static_cast<const T*>(a.x[n]) + t * a.xs[n][0];
+      const T* dy = kBack ? static_cast<const T*>(a.dy[n]) + t * a.gs[n][0] : nullptr;
+      T* y = static_cast<T*>(a.y[n]) + t * a.ys[n][0];
+      float u[K][2][V], g[kBack ? K : 1][2][V];
+      auto fetch = [&](int group) {
+        const int h = group * rows + row;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (h < a.heads[n] && has[k][e]) {
+              get<T, V>(x + h * a.xs[n][1] + at[k][e], u[k][e]);
+              if constexpr (kBack) get<T, V>(dy + h * a.gs[n][1] + at[k][e], g[k][e]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                u[k][e][i] = 0.f;
+                if constexpr (kBack) g[k][e][i] = 0.f;
+              }
+            }
+          }
+      };
+      for (int group = from; group < to; ++group) {
+        fetch(group);
+        const int h = group * rows + row;
+        float rstd = 1.f;
+        if (a.norm) {
+          float sq[1] = {0.f};
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < V; ++i) sq[0] += u[k][e][i] * u[k][e][i];
+          lane_sum(sq, a.lanes_log2);
+          rstd = rsqrtf(sq[0] / a.dim + a.eps);
+        }
+        if constexpr (!kBack) {
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            if (a.norm) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < V; ++i) u[k][e][i] *= rstd * w[n][k][e][i];
+            }
+            turn<V>(a.interleaved, u[k], c[k], s[k]);
+          }
+        } else {
+          float dot[1] = {0.f};
+#pragma unroll
+          for (int k = 0; k < K; ++k) {
+            turn<V>(a.interleaved, g[k], c[k], s[k]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                const float z = u[k][e][i] * rstd;
+                dw[n][k][e][i] += g[k][e][i] * z;
+                g[k][e][i] *= w[n][k][e][i];
+                dot[0] += g[k][e][i] * z;
+                u[k][e][i] = z;
+              }
+          }
+          lane_sum(dot, a.lanes_log2);
+          const float mean = dot[0] / a.dim;
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int i = 0; i < V; ++i) u[k][e][i] = rstd * (g[k][e][i] - u[k][e][i] * mean);
+        }
+        if (h < a.heads[n]) {
+#pragma unroll
+          for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (has[k][e]) put<T, V>(y + h * a.ys[n][1] + at[k][e], u[k][e]);
+        }
+      }
+    };
+    side(0, first, min(last, a.groups[0]));
+    side(1, max(first - a.groups[0], 0), last - a.groups[0]);
+  }
+  if constexpr (kBack) {
+    // the CTA's rows in a fixed order: row groups of a warp, then warps
+    __shared__ float part[kWarps][2][kMaxDim];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float v = dw[n][k][e][i];
+            for (int d = L; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+            if (row == 0 && has[k][e]) part[warp][n][at[k][e] + i] = v;
+          }
+    __syncthreads();
+    for (int j = threadIdx.x; j < 2 * a.dim; j += kThreads) {
+      const int n = j >= a.dim, d = j - n * a.dim;
+      float v = 0.f;
+#pragma unroll
+      for (int x = 0; x < kWarps; ++x) v += part[x][n][d];
+      a.partial[static_cast<long long>(blockIdx.x) * 2 * a.dim + j] = v;
+    }
+  }
+}
+
+// The weights' gradients: 32 columns a CTA, the CTAs' sums in 8 parts of a fixed order.
+__global__ void __launch_bounds__(256) k_weight_sums(int ctas, int dim, const float* partial, float* dq, float* dk,
+                                                     int accumulate) {
+  __shared__ float part[8][33];
+  const int col = blockIdx.x * 32 + (threadIdx.x & 31), p = threadIdx.x >> 5;
+  float v = 0.f;
+  if (col < 2 * dim)
+    for (int c = p; c < ctas; c += 8) v += partial[static_cast<long long>(c) * 2 * dim + col];
+  part[p][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (p == 0 && col < 2 * dim) {
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v += part[i][threadIdx.x & 31];
+    float* out = col < dim ? dq : dk;
+    if (out) {
+      out += col < dim ? col : col - dim;
+      *out = accumulate ? *out + v : v;
+    }
+  }
+}
+
+// The widest piece that divides a row's parts and suits every pointer and stride.
+int piece_width(const RotArgs& a, bool back, int es) {
+  int v = 16 / es;
+  auto fits = [&](long long n) {
+    while (n % v) v /= 2;
+  };
+  fits(a.dim);
+  fits(a.interleaved ? a.rotary : a.rotary / 2);
+  for (int n = 0; n < 2; ++n) {
+    if (a.heads[n] == 0) continue;
+    const void* ptrs[3] = {a.x[n], a.y[n], back ? a.dy[n] : nullptr};
+    for (const void* p : ptrs) fits(static_cast<long long>(reinterpret_cast<uintptr_t>(p) / es % 16));
+    for (int i = 0; i < 2; ++i) {
+      fits(a.xs[n][i]);
+      fits(a.ys[n][i]);
+      if (back) fits(a.gs[n][i]);
+    }
+  }
+  return v;
+}
+
+int back_ctas(long long tokens) {
+  const long long want = (tokens + kWarps - 1) / kWarps, most = 2ll * num_sms();
+  return static_cast<int>(want < most ? want : most);
+}
+
+template <class T, int V, bool kBack>
+pc_status_t launch_width(RotArgs& a, cudaStream_t s) {
+  const int slots = (a.dim + 2 * V - 1) / (2 * V);
+  a.lanes_log2 = 0;
+  while ((1 << a.lanes_log2) < slots && a.lanes_log2 < 5) ++a.lanes_log2;
+  const int K = (slots + 31) / 32, rows = 32 >> a.lanes_log2;
+  for (int n = 0; n < 2; ++n) a.groups[n] = (a.heads[n] + rows - 1) / rows;
+  const int all = a.groups[0] + a.groups[1];
+  // A warp takes all of a token's heads where the tokens fill the GPU, fewer where they do not
+  // (forward): the angles are formed once a warp.
+  a.chunks = 1;
+  if (!kBack) {
+    const long long fill = 16ll * num_sms();
+    while (a.chunks < all && a.tokens * a.chunks < fill) ++a.chunks;
+  }
+  a.steps = (all + a.chunks - 1) / a.chunks;
+  a.chunks = (all + a.steps - 1) / a.steps;
+  long long ctas = (a.tokens * a.chunks + kWarps - 1) / kWarps;
+  if (kBack) ctas = back_ctas(a.tokens);
+  else if (ctas > 24ll * num_sms()) ctas = 24ll * num_sms();
+  auto* kernel = K <= 1 ? k_qk_norm_rotary<T, V, 1, kBack> : nullptr;
+  if constexpr (V <= 2) {
+    if (K == 2) kernel = k_qk_norm_rotary<T, V, 2, kBack>;
+  }
+  if constexpr (V == 1) {
+    if (K > 2) kernel = k_qk_norm_rotary<T, V, 4, kBack>;
+  }
+  kernel<<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(a);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+template <class T, bool kBack>
+pc_status_t launch(RotArgs& a, cudaStream_t s) {
+  const int v = piece_width(a, kBack, sizeof(T));
+  if constexpr (sizeof(T) == 2) {
+    if (v == 8) return launch_width<T, 8, kBack>(a, s);
+  }
+  if (v >= 4) return launch_width<T, 4, kBack>(a, s);
+  if (v == 2) return launch_width<T, 2, kBack>(a, s);
+  return launch_width<T, 1, kBack>(a, s);
+}
+
+pc_status_t check_rot(long long tokens, int Hq, int Hk, int dim, int rotary, int layout, const int32_t* positions,
+                      const float* frequencies, float eps, float amplitude, pc_dtype_t dt) {
+  PC_TRY(check_dtype(dt));
+  PC_CHECK(tokens >= 0 && tokens < (1ll << 31), PC_ERR_SHAPE, "tokens must be in [0, 2^31) (got %lld)", tokens);
+  PC_CHECK(Hq >= 0 && Hk >= 0 && Hq + static_cast<long long>(Hk) >= 1 && Hq <= 65535 && Hk <= 65535, PC_ERR_SHAPE,
+           "heads must be in [0, 65535], one at least (got %d, %d)", Hq, Hk);
+  PC_CHECK(dim >= 1, PC_ERR_SHAPE, "head size must be >= 1 (got %d)", dim);
+  PC_CHECK(dim <= kMaxDim, PC_ERR_UNSUPPORTED, "head sizes up to %d (got %d)", kMaxDim, dim);
+  PC_CHECK(rotary >= 0 && rotary <= dim && rotary % 2 == 0, PC_ERR_SHAPE,
+           "rotated features must be even, from 0 to the head size %d (got %d)", dim, rotary);
+  PC_CHECK(layout == PC_ROTARY_HALF || layout == PC_ROTARY_INTERLEAVED, PC_ERR_UNSUPPORTED,
+           "unknown layout %d; valid ones are PC_ROTARY_HALF (0) and PC_ROTARY_INTERLEAVED (1)", layout);
+  PC_CHECK(eps >= 0.f && eps < INFINITY, PC_ERR_SHAPE, "eps must be finite and >= 0");
+  PC_CHECK(amplitude > -INFINITY && amplitude < INFINITY, PC_ERR_SHAPE, "amplitude must be finite");
+  if (tokens > 0 && rotary > 0)
+    PC_CHECK(positions && frequencies, PC_ERR_NULL, "positions and frequencies must not be NULL");
+  return PC_OK;
+}
+
+pc_status_t check_side(const char* name, const void* p, const char* out_name, const void* out, const long long* is,
+                       const long long* os, long long tokens, int heads, pc_dtype_t dt) {
+  PC_CHECK(p, PC_ERR_NULL, "%s must not be NULL", name);
+  PC_CHECK(out, PC_ERR_NULL, "%s must not be NULL", out_name);
+  const uintptr_t es = dtype_bytes(dt);
+  PC_CHECK(reinterpret_cast<uintptr_t>(p) % es == 0, PC_ERR_ALIGNMENT, "%s is not aligned to its type", name);
+  PC_CHECK(reinterpret_cast<uintptr_t>(out) % es == 0, PC_ERR_ALIGNMENT, "%s is not aligned to its type", out_name);
+  PC_CHECK((tokens <= 1 || os[0] != 0) && (heads <= 1 || os[1] != 0), PC_ERR_SHAPE, "%s: stride 0", out_name);
+  PC_CHECK(p != out || ((tokens <= 1 || is[0] == os[0]) && (heads <= 1 || is[1] == os[1])), PC_ERR_SHAPE,
+           "%s is %s at other strides", out_name, name);
+  return PC_OK;
+}
+
+}  // namespace
+}  // namespace pc
+
+extern "C" {
+
+pc_status_t pc_qk_norm_rotary_fwd(long long tokens, int Hq, int Hk, int dim, int rotary, const void* q, const void* k,
+                                  const long long* strides, const float* q_weight, const float* k_weight,
+                                  const int32_t* positions, const float* frequencies, float eps, float amplitude,
+                                  pc_rotary_t layout, int norm, void* q_out, void* k_out, pc_dtype_t dtype,
+                                  cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_rot(tokens, Hq, Hk, dim, rotary, layout, positions, frequencies, eps, amplitude, dtype));
+  if (tokens == 0) return PC_OK;
+  PC_CHECK(strides, PC_ERR_NULL, "strides must not be NULL");
+  if (Hq) PC_TRY(pc::check_side("q", q, "q_out", q_out, strides, strides + 4, tokens, Hq, dtype));
+  if (Hk) PC_TRY(pc::check_side("k", k, "k_out", k_out, strides + 2, strides + 6, tokens, Hk, dtype));
+  PC_CHECK(!Hq || !Hk || q_out != k_out, PC_ERR_UNSUPPORTED, "q_out may not be k_out itself");
+  pc::RotArgs a{};
+  const void* x[2] = {q, k};
+  void* y[2] = {q_out, k_out};
+  for (int n = 0; n < 2; ++n) {
+    a.x[n] = x[n];
+    a.y[n] = y[n];
+    for (int i = 0; i < 2; ++i) {
+      a.xs[n][i] = strides[2 * n + i];
+      a.ys[n][i] = strides[4 + 2 * n + i];
+    }
+  }
+  a.weight[0] = q_weight;
+  a.weight[1] = k_weight;
+  a.heads[0] = Hq;
+  a.heads[1] = Hk;
+  a.positions = positions;
+  a.frequencies = frequencies;
+  a.tokens = tokens;
+  a.dim = dim;
+  a.rotary = rotary;
+  a.interleaved = layout == PC_ROTARY_INTERLEAVED;
+  a.norm = norm != 0;
+  a.eps = eps;
+  a.amplitude = amplitude;
+  a.sign = 1.f;
+  return dtype == PC_BF16 ? pc::launch<__nv_bfloat16, false>(a, stream) : pc::launch<float, false>(a, stream);
+}
+
+pc_status_t pc_qk_norm_rotary_bwd_workspace(long long tokens, int Hq, int Hk, int dim, int norm, size_t* bytes) {
+  pc::clear_error();
+  PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
+  PC_TRY(pc::check_rot(tokens, Hq, Hk, dim, 0, 0, nullptr, nullptr, 0.f, 1.f, PC_F32));
+  *bytes = norm ? static_cast<size_t>(pc::back_ctas(tokens)) * 2 * dim * sizeof(float) : 0;
+  return PC_OK;
+}
+
+pc_status_t pc_qk_norm_rotary_bwd(long long tokens, int Hq, int Hk, int dim, int rotary, const void* dq_out,
+                                  const void* dk_out, const void* q, const void* k, const long long* strides,
+                                  const float* q_weight, const float* k_weight, const int32_t* positions,
+                                  const float* frequencies, float eps, float amplitude, pc_rotary_t layout, int norm,
+                                  void* dq, void* dk, float* dq_weight, float* dk_weight, int accumulate, pc_dtype_t dtype,
+                                  void* ws, size_t ws_bytes, cudaStream_t stream) {
+  pc::clear_error();
+  PC_TRY(pc::check_rot(tokens, Hq, Hk, dim, rotary, layout, positions, frequencies, eps, amplitude, dtype));
+  if (tokens > 0) {
+    PC_CHECK(strides, PC_ERR_NULL, "strides must not be NULL");
+    PC_CHECK(!Hq || !Hk || dq != dk, PC_ERR_UNSUPPORTED, "dq may not be dk itself");
+    if (Hq) PC_TRY(pc::check_side("dq_out", dq_out, "dq", dq, strides, strides + 8, tokens, Hq, dtype));
+    if (Hk) PC_TRY(pc::check_side("dk_out", dk_out, "dk", dk, strides + 2, strides + 10, tokens, Hk, dtype));
+    if (norm) {
+      if (Hq) PC_TRY(pc::check_side("q", q, "dq", dq, strides + 4, strides + 8, tokens, Hq, dtype));
+      if (Hk) PC_TRY(pc::check_side("k", k, "dk", dk, strides + 6, strides + 10, tokens, Hk, dtype));
+    }
+  }
+  const size_t need = norm ? static_cast<size_t>(pc::back_ctas(tokens)) * 2 * dim * sizeof(float) : 0;
+  PC_CHECK(need == 0 || (ws && ws_bytes >= need), PC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  PC_CHECK(need == 0 || pc::aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
+  if (tokens == 0) {
+    for (float* w : {dq_weight, dk_weight})
+      if (w && norm && !accumulate) PC_CUDA(cudaMemsetAsync(w, 0, sizeof(float) * dim, stream));
+    return PC_OK;
+  }
+  pc::RotArgs a{};
+  const void *x[2] = {q, k}, *g[2] = {dq_out, dk_out};
+  void* y[2] = {dq, dk};
+  for (int n = 0; n < 2; ++n) {
+    // without a norm the gradient is the forward of the opposite angles
+    a.x[n] = norm ? x[n] : g[n];
+    a.dy[n] = g[n];
+    a.y[n] = y[n];
+    for (int i = 0; i < 2; ++i) {
+      a.gs[n][i] = strides[2 * n + i];
+      a.xs[n][i] = norm ? strides[4 + 2 * n + i] : a.gs[n][i];
+      a.ys[n][i] = strides[8 + 2 * n + i];
+    }
+  }
+  a.weight[0] = q_weight;
+  a.weight[1] = k_weight;
+  a.heads[0] = Hq;
+  a.heads[1] = Hk;
+  a.positions = positions;
+  a.frequencies = frequencies;
+  a.partial = static_cast<float*>(ws);
+  a.tokens = tokens;
+  a.dim = dim;
+  a.rotary = rotary;
+  a.interleaved = layout == PC_ROTARY_INTERLEAVED;
+  a.norm = norm != 0;
+  a.eps = eps;
+  a.amplitude = amplitude;
+  a.sign = -1.f;
+  if (!norm)
+    return dtype == PC_BF16 ? pc::launch<__nv_bfloat16, false>(a, stream) : pc::launch<float, false>(a, stream);
+  if (dtype == PC_BF16) PC_TRY((pc::launch<__nv_bfloat16, true>(a, stream)));
+  else PC_TRY((pc::launch<float, true>(a, stream)));
+  if (dq_weight || dk_weight) {
+    pc::k_weight_sums<<<(2 * dim + 31) / 32, 256, 0, stream>>>(pc::back_ctas(tokens), dim, a.partial, dq_weight, dk_weight,
+                                                               accumulate != 0);
+    PC_LAUNCH_CHECK();
+  }
+  return PC_OK;
+}
+
+}  // extern "C"
