@@ -178,11 +178,11 @@ pc_status_t find_encode() {
 }  // namespace
 
 pc_status_t encode_bf16_map4(CUtensorMap* map, const void* base, const long long (&dims)[4],
-                             const long long (&strides)[3], int box_cols, int box_rows) {
+                             const long long (&strides)[3], int box_cols, int box_rows, int box_depth) {
   PC_TRY(find_encode());
   const cuuint64_t d[4] = {cuuint64_t(dims[0]), cuuint64_t(dims[1]), cuuint64_t(dims[2]), cuuint64_t(dims[3])};
   const cuuint64_t st[3] = {cuuint64_t(strides[0]) * 2, cuuint64_t(strides[1]) * 2, cuuint64_t(strides[2]) * 2};
-  const cuuint32_t box[4] = {cuuint32_t(box_cols), cuuint32_t(box_rows), 1, 1};
+  const cuuint32_t box[4] = {cuuint32_t(box_cols), cuuint32_t(box_rows), cuuint32_t(box_depth), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, box, estr,
                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

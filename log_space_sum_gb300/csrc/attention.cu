@@ -8,9 +8,11 @@
 // stored. The gradient forms the probabilities again from lse, in two kernels (dk and dv by tiles of keys,
 // dq by tiles of rows): seven products instead of five, but no sum is left to atomics, whose order
 // would change the bits, and the heads of a group add up in the tile of their keys.
+#include <cfloat>
 #include <climits>
 
 #include "attention_simt.cuh"
+#include "attention_tc.cuh"
 #include "pc_host.h"
 
 namespace pc {
@@ -95,15 +97,16 @@ int simt_splits(const AttnArgs& a) {
 }
 
 size_t part_bytes(const AttnArgs& a, int splits) {
-  return splits <= 1 ? 0 : static_cast<size_t>(splits) * a.T * a.H * (a.D + 2) * sizeof(float) + 256;
+  return splits <= 1 ? 0 : static_cast<size_t>(splits) * a.T * a.H * (a.D + 2) * sizeof(float) + 512;
 }
 
 void carve_parts(AttnArgs& a, int splits, void* ws) {
   a.splits = splits;
   if (splits <= 1) return;
   Carver c(ws);
-  a.part_ml = static_cast<float2*>(c.take(static_cast<size_t>(splits) * a.T * a.H * sizeof(float2)));
-  a.part_o = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(splits) * a.T * a.H);
+  const size_t rows = static_cast<size_t>(splits) * a.T * a.H;
+  a.part_o = static_cast<float*>(c.take(rows * a.D * sizeof(float)));
+  a.part_ml = static_cast<float2*>(c.take(rows * sizeof(float2)));
 }
 
 template <class T, int DP>
@@ -139,6 +142,107 @@ pc_status_t launch_simt(AttnArgs& a, void* ws, cudaStream_t s, int* launches) {
     ++*launches;
   }
   return PC_OK;
+}
+
+// ------------------------------------------------------------- tensor cores
+bool tc_sizes(const AttnArgs& a, pc_dtype_t dt) {
+  if (dt != PC_BF16 || a.D % 8 != 0 || a.D > 128) return false;
+  // a page fills a tile of keys, or whole groups of 16 of one
+  return !a.page || (a.pages > 0 && (a.page % 128 == 0 || a.page == 16 || a.page == 32 || a.page == 64));
+}
+
+// One dimension of a tensor map: a stride of whole 16-byte pieces; any where there is but one element.
+bool tc_stride(long long extent, long long& stride) {
+  if (extent <= 1) stride = 8;
+  return stride > 0 && stride % 8 == 0 && stride < (1ll << 38);
+}
+
+// Map of [outer][heads][rows][D] with boxes of box_rows rows; heads that share one (stride 0) are left out. False: not for TMA.
+bool tc_key_map(CUtensorMap* map, int* ext, const void* p, int D, int rows, long long row_stride, int heads, long long head_stride,
+                int outer, long long outer_stride, int box_rows, pc_status_t* st) {
+  *ext = heads > 1 && head_stride != 0;
+  const int h = *ext ? heads : 1;
+  if (!aligned16(p) || !tc_stride(rows, row_stride) || !tc_stride(h, head_stride) || !tc_stride(outer, outer_stride)) return false;
+  const long long dims[4] = {D, rows, h, outer}, strides[3] = {row_stride, head_stride, outer_stride};
+  *st = encode_bf16_map4(map, p, dims, strides, 64, box_rows);
+  return true;
+}
+
+// Map of rows [T][H][D] in boxes of per tokens by pack heads.
+bool tc_row_map(CUtensorMap* map, const AttnArgs& a, const void* p, const long long* s, int per, pc_status_t* st) {
+  long long token = s[0], head = s[1];
+  if (!aligned16(p) || !tc_stride(a.T, token) || !tc_stride(a.H, head)) return false;
+  const long long dims[4] = {a.D, a.H, a.T, 1}, strides[3] = {head, token, 8};
+  *st = encode_bf16_map4(map, p, dims, strides, 64, a.pack, per);
+  return true;
+}
+
+// An output's rows in 16-byte pieces.
+bool tc_out(const AttnArgs& a, const void* p, const long long* s, int heads) {
+  long long token = s[0], head = s[1];
+  return aligned16(p) && (a.T <= 1 || token % 8 == 0) && (heads <= 1 || head % 8 == 0);
+}
+
+// Ranges of the keys: where the tiles of rows leave SMs without work, none with fewer than four tiles of keys.
+int tc_splits(const AttnArgs& a) {
+  if (!a.page) return 1;
+  const long long ctas = tiles_of(a, 2 * (kAtC / a.pack)) * (a.H / a.pack);
+  const long long most = static_cast<long long>(a.width) * a.page / (4 * kAtC), want = num_sms() / (ctas ? ctas : 1);
+  long long s = want < most ? want : most;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return s < 1 ? 1 : static_cast<int>(s);
+}
+
+template <int DP>
+pc_status_t launch_tc_dim(const AttnTcArgs& t, cudaStream_t s) {
+  const AttnArgs& a = t.a;
+  constexpr int smem = AtShape<DP>::kBytes;
+  const long long ctas = tiles_of(a, 2 * t.per) * (a.H / a.pack) * a.splits;
+  PC_CHECK(ctas < INT_MAX, PC_ERR_SHAPE, "%lld tiles of rows: fewer than 2^31 wanted", ctas);
+  PC_TRY((allow_smem<k_attn_tc<DP>>(smem)));
+  k_attn_tc<DP><<<static_cast<unsigned>(ctas), kAtThreads, smem, s>>>(t);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+// Runs on the tensor cores where the sizes, strides and alignments allow.
+pc_status_t try_tc(const AttnArgs& from, pc_dtype_t dt, void* ws, cudaStream_t s, int* launches, bool* done) {
+  *done = false;
+  if (!tc_sizes(from, dt) || !tc_out(from, from.o, from.os, from.H)) return PC_OK;
+  AttnTcArgs t{};
+  t.a = from;
+  AttnArgs& a = t.a;
+  t.per = kAtC / a.pack;
+  t.box = a.page && a.page < kAtC ? a.page : kAtC;
+  pc_status_t st = PC_OK;
+  if (!tc_row_map(&t.q, a, a.q, a.qs, t.per, &st)) return PC_OK;
+  PC_TRY(st);
+  const int rows = a.page ? a.page : a.T, outer = a.page ? a.pages : 1;
+  if (!tc_key_map(&t.k, &t.k_ext, a.k, a.D, rows, a.ks[1], a.Hk, a.ks[2], outer, a.ks[0], t.box, &st)) return PC_OK;
+  PC_TRY(st);
+  if (!tc_key_map(&t.v, &t.v_ext, a.v, a.D, rows, a.vs[1], a.Hk, a.vs[2], outer, a.vs[0], t.box, &st)) return PC_OK;
+  PC_TRY(st);
+  a.scale *= kLog2e;
+  if (a.scale == 0.f) a.scale = FLT_MIN;  // keys that are hidden by an infinite score stay hidden
+  carve_parts(a, tc_splits(a), ws);
+  PC_TRY(a.D <= 64 ? launch_tc_dim<64>(t, s) : launch_tc_dim<128>(t, s));
+  ++*launches;
+  if (a.splits > 1) {
+    PC_TRY(launch_join<__nv_bfloat16>(a, s));
+    ++*launches;
+  }
+  *done = true;
+  return PC_OK;
+}
+
+pc_status_t run_fwd(AttnArgs& a, pc_dtype_t dt, void* ws, cudaStream_t s) {
+  a.status = device_status_word();
+  PC_CHECK(a.status, PC_ERR_CUDA, "device status word unavailable");
+  int launches = 0;
+  bool done = false;
+  PC_TRY(try_tc(a, dt, ws, s, &launches, &done));
+  if (done) return PC_OK;
+  return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, ws, s, &launches) : launch_simt<float>(a, ws, s, &launches);
 }
 
 template <class T, int DP>
@@ -218,7 +322,11 @@ AttnArgs make_args(int B, int T, int H, int Hk, int D, float scale, const int32_
 // The planners look at sizes alone; a workspace is sized for sequences of any lengths.
 const int32_t* some_starts() { return reinterpret_cast<const int32_t*>(uintptr_t(4)); }
 
-size_t paged_bytes(const AttnArgs& a) { return part_bytes(a, simt_splits(a)); }
+size_t paged_bytes(const AttnArgs& a, pc_dtype_t dt) {
+  int splits = simt_splits(a);
+  if (tc_sizes(a, dt) && tc_splits(a) > splits) splits = tc_splits(a);
+  return part_bytes(a, splits);
+}
 
 }  // namespace
 }  // namespace pc
@@ -258,10 +366,7 @@ pc_status_t pc_attention_fwd(int B, int T, int H, int Hk, int D, const void* q, 
     a.vs[1 + i] = strides[4 + i];
     a.os[i] = strides[6 + i];
   }
-  a.status = pc::device_status_word();
-  int launches = 0;
-  return dtype == PC_BF16 ? pc::launch_simt<__nv_bfloat16>(a, nullptr, stream, &launches)
-                          : pc::launch_simt<float>(a, nullptr, stream, &launches);
+  return pc::run_fwd(a, dtype, nullptr, stream);
 }
 
 pc_status_t pc_attention_bwd(int B, int T, int H, int Hk, int D, const void* q, const void* k, const void* v, const void* o,
@@ -324,7 +429,7 @@ pc_status_t pc_paged_attention_workspace(int B, int T, int H, int Hk, int D, int
     a.page = page_size;
     a.width = width;
     a.pages = pages;
-    const size_t n = pc::paged_bytes(a);
+    const size_t n = pc::paged_bytes(a, dtype);
     if (n > *bytes) *bytes = n;
   }
   return PC_OK;
@@ -369,14 +474,10 @@ pc_status_t pc_paged_attention(int B, int T, int H, int Hk, int D, int pages, in
   a.page = page_size;
   a.pages = pages;
   a.width = width;
-  const size_t need = pc::paged_bytes(a);
+  const size_t need = pc::paged_bytes(a, dtype);
   PC_CHECK(need == 0 || (ws && ws_bytes >= need), PC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   PC_CHECK(need == 0 || pc::aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
-  a.status = pc::device_status_word();
-  PC_CHECK(a.status, PC_ERR_CUDA, "device status word unavailable");
-  int launches = 0;
-  return dtype == PC_BF16 ? pc::launch_simt<__nv_bfloat16>(a, ws, stream, &launches)
-                          : pc::launch_simt<float>(a, ws, stream, &launches);
+  return pc::run_fwd(a, dtype, ws, stream);
 }
 
 }  // extern "C"

@@ -81,6 +81,16 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, int tile, int p
   return {-1, 0};
 }
 
+// The keys that rows [t0, t0 + per) of a sequence see: none of them lies past the table.
+__device__ __forceinline__ int attn_keys(const AttnArgs& a, const AttnSeq& s, int t0, int per) {
+  if (t0 >= s.n) return 0;
+  const int keys = max(s.ctx - s.n + min(t0 + per, s.n), 0);
+  if (!a.page) return keys;
+  const long long held = static_cast<long long>(a.width) * a.page;
+  if (keys > held) atomicOr(a.status, kErrPage);
+  return static_cast<int>(min(static_cast<long long>(keys), held));
+}
+
 // Row of cached token j of sequence b in the pages, or -1 where the table has no page for it (flagged).
 __device__ __forceinline__ long long paged_row(const AttnArgs& a, int b, int j, const long long* strides) {
   const int col = j / a.page;

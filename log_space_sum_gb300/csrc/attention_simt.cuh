@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_simt(const __grid_constan
     l[i] = 0.f;
   }
   simt_zero(acc);
-  const int keys = max(before + min(t0 + per, s.n), 0), tiles = (keys + BT - 1) / BT;
+  const int keys = attn_keys(a, s, t0, per), tiles = (keys + BT - 1) / BT;
   const int j_first = static_cast<int>(static_cast<long long>(tiles) * split / a.splits);
   const int j_last = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / a.splits);
   const float k2 = a.scale * kLog2e;

@@ -1,0 +1,406 @@
+// Softmax attention forward on the tensor cores: bf16 elements, head sizes padded to 64 or 128, packed
+// prompts or a paged cache.
+//
+// A CTA takes two tiles of 128 rows (a token and a head of the group each) and walks the keys that they see
+// in tiles of 128:
+//
+//   scores  S = Q K^T     A = Q, B = K (K-major shared memory, by TMA), S in tensor memory
+//   softmax               one row per thread: the running maximum m and sum l, P = exp2(S scale - m) rounded to
+//                         bf16 and written over S
+//   output  O += P V      A = P in tensor memory, B = V (MN-major)
+//
+//   warps 0-3    softmax of the first tile's rows, warps 4-7 of the second's
+//   warp 8       TMA: Q once, then K and V tiles through one ring
+//   warp 9       MMA issuer: while one tile's softmax runs, the other's products do; zeros the rows of the last V
+//                tile that lie behind the keys, as what is there may be no number
+//
+// m is raised, and O in tensor memory multiplied by the ratio, only when a row's maximum has grown by more than 2^8:
+// P then holds values up to 256, whose relative rounding is the same, and l is summed in float32 from the
+// probabilities before their rounding. S of the next tile of keys is issued behind O of this one: MMAs of one thread
+// end in the order of their issue, so the arrival of S says that O may be touched.
+//
+// Bound by the tensor core: 2 x 128 x 128 x D products a tile of rows and keys, 512 cycles each at D = 128.
+#pragma once
+
+#include "attention.cuh"
+
+namespace pc {
+
+constexpr int kAtC = 128;          // rows and keys of a tile
+constexpr int kAtThreads = 384;
+
+struct AttnTcArgs {
+  AttnArgs a;
+  CUtensorMap q, k, v;
+  int k_ext, v_ext;         // 1: the map has the heads, 0: they share one
+  int box;                  // keys of one TMA box: 128, or a page's where it is smaller
+  int per;                  // tokens of a tile of rows
+};
+
+template <int DP>
+struct AtShape {
+  static constexpr uint32_t kTile = kAtC * DP * 2;
+  static constexpr int kSlots = DP == 128 ? 5 : 8;  // K and V in turn
+  static constexpr uint32_t kRing = 2 * kTile;      // behind the two Q tiles
+  static constexpr uint32_t kFixed = kRing + kSlots * kTile;
+  static constexpr uint32_t kBytes = kFixed + 512 + 1008;
+  static_assert(kBytes <= 232448, "shared memory per CTA");
+  static constexpr uint32_t kS = 0, kO = 256;  // tensor memory columns: S of both tiles, O of both
+};
+
+template <int kRegs>
+__device__ __forceinline__ void at_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void at_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+__device__ __forceinline__ float at_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void at_add2(float& a0, float& a1, float b0, float b1) {
+  add2(a0, a1, __float_as_uint(b0), __float_as_uint(b1));
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant__ AttnTcArgs args) {
+  using S = AtShape<DP>;
+  constexpr int C = kAtC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kFixed);
+  uint64_t *full = bars, *empty = bars + 8, *q_full = bars + 16, *s_full = bars + 17, *p_ready = bars + 19,
+           *o_full = bars + 21, *mma_done = bars + 24;
+  auto* limit = reinterpret_cast<unsigned long long*>(bars + 25);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+  uint32_t* bad = tmem_slot + 2;  // [16]: missing boxes of the last tiles of keys, a bit each
+
+  const AttnArgs& a = args.a;
+  const int heads = a.H / a.pack, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int hp = blockIdx.x % heads, rest = blockIdx.x / heads, split = rest % a.splits;
+  // the last tiles of a sequence see most keys: they come first
+  const int tiles = gridDim.x / (heads * a.splits);
+  const AttnTile tile = attn_tile(a, tiles - 1 - rest / a.splits, 2 * args.per);
+  if (tile.b < 0) return;
+  const AttnSeq s = attn_seq(a, tile.b);
+  const int hk = hp * a.pack / a.group, per = args.per, t0 = tile.at * 2 * per;
+  int keys[2], first, last[2];  // the tiles of keys [first, last) are this CTA's
+  keys[0] = attn_keys(a, s, t0, per);
+  keys[1] = attn_keys(a, s, t0 + per, per);
+  const int top_keys = max(keys[0], keys[1]), all = (top_keys + C - 1) / C;
+  first = static_cast<int>(static_cast<long long>(all) * split / a.splits);
+  const int end = static_cast<int>(static_cast<long long>(all) * (split + 1) / a.splits);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) last[x] = max(min(end, (keys[x] + C - 1) / C), first);
+  const int n_tiles = end - first;
+  // the tile whose last rows of V are behind the keys, or -1
+  const int tail = n_tiles > 0 && end == all && top_keys % C ? all - 1 : -1;
+  unsigned* status = a.status;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < S::kSlots; ++i) {
+        mbar_init(&full[i], 1);
+        mbar_init(&empty[i], 1);
+      }
+      mbar_init(q_full, 1);
+      for (int x = 0; x < 2; ++x) {
+        mbar_init(&s_full[x], 1);
+        mbar_init(&p_ready[x], 4);
+        mbar_init(&o_full[x], 1);
+      }
+      mbar_init(mma_done, 1);
+      *limit = first_wait_limit(status);
+      fence_barrier_init();
+    }
+    __syncwarp();
+    tmem_alloc(tmem_slot, 512);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < 8) {
+    at_regs_up<224>();
+    // ------------------------------------------------------------ softmax, row r of tile x per thread
+    const int x = warp >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t s_col = lanes + S::kS + x * C, o_col = lanes + S::kO + x * DP;
+    const int token = t0 + x * per + r / a.pack, h = hp * a.pack + r % a.pack;
+    const bool there = r < per * a.pack && token < s.n;
+    const int see = there ? min(s.ctx - s.n + token, keys[x] - 1) : -1;  // the last key of the row
+    const int see_all = __reduce_min_sync(0xffffffffu, see);
+    const float k2 = a.scale;  // times log2(e), not zero
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = first; j < last[x]; ++j) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[x], (j - first) & 1, status, kErrTimeoutEpilogue, *limit));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t v[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_32x32_async(s_col + c * 32, v[c]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_wait_ld(v[c]);
+      auto at = [&](int c) -> float { return __uint_as_float(v[c / 32][c % 32]); };
+      const int left = see - j * C;  // the columns 0 .. left are seen
+      const uint32_t hidden = k2 > 0.f ? 0xff800000u : 0x7f800000u;
+      if (see_all < j * C + C - 1) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+          if (c > left) v[c / 32][c % 32] = hidden;
+      }
+      if (a.page) {
+        const uint32_t gone = bad[j & 15];
+        if (gone) {
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            if (gone >> (c / 16) & 1) v[c / 32][c % 32] = hidden;
+        }
+      }
+      float best[4];
+      if (k2 > 0.f) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) best[c] = at(c);
+#pragma unroll
+        for (int c = 4; c < C; ++c) best[c % 4] = fmaxf(best[c % 4], at(c));
+        best[0] = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])) * k2;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) best[c] = at(c);
+#pragma unroll
+        for (int c = 4; c < C; ++c) best[c % 4] = fminf(best[c % 4], at(c));
+        best[0] = fminf(fminf(best[0], best[1]), fminf(best[2], best[3])) * k2;
+      }
+      if (j == first) {
+        m = best[0];
+      } else {
+        const bool raise = best[0] > m + 8.f;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float by = raise ? at_exp2(m - best[0]) : 1.f;  // 0 for the first key that is seen
+          if (raise) m = best[0];
+          l *= by;
+#pragma unroll 1
+          for (int c = 0; c < DP; c += 32) {
+            float o[32];
+            tmem_ld_32x32(o_col + c, o);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mul2(o[i], o[i + 1], by, by);
+            tmem_st_32x32(o_col + c, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : -m;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float e0 = __uint_as_float(v[c][2 * i]), e1 = __uint_as_float(v[c][2 * i + 1]);
+          fma2(e0, e1, k2, base, base);
+          e0 = at_exp2(e0);
+          e1 = at_exp2(e1);
+          at_add2(sum[(i & 1) * 2], sum[(i & 1) * 2 + 1], e0, e1);
+          p[i] = pack_bf16x2(e0, e1);
+        }
+        tmem_st_32x16(s_col + c * 16, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_ready[x]);
+    }
+    if (ok && last[x] > first) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[x], 0, status, kErrTimeoutEpilogue, *limit));
+      tc_fence_after();
+    }
+    if (ok) {
+      const float by = l == 0.f ? 0.f : 1.f / l;
+      const bool some = last[x] > first;  // (uniform) otherwise O was never written
+      const long long t = s.start + token;
+      const bool joined = a.splits > 1;
+      const long long row = joined ? split * static_cast<long long>(a.T) * a.H + t * a.H + h : 0;
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + t * a.os[0] + h * a.os[1];
+#pragma unroll 1
+      for (int c = 0; c < DP; c += 32) {
+        float u[32];
+        if (some) tmem_ld_32x32(o_col + c, u);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) u[i] = some && l != 0.f ? u[i] * by : 0.f;
+        if (there) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 8) {
+            if (c + i >= a.D) continue;
+            if (joined) {
+              float4* p = reinterpret_cast<float4*>(a.part_o + row * a.D + c + i);
+              p[0] = make_float4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+              p[1] = make_float4(u[i + 4], u[i + 5], u[i + 6], u[i + 7]);
+            } else {
+              *reinterpret_cast<uint4*>(o + c + i) =
+                  make_uint4(pack_bf16x2(u[i], u[i + 1]), pack_bf16x2(u[i + 2], u[i + 3]), pack_bf16x2(u[i + 4], u[i + 5]),
+                             pack_bf16x2(u[i + 6], u[i + 7]));
+            }
+          }
+        }
+      }
+      if (there) {
+        if (joined) a.part_ml[row] = make_float2(m, l);
+        else if (a.lse) a.lse[static_cast<long long>(h) * a.T + t] = (m + log2f(l)) * kLn2;
+      }
+    }
+  } else {
+    at_regs_down<48>();
+    if (warp == 8) {
+      // ------------------------------------------------------------ TMA producer
+      const int boxes = C / args.box;
+      int issued = 0;
+      bool ok = true;
+      if (n_tiles > 0) {
+        if (lane == 0) {
+          const int parts = (last[0] > first) + (last[1] > first);
+          mbar_arrive_expect_tx(q_full, parts * per * a.pack * DP * 2);
+          for (int x = 0; x < 2; ++x)
+            if (last[x] > first)
+              for (int d = 0; d < DP; d += 64)
+                tma_load_4d(smem + x * S::kTile + d * C * 2, &args.q, q_full, d, hp * a.pack,
+                            s.start + t0 + x * per, 0);
+        }
+        int page = a.pages;  // of this lane's box of keys; a.pages: none, whose box is zeros
+        auto lookup = [&](int j) {
+          if (!a.page || lane >= boxes) return;
+          const int key = j * C + lane * args.box;
+          page = a.pages;
+          if (key < top_keys) {
+            const int col = key / a.page;  // (keys end within the table)
+            const int id = a.tables[static_cast<long long>(tile.b) * a.width + col];
+            if (id >= 0 && id < a.pages) page = id;
+          }
+        };
+        lookup(first);
+        for (int n = 0; ok && n < 2 * n_tiles; ++n) {  // K, V, K, V, ...
+          const int j = first + n / 2, slot = n % S::kSlots;
+          uint8_t* to = smem + S::kRing + slot * S::kTile;
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[slot], ((n / S::kSlots) & 1) ^ 1, status, kErrTimeoutProducer));
+          if (!ok) break;
+          if (n % 2 == 0 && a.page) {
+            const bool gone = lane < boxes && j * C + lane * args.box < top_keys && page == a.pages;
+            if (gone) atomicOr(status, kErrPage);
+            // bits of 16 keys
+            uint32_t bits = gone ? ((1u << (args.box / 16)) - 1) << (lane * args.box / 16) : 0u;
+            bits = __reduce_or_sync(0xffffffffu, bits);
+            if (lane == 0) bad[j & 15] = bits;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_expect_tx(&full[slot], S::kTile);
+          __syncwarp();
+          const CUtensorMap* map = n % 2 ? &args.v : &args.k;
+          const int head = hk * (n % 2 ? args.v_ext : args.k_ext);
+          if (lane < boxes) {
+            for (int d = 0; d < DP; d += 64) {
+              if (a.page)
+                tma_load_4d(to + d * C * 2 + lane * args.box * 128, map, &full[slot], d, (j * C + lane * args.box) % a.page, head,
+                            page);
+              else
+                tma_load_4d(to + d * C * 2, map, &full[slot], d, s.start + j * C, head, 0);
+            }
+          }
+          issued = n + 1;
+          if (n % 2 == 1 && j + 1 < end) lookup(j + 1);
+        }
+        for (int n = max(issued - S::kSlots, 0); n < issued; ++n)  // every copy lands before the CTA leaves
+          mbar_wait(&full[n % S::kSlots], (n / S::kSlots) & 1, status, kErrTimeoutDrain);
+        mbar_wait(q_full, 0, status, kErrTimeoutDrain);
+      }
+    } else if (warp == 9) {
+      // ----------------- MMA issuer: the whole warp in step (uniform addresses), one lane issues
+      constexpr uint32_t idesc_s = umma_idesc(1, 128, C);
+      constexpr uint32_t idesc_o = umma_idesc(1, 128, DP) | kIdescBMN;
+      const bool leader = elect_one();
+      auto wait = [&](uint64_t* bar, uint32_t ph) {
+        const bool got = __all_sync(0xffffffffu, mbar_wait(bar, ph, status, kErrTimeoutMma));
+        tc_fence_after();
+        return got;
+      };
+      const uint32_t base = smem_addr(smem);
+      auto slot_addr = [&](int n) { return base + S::kRing + (n % S::kSlots) * S::kTile; };
+      auto slot_full = [&](int n) { return wait(&full[n % S::kSlots], (n / S::kSlots) & 1); };
+      auto scores = [&](int x, int n) {  // S of tile x and of the n-th tile of keys
+        const uint64_t q = umma_desc_sw128(base + x * S::kTile), k = umma_desc_sw128(slot_addr(2 * n));
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < DP / 16; ++kk) {
+            const uint32_t off = ((kk / 4) * C * 128 + (kk % 4) * 32) >> 4;
+            umma_bf16(tmem + S::kS + x * C, q + off, k + off, idesc_s, kk ? 1u : 0u);
+          }
+          umma_commit(&s_full[x]);
+        }
+        __syncwarp();
+      };
+      auto output = [&](int x, int n) {  // O += P V
+        const uint64_t v = umma_desc_sw128_mn(slot_addr(2 * n + 1), C * 128);
+        if (leader) {
+#pragma unroll
+          for (int kk = 0; kk < C / 16; ++kk)
+            umma_bf16_ts(tmem + S::kO + x * DP, tmem + S::kS + x * C + kk * 8, v + kk * (2048 >> 4), idesc_o,
+                         n > 0 || kk > 0 ? 1u : 0u);
+          if (first + n + 1 == last[x]) umma_commit(&o_full[x]);
+        }
+        __syncwarp();
+      };
+      auto release = [&](int n) {
+        if (leader) umma_commit(&empty[n % S::kSlots]);
+        __syncwarp();
+      };
+      bool ok = n_tiles > 0 && wait(q_full, 0) && slot_full(0);
+      if (ok) {
+        for (int x = 0; x < 2; ++x)
+          if (first < last[x]) scores(x, 0);
+        release(0);
+      }
+      for (int n = 0; ok && n < n_tiles; ++n) {
+        const int j = first + n;
+        ok = slot_full(2 * n + 1);
+        if (ok && j == tail) {  // rows behind the keys: zeros (the softmax of this tile runs meanwhile)
+          const uint32_t v = slot_addr(2 * n + 1);
+          for (int i = (top_keys - j * C) * 8 + lane; i < C * 8; i += 32)
+#pragma unroll
+            for (int d = 0; d < DP; d += 64) st_shared_v4(v + d * C * 2 + i * 16, 0u, 0u, 0u, 0u);
+          fence_async_shared();
+          __syncwarp();
+        }
+        ok = ok && (n + 1 == n_tiles || slot_full(2 * n + 2));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (ok && j < last[x]) {
+            ok = wait(&p_ready[x], n & 1);
+            if (ok) {
+              output(x, n);
+              if (j + 1 < last[x]) scores(x, n + 1);
+            }
+          }
+        }
+        if (ok) {
+          release(2 * n + 1);
+          if (n + 1 < n_tiles) release(2 * n + 2);
+        }
+      }
+      if (leader) umma_commit(mma_done);
+      __syncwarp();
+      mbar_wait(mma_done, 0, status, kErrTimeoutDrain);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace pc

@@ -191,9 +191,9 @@ pc_status_t encode_operand_map(CUtensorMap* map, const Operand& op, pc_precision
                                int box_rows, int part, bool swizzle = true, long long group_stride = 0);
 
 // 4-D tensor map over bf16 data: dims innermost first (the innermost contiguous), strides of
-// dims 1..3 in elements (multiples of 8), box {box_cols, box_rows, 1, 1} with 128-byte
+// dims 1..3 in elements (multiples of 8), box {box_cols, box_rows, box_depth, 1} with 128-byte
 // swizzle, zero fill outside the tensor.
 pc_status_t encode_bf16_map4(CUtensorMap* map, const void* base, const long long (&dims)[4],
-                             const long long (&strides)[3], int box_cols, int box_rows);
+                             const long long (&strides)[3], int box_cols, int box_rows, int box_depth = 1);
 
 }  // namespace pc
