@@ -13,6 +13,7 @@
 
 #include "attention_simt.cuh"
 #include "attention_tc.cuh"
+#include "attention_bwd_tc.cuh"
 #include "pc_host.h"
 
 namespace pc {
@@ -276,6 +277,56 @@ pc_status_t launch_bwd(const AttnBwdArgs& b, cudaStream_t s, int* launches) {
                      : launch_simt_bwd_dim<T, 256>(b, s);
 }
 
+template <int DP>
+pc_status_t launch_bwd_tc_dim(const AttnBwdTcArgs& t, cudaStream_t s) {
+  const AttnArgs& a = t.b.a;
+  constexpr int smem = AtBwdShape<DP>::kBytes, kLanesRow = DP / 8;
+  const long long rows = (static_cast<long long>(a.T) * a.H * kLanesRow + 255) / 256;
+  const long long keys = tiles_of(a, kAtC) * a.Hk, tiles = tiles_of(a, t.per) * (a.H / a.pack);
+  PC_CHECK(rows < INT_MAX && keys < INT_MAX && tiles < INT_MAX, PC_ERR_SHAPE, "T * H = %lld rows: too many",
+           static_cast<long long>(a.T) * a.H);
+  PC_TRY((allow_smem<k_attn_dkdv_tc<DP>>(smem)));
+  PC_TRY((allow_smem<k_attn_dq_tc<DP>>(smem)));
+  k_attn_rows_tc<kLanesRow><<<static_cast<unsigned>(rows), 256, 0, s>>>(t);
+  PC_LAUNCH_CHECK();
+  k_attn_dkdv_tc<DP><<<static_cast<unsigned>(keys), kAtThreads, smem, s>>>(t);
+  PC_LAUNCH_CHECK();
+  k_attn_dq_tc<DP><<<static_cast<unsigned>(tiles), kAtThreads, smem, s>>>(t);
+  PC_LAUNCH_CHECK();
+  return PC_OK;
+}
+
+// The gradient on the tensor cores where the sizes, strides and alignments allow.
+pc_status_t try_bwd_tc(const AttnBwdArgs& from, pc_dtype_t dt, cudaStream_t s, int* launches, bool* done) {
+  *done = false;
+  const AttnArgs& a = from.a;
+  if (!tc_sizes(a, dt) || !tc_out(a, a.o, a.os, a.H) || !tc_out(a, from.d_o, from.gs, a.H) || !tc_out(a, from.dq, from.dqs, a.H) ||
+      !tc_out(a, from.dk, from.dks, a.Hk) || !tc_out(a, from.dv, from.dvs, a.Hk))
+    return PC_OK;
+  AttnBwdTcArgs t{};
+  t.b = from;
+  t.per = kAtC / a.pack;
+  t.k2 = a.scale * kLog2e;
+  t.delta = from.delta;
+  t.lse2 = from.delta + static_cast<long long>(a.T) * a.H;
+  pc_status_t st = PC_OK;
+  if (!tc_row_map(&t.q, a, a.q, a.qs, t.per, &st)) return PC_OK;
+  PC_TRY(st);
+  if (!tc_row_map(&t.d_o, a, from.d_o, from.gs, t.per, &st)) return PC_OK;
+  PC_TRY(st);
+  if (!tc_key_map(&t.k, &t.k_ext, a.k, a.D, a.T, a.ks[1], a.Hk, a.ks[2], 1, 8, kAtC, &st)) return PC_OK;
+  PC_TRY(st);
+  if (!tc_key_map(&t.v, &t.v_ext, a.v, a.D, a.T, a.vs[1], a.Hk, a.vs[2], 1, 8, kAtC, &st)) return PC_OK;
+  PC_TRY(st);
+  PC_TRY(a.D <= 64 ? launch_bwd_tc_dim<64>(t, s) : launch_bwd_tc_dim<128>(t, s));
+  *launches += 3;
+  *done = true;
+  return PC_OK;
+}
+
+// Workspace of the gradient: delta, and on the tensor cores the rows' logarithms in their tiles' order.
+size_t bwd_bytes(int T, int H, pc_dtype_t dt) { return static_cast<size_t>(T) * H * sizeof(float) * (dt == PC_BF16 ? 2 : 1); }
+
 // ------------------------------------------------------------------------- checks
 pc_status_t check_attn(int B, int T, int H, int Hk, int D, pc_dtype_t dt) {
   PC_TRY(check_dtype(dt));
@@ -337,7 +388,7 @@ pc_status_t pc_attention_bwd_workspace(int B, int T, int H, int Hk, int D, pc_dt
   pc::clear_error();
   PC_CHECK(bytes, PC_ERR_NULL, "bytes must not be NULL");
   PC_TRY(pc::check_attn(B, T, H, Hk, D, dtype));
-  *bytes = static_cast<size_t>(T) * H * sizeof(float);
+  *bytes = pc::bwd_bytes(T, H, dtype);
   return PC_OK;
 }
 
@@ -384,7 +435,7 @@ pc_status_t pc_attention_bwd(int B, int T, int H, int Hk, int D, const void* q, 
   for (int i = 5; i < 8; ++i)
     for (int j = 0; j < i; ++j) PC_CHECK(all[i] != all[j], PC_ERR_UNSUPPORTED, "%s may not be %s itself", names[i], names[j]);
   for (int i = 5; i < 8; ++i) PC_TRY(pc::check_out(names[i], strides + 2 * i, T, i == 5 ? H : Hk));
-  const size_t need = static_cast<size_t>(T) * H * sizeof(float);
+  const size_t need = pc::bwd_bytes(T, H, dtype);
   PC_CHECK(ws && ws_bytes >= need, PC_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
   PC_CHECK(pc::aligned16(ws), PC_ERR_ALIGNMENT, "workspace is not 16-byte aligned");
   pc::AttnBwdArgs b{};
@@ -410,7 +461,11 @@ pc_status_t pc_attention_bwd(int B, int T, int H, int Hk, int D, const void* q, 
     b.dks[i] = strides[12 + i];
     b.dvs[i] = strides[14 + i];
   }
+  PC_CHECK(b.a.status, PC_ERR_CUDA, "device status word unavailable");
   int launches = 0;
+  bool done = false;
+  PC_TRY(pc::try_bwd_tc(b, dtype, stream, &launches, &done));
+  if (done) return PC_OK;
   return dtype == PC_BF16 ? pc::launch_bwd<__nv_bfloat16>(b, stream, &launches) : pc::launch_bwd<float>(b, stream, &launches);
 }
 

@@ -81,6 +81,62 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, int tile, int p
   return {-1, 0};
 }
 
+// The tile of the given rank when all sequences' tiles are sorted by cost, the dearest first: with rows (kKeys false)
+// the last of a sequence, which see most keys, with keys its first, which most rows see. (Past 128 sequences the
+// search would cost more than the order gives: sequence by sequence, then.) The whole warp takes part.
+template <bool kKeys>
+__device__ __forceinline__ AttnTile attn_tile_by_cost(const AttnArgs& a, int rank, int per) {
+  if (!a.starts) {
+    const int each = (a.T / a.B + per - 1) / per;
+    if (each == 0 || rank >= a.B * each) return {-1, 0};
+    return {rank % a.B, kKeys ? rank / a.B : each - 1 - rank / a.B};
+  }
+  if (a.B > 128) {
+    AttnTile tile = attn_tile(a, rank, per);
+    if (!kKeys && tile.b >= 0) tile.at = (attn_seq(a, tile.b).n + per - 1) / per - 1 - tile.at;
+    return tile;
+  }
+  const int lane = threadIdx.x & 31;
+  int n[4], top = 0;  // tiles of this lane's sequences
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = lane + 32 * i;
+    n[i] = b < a.B ? (attn_seq(a, b).n + per - 1) / per : 0;
+    top = max(top, n[i]);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  auto dearer = [&](int e) {  // tiles of cost e or more, of 1 .. n
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum += max(n[i] - e + 1, 0);
+    return __reduce_add_sync(0xffffffffu, sum);
+  };
+  if (rank >= dearer(1)) return {-1, 0};
+  int lo = 1, hi = top + 1, above = 0;  // dearer(lo) > rank >= dearer(hi) = above
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1, got = dearer(mid);
+    if (got > rank) {
+      lo = mid;
+    } else {
+      hi = mid;
+      above = got;
+    }
+  }
+  int left = rank - above;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned has = __ballot_sync(0xffffffffu, n[i] >= lo);
+    const int count = __popc(has);
+    if (left < count) {
+      const unsigned it = __ballot_sync(0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == left);
+      const int l = __ffs(it) - 1;
+      return {l + 32 * i, kKeys ? __shfl_sync(0xffffffffu, n[i], l) - lo : lo - 1};
+    }
+    left -= count;
+  }
+  return {-1, 0};
+}
+
 // The keys that rows [t0, t0 + per) of a sequence see: none of them lies past the table.
 __device__ __forceinline__ int attn_keys(const AttnArgs& a, const AttnSeq& s, int t0, int per) {
   if (t0 >= s.n) return 0;

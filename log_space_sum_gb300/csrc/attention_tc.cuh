@@ -81,9 +81,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
   const AttnArgs& a = args.a;
   const int heads = a.H / a.pack, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hp = blockIdx.x % heads, rest = blockIdx.x / heads, split = rest % a.splits;
-  // the last tiles of a sequence see most keys: they come first
-  const int tiles = gridDim.x / (heads * a.splits);
-  const AttnTile tile = attn_tile(a, tiles - 1 - rest / a.splits, 2 * args.per);
+  const AttnTile tile = attn_tile_by_cost<false>(a, rest / a.splits, 2 * args.per);
   if (tile.b < 0) return;
   const AttnSeq s = attn_seq(a, tile.b);
   const int hk = hp * a.pack / a.group, per = args.per, t0 = tile.at * 2 * per;
