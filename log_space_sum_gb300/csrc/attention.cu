@@ -184,24 +184,23 @@ bool tc_out(const AttnArgs& a, const void* p, const long long* s, int heads) {
   return aligned16(p) && (a.T <= 1 || token % 8 == 0) && (heads <= 1 || head % 8 == 0);
 }
 
-// Ranges of the keys: where the tiles of rows leave SMs without work, none with fewer than four tiles of keys.
-int tc_splits(const AttnArgs& a) {
-  if (!a.page) return 1;
-  const long long ctas = tiles_of(a, 2 * (kAtC / a.pack)) * (a.H / a.pack);
-  const long long most = static_cast<long long>(a.width) * a.page / (4 * kAtC), want = num_sms() / (ctas ? ctas : 1);
-  long long s = want < most ? want : most;
-  if (s > kMaxSplits) s = kMaxSplits;
-  return s < 1 ? 1 : static_cast<int>(s);
+// Parts that are joined: of rows of the two segments that a CTA's range may share with its neighbours.
+size_t tc_part_bytes(const AttnArgs& a) {
+  if (!a.page) return 0;
+  return static_cast<size_t>(num_sms()) * (2 * 2 * kAtC * (a.D + 2) * sizeof(float) + sizeof(AttnPart)) + 768;
 }
 
 template <int DP>
 pc_status_t launch_tc_dim(const AttnTcArgs& t, cudaStream_t s) {
   const AttnArgs& a = t.a;
   constexpr int smem = AtShape<DP>::kBytes;
-  const long long ctas = tiles_of(a, 2 * t.per) * (a.H / a.pack) * a.splits;
-  PC_CHECK(ctas < INT_MAX, PC_ERR_SHAPE, "%lld tiles of rows: fewer than 2^31 wanted", ctas);
+  long long ctas = num_sms();
+  if (!a.page && tiles_of(a, 2 * t.per) * (a.H / a.pack) < ctas) ctas = tiles_of(a, 2 * t.per) * (a.H / a.pack);
   PC_TRY((allow_smem<k_attn_tc<DP>>(smem)));
   k_attn_tc<DP><<<static_cast<unsigned>(ctas), kAtThreads, smem, s>>>(t);
+  PC_LAUNCH_CHECK();
+  if (!a.page) return PC_OK;
+  k_attn_tc_join<<<dim3(static_cast<unsigned>(ctas), 8), 256, 0, s>>>(t);
   PC_LAUNCH_CHECK();
   return PC_OK;
 }
@@ -225,13 +224,15 @@ pc_status_t try_tc(const AttnArgs& from, pc_dtype_t dt, void* ws, cudaStream_t s
   PC_TRY(st);
   a.scale *= kLog2e;
   if (a.scale == 0.f) a.scale = FLT_MIN;  // keys that are hidden by an infinite score stay hidden
-  carve_parts(a, tc_splits(a), ws);
-  PC_TRY(a.D <= 64 ? launch_tc_dim<64>(t, s) : launch_tc_dim<128>(t, s));
-  ++*launches;
-  if (a.splits > 1) {
-    PC_TRY(launch_join<__nv_bfloat16>(a, s));
-    ++*launches;
+  if (a.page) {
+    Carver c(ws);
+    const size_t rows = static_cast<size_t>(num_sms()) * 2 * 2 * kAtC;
+    a.part_o = static_cast<float*>(c.take(rows * a.D * sizeof(float)));
+    a.part_ml = static_cast<float2*>(c.take(rows * sizeof(float2)));
+    a.part_head = static_cast<AttnPart*>(c.take(num_sms() * sizeof(AttnPart)));
   }
+  PC_TRY(a.D <= 64 ? launch_tc_dim<64>(t, s) : launch_tc_dim<128>(t, s));
+  *launches += a.page ? 2 : 1;
   *done = true;
   return PC_OK;
 }
@@ -374,9 +375,8 @@ AttnArgs make_args(int B, int T, int H, int Hk, int D, float scale, const int32_
 const int32_t* some_starts() { return reinterpret_cast<const int32_t*>(uintptr_t(4)); }
 
 size_t paged_bytes(const AttnArgs& a, pc_dtype_t dt) {
-  int splits = simt_splits(a);
-  if (tc_sizes(a, dt) && tc_splits(a) > splits) splits = tc_splits(a);
-  return part_bytes(a, splits);
+  const size_t simt = part_bytes(a, simt_splits(a)), tc = tc_sizes(a, dt) ? tc_part_bytes(a) : 0;
+  return simt > tc ? simt : tc;
 }
 
 }  // namespace

@@ -11,6 +11,11 @@
 
 namespace pc {
 
+// A unit of work in several parts: how many (0: none), its first token, the sequence's tokens from there on, its heads.
+struct AttnPart {
+  int parts, token, left, hp;
+};
+
 struct AttnArgs {
   const void *q, *k, *v;
   void* o;
@@ -27,6 +32,8 @@ struct AttnArgs {
   int splits;
   float* part_o;           // [splits][T * H][D]
   float2* part_ml;         // [splits][T * H]
+  // tensor cores: two places a CTA, of 256 rows each, and for each CTA the unit whose first part it holds
+  AttnPart* part_head;
   unsigned* status;
 };
 

@@ -70,14 +70,6 @@ struct AtBwdShape {
   static_assert(kBytes <= 232448, "shared memory per CTA");
 };
 
-// The lanes of a warp in step at a barrier, for the roles of one kernel.
-__device__ __forceinline__ bool at_wait(uint64_t* bar, uint32_t parity, unsigned* status, unsigned code,
-                                        unsigned long long limit = kWaitLimitNs) {
-  const bool got = __all_sync(0xffffffffu, mbar_wait(bar, parity, status, code, limit));
-  tc_fence_after();
-  return got;
-}
-
 // Zeros rows [from, to) of a tile (by one warp), for products that read it whole.
 template <int DP>
 __device__ __forceinline__ void at_zero_rows(uint32_t tile, int from, int to) {
