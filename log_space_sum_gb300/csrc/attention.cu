@@ -14,6 +14,7 @@
 #include "attention_simt.cuh"
 #include "attention_tc.cuh"
 #include "attention_bwd_tc.cuh"
+#include "attention_step.cuh"
 #include "pc_host.h"
 
 namespace pc {
@@ -184,23 +185,24 @@ bool tc_out(const AttnArgs& a, const void* p, const long long* s, int heads) {
   return aligned16(p) && (a.T <= 1 || token % 8 == 0) && (heads <= 1 || head % 8 == 0);
 }
 
-// Parts that are joined: of rows of the two segments that a CTA's range may share with its neighbours.
-size_t tc_part_bytes(const AttnArgs& a) {
-  if (!a.page) return 0;
-  return static_cast<size_t>(num_sms()) * (2 * 2 * kAtC * (a.D + 2) * sizeof(float) + sizeof(AttnPart)) + 768;
+// Units over a cache: ranges of the keys, where the units leave SMs without work, none with fewer than four tiles.
+int tc_splits(const AttnArgs& a) {
+  if (!a.page) return 1;
+  const long long ctas = tiles_of(a, 2 * (kAtC / a.pack)) * (a.H / a.pack);
+  const long long most = static_cast<long long>(a.width) * a.page / (4 * kAtC), want = num_sms() / (ctas ? ctas : 1);
+  long long s = want < most ? want : most;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return s < 1 ? 1 : static_cast<int>(s);
 }
 
 template <int DP>
 pc_status_t launch_tc_dim(const AttnTcArgs& t, cudaStream_t s) {
   const AttnArgs& a = t.a;
   constexpr int smem = AtShape<DP>::kBytes;
-  long long ctas = num_sms();
-  if (!a.page && tiles_of(a, 2 * t.per) * (a.H / a.pack) < ctas) ctas = tiles_of(a, 2 * t.per) * (a.H / a.pack);
+  const long long ctas = tiles_of(a, 2 * t.per) * (a.H / a.pack) * a.splits;
+  PC_CHECK(ctas < INT_MAX, PC_ERR_SHAPE, "%lld tiles of rows: fewer than 2^31 wanted", ctas);
   PC_TRY((allow_smem<k_attn_tc<DP>>(smem)));
   k_attn_tc<DP><<<static_cast<unsigned>(ctas), kAtThreads, smem, s>>>(t);
-  PC_LAUNCH_CHECK();
-  if (!a.page) return PC_OK;
-  k_attn_tc_join<<<dim3(static_cast<unsigned>(ctas), 8), 256, 0, s>>>(t);
   PC_LAUNCH_CHECK();
   return PC_OK;
 }
@@ -224,15 +226,79 @@ pc_status_t try_tc(const AttnArgs& from, pc_dtype_t dt, void* ws, cudaStream_t s
   PC_TRY(st);
   a.scale *= kLog2e;
   if (a.scale == 0.f) a.scale = FLT_MIN;  // keys that are hidden by an infinite score stay hidden
-  if (a.page) {
-    Carver c(ws);
-    const size_t rows = static_cast<size_t>(num_sms()) * 2 * 2 * kAtC;
-    a.part_o = static_cast<float*>(c.take(rows * a.D * sizeof(float)));
-    a.part_ml = static_cast<float2*>(c.take(rows * sizeof(float2)));
-    a.part_head = static_cast<AttnPart*>(c.take(num_sms() * sizeof(AttnPart)));
-  }
+  carve_parts(a, tc_splits(a), ws);
   PC_TRY(a.D <= 64 ? launch_tc_dim<64>(t, s) : launch_tc_dim<128>(t, s));
-  *launches += a.page ? 2 : 1;
+  ++*launches;
+  if (a.splits > 1) {
+    PC_TRY(launch_join<__nv_bfloat16>(a, s));
+    ++*launches;
+  }
+  *done = true;
+  return PC_OK;
+}
+
+// ------------------------------------------------------------- few new tokens over a cache
+// Rows of a sequence's unit: 16, or 32 where the sequences' tokens fill more.
+int step_rows(const AttnArgs& a) { return static_cast<long long>(a.T) * a.pack <= 16ll * a.B ? 16 : 32; }
+
+// Where a sequence's rows fill no more than that the cache's bandwidth decides, and tiles of 128 rows would stand empty.
+bool step_sizes(const AttnArgs& a, pc_dtype_t dt) {
+  return dt == PC_BF16 && a.page && a.page % kStKeys == 0 && a.pages > 0 && a.D % 8 == 0 && a.D <= 128 &&
+         static_cast<long long>(a.T) * a.pack <= 32ll * a.B;
+}
+
+int step_ctas() { return 2 * num_sms(); }
+
+size_t step_bytes(const AttnArgs& a) {
+  return static_cast<size_t>(step_ctas()) * (2 * step_rows(a) * (a.D * sizeof(float) + sizeof(float2)) + sizeof(AttnPart)) + 768;
+}
+
+template <int DP, int MB>
+pc_status_t launch_step_dim(const AttnStepArgs& t, cudaStream_t s) {
+  constexpr int smem = StShape<DP>::kBytes;
+  PC_TRY((allow_smem<k_attn_step<DP, MB>>(smem)));
+  k_attn_step<DP, MB><<<step_ctas(), kStThreads, smem, s>>>(t);
+  PC_LAUNCH_CHECK();
+  // its start overlaps the first kernel's end
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(step_ctas(), MB * 4);
+  config.blockDim = dim3(128);
+  config.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &attr;
+  config.numAttrs = 1;
+  PC_CUDA(cudaLaunchKernelEx(&config, k_attn_step_join, t, MB * 16));
+  count_launch();
+  return PC_OK;
+}
+
+// 16-byte pieces of a cache's rows, and of q's in 4-byte ones.
+bool step_strides(const AttnArgs& a) {
+  long long all = 0;
+  for (int i = 0; i < 3; ++i) all |= a.ks[i] | a.vs[i];
+  return aligned16(a.k) && aligned16(a.v) && all % 8 == 0 && reinterpret_cast<uintptr_t>(a.q) % 4 == 0 && a.qs[0] % 2 == 0 &&
+         a.qs[1] % 2 == 0;
+}
+
+pc_status_t try_step(const AttnArgs& from, pc_dtype_t dt, void* ws, cudaStream_t s, int* launches, bool* done) {
+  *done = false;
+  if (!step_sizes(from, dt) || !step_strides(from)) return PC_OK;
+  AttnStepArgs t{};
+  t.a = from;
+  AttnArgs& a = t.a;
+  a.scale *= kLog2e;
+  const int rows = step_rows(a);
+  t.per = rows / a.pack;
+  Carver c(ws);
+  const size_t parts = static_cast<size_t>(step_ctas()) * 2 * rows;
+  a.part_o = static_cast<float*>(c.take(parts * a.D * sizeof(float)));
+  a.part_ml = static_cast<float2*>(c.take(parts * sizeof(float2)));
+  a.part_head = static_cast<AttnPart*>(c.take(step_ctas() * sizeof(AttnPart)));
+  if (a.D <= 64) PC_TRY((rows == 16 ? launch_step_dim<64, 1>(t, s) : launch_step_dim<64, 2>(t, s)));
+  else PC_TRY((rows == 16 ? launch_step_dim<128, 1>(t, s) : launch_step_dim<128, 2>(t, s)));
+  *launches += 2;
   *done = true;
   return PC_OK;
 }
@@ -242,7 +308,8 @@ pc_status_t run_fwd(AttnArgs& a, pc_dtype_t dt, void* ws, cudaStream_t s) {
   PC_CHECK(a.status, PC_ERR_CUDA, "device status word unavailable");
   int launches = 0;
   bool done = false;
-  PC_TRY(try_tc(a, dt, ws, s, &launches, &done));
+  PC_TRY(try_step(a, dt, ws, s, &launches, &done));
+  if (!done) PC_TRY(try_tc(a, dt, ws, s, &launches, &done));
   if (done) return PC_OK;
   return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, ws, s, &launches) : launch_simt<float>(a, ws, s, &launches);
 }
@@ -375,8 +442,10 @@ AttnArgs make_args(int B, int T, int H, int Hk, int D, float scale, const int32_
 const int32_t* some_starts() { return reinterpret_cast<const int32_t*>(uintptr_t(4)); }
 
 size_t paged_bytes(const AttnArgs& a, pc_dtype_t dt) {
-  const size_t simt = part_bytes(a, simt_splits(a)), tc = tc_sizes(a, dt) ? tc_part_bytes(a) : 0;
-  return simt > tc ? simt : tc;
+  size_t most = part_bytes(a, simt_splits(a));  // in whichever variant strides and alignments will allow
+  const size_t tc = tc_sizes(a, dt) ? part_bytes(a, tc_splits(a)) : 0, step = step_sizes(a, dt) ? step_bytes(a) : 0;
+  if (tc > most) most = tc;
+  return step > most ? step : most;
 }
 
 }  // namespace

@@ -32,7 +32,7 @@ struct AttnArgs {
   int splits;
   float* part_o;           // [splits][T * H][D]
   float2* part_ml;         // [splits][T * H]
-  // tensor cores: two places a CTA, of 256 rows each, and for each CTA the unit whose first part it holds
+  // few rows over a cache: two places a CTA, and for each CTA the unit whose first part it holds
   AttnPart* part_head;
   unsigned* status;
 };

@@ -1,0 +1,448 @@
+// Softmax attention of few new tokens over a paged cache: bf16 elements, head sizes padded to 64 or 128, pages of whole
+// groups of 16 tokens.
+//
+// Bound by the cache: each key and value is read once for the 16 or 32 rows (a token and a head of the group each) that
+// see it, and multiplied with far less than the tensor cores could. So no tile waits for another: a warp streams groups of
+// 16 keys through shared memory of its own (cp.async, three groups in flight) and keeps its rows' running maximum, sum and
+// output in registers, with 16 x 8 x 16 products (mma.sync; tcgen05 would hold tiles of 128 keys back for its longer chain
+// from scores to outputs: 213 us against 279 for 64 sequences to 8192):
+//
+//   S = Q K^T    A = Q in registers, B = K (ldmatrix)
+//   O += P V     A = P, the registers of S rounded to bf16, B = V (ldmatrix, transposed)
+//
+// The four warps of a CTA take the groups in turn and add up what they have at the end of a unit of work. Two CTAs
+// stay on each SM, so that one's loads run while the other adds up.
+//
+// Work: all units' tiles of 128 keys in one row (sequence by sequence), cut into even ranges, one a CTA: a token of one
+// long sequence fills the GPU as many sequences of any lengths do. What a cut goes through is joined by a second kernel.
+#pragma once
+
+#include "attention.cuh"
+
+namespace pc {
+
+constexpr int kStThreads = 128, kStWarps = kStThreads / 32, kStStages = 3;
+constexpr int kStKeys = 16, kStTile = 128;  // keys of a group, and of a tile that ranges are counted in
+
+struct AttnStepArgs {
+  AttnArgs a;
+  int per;  // tokens of a unit's rows
+};
+
+template <int DP>
+struct StShape {
+  static constexpr int kGroup = kStKeys * DP * 2;               // bytes of a group's keys
+  static constexpr int kWarp = kStStages * 2 * kGroup;          // a warp's ring
+  static constexpr int kBytes = kStWarps * kWarp + kStWarps * 32 * 8;
+};
+
+// One stretch of work of a CTA: tiles [first, end) of the keys that a unit's rows see.
+struct StSegment {
+  int b, hp, t0;   // sequence (-1: no more work), heads, first token of the rows
+  int first, end;
+  int slot;        // where the part goes that others have to be joined with; -1: the rows' output is whole
+};
+
+// The parts of a CTA's range (for a whole warp).
+struct StRanges {
+  const AttnArgs& a;
+  const int per, heads;
+  int b, at, hp, j, cost, tiles;  // where the range stands
+  long long left, grid, all, pos;
+  AttnSeq s;
+
+  __device__ __forceinline__ StRanges(const AttnArgs& args, int tokens) : a(args), per(tokens), heads(args.H / args.pack) {
+    const int lane = threadIdx.x & 31;
+    left = 0;
+    all = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      long long v = sequence_cost(b0 + lane);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+      all += v;
+    }
+    // a tile a CTA at least
+    grid = min(static_cast<long long>(gridDim.x), all);
+    if (blockIdx.x >= grid) return;
+    pos = blockIdx.x * all / grid;
+    left = (blockIdx.x + 1) * all / grid - pos;
+    long long skip = pos;
+    for (b = 0;; b += 32) {
+      const long long own = sequence_cost(b + lane);
+      long long sum = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += y;
+      }
+      const unsigned here = __ballot_sync(0xffffffffu, sum > skip);
+      if (here) {
+        const int l = __ffs(here) - 1;
+        skip -= __shfl_sync(0xffffffffu, sum - own, l);
+        b += l;
+        break;
+      }
+      skip -= __shfl_sync(0xffffffffu, sum, 31);
+    }
+    open();
+    for (at = 0;; ++at) {
+      cost = unit_cost(s, at);
+      if (skip < static_cast<long long>(cost) * heads) break;
+      skip -= static_cast<long long>(cost) * heads;
+    }
+    hp = static_cast<int>(skip / cost);
+    j = static_cast<int>(skip % cost);
+  }
+
+  // Tiles of keys of a unit (one at least: rows that see nothing have an output too), of all of a sequence's.
+  __device__ __forceinline__ int unit_cost(const AttnSeq& q, int unit) {
+    return max((attn_keys(a, q, unit * per, per) + kStTile - 1) / kStTile, 1);
+  }
+  __device__ __forceinline__ long long sequence_cost(int seq) {
+    if (seq >= a.B) return 0;
+    const AttnSeq q = attn_seq(a, seq);
+    long long sum = 0;
+    for (int i = 0; i * per < q.n; ++i) sum += unit_cost(q, i);
+    return sum * heads;
+  }
+  __device__ __forceinline__ void open() {
+    s = attn_seq(a, b);
+    tiles = (s.n + per - 1) / per;
+  }
+
+  __device__ __forceinline__ StSegment next() {
+    StSegment g{-1, 0, 0, 0, 0, -1};
+    if (left <= 0) return g;
+    const int len = static_cast<int>(min(left, static_cast<long long>(cost - j)));
+    g.b = b;
+    g.hp = hp;
+    g.t0 = at * per;
+    g.first = j;
+    g.end = j + len;
+    if (len < cost) {
+      g.slot = 2 * blockIdx.x + (j == 0 ? 1 : 0);
+      if (j == 0 && threadIdx.x == 0) {
+        // the CTAs that hold the rest: tile x is in the range of CTA ((x + 1) grid - 1) / all
+        const long long end = pos + cost - 1;
+        a.part_head[blockIdx.x] = {static_cast<int>(((end + 1) * grid - 1) / all - blockIdx.x) + 1, s.start + g.t0, s.n - g.t0, hp};
+      }
+    }
+    left -= len;
+    pos += len;
+    j += len;
+    if (j == cost && left > 0) {
+      j = 0;
+      if (++hp == heads) {
+        hp = 0;
+        if (++at == tiles) {
+          at = 0;
+          do ++b;
+          while (attn_seq(a, b).n == 0);
+          open();
+        }
+        cost = unit_cost(s, at);
+      }
+    }
+    return g;
+  }
+};
+
+__device__ __forceinline__ void st_copy(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void st_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void st_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
+// d += a b, 16 x 8 x 16.
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// MB: blocks of 16 rows.
+template <int DP, int MB>
+__global__ void __launch_bounds__(kStThreads, 2) k_attn_step(const __grid_constant__ AttnStepArgs args) {
+  using S = StShape<DP>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const AttnArgs& a = args.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, per = args.per;
+  const uint32_t ring = smem_addr(smem) + warp * S::kWarp;
+  float2* ml = reinterpret_cast<float2*>(smem + kStWarps * S::kWarp);  // [warp][row]
+  if (threadIdx.x == 0) a.part_head[blockIdx.x].parts = 0;
+  const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16*>(a.k), *vp = static_cast<const __nv_bfloat16*>(a.v);
+  const float k2 = a.scale;  // times log2(e)
+  // a lane's 16-byte pieces of a group: rows lane / kRow + i kStep, piece lane % kRow
+  constexpr int kRow = DP / 8, kStep = 32 / kRow;
+  const int c_row = lane / kRow, c_piece = lane % kRow;
+  const bool c_there = c_piece * 8 < a.D;
+  StRanges work(a, per);
+  for (;;) {
+    const StSegment g = work.next();
+    if (g.b < 0) break;
+    const AttnSeq s = attn_seq(a, g.b);
+    const int before = s.ctx - s.n, keys = attn_keys(a, s, g.t0, per), hk = g.hp * a.pack / a.group;
+    const int from = g.first * kStTile, to = min(g.end * kStTile, keys);  // keys of the segment
+    const int groups = to > from ? (to - from + kStKeys - 1) / kStKeys : 0;
+    // rows lane / 4 and lane / 4 + 8 of each block
+    uint32_t q[MB][DP / 16][4];
+    int see[MB][2];
+    float m[MB][2], l[MB][2], o[MB][DP / 8][4];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = mb * 16 + lane / 4 + e * 8, token = g.t0 + r / a.pack;
+        const bool there = r < per * a.pack && token < s.n;
+        see[mb][e] = there ? min(before + token, keys - 1) : -1;
+        m[mb][e] = -INFINITY;
+        l[mb][e] = 0.f;
+        const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(a.q) +
+                                   (there ? (s.start + static_cast<long long>(token)) * a.qs[0] + (g.hp * a.pack + r % a.pack) * a.qs[1] : 0);
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int d = k * 16 + half * 8 + (lane % 4) * 2;
+            q[mb][k][half * 2 + e] = there && d < a.D ? *reinterpret_cast<const uint32_t*>(row + d) : 0u;
+          }
+      }
+#pragma unroll
+      for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[mb][n][e] = 0.f;
+    }
+    const int32_t* table = a.tables + static_cast<long long>(g.b) * a.width;
+    const int mine = groups > warp ? (groups - warp + kStWarps - 1) / kStWarps : 0;  // this warp's groups
+    // the page of its i-th group, -1 where there is none
+    auto page_of = [&](int i) {
+      if (i >= mine) return -1;
+      const int id = table[(from + (warp + i * kStWarps) * kStKeys) / a.page];  // (keys end within the table)
+      if (id >= 0 && id < a.pages) return id;
+      atomicOr(a.status, kErrPage);
+      return -1;
+    };
+    auto fetch = [&](int i, int page) {
+      if (i < mine && page >= 0) {
+        const int key = from + (warp + i * kStWarps) * kStKeys, slot = key % a.page;
+        const __nv_bfloat16* kb = kp + page * a.ks[0] + slot * a.ks[1] + hk * a.ks[2] + c_piece * 8;
+        const __nv_bfloat16* vb = vp + page * a.vs[0] + slot * a.vs[1] + hk * a.vs[2] + c_piece * 8;
+        const uint32_t at = ring + (i % kStStages) * 2 * S::kGroup;
+#pragma unroll
+        for (int e = 0; e < kStKeys / kStep; ++e) {
+          const int r = c_row + e * kStep;
+          const bool there = c_there && key + r < to;  // zeros otherwise
+          const uint32_t off = r * DP * 2 + ((c_piece ^ (r & 7)) << 4);
+          st_copy(at + off, there ? kb + r * a.ks[1] : kp, there);
+          st_copy(at + S::kGroup + off, there ? vb + r * a.vs[1] : vp, there);
+        }
+      }
+      st_commit();
+    };
+    int pages[kStStages];  // of the groups in flight
+#pragma unroll
+    for (int i = 0; i < kStStages; ++i) pages[i] = page_of(i);
+#pragma unroll
+    for (int i = 0; i < kStStages - 1; ++i) fetch(i, pages[i]);
+    int coming = page_of(kStStages);
+    for (int i = 0; i < mine; ++i) {
+      fetch(i + kStStages - 1, pages[kStStages - 1]);
+      const int page = pages[0];
+#pragma unroll
+      for (int e = 0; e + 1 < kStStages; ++e) pages[e] = pages[e + 1];
+      pages[kStStages - 1] = coming;
+      coming = page_of(i + kStStages + 1);
+      st_wait<kStStages - 1>();
+      __syncwarp();
+      if (page >= 0) {
+        const uint32_t at = ring + (i % kStStages) * 2 * S::kGroup;
+        const int key = from + (warp + i * kStWarps) * kStKeys;
+        float sc[MB][2][4];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mb][n][e] = 0.f;
+        {
+          const int r = (lane & 7) + (lane >> 4) * 8, piece = (lane >> 3) & 1;
+          const uint32_t row = at + r * DP * 2;
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            uint32_t b[4];
+            ldmatrix_x4(row + (((2 * k + piece) ^ (r & 7)) << 4), b);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+              mma_16816(sc[mb][0], q[mb][k], b[0], b[1]);
+              mma_16816(sc[mb][1], q[mb][k], b[2], b[3]);
+            }
+          }
+        }
+        uint32_t p[MB][4];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb) {
+          float by[2];
+          bool raised = false;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float& v = sc[mb][n][e * 2 + c];
+                v = key + n * 8 + (lane % 4) * 2 + c <= see[mb][e] ? v * k2 : -INFINITY;
+                top = fmaxf(top, v);
+              }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // as on the tensor cores: m is raised only by more than 2^8
+            const bool raise = top > m[mb][e] + 8.f || (m[mb][e] == -INFINITY && top > m[mb][e]);
+            by[e] = raise ? exp2f(m[mb][e] - top) : 1.f;
+            if (raise) m[mb][e] = top;
+            raised = raised || raise;
+            const float base = m[mb][e] == -INFINITY ? 0.f : m[mb][e];
+            float sum = 0.f;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                float& v = sc[mb][n][e * 2 + c];
+                v = exp2f(v - base);
+                sum += v;
+              }
+            l[mb][e] = l[mb][e] * by[e] + sum;
+          }
+          if (__any_sync(0xffffffffu, raised)) {
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n) {
+              o[mb][n][0] *= by[0];
+              o[mb][n][1] *= by[0];
+              o[mb][n][2] *= by[1];
+              o[mb][n][3] *= by[1];
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            p[mb][n * 2] = pack_bf16x2(sc[mb][n][0], sc[mb][n][1]);
+            p[mb][n * 2 + 1] = pack_bf16x2(sc[mb][n][2], sc[mb][n][3]);
+          }
+        }
+        {
+          const int r = (lane & 7) + ((lane >> 3) & 1) * 8, piece = lane >> 4;
+          const uint32_t row = at + S::kGroup + r * DP * 2;
+#pragma unroll
+          for (int n = 0; n < DP / 16; ++n) {
+            uint32_t b[4];
+            ldmatrix_x4_trans(row + (((2 * n + piece) ^ (r & 7)) << 4), b);
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+              mma_16816(o[mb][2 * n], p[mb], b[0], b[1]);
+              mma_16816(o[mb][2 * n + 1], p[mb], b[2], b[3]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // the group's place may be written again
+    }
+    st_wait<0>();
+    __syncwarp();
+    // the warps' shares: O in the place of each one's ring, sums over the four lanes of a row
+    float* own = reinterpret_cast<float*>(smem + warp * S::kWarp);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = mb * 16 + lane / 4 + e * 8;
+        float sum = l[mb][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        if (lane % 4 == 0) ml[warp * 32 + r] = make_float2(m[mb][e], sum);
+        if (g.t0 + r / a.pack < s.n)
+#pragma unroll
+          for (int n = 0; n < DP / 8; ++n)
+            *reinterpret_cast<float2*>(own + r * DP + n * 8 + (lane % 4) * 2) = make_float2(o[mb][n][e * 2], o[mb][n][e * 2 + 1]);
+      }
+    __syncthreads();
+    const int rows = min(per * a.pack, (s.n - g.t0) * a.pack);
+    constexpr int kAtOnce = kStThreads / DP;  // rows side by side
+    for (int r = threadIdx.x / DP; r < rows; r += kAtOnce) {
+      const int d = threadIdx.x % DP;
+      float2 part[kStWarps];
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kStWarps; ++w) {
+        part[w] = ml[w * 32 + r];
+        top = fmaxf(top, part[w].x);
+      }
+      float sum = 0.f, acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < kStWarps; ++w) {
+        const float by = part[w].y == 0.f ? 0.f : exp2f(part[w].x - top);
+        sum += part[w].y * by;
+        if (part[w].y != 0.f) acc += reinterpret_cast<const float*>(smem + w * S::kWarp)[r * DP + d] * by;
+      }
+      const float out = sum == 0.f ? 0.f : acc / sum;
+      const int h = g.hp * a.pack + r % a.pack;
+      const long long t = s.start + g.t0 + r / a.pack;
+      if (g.slot >= 0) {
+        const long long row = static_cast<long long>(g.slot) * MB * 16 + r;
+        if (d < a.D) a.part_o[row * a.D + d] = out;
+        if (d == 0) a.part_ml[row] = make_float2(top, sum);
+      } else {
+        if (d < a.D) attn_store(static_cast<__nv_bfloat16*>(a.o) + t * a.os[0] + h * a.os[1] + d, out);
+        if (d == 0 && a.lse) a.lse[static_cast<long long>(h) * a.T + t] = (top + log2f(sum)) * kLn2;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the parts of units that cuts go through: CTA (c, y) the unit whose first part CTA c holds, a row at a time.
+__global__ void __launch_bounds__(128) k_attn_step_join(const __grid_constant__ AttnStepArgs args, int slot_rows) {
+  const AttnArgs& a = args.a;
+  grid_dependency_wait();
+  const AttnPart head = a.part_head[blockIdx.x];
+  const int lane = threadIdx.x & 31, d = threadIdx.x;
+  __shared__ float weight[4][32];
+  for (int r = blockIdx.y; head.parts > 0 && r < min(args.per, head.left) * a.pack; r += gridDim.y) {
+    // the first part lies at CTA c's odd slot, the others at the even ones of those behind it
+    auto at = [&](int i) { return (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * slot_rows + r; };
+    float top = -INFINITY;
+    for (int i = lane; i < head.parts; i += 32) top = fmaxf(top, a.part_ml[at(i)].x);
+#pragma unroll
+    for (int e = 16; e; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc = 0.f;
+    for (int i0 = 0; i0 < head.parts; i0 += 32) {
+      const int i = i0 + lane;
+      const float2 v = i < head.parts ? a.part_ml[at(i)] : make_float2(-INFINITY, 0.f);
+      const float w = v.y == 0.f ? 0.f : v.y * exp2f(v.x - base);
+      sum += w;
+      __syncwarp();
+      weight[threadIdx.x >> 5][lane] = w;
+      __syncwarp();
+      const int some = min(32, head.parts - i0);
+      if (d < a.D) {
+#pragma unroll 8
+        for (int e = 0; e < some; ++e) acc += weight[threadIdx.x >> 5][e] * a.part_o[at(i0 + e) * a.D + d];
+      }
+    }
+#pragma unroll
+    for (int e = 16; e; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
+    const int h = head.hp * a.pack + r % a.pack;
+    const long long t = head.token + r / a.pack;
+    if (d < a.D) attn_store(static_cast<__nv_bfloat16*>(a.o) + t * a.os[0] + h * a.os[1] + d, sum == 0.f ? 0.f : acc / sum);
+    if (d == 0 && a.lse) a.lse[static_cast<long long>(h) * a.T + t] = (top + log2f(sum)) * kLn2;
+  }
+}
+
+}  // namespace pc
