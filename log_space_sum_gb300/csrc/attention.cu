@@ -262,7 +262,7 @@ pc_status_t launch_step_dim(const AttnStepArgs& t, cudaStream_t s) {
   // its start overlaps the first kernel's end
   cudaLaunchConfig_t config{};
   config.gridDim = dim3(step_ctas(), MB * 4);
-  config.blockDim = dim3(128);
+  config.blockDim = dim3(kStJoinWarps * 32);
   config.stream = s;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

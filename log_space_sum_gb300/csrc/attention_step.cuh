@@ -406,13 +406,16 @@ __global__ void __launch_bounds__(kStThreads, 2) k_attn_step(const __grid_consta
   }
 }
 
-// Joins the parts of units that cuts go through: CTA (c, y) the unit whose first part CTA c holds, a row at a time.
-__global__ void __launch_bounds__(128) k_attn_step_join(const __grid_constant__ AttnStepArgs args, int slot_rows) {
+// Joins the parts of units that cuts go through: CTA (c, y) the unit whose first part CTA c holds, a row at a time, its
+// parts spread over the warps.
+constexpr int kStJoinWarps = 8;
+
+__global__ void __launch_bounds__(kStJoinWarps * 32) k_attn_step_join(const __grid_constant__ AttnStepArgs args, int slot_rows) {
   const AttnArgs& a = args.a;
   grid_dependency_wait();
   const AttnPart head = a.part_head[blockIdx.x];
-  const int lane = threadIdx.x & 31, d = threadIdx.x;
-  __shared__ float weight[4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ float share[kStJoinWarps][128];
   for (int r = blockIdx.y; head.parts > 0 && r < min(args.per, head.left) * a.pack; r += gridDim.y) {
     // the first part lies at CTA c's odd slot, the others at the even ones of those behind it
     auto at = [&](int i) { return (2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0)) * slot_rows + r; };
@@ -421,27 +424,39 @@ __global__ void __launch_bounds__(128) k_attn_step_join(const __grid_constant__ 
 #pragma unroll
     for (int e = 16; e; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
     const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, acc = 0.f;
+    float sum = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
     for (int i0 = 0; i0 < head.parts; i0 += 32) {
       const int i = i0 + lane;
       const float2 v = i < head.parts ? a.part_ml[at(i)] : make_float2(-INFINITY, 0.f);
       const float w = v.y == 0.f ? 0.f : v.y * exp2f(v.x - base);
       sum += w;
-      __syncwarp();
-      weight[threadIdx.x >> 5][lane] = w;
-      __syncwarp();
-      const int some = min(32, head.parts - i0);
-      if (d < a.D) {
-#pragma unroll 8
-        for (int e = 0; e < some; ++e) acc += weight[threadIdx.x >> 5][e] * a.part_o[at(i0 + e) * a.D + d];
+#pragma unroll
+      for (int k = 0; k < 32 / kStJoinWarps; ++k) {
+        const int e = warp + k * kStJoinWarps;
+        const float we = __shfl_sync(0xffffffffu, w, e);
+        if (i0 + e < head.parts && lane * 4 < a.D) {
+          const float4 o = *reinterpret_cast<const float4*>(a.part_o + at(i0 + e) * a.D + lane * 4);
+          acc[0] += we * o.x;
+          acc[1] += we * o.y;
+          acc[2] += we * o.z;
+          acc[3] += we * o.w;
+        }
       }
     }
 #pragma unroll
     for (int e = 16; e; e >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, e);
-    const int h = head.hp * a.pack + r % a.pack;
+    *reinterpret_cast<float4*>(&share[warp][lane * 4]) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    __syncthreads();
+    const int h = head.hp * a.pack + r % a.pack, d = threadIdx.x;
     const long long t = head.token + r / a.pack;
-    if (d < a.D) attn_store(static_cast<__nv_bfloat16*>(a.o) + t * a.os[0] + h * a.os[1] + d, sum == 0.f ? 0.f : acc / sum);
+    if (d < a.D) {
+      float out = 0.f;
+#pragma unroll
+      for (int e = 0; e < kStJoinWarps; ++e) out += share[e][d];
+      attn_store(static_cast<__nv_bfloat16*>(a.o) + t * a.os[0] + h * a.os[1] + d, sum == 0.f ? 0.f : out / sum);
+    }
     if (d == 0 && a.lse) a.lse[static_cast<long long>(h) * a.T + t] = (top + log2f(sum)) * kLn2;
+    __syncthreads();
   }
 }
 

@@ -15,6 +15,8 @@
 // is off by 0.004 radians at position 131072). They are formed once for all the heads of a token that
 // a warp takes. Norms, sums, rotations and the weights' gradients are float32; the only rounding to
 // bf16 is that of y and dx.
+#include <climits>
+
 #include "pc_device.cuh"
 #include "pc_host.h"
 
@@ -42,8 +44,7 @@ template <>
 struct Piece<float, 1> { using type = uint32_t; };
 
 template <class T, int V>
-__device__ __forceinline__ void get(const T* p, float (&v)[V]) {
-  typename Piece<T, V>::type u = *reinterpret_cast<const typename Piece<T, V>::type*>(p);
+__device__ __forceinline__ void unpack(const typename Piece<T, V>::type& u, float (&v)[V]) {
   const T* e = reinterpret_cast<const T*>(&u);
 #pragma unroll
   for (int i = 0; i < V; ++i) v[i] = static_cast<float>(e[i]);
@@ -69,7 +70,7 @@ struct RotArgs {
   int heads[2], dim, rotary, interleaved, norm, lanes_log2;
   int groups[2];         // warps' steps over a token's heads: 32 / L rows each
   int steps, chunks;     // steps of a warp, and how many warps share a token
-  float eps, amplitude, sign;
+  float eps, amplitude, sign, inv_dim;
 };
 
 // f / 2 pi as a fraction of a turn in 64 bits: the float's 24-bit significand times 2^96 / 2 pi,
@@ -100,12 +101,22 @@ __device__ __forceinline__ void turn_cos_sin(unsigned long long turns, float& c,
   }
 }
 
-// Lane's place in a row: where its slot's two pieces lie and whether they are there.
-template <int V>
+// Lane's place in a row: where its slot's two pieces lie and whether they are there. Interleaved pairs lie within a piece: the
+// two are half a row apart, so that the lanes' pieces follow one another; pairs of the half layout lie across the two.
+template <int V, bool kInter>
 __device__ __forceinline__ void slot_places(const RotArgs& a, int slot, int (&at)[2], bool (&has)[2]) {
   const int half = a.rotary / 2;
-  if (a.interleaved || slot * V >= half) {
-    const int base = a.interleaved ? slot * 2 * V : a.rotary + 2 * (slot * V - half);
+  if (kInter && V > 1) {
+    at[0] = slot * V;
+    at[1] = ((a.dim + 2 * V - 1) / (2 * V) + slot) * V;
+    has[0] = at[0] < (a.dim + 2 * V - 1) / (2 * V) * V;
+    has[1] = at[1] < a.dim;
+    if (!has[1]) at[1] = 0;
+    if (!has[0]) at[0] = 0, at[1] = 0, has[1] = false;
+    return;
+  }
+  if (kInter || slot * V >= half) {
+    const int base = kInter ? slot * 2 * V : a.rotary + 2 * (slot * V - half);
     at[0] = base;
     at[1] = base + V;
   } else {
@@ -118,123 +129,165 @@ __device__ __forceinline__ void slot_places(const RotArgs& a, int slot, int (&at
     if (!has[e]) at[e] = 0;
   }
 }
-// Index of the frequency of the slot's pair i; past R / 2: none.
-template <int V>
-__device__ __forceinline__ int pair_index(const RotArgs& a, int slot, int i) {
+// Number of the slot's i-th pair; R / 2 or more: none of those that are turned.
+template <int V, bool kInter>
+__device__ __forceinline__ int pair_of(int slot, const int (&at)[2], const bool (&has)[2], int i) {
+  if (kInter && V > 1) return has[i / (V / 2 > 0 ? V / 2 : 1)] ? at[i / (V / 2 > 0 ? V / 2 : 1)] / 2 + i % (V / 2 > 0 ? V / 2 : 1) : INT_MAX;
   return slot * V + i;
 }
 
-template <int V>
-__device__ __forceinline__ void turn(bool interleaved, float (&u)[2][V], const float (&c)[V], const float (&s)[V]) {
-  if (V > 1 && interleaved) {
+template <int V, bool kInter>
+__device__ __forceinline__ void turn(float (&u)[2][V], const float (&c)[V], const float (&s)[V]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {  // pair i: elements 2i, 2i + 1 of the 2V
-      float& p = u[(2 * i) / V][(2 * i) % V];
-      float& q = u[(2 * i + 1) / V][(2 * i + 1) % V];
-      const float x = p, y = q;
-      p = x * c[i] - y * s[i];
-      q = y * c[i] + x * s[i];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const float x = u[0][i], y = u[1][i];
-      u[0][i] = x * c[i] - y * s[i];
-      u[1][i] = y * c[i] + x * s[i];
-    }
+  for (int i = 0; i < V; ++i) {
+    float& p = kInter && V > 1 ? u[(2 * i) / V][(2 * i) % V] : u[0][i];
+    float& q = kInter && V > 1 ? u[(2 * i) / V][(2 * i + 1) % V] : u[1][i];
+    const float x = p, y = q;
+    p = x * c[i] - y * s[i];
+    q = y * c[i] + x * s[i];
   }
 }
 
 template <int N>
 __device__ __forceinline__ void lane_sum(float (&v)[N], int lanes_log2) {
-  for (int w = 0; w < lanes_log2; ++w) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1 << w);
+  for (int w = 0; w < 5; ++w) {
+    if (w < lanes_log2) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 1 << w);
+    }
   }
 }
 
-// A warp takes one token's heads, `steps` groups of 32 / L rows (fewer for the last chunk); with
-// kBack the warps of a CTA walk tokens, and sum the weights' gradients.
-template <class T, int V, int K, bool kBack>
-__global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) k_qk_norm_rotary(const __grid_constant__ RotArgs a) {
+// A warp takes tokens, each with `steps` groups of 32 / L rows (fewer for the last chunk of a token's heads, where warps
+// share them), as one stream of groups: the loads of the next kAhead groups are under way while one is worked on. With kBack the
+// warps also sum the weights' gradients. The turns' steps and the weights lie in shared memory.
+template <class T, int V, int K, bool kInter, bool kBack>
+__global__ void __launch_bounds__(kThreads, K > 1 ? 1 : kBack ? 2 : 3) k_qk_norm_rotary(const __grid_constant__ RotArgs a) {
+  constexpr int kAhead = 1;
+  using Raw = typename Piece<T, V>::type;
+  __shared__ unsigned long long steps[kMaxDim / 2];
+  __shared__ __align__(16) float weights[2][kMaxDim];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int L = 1 << a.lanes_log2, row = lane >> a.lanes_log2, rows = 32 >> a.lanes_log2;
+  for (int i = threadIdx.x; i < a.rotary / 2; i += kThreads) steps[i] = turn_step(a.frequencies[i]);
+  for (int i = threadIdx.x; i < a.dim; i += kThreads)
+#pragma unroll
+    for (int n = 0; n < 2; ++n) weights[n][i] = a.weight[n] ? a.weight[n][i] : 1.f;
+  __syncthreads();
   int at[K][2];
   bool has[K][2];
-  unsigned long long step[K][V];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int slot = (lane & (L - 1)) + k * L;
-    slot_places<V>(a, slot, at[k], has[k]);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int p = pair_index<V>(a, slot, i);
-      step[k][i] = p < a.rotary / 2 ? turn_step(a.frequencies[p]) : 0ull;
-    }
-  }
-  float w[2][K][2][V];
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < V; ++i) w[n][k][e][i] = a.weight[n] && has[k][e] ? __ldg(a.weight[n] + at[k][e] + i) : 1.f;
-  float dw[kBack ? 2 : 1][kBack ? K : 1][2][V];
-  if constexpr (kBack) {
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
+  for (int k = 0; k < K; ++k) slot_places<V, kInter>(a, (lane & (L - 1)) + k * L, at[k], has[k]);
+  float dw[kBack ? K : 1][2][V];
+  __shared__ float part[kBack ? kWarps : 1][2][kBack ? kMaxDim : 1];
+  // the gradient takes all tokens' queries, then all keys: one weight's sums at a time
+  for (int pass = 0; pass < (kBack ? 2 : 1); ++pass) {
+    if constexpr (kBack) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int i = 0; i < V; ++i) dw[n][k][e][i] = 0.f;
-  }
-  const long long units = a.tokens * a.chunks, all = static_cast<long long>(gridDim.x) * kWarps;
-  for (long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp; unit < units; unit += all) {
-    const long long t = unit / a.chunks;
-    const int first = static_cast<int>(unit % a.chunks) * a.steps;
-    const int last = min(first + a.steps, a.groups[0] + a.groups[1]);
-    const unsigned long long pos = a.rotary ? static_cast<unsigned long long>(static_cast<long long>(a.positions[t])) : 0ull;
-    float c[K][V], s[K][V];
-#pragma unroll
-    for (int k = 0; k < K; ++k)
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        turn_cos_sin<T>(pos * step[k][i], c[k][i], s[k][i]);
-        const bool turned = pair_index<V>(a, (lane & (L - 1)) + k * L, i) < a.rotary / 2;
-        c[k][i] = turned ? c[k][i] * a.amplitude : 1.f;
-        s[k][i] = turned ? s[k][i] * a.amplitude * a.sign : 0.f;
+          for (int i = 0; i < V; ++i) dw[k][e][i] = 0.f;
+    }
+    const int first = kBack && pass ? a.groups[0] : 0, groups = kBack && !pass ? a.groups[0] : a.groups[0] + a.groups[1];
+    const long long units = groups > first ? a.tokens * a.chunks : 0, all = static_cast<long long>(gridDim.x) * kWarps;
+    // where the stream of groups stands: a unit of work, the group, the last one of the unit, this lane's row
+    struct Place {
+      long long unit, t;
+      int group, last;
+      const T *x, *g;
+      T* y;
+    };
+    auto row_of = [&](Place& p) {  // the first group of the unit, or of the keys
+      const int n = p.group >= a.groups[0];
+      const long long h = (p.group - (n ? a.groups[0] : 0)) * rows + row;
+      p.x = static_cast<const T*>(a.x[n]) + p.t * a.xs[n][0] + h * a.xs[n][1];
+      if constexpr (kBack) p.g = static_cast<const T*>(a.dy[n]) + p.t * a.gs[n][0] + h * a.gs[n][1];
+      p.y = static_cast<T*>(a.y[n]) + p.t * a.ys[n][0] + h * a.ys[n][1];
+    };
+    auto open = [&](Place& p) {
+      if (p.unit >= units) return;
+      if (kBack || a.chunks == 1) {
+        p.t = p.unit;
+        p.group = first;
+        p.last = groups;
+      } else {
+        p.t = p.unit / a.chunks;
+        p.group = static_cast<int>(p.unit - p.t * a.chunks) * a.steps;
+        p.last = min(p.group + a.steps, groups);
       }
-    auto side = [&](const int n, int from, int to) {  // queries, then keys
-      if (from >= to) return;
-      const T* x = static_cast<const T*>(a.x[n]) + t * a.xs[n][0];
-      const T* dy = kBack ? static_cast<const T*>(a.dy[n]) + t * a.gs[n][0] : nullptr;
-      T* y = static_cast<T*>(a.y[n]) + t * a.ys[n][0];
-      float u[K][2][V], g[kBack ? K : 1][2][V];
-      auto fetch = [&](int group) {
-        const int h = group * rows + row;
+      row_of(p);
+    };
+    auto advance = [&](Place& p) {
+      if (++p.group == p.last) {
+        p.unit += all;
+        open(p);
+      } else if (p.group == a.groups[0]) {
+        row_of(p);
+      } else {
+        const int n = p.group > a.groups[0];
+        p.x += a.xs[n][1] * rows;
+        if constexpr (kBack) p.g += a.gs[n][1] * rows;
+        p.y += a.ys[n][1] * rows;
+      }
+    };
+    struct Loads {
+      Raw x[K][2], g[kBack ? K : 1][2];
+      int position;
+    };
+    // rows of the group that there are
+    auto there = [&](const Place& p) {
+      const int n = p.group >= a.groups[0];
+      return (p.group - (n ? a.groups[0] : 0)) * rows + row < a.heads[n];
+    };
+    auto fetch = [&](const Place& p, Loads& f) {
+      if (p.unit >= units) return;
+      const bool on = there(p);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          f.x[k][e] = Raw{};
+          if constexpr (kBack) f.g[k][e] = Raw{};
+          if (on && has[k][e]) {
+            f.x[k][e] = *reinterpret_cast<const Raw*>(p.x + at[k][e]);
+            if constexpr (kBack) f.g[k][e] = *reinterpret_cast<const Raw*>(p.g + at[k][e]);
+          }
+        }
+      if (a.rotary) f.position = a.positions[p.t];
+    };
+    float c[K][V], s[K][V];
+    long long turned = -1;  // the unit whose angles c and s hold
+    auto work = [&](const Place& p, const Loads& f) {
+      if (p.unit != turned) {
+        turned = p.unit;
+        const unsigned long long pos = a.rotary ? static_cast<unsigned long long>(static_cast<long long>(f.position)) : 0ull;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int pair = pair_of<V, kInter>((lane & (L - 1)) + k * L, at[k], has[k], i);
+            c[k][i] = 1.f;
+            s[k][i] = 0.f;
+            if (pair < a.rotary / 2) {
+              turn_cos_sin<T>(pos * steps[pair], c[k][i], s[k][i]);
+              c[k][i] *= a.amplitude;
+              s[k][i] *= a.amplitude * a.sign;
+            }
+          }
+      }
+      const int n = p.group >= a.groups[0];
+      {
+        float u[K][2][V], g[kBack ? K : 1][2][V];
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (h < a.heads[n] && has[k][e]) {
-              get<T, V>(x + h * a.xs[n][1] + at[k][e], u[k][e]);
-              if constexpr (kBack) get<T, V>(dy + h * a.gs[n][1] + at[k][e], g[k][e]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < V; ++i) {
-                u[k][e][i] = 0.f;
-                if constexpr (kBack) g[k][e][i] = 0.f;
-              }
-            }
+            unpack<T, V>(f.x[k][e], u[k][e]);
+            if constexpr (kBack) unpack<T, V>(f.g[k][e], g[k][e]);
           }
-      };
-      for (int group = from; group < to; ++group) {
-        fetch(group);
-        const int h = group * rows + row;
         float rstd = 1.f;
         if (a.norm) {
           float sq[1] = {0.f};
@@ -245,8 +298,24 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) k_qk_norm_rotary(con
 #pragma unroll
               for (int i = 0; i < V; ++i) sq[0] += u[k][e][i] * u[k][e][i];
           lane_sum(sq, a.lanes_log2);
-          rstd = rsqrtf(sq[0] / a.dim + a.eps);
+          rstd = rsqrtf(sq[0] * a.inv_dim + a.eps);
         }
+        float w[K][2][V];
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if constexpr (V >= 4) {
+#pragma unroll
+              for (int i = 0; i < V; i += 4) {
+                const float4 f4 = *reinterpret_cast<const float4*>(&weights[n][at[k][e] + i]);
+                w[k][e][i] = f4.x, w[k][e][i + 1] = f4.y, w[k][e][i + 2] = f4.z, w[k][e][i + 3] = f4.w;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < V; ++i) w[k][e][i] = weights[n][at[k][e] + i];
+            }
+          }
         if constexpr (!kBack) {
 #pragma unroll
           for (int k = 0; k < K; ++k) {
@@ -254,28 +323,28 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) k_qk_norm_rotary(con
 #pragma unroll
               for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int i = 0; i < V; ++i) u[k][e][i] *= rstd * w[n][k][e][i];
+                for (int i = 0; i < V; ++i) u[k][e][i] *= rstd * w[k][e][i];
             }
-            turn<V>(a.interleaved, u[k], c[k], s[k]);
+            turn<V, kInter>(u[k], c[k], s[k]);
           }
         } else {
           float dot[1] = {0.f};
 #pragma unroll
           for (int k = 0; k < K; ++k) {
-            turn<V>(a.interleaved, g[k], c[k], s[k]);
+            turn<V, kInter>(g[k], c[k], s[k]);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int i = 0; i < V; ++i) {
                 const float z = u[k][e][i] * rstd;
-                dw[n][k][e][i] += g[k][e][i] * z;
-                g[k][e][i] *= w[n][k][e][i];
+                dw[k][e][i] += g[k][e][i] * z;
+                g[k][e][i] *= w[k][e][i];
                 dot[0] += g[k][e][i] * z;
                 u[k][e][i] = z;
               }
           }
           lane_sum(dot, a.lanes_log2);
-          const float mean = dot[0] / a.dim;
+          const float mean = dot[0] * a.inv_dim;
 #pragma unroll
           for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -283,33 +352,49 @@ __global__ void __launch_bounds__(kThreads, K == 1 ? 2 : 1) k_qk_norm_rotary(con
 #pragma unroll
               for (int i = 0; i < V; ++i) u[k][e][i] = rstd * (g[k][e][i] - u[k][e][i] * mean);
         }
-        if (h < a.heads[n]) {
+        if (there(p)) {
 #pragma unroll
           for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              if (has[k][e]) put<T, V>(y + h * a.ys[n][1] + at[k][e], u[k][e]);
+              if (has[k][e]) put<T, V>(p.y + at[k][e], u[k][e]);
         }
       }
     };
-    side(0, first, min(last, a.groups[0]));
-    side(1, max(first - a.groups[0], 0), last - a.groups[0]);
-  }
-  if constexpr (kBack) {
-    // the CTA's rows in a fixed order: row groups of a warp, then warps
-    __shared__ float part[kWarps][2][kMaxDim];
+    Place now{static_cast<long long>(blockIdx.x) * kWarps + warp, 0, 0, 0, nullptr, nullptr, nullptr}, next;
+    open(now);
+    next = now;
+    Loads loads[kAhead + 1];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int i = 0; i < kAhead; ++i) {
+      fetch(next, loads[i]);
+      if (next.unit < units) advance(next);
+    }
+    while (now.unit < units) {
+#pragma unroll
+      for (int i = 0; i <= kAhead; ++i) {
+        if (now.unit >= units) break;
+        fetch(next, loads[(i + kAhead) % (kAhead + 1)]);
+        if (next.unit < units) advance(next);
+        work(now, loads[i]);
+        advance(now);
+      }
+    }
+    if constexpr (kBack) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            float v = dw[n][k][e][i];
+            float v = dw[k][e][i];  // (rows that are not there added nothing)
             for (int d = L; d < 32; d <<= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-            if (row == 0 && has[k][e]) part[warp][n][at[k][e] + i] = v;
+            if (row == 0 && has[k][e]) part[warp][pass][at[k][e] + i] = v;
           }
+    }
+  }
+  if constexpr (kBack) {
+    // the CTA's rows in a fixed order: row groups of a warp, then warps
     __syncthreads();
     for (int j = threadIdx.x; j < 2 * a.dim; j += kThreads) {
       const int n = j >= a.dim, d = j - n * a.dim;
@@ -369,7 +454,7 @@ int back_ctas(long long tokens) {
   return static_cast<int>(want < most ? want : most);
 }
 
-template <class T, int V, bool kBack>
+template <class T, int V, bool kInter, bool kBack>
 pc_status_t launch_width(RotArgs& a, cudaStream_t s) {
   const int slots = (a.dim + 2 * V - 1) / (2 * V);
   a.lanes_log2 = 0;
@@ -389,27 +474,33 @@ pc_status_t launch_width(RotArgs& a, cudaStream_t s) {
   long long ctas = (a.tokens * a.chunks + kWarps - 1) / kWarps;
   if (kBack) ctas = back_ctas(a.tokens);
   else if (ctas > 24ll * num_sms()) ctas = 24ll * num_sms();
-  auto* kernel = K <= 1 ? k_qk_norm_rotary<T, V, 1, kBack> : nullptr;
+  auto* kernel = K <= 1 ? k_qk_norm_rotary<T, V, 1, kInter, kBack> : nullptr;
   if constexpr (V <= 2) {
-    if (K == 2) kernel = k_qk_norm_rotary<T, V, 2, kBack>;
+    if (K == 2) kernel = k_qk_norm_rotary<T, V, 2, kInter, kBack>;
   }
   if constexpr (V == 1) {
-    if (K > 2) kernel = k_qk_norm_rotary<T, V, 4, kBack>;
+    if (K > 2) kernel = k_qk_norm_rotary<T, V, 4, kInter, kBack>;
   }
   kernel<<<static_cast<unsigned>(ctas), kThreads, 0, s>>>(a);
   PC_LAUNCH_CHECK();
   return PC_OK;
 }
 
-template <class T, bool kBack>
-pc_status_t launch(RotArgs& a, cudaStream_t s) {
+template <class T, bool kInter, bool kBack>
+pc_status_t launch_layout(RotArgs& a, cudaStream_t s) {
   const int v = piece_width(a, kBack, sizeof(T));
   if constexpr (sizeof(T) == 2) {
-    if (v == 8) return launch_width<T, 8, kBack>(a, s);
+    if (v == 8) return launch_width<T, 8, kInter, kBack>(a, s);
   }
-  if (v >= 4) return launch_width<T, 4, kBack>(a, s);
-  if (v == 2) return launch_width<T, 2, kBack>(a, s);
-  return launch_width<T, 1, kBack>(a, s);
+  if (v >= 4) return launch_width<T, 4, kInter, kBack>(a, s);
+  if (v == 2) return launch_width<T, 2, kInter, kBack>(a, s);
+  return launch_width<T, 1, kInter, kBack>(a, s);
+}
+
+template <class T, bool kBack>
+pc_status_t launch(RotArgs& a, cudaStream_t s) {
+  a.inv_dim = 1.f / a.dim;
+  return a.interleaved ? launch_layout<T, true, kBack>(a, s) : launch_layout<T, false, kBack>(a, s);
 }
 
 pc_status_t check_rot(long long tokens, int Hq, int Hk, int dim, int rotary, int layout, const int32_t* positions,
