@@ -112,7 +112,7 @@ PCSUM_API pc_status_t pc_device_status(pc_stream_t stream);
 
 /* Limit, in nanoseconds, of the first waits of the tensor-core contraction kernel on the
  * current device (a free ring slot, a filled slot, a free or complete accumulator); in the
- * kernels of linear attention and of the orthogonalised update, of the waits for a complete
+ * kernels of linear attention, softmax attention and the orthogonalised update, of the waits for a complete
  * accumulator (where one is formed in slices, none). 0 restores the default of 2 s. A kernel whose wait runs out records PC_ERR_TIMEOUT
  * for pc_device_status, skips the rest of its tile and exits cleanly: waits for work it
  * has already issued (copies landing, MMAs completing before tensor memory is freed)
@@ -129,7 +129,8 @@ PCSUM_API pc_status_t pc_set_wait_limit_ns(unsigned long long ns);
  * the HMM's chain contractions: each chain of T-1 consecutive launches of one kind is
  * one record (events between them would break their programmatic overlap), and so is a call
  * of linear attention over whole sequences (its products are those of the recurrence over T
- * tokens of each sequence: two in the forward, five in the gradient).
+ * tokens of each sequence: two in the forward, five in the gradient) and of softmax attention, packed or over a
+ * paged cache (its sequences' lengths are on the device: flops[i] = 0).
  * pc_profile_stop synchronises the device, then writes for each record i
  * (i < *count <= capacity): ms[i] = elapsed device time, kind[i] = which contraction
  * (PC_KIND_*), flops[i] = the algorithmic flops of its launches, 2*M*N*K each (each
@@ -146,7 +147,7 @@ typedef enum {
   PC_KIND_HCLT_FWD = 6, PC_KIND_HCLT_ELEM = 7, PC_KIND_HCLT_PARAM = 8,
   PC_KIND_LOWRANK_FWD = 9, PC_KIND_LOWRANK_BWD = 10, PC_KIND_EM_MSTEP = 11,
   PC_KIND_HMM_MEM = 12, PC_KIND_HCLT_MEM = 13, PC_KIND_ORTHOGONALIZE = 14,
-  PC_KIND_LINEAR_ATTENTION = 15
+  PC_KIND_LINEAR_ATTENTION = 15, PC_KIND_ATTENTION = 16
 } pc_kind_t;
 PCSUM_API pc_status_t pc_profile_start(int capacity);
 PCSUM_API pc_status_t pc_profile_stop(int* count, float* ms, int* kind, long long* flops,

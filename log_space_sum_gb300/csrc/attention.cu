@@ -306,12 +306,13 @@ pc_status_t try_step(const AttnArgs& from, pc_dtype_t dt, void* ws, cudaStream_t
 pc_status_t run_fwd(AttnArgs& a, pc_dtype_t dt, void* ws, cudaStream_t s) {
   a.status = device_status_word();
   PC_CHECK(a.status, PC_ERR_CUDA, "device status word unavailable");
-  int launches = 0;
+  ProfileGroup record(s, PC_KIND_ATTENTION, 0);
   bool done = false;
-  PC_TRY(try_step(a, dt, ws, s, &launches, &done));
-  if (!done) PC_TRY(try_tc(a, dt, ws, s, &launches, &done));
+  PC_TRY(try_step(a, dt, ws, s, &record.launches, &done));
+  if (!done) PC_TRY(try_tc(a, dt, ws, s, &record.launches, &done));
   if (done) return PC_OK;
-  return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, ws, s, &launches) : launch_simt<float>(a, ws, s, &launches);
+  return dt == PC_BF16 ? launch_simt<__nv_bfloat16>(a, ws, s, &record.launches)
+                       : launch_simt<float>(a, ws, s, &record.launches);
 }
 
 template <class T, int DP>
@@ -531,11 +532,12 @@ pc_status_t pc_attention_bwd(int B, int T, int H, int Hk, int D, const void* q, 
     b.dvs[i] = strides[14 + i];
   }
   PC_CHECK(b.a.status, PC_ERR_CUDA, "device status word unavailable");
-  int launches = 0;
+  pc::ProfileGroup record(stream, PC_KIND_ATTENTION, 0);
   bool done = false;
-  PC_TRY(pc::try_bwd_tc(b, dtype, stream, &launches, &done));
+  PC_TRY(pc::try_bwd_tc(b, dtype, stream, &record.launches, &done));
   if (done) return PC_OK;
-  return dtype == PC_BF16 ? pc::launch_bwd<__nv_bfloat16>(b, stream, &launches) : pc::launch_bwd<float>(b, stream, &launches);
+  return dtype == PC_BF16 ? pc::launch_bwd<__nv_bfloat16>(b, stream, &record.launches)
+                          : pc::launch_bwd<float>(b, stream, &record.launches);
 }
 
 pc_status_t pc_paged_attention_workspace(int B, int T, int H, int Hk, int D, int pages, int page_size, int width,

@@ -473,7 +473,7 @@ pc_status_t launch_width(RotArgs& a, cudaStream_t s) {
   a.chunks = (all + a.steps - 1) / a.steps;
   long long ctas = (a.tokens * a.chunks + kWarps - 1) / kWarps;
   if (kBack) ctas = back_ctas(a.tokens);
-  else if (ctas > 24ll * num_sms()) ctas = 24ll * num_sms();
+  else if (ctas > 3ll * num_sms()) ctas = 3ll * num_sms();  // what stays on the SMs: a warp's tokens follow one another
   auto* kernel = K <= 1 ? k_qk_norm_rotary<T, V, 1, kInter, kBack> : nullptr;
   if constexpr (V <= 2) {
     if (K == 2) kernel = k_qk_norm_rotary<T, V, 2, kInter, kBack>;
