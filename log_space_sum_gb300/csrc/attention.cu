@@ -219,6 +219,8 @@ pc_status_t try_tc(const AttnArgs& from, pc_dtype_t dt, void* ws, cudaStream_t s
   pc_status_t st = PC_OK;
   if (!tc_row_map(&t.q, a, a.q, a.qs, t.per, &st)) return PC_OK;
   PC_TRY(st);
+  if (!tc_row_map(&t.o, a, a.o, a.os, t.per, &st)) return PC_OK;
+  PC_TRY(st);
   const int rows = a.page ? a.page : a.T, outer = a.page ? a.pages : 1;
   if (!tc_key_map(&t.k, &t.k_ext, a.k, a.D, rows, a.ks[1], a.Hk, a.ks[2], outer, a.ks[0], t.box, &st)) return PC_OK;
   PC_TRY(st);

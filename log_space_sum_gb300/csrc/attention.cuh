@@ -88,27 +88,33 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, int tile, int p
   return {-1, 0};
 }
 
-// The tile of the given rank when all sequences' tiles are sorted by cost, the dearest first: with rows (kKeys false)
-// the last of a sequence, which see most keys, with keys its first, which most rows see. (Past 128 sequences the
+// The tile of the given rank when all sequences' tiles are sorted by cost, the dearest first, and its sequence: with rows
+// (kKeys false) the last of a sequence, which see most keys, with keys its first, which most rows see. (Past 128 sequences the
 // search would cost more than the order gives: sequence by sequence, then.) The whole warp takes part.
 template <bool kKeys>
-__device__ __forceinline__ AttnTile attn_tile_by_cost(const AttnArgs& a, int rank, int per) {
+__device__ __forceinline__ AttnTile attn_tile_by_cost(const AttnArgs& a, int rank, int per, AttnSeq& s) {
   if (!a.starts) {
-    const int each = (a.T / a.B + per - 1) / per;
+    const int n = a.T / a.B, each = (n + per - 1) / per;
     if (each == 0 || rank >= a.B * each) return {-1, 0};
+    s = attn_seq(a, rank % a.B);
     return {rank % a.B, kKeys ? rank / a.B : each - 1 - rank / a.B};
   }
   if (a.B > 128) {
     AttnTile tile = attn_tile(a, rank, per);
-    if (!kKeys && tile.b >= 0) tile.at = (attn_seq(a, tile.b).n + per - 1) / per - 1 - tile.at;
+    if (tile.b < 0) return tile;
+    s = attn_seq(a, tile.b);
+    if (!kKeys) tile.at = (s.n + per - 1) / per - 1 - tile.at;
     return tile;
   }
   const int lane = threadIdx.x & 31;
+  AttnSeq all[4];
   int n[4], top = 0;  // tiles of this lane's sequences
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int b = lane + 32 * i;
-    n[i] = b < a.B ? (attn_seq(a, b).n + per - 1) / per : 0;
+    all[i] = {0, 0, 0};
+    if (32 * i < a.B && b < a.B) all[i] = attn_seq(a, b);
+    n[i] = (all[i].n + per - 1) / per;
     top = max(top, n[i]);
   }
   top = __reduce_max_sync(0xffffffffu, top);
@@ -137,6 +143,7 @@ __device__ __forceinline__ AttnTile attn_tile_by_cost(const AttnArgs& a, int ran
     if (left < count) {
       const unsigned it = __ballot_sync(0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == left);
       const int l = __ffs(it) - 1;
+      s = {__shfl_sync(0xffffffffu, all[i].start, l), __shfl_sync(0xffffffffu, all[i].n, l), __shfl_sync(0xffffffffu, all[i].ctx, l)};
       return {l + 32 * i, kKeys ? __shfl_sync(0xffffffffu, n[i], l) - lo : lo - 1};
     }
     left -= count;

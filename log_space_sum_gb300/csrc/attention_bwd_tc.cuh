@@ -136,9 +136,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_dkdv_tc(const __grid_con
   const AttnArgs& a = args.b.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.x % a.Hk, per = args.per, rows = per * a.pack;
-  const AttnTile tile = attn_tile_by_cost<true>(a, blockIdx.x / a.Hk, C);
+  AttnSeq s{0, 0, 0};
+  const AttnTile tile = attn_tile_by_cost<true>(a, blockIdx.x / a.Hk, C, s);
   if (tile.b < 0) return;
-  const AttnSeq s = attn_seq(a, tile.b);
   const int j0 = tile.at * C;
   // rows of the tokens from the tile's first key on, for each `pack` heads of the group in turn
   const int i_first = j0 / per, i_each = (s.n + per - 1) / per - i_first, folds = a.group / a.pack, steps = i_each * folds;
@@ -392,9 +392,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_dq_tc(const __grid_const
   const AttnArgs& a = args.b.a;
   const int heads = a.H / a.pack, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hp = blockIdx.x % heads, hk = hp * a.pack / a.group, per = args.per;
-  const AttnTile tile = attn_tile_by_cost<false>(a, blockIdx.x / heads, per);
+  AttnSeq s{0, 0, 0};
+  const AttnTile tile = attn_tile_by_cost<false>(a, blockIdx.x / heads, per, s);
   if (tile.b < 0) return;
-  const AttnSeq s = attn_seq(a, tile.b);
   const int t0 = tile.at * per, keys = min(t0 + per, s.n), steps = (keys + C - 1) / C;
   unsigned* status = a.status;
 

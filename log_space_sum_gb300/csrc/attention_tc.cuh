@@ -11,6 +11,8 @@
 //
 //   warps 0-3    softmax of the first tile's rows, warps 4-7 of the second's
 //   warp 8       TMA: Q once, then K and V tiles through one ring
+//   warp 10      TMA stores of whole tiles' outputs, staged in the place of Q (a thread a row straight to global memory took 3.1
+//                us a CTA, every piece of 16 bytes in a line of its own)
 //   warp 9       MMA issuer: while one tile's softmax runs, the other's products do; zeros the rows of the last V
 //                tile that lie behind the keys, as what is there may be no number
 //
@@ -31,7 +33,7 @@ constexpr int kAtThreads = 384;
 
 struct AttnTcArgs {
   AttnArgs a;
-  CUtensorMap q, k, v;
+  CUtensorMap q, k, v, o;
   int k_ext, v_ext;         // 1: the map has the heads, 0: they share one
   int box;                  // keys of one TMA box: 128, or a page's where it is smaller
   int per;                  // tokens of a tile of rows
@@ -93,6 +95,15 @@ __device__ __forceinline__ void at_add2(float& a0, float& a1, float b0, float b1
   add2(a0, a1, __float_as_uint(b0), __float_as_uint(b1));
 }
 
+// 32 columns of row r of a tile as bf16, in 128-byte swizzled rows of 64, as a TMA store of the tile reads them.
+__device__ __forceinline__ void at_stage(uint32_t tile, int r, int c, const float (&u)[32]) {
+  const uint32_t row = tile + (c / 64) * kAtC * 128 + r * 128;
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    st_shared_v4(row + ((((c % 64 + i) / 8) ^ (r & 7)) << 4), pack_bf16x2(u[i], u[i + 1]), pack_bf16x2(u[i + 2], u[i + 3]),
+                 pack_bf16x2(u[i + 4], u[i + 5]), pack_bf16x2(u[i + 6], u[i + 7]));
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant__ AttnTcArgs args) {
   using S = AtShape<DP>;
@@ -100,17 +111,37 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kFixed);
   uint64_t *full = bars, *empty = bars + 8, *q_full = bars + 16, *s_full = bars + 17, *p_ready = bars + 19,
-           *o_full = bars + 21, *mma_done = bars + 24;
-  auto* limit = reinterpret_cast<unsigned long long*>(bars + 25);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+           *o_full = bars + 21, *o_staged = bars + 23, *mma_done = bars + 25;
+  auto* limit = reinterpret_cast<unsigned long long*>(bars + 26);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 27);
   uint32_t* bad = tmem_slot + 2;  // [16]: missing boxes of the last tiles of keys, a bit each
 
   const AttnArgs& a = args.a;
   const int heads = a.H / a.pack, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hp = blockIdx.x % heads, rest = blockIdx.x / heads, split = rest % a.splits;
-  const AttnTile tile = attn_tile_by_cost<false>(a, rest / a.splits, 2 * args.per);
+  // one warp sets up the barriers, another takes the tensor memory, while all find their work
+  if (warp == 8 && lane == 0) {
+    tma_prefetch_map(&args.q);
+    tma_prefetch_map(&args.k);
+    tma_prefetch_map(&args.v);
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 1);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&s_full[x], 1);
+      mbar_init(&p_ready[x], 4);
+      mbar_init(&o_full[x], 1);
+      mbar_init(&o_staged[x], 4);
+    }
+    mbar_init(mma_done, 1);
+    *limit = first_wait_limit(a.status);
+    fence_barrier_init();
+  }
+  AttnSeq s{0, 0, 0};
+  const AttnTile tile = attn_tile_by_cost<false>(a, rest / a.splits, 2 * args.per, s);
   if (tile.b < 0) return;
-  const AttnSeq s = attn_seq(a, tile.b);
   const int hk = hp * a.pack / a.group, per = args.per, t0 = tile.at * 2 * per;
   int keys[2], first, last[2];  // the tiles of keys [first, last) are this CTA's
   keys[0] = attn_keys(a, s, t0, per);
@@ -125,29 +156,24 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
   const int tail = n_tiles > 0 && end == all && top_keys % C ? all - 1 : -1;
   unsigned* status = a.status;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      for (int i = 0; i < S::kSlots; ++i) {
-        mbar_init(&full[i], 1);
-        mbar_init(&empty[i], 1);
-      }
-      mbar_init(q_full, 1);
-      for (int x = 0; x < 2; ++x) {
-        mbar_init(&s_full[x], 1);
-        mbar_init(&p_ready[x], 4);
-        mbar_init(&o_full[x], 1);
-      }
-      mbar_init(mma_done, 1);
-      *limit = first_wait_limit(status);
-      fence_barrier_init();
-    }
-    __syncwarp();
-    tmem_alloc(tmem_slot, 512);
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
+  // Q's copies start before the CTA meets
+  if (warp == 8 && lane == 0 && n_tiles > 0) {
+    const int parts = (last[0] > first) + (last[1] > first);
+    mbar_arrive_expect_tx(q_full, parts * per * a.pack * DP * 2);
+    for (int x = 0; x < 2; ++x)
+      if (last[x] > first)
+        for (int d = 0; d < DP; d += 64)
+          tma_load_4d(smem + x * S::kTile + d * C * 2, &args.q, q_full, d, hp * a.pack, s.start + t0 + x * per, 0);
   }
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+
+  // a tile of rows whose output is stored as a whole
+  auto whole = [&](int x) { return a.splits == 1 && t0 + (x + 1) * per <= s.n; };
 
   if (warp < 8) {
     at_regs_up<224>();
@@ -249,7 +275,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
       const float by = l == 0.f ? 0.f : 1.f / l;
       const bool some = last[x] > first;  // (uniform) otherwise O was never written
       const long long t = s.start + token;
-      const bool joined = a.splits > 1;
+      const bool joined = a.splits > 1, staged = whole(x);
       const long long row = joined ? split * static_cast<long long>(a.T) * a.H + t * a.H + h : 0;
       __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + t * a.os[0] + h * a.os[1];
 #pragma unroll 1
@@ -258,7 +284,9 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
         if (some) tmem_ld_32x32(o_col + c, u);
 #pragma unroll
         for (int i = 0; i < 32; ++i) u[i] = some && l != 0.f ? u[i] * by : 0.f;
-        if (there) {
+        if (staged) {
+          at_stage(smem_addr(smem) + x * S::kTile, r, c, u);
+        } else if (there) {
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             if (c + i >= a.D) continue;
@@ -274,6 +302,11 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
           }
         }
       }
+      if (staged) {
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_staged[x]);
+      }
       if (there) {
         if (joined) a.part_ml[row] = make_float2(m, l);
         else if (a.lse) a.lse[static_cast<long long>(h) * a.T + t] = (m + log2f(l)) * kLn2;
@@ -287,15 +320,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
       int issued = 0;
       bool ok = true;
       if (n_tiles > 0) {
-        if (lane == 0) {
-          const int parts = (last[0] > first) + (last[1] > first);
-          mbar_arrive_expect_tx(q_full, parts * per * a.pack * DP * 2);
-          for (int x = 0; x < 2; ++x)
-            if (last[x] > first)
-              for (int d = 0; d < DP; d += 64)
-                tma_load_4d(smem + x * S::kTile + d * C * 2, &args.q, q_full, d, hp * a.pack,
-                            s.start + t0 + x * per, 0);
-        }
         int page = a.pages;  // of this lane's box of keys; a.pages: none, whose box is zeros
         auto lookup = [&](int j) {
           if (!a.page || lane >= boxes) return;
@@ -418,6 +442,12 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
       if (leader) umma_commit(mma_done);
       __syncwarp();
       mbar_wait(mma_done, 0, status, kErrTimeoutDrain);
+    } else if (warp == 10 && lane == 0) {
+      for (int x = 0; x < 2; ++x)
+        if (whole(x) && mbar_wait(&o_staged[x], 0, status, kErrTimeoutEpilogue))
+          for (int d = 0; d < DP; d += 64)
+            tma_store_4d(&args.o, smem + x * S::kTile + d * C * 2, d, hp * a.pack, s.start + t0 + x * per, 0);
+      bulk_commit_wait_read();
     }
   }
   tc_fence_before();
