@@ -352,9 +352,10 @@ template <int DP>
 pc_status_t launch_bwd_tc_dim(const AttnBwdTcArgs& t, cudaStream_t s) {
   const AttnArgs& a = t.b.a;
   constexpr int smem = AtBwdShape<DP>::kBytes, kLanesRow = DP / 8;
-  const long long rows = (static_cast<long long>(a.T) * a.H * kLanesRow + 255) / 256;
+  const long long at_once = 256 / kLanesRow * kAtRowsAtOnce, rows = (static_cast<long long>(a.T) * a.H + at_once - 1) / at_once;
   const long long keys = tiles_of(a, kAtC) * a.Hk, tiles = tiles_of(a, t.per) * (a.H / a.pack);
-  PC_CHECK(rows < INT_MAX && keys < INT_MAX && tiles < INT_MAX, PC_ERR_SHAPE, "T * H = %lld rows: too many",
+  PC_CHECK(static_cast<long long>(a.T) * a.H < INT_MAX && keys < INT_MAX && tiles < INT_MAX, PC_ERR_SHAPE,
+           "T * H = %lld rows: fewer than 2^31 wanted",
            static_cast<long long>(a.T) * a.H);
   PC_TRY((allow_smem<k_attn_dkdv_tc<DP>>(smem)));
   PC_TRY((allow_smem<k_attn_dq_tc<DP>>(smem)));
@@ -388,6 +389,8 @@ pc_status_t try_bwd_tc(const AttnBwdArgs& from, pc_dtype_t dt, cudaStream_t s, i
   if (!tc_key_map(&t.k, &t.k_ext, a.k, a.D, a.T, a.ks[1], a.Hk, a.ks[2], 1, 8, kAtC, &st)) return PC_OK;
   PC_TRY(st);
   if (!tc_key_map(&t.v, &t.v_ext, a.v, a.D, a.T, a.vs[1], a.Hk, a.vs[2], 1, 8, kAtC, &st)) return PC_OK;
+  PC_TRY(st);
+  if (!tc_row_map(&t.dq, a, from.dq, from.dqs, t.per, &st)) return PC_OK;
   PC_TRY(st);
   PC_TRY(a.D <= 64 ? launch_bwd_tc_dim<64>(t, s) : launch_bwd_tc_dim<128>(t, s));
   *launches += 3;

@@ -12,6 +12,8 @@
 // nothing is added by atomics: S and dP are formed twice (seven products instead of five) for sums of a fixed order.
 // Products of the next tile are issued between those of this one, while the warps form P or dS:
 //   dk, dv:  dV(i) S(i+1) | dK(i) dP(i+1)          dq:  dP(j+1) dQ(j) S(j+2)
+// Whole tiles of dq are staged in the place of Q and leave by TMA (456 -> 433 us; dk and dv, of fewer and longer CTAs, do not:
+// 477 us against 504, with registers spilt).
 // Warps 0-3 take the columns 0 .. 63 of a tile's lanes, warps 4-7 the others; each writes its bf16 operand over columns that
 // it has read itself, so that an operand's second half starts at column 64.
 #pragma once
@@ -23,39 +25,51 @@ namespace pc {
 
 struct AttnBwdTcArgs {
   AttnBwdArgs b;
-  CUtensorMap q, d_o, k, v;
+  CUtensorMap q, d_o, k, v, dq;
   int k_ext, v_ext;
   int per;            // tokens of a tile of rows
   float k2;           // scale log2(e)
   float *lse2, *delta;  // [H / pack][T][pack]: lse log2(e) and delta by rows
 };
 
-// Eight lanes of 16 bytes (D <= 64) or sixteen a row: delta and lse in the order of the tiles' rows.
+// Eight lanes of 16 bytes (D <= 64) or sixteen a row, four rows a thread at a time: delta and lse in the order of the tiles'
+// rows.
+constexpr int kAtRowsAtOnce = 4;
+
 template <int kLanesRow>
 __global__ void __launch_bounds__(256) k_attn_rows_tc(const __grid_constant__ AttnBwdTcArgs args) {
   const AttnArgs& a = args.b.a;
-  const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / kLanesRow;
+  constexpr int kRows = 256 / kLanesRow;
+  const unsigned all = static_cast<unsigned>(a.T) * a.H;
+  const unsigned row0 = blockIdx.x * (kRows * kAtRowsAtOnce) + threadIdx.x / kLanesRow;
   const int d = threadIdx.x % kLanesRow * 8;
-  const bool on = row < static_cast<long long>(a.T) * a.H;
-  const int t = on ? static_cast<int>(row / a.H) : 0, h = on ? static_cast<int>(row % a.H) : 0;
-  float v = 0.f;
-  if (on && d < a.D) {
-    const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + t * a.os[0] + h * a.os[1] + d);
-    const uint4 y =
-        *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(args.b.d_o) + t * args.b.gs[0] + h * args.b.gs[1] + d);
-    const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+  uint4 x[kAtRowsAtOnce], y[kAtRowsAtOnce];
+#pragma unroll
+  for (int e = 0; e < kAtRowsAtOnce; ++e) {
+    const unsigned row = row0 + e * kRows, t = row / a.H, h = row - t * a.H;
+    x[e] = y[e] = make_uint4(0u, 0u, 0u, 0u);
+    if (row < all && d < a.D) {
+      x[e] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + t * a.os[0] + h * a.os[1] + d);
+      y[e] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(args.b.d_o) + t * args.b.gs[0] + h * args.b.gs[1] + d);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < kAtRowsAtOnce; ++e) {
+    const uint32_t xs[4] = {x[e].x, x[e].y, x[e].z, x[e].w}, ys[4] = {y[e].x, y[e].y, y[e].z, y[e].w};
+    float v = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v += __uint_as_float(xs[i] << 16) * __uint_as_float(ys[i] << 16);
       v += __uint_as_float(xs[i] & 0xFFFF0000u) * __uint_as_float(ys[i] & 0xFFFF0000u);
     }
-  }
 #pragma unroll
-  for (int w = kLanesRow / 2; w; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
-  if (on && d == 0) {
-    const long long at = (static_cast<long long>(h / a.pack) * a.T + t) * a.pack + h % a.pack;
-    args.delta[at] = v;
-    args.lse2[at] = args.b.lse[static_cast<long long>(h) * a.T + t] * kLog2e;
+    for (int w = kLanesRow / 2; w; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
+    const unsigned row = row0 + e * kRows, t = row / a.H, h = row - t * a.H;
+    if (row < all && d == 0) {
+      const long long at = (static_cast<long long>(h / a.pack) * a.T + t) * a.pack + h % a.pack;
+      args.delta[at] = v;
+      args.lse2[at] = args.b.lse[static_cast<long long>(h) * a.T + t] * kLog2e;
+    }
   }
 }
 
@@ -172,7 +186,6 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_dkdv_tc(const __grid_con
   if (rows < C && warp >= 4) {  // rows that no copy writes
     for (int slot = warp - 4; slot < S::kSlots; slot += 8) at_zero_rows<DP>(smem_addr(smem) + S::kRing + slot * S::kTile, rows, C);
   }
-  grid_dependency_wait();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -385,44 +398,52 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_dq_tc(const __grid_const
   extern __shared__ __align__(1024) uint8_t smem[];
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
   uint64_t *full = bars, *empty = bars + 8, *q_full = bars + 16, *s_full = bars + 17, *dp_full = bars + 19,
-           *ds_ready = bars + 20, *acc_full = bars + 21, *mma_done = bars + 22;
-  auto* limit = reinterpret_cast<unsigned long long*>(bars + 23);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+           *ds_ready = bars + 20, *acc_full = bars + 21, *mma_done = bars + 22, *staged = bars + 23;
+  auto* limit = reinterpret_cast<unsigned long long*>(bars + 24);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
 
   const AttnArgs& a = args.b.a;
   const int heads = a.H / a.pack, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hp = blockIdx.x % heads, hk = hp * a.pack / a.group, per = args.per;
+  // one warp sets up the barriers, another takes the tensor memory, while all find their work
+  if (warp == 8 && lane == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(&s_full[0], 1);
+    mbar_init(&s_full[1], 1);
+    mbar_init(dp_full, 1);
+    mbar_init(ds_ready, 8);
+    mbar_init(acc_full, 1);
+    mbar_init(staged, 8);
+    mbar_init(mma_done, 1);
+    *limit = first_wait_limit(a.status);
+    fence_barrier_init();
+  }
   AttnSeq s{0, 0, 0};
   const AttnTile tile = attn_tile_by_cost<false>(a, blockIdx.x / heads, per, s);
   if (tile.b < 0) return;
   const int t0 = tile.at * per, keys = min(t0 + per, s.n), steps = (keys + C - 1) / C;
   unsigned* status = a.status;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      for (int i = 0; i < S::kSlots; ++i) {
-        mbar_init(&full[i], 1);
-        mbar_init(&empty[i], 1);
-      }
-      mbar_init(q_full, 1);
-      mbar_init(&s_full[0], 1);
-      mbar_init(&s_full[1], 1);
-      mbar_init(dp_full, 1);
-      mbar_init(ds_ready, 8);
-      mbar_init(acc_full, 1);
-      mbar_init(mma_done, 1);
-      *limit = first_wait_limit(status);
-      fence_barrier_init();
+  if (warp == 0) tmem_alloc(tmem_slot, 512);
+  if (warp == 8 && lane == 0) {  // the resident operands' copies start before the CTA meets
+    mbar_arrive_expect_tx(q_full, 2 * per * a.pack * DP * 2);
+    for (int d = 0; d < DP; d += 64) {
+      tma_load_4d(smem + d * C * 2, &args.q, q_full, d, hp * a.pack, s.start + t0, 0);
+      tma_load_4d(smem + S::kTile + d * C * 2, &args.d_o, q_full, d, hp * a.pack, s.start + t0, 0);
     }
-    __syncwarp();
-    tmem_alloc(tmem_slot, 512);
   }
-  grid_dependency_wait();
+  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t dp_at = tmem + 2 * C, dq_at = tmem + 3 * C;  // S: two in turn
+
+  const bool whole = t0 + per <= s.n;
 
   if (warp < 8) {
     at_regs_up<208>();
@@ -481,18 +502,27 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_dq_tc(const __grid_const
       __nv_bfloat16* row = static_cast<__nv_bfloat16*>(args.b.dq) + (s.start + static_cast<long long>(token)) * args.b.dqs[0] +
                            h * args.b.dqs[1];
 #pragma unroll 1
-      for (int c = part * (DP / 2); c < (part + 1) * (DP / 2); c += 32)
-        at_store_row(dq_at + lanes, c, a.D, a.scale, there, row);
+      for (int c = part * (DP / 2); c < (part + 1) * (DP / 2); c += 32) {
+        if (whole) {
+          float u[32];
+          tmem_ld_32x32(dq_at + lanes + c, u);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) u[i] *= a.scale;
+          at_stage(smem_addr(smem), r, c, u);
+        } else {
+          at_store_row(dq_at + lanes, c, a.D, a.scale, there, row);
+        }
+      }
+      if (whole) {
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(staged);
+      }
     }
   } else {
     at_regs_down<64>();
     if (warp == 8 && lane == 0) {
       // ------------------------------------------------------------ TMA producer: Q, dO, then K, V, K, V, ...
-      mbar_arrive_expect_tx(q_full, 2 * per * a.pack * DP * 2);
-      for (int d = 0; d < DP; d += 64) {
-        tma_load_4d(smem + d * C * 2, &args.q, q_full, d, hp * a.pack, s.start + t0, 0);
-        tma_load_4d(smem + S::kTile + d * C * 2, &args.d_o, q_full, d, hp * a.pack, s.start + t0, 0);
-      }
       int issued = 0;
       for (int n = 0; n < 2 * steps; ++n) {
         const int slot = n % S::kSlots, j = n / 2;
@@ -566,6 +596,10 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_dq_tc(const __grid_const
       if (leader) umma_commit(mma_done);
       __syncwarp();
       mbar_wait(mma_done, 0, status, kErrTimeoutDrain);
+    } else if (warp == 11 && lane == 0 && whole) {
+      if (mbar_wait(staged, 0, status, kErrTimeoutEpilogue))
+        for (int d = 0; d < DP; d += 64) tma_store_4d(&args.dq, smem + d * C * 2, d, hp * a.pack, s.start + t0, 0);
+      bulk_commit_wait_read();
     }
   }
   tc_fence_before();

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
 
   const AttnArgs& a = args.a;
   const int heads = a.H / a.pack, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hp = blockIdx.x % heads, rest = blockIdx.x / heads, split = rest % a.splits;
+  const int hp = blockIdx.x % heads, split = a.splits > 1 ? blockIdx.x / heads % a.splits : 0;
   // one warp sets up the barriers, another takes the tensor memory, while all find their work
   if (warp == 8 && lane == 0) {
     tma_prefetch_map(&args.q);
@@ -140,15 +140,19 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
     fence_barrier_init();
   }
   AttnSeq s{0, 0, 0};
-  const AttnTile tile = attn_tile_by_cost<false>(a, rest / a.splits, 2 * args.per, s);
+  const AttnTile tile = attn_tile_by_cost<false>(a, a.splits > 1 ? blockIdx.x / heads / a.splits : blockIdx.x / heads, 2 * args.per, s);
   if (tile.b < 0) return;
   const int hk = hp * a.pack / a.group, per = args.per, t0 = tile.at * 2 * per;
   int keys[2], first, last[2];  // the tiles of keys [first, last) are this CTA's
   keys[0] = attn_keys(a, s, t0, per);
   keys[1] = attn_keys(a, s, t0 + per, per);
   const int top_keys = max(keys[0], keys[1]), all = (top_keys + C - 1) / C;
-  first = static_cast<int>(static_cast<long long>(all) * split / a.splits);
-  const int end = static_cast<int>(static_cast<long long>(all) * (split + 1) / a.splits);
+  first = 0;
+  int end = all;
+  if (a.splits > 1) {
+    first = static_cast<int>(static_cast<long long>(all) * split / a.splits);
+    end = static_cast<int>(static_cast<long long>(all) * (split + 1) / a.splits);
+  }
 #pragma unroll
   for (int x = 0; x < 2; ++x) last[x] = max(min(end, (keys[x] + C - 1) / C), first);
   const int n_tiles = end - first;
