@@ -550,7 +550,7 @@ PCSUM_API pc_status_t pc_orthogonalize(int batch, int rows, int cols, const void
  *   q_weight, k_weight [dim]      float32
  *   positions [tokens]            int32, any; frequencies [rotary / 2] float32, finite, radians a position
  * Angles are exact to 2^-32 of a turn at any position. An output may be its own input, at the same
- * strides. tokens may be 0. Errors: PC_ERR_UNSUPPORTED (element type, layout, dim above 256), PC_ERR_SHAPE
+ * strides, and may not overlap anything else. tokens may be 0. Errors: PC_ERR_UNSUPPORTED (element type, layout, dim above 256), PC_ERR_SHAPE
  * (rotary odd or above dim, ...), PC_ERR_NULL, PC_ERR_ALIGNMENT. */
 PCSUM_API pc_status_t pc_qk_norm_rotary_fwd(long long tokens, int Hq, int Hk, int dim, int rotary, const void* q,
                                             const void* k, const long long* strides, const float* q_weight,
@@ -637,7 +637,7 @@ PCSUM_API pc_status_t pc_paged_attention(int B, int T, int H, int Hk, int D, int
  *   positions, slots [tokens]     (int32, int64) of the new tokens, packed by request: slot = page * page_size + place in the
  *                                 page, or -1: no page, past the table's width, or behind the last request's tokens
  *   taken [1]                     pages that all requests need, also where that is more than free_pages
- * B up to 16384. Totals of tokens and pages below 2^31. Errors: PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_UNSUPPORTED. */
+ * No output may overlap an input. B up to 16384. Totals of tokens and pages below 2^31. Errors: PC_ERR_SHAPE, PC_ERR_NULL, PC_ERR_UNSUPPORTED. */
 PCSUM_API pc_status_t pc_paged_plan(int B, int width, int page_size, int free_pages, int tokens, const int32_t* cached,
                                     const int32_t* added, const int32_t* free_list, int32_t* tables, int32_t* starts,
                                     int32_t* lengths, int32_t* positions, long long* slots, int32_t* taken,

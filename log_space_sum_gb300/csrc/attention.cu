@@ -317,21 +317,25 @@ pc_status_t run_fwd(AttnArgs& a, pc_dtype_t dt, void* ws, cudaStream_t s) {
                        : launch_simt<float>(a, ws, s, &record.launches);
 }
 
-template <class T, int DP>
-pc_status_t launch_simt_bwd_dim(const AttnBwdArgs& b, cudaStream_t s) {
+template <class T, int DP, int BT>
+pc_status_t launch_simt_bwd_tile(const AttnBwdArgs& b, cudaStream_t s) {
   const AttnArgs& a = b.a;
-  constexpr int BT = simt_bt(DP);
   using S = SimtTile<DP, BT>;
-  constexpr int smem = (4 * S::kRows + 2 * S::kScores) * 4, smem_dq = (4 * S::kRows + S::kScores) * 4;
-  const long long keys = tiles_of(a, BT), rows = tiles_of(a, BT / a.pack);
-  PC_CHECK(keys < INT_MAX && rows < INT_MAX, PC_ERR_SHAPE, "%lld tiles of rows: fewer than 2^31 wanted", rows);
-  PC_TRY((allow_smem<k_attn_simt_dkdv<T, DP, BT>>(smem)));
-  PC_TRY((allow_smem<k_attn_simt_dq<T, DP, BT>>(smem_dq)));
-  k_attn_simt_dkdv<T, DP, BT><<<dim3(static_cast<unsigned>(keys), a.Hk), kSimtThreads, smem, s>>>(b);
-  PC_LAUNCH_CHECK();
-  k_attn_simt_dq<T, DP, BT><<<dim3(static_cast<unsigned>(rows), a.H / a.pack), kSimtThreads, smem_dq, s>>>(b);
+  constexpr int smem = (4 * S::kRows + 2 * S::kScores) * 4;
+  const long long keys = tiles_of(a, BT) * a.Hk, rows = tiles_of(a, BT / a.pack) * (a.H / a.pack);
+  PC_CHECK(keys + rows < INT_MAX, PC_ERR_SHAPE, "%lld tiles of rows: fewer than 2^31 wanted", keys + rows);
+  PC_TRY((allow_smem<k_attn_simt_bwd<T, DP, BT>>(smem)));
+  k_attn_simt_bwd<T, DP, BT><<<static_cast<unsigned>(keys + rows), kSimtThreads, smem, s>>>(b, static_cast<int>(keys));
   PC_LAUNCH_CHECK();
   return PC_OK;
+}
+
+// Tiles of 32 where those of 64 would leave half of the SMs without a CTA (XX -> XX us for 3 sequences to 333).
+template <class T, int DP>
+pc_status_t launch_simt_bwd_dim(const AttnBwdArgs& b, cudaStream_t s) {
+  constexpr int BT = simt_bt(DP);
+  if (BT > 32 && tiles_of(b.a, BT) * b.a.Hk < num_sms()) return launch_simt_bwd_tile<T, DP, 32>(b, s);
+  return launch_simt_bwd_tile<T, DP, BT>(b, s);
 }
 
 template <class T>
@@ -341,7 +345,7 @@ pc_status_t launch_bwd(const AttnBwdArgs& b, cudaStream_t s, int* launches) {
   PC_CHECK(ctas < INT_MAX, PC_ERR_SHAPE, "T * H = %lld rows: fewer than 2^34 wanted", static_cast<long long>(a.T) * a.H);
   k_attn_delta<T><<<static_cast<unsigned>(ctas), 256, 0, s>>>(b);
   PC_LAUNCH_CHECK();
-  *launches += 3;
+  *launches += 2;
   const int dp = simt_dim(a.D);
   return dp == 64    ? launch_simt_bwd_dim<T, 64>(b, s)
          : dp == 128 ? launch_simt_bwd_dim<T, 128>(b, s)

@@ -68,11 +68,15 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, int tile, int p
     return {tile / each, tile % each};
   }
   int base = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const int b = b0 + lane;
-    int n = 0;
-    if (b < a.B) n = (attn_seq(a, b).n + per - 1) / per;
-    int sum = n;
+  for (int b0 = 0; b0 < a.B; b0 += 128) {  // four sequences a lane
+    int n[4], own = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = b0 + lane * 4 + i;
+      n[i] = b < a.B ? (attn_seq(a, b).n + per - 1) / per : 0;
+      own += n[i];
+    }
+    int sum = own;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, sum, d);
@@ -81,7 +85,14 @@ __device__ __forceinline__ AttnTile attn_tile(const AttnArgs& a, int tile, int p
     const unsigned here = __ballot_sync(0xffffffffu, base + sum > tile);
     if (here) {
       const int l = __ffs(here) - 1;
-      return {b0 + l, tile - base - __shfl_sync(0xffffffffu, sum - n, l)};
+      int left = tile - base - (sum - own), at = 0;  // (of lane l)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (at == i && left >= n[i]) {
+          left -= n[i];
+          ++at;
+        }
+      return {b0 + l * 4 + __shfl_sync(0xffffffffu, at, l), __shfl_sync(0xffffffffu, left, l)};
     }
     base += __shfl_sync(0xffffffffu, sum, 31);
   }

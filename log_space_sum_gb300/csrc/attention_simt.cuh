@@ -302,14 +302,14 @@ __device__ __forceinline__ void simt_ds(const float* Q, const float* K, const fl
 
 // dk and dv of one tile of keys: all rows of the group's heads from its first token on.
 template <class T, int DP, int BT>
-__global__ void __launch_bounds__(kSimtThreads) k_attn_simt_dkdv(const __grid_constant__ AttnBwdArgs b) {
+__device__ __forceinline__ void simt_dkdv(const AttnBwdArgs& b, int rank, int hk) {
   using S = SimtTile<DP, BT>;
   constexpr int M = S::M;
   const AttnArgs& a = b.a;
   extern __shared__ float simt_smem[];
   float *Q = simt_smem, *G = Q + S::kRows, *K = G + S::kRows, *V = K + S::kRows, *P = V + S::kRows, *D = P + S::kScores;
-  const int per = BT / a.pack, hk = blockIdx.y;
-  const AttnTile tile = attn_tile(a, blockIdx.x, BT);
+  const int per = BT / a.pack;
+  const AttnTile tile = attn_tile(a, rank, BT);
   if (tile.b < 0) return;
   const AttnSeq s = attn_seq(a, tile.b);
   const int ty = threadIdx.x >> 4, j0 = tile.at * BT;
@@ -368,14 +368,14 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_simt_dkdv(const __grid_co
 
 // dq of one tile of rows.
 template <class T, int DP, int BT>
-__global__ void __launch_bounds__(kSimtThreads) k_attn_simt_dq(const __grid_constant__ AttnBwdArgs b) {
+__device__ __forceinline__ void simt_dq(const AttnBwdArgs& b, int rank, int hp) {
   using S = SimtTile<DP, BT>;
   constexpr int M = S::M;
   const AttnArgs& a = b.a;
   extern __shared__ float simt_smem[];
   float *Q = simt_smem, *G = Q + S::kRows, *K = G + S::kRows, *V = K + S::kRows, *D = V + S::kRows;
-  const int per = BT / a.pack, hp = blockIdx.y, hk = hp * a.pack / a.group;
-  const AttnTile tile = attn_tile(a, blockIdx.x, per);
+  const int per = BT / a.pack, hk = hp * a.pack / a.group;
+  const AttnTile tile = attn_tile(a, rank, per);
   if (tile.b < 0) return;
   const AttnSeq s = attn_seq(a, tile.b);
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15, t0 = tile.at * per;
@@ -423,6 +423,18 @@ __global__ void __launch_bounds__(kSimtThreads) k_attn_simt_dq(const __grid_cons
     if (there(r))
       simt_store<T, DP>(static_cast<T*>(b.dq) + (s.start + t0 + r / a.pack) * b.dqs[0] + head(r) * b.dqs[1], a.D, dq[i],
                         a.scale);
+  }
+}
+
+// Both in one launch, so that they fill the GPU together: the first key_ctas CTAs the tiles of keys, the others those of rows.
+template <class T, int DP, int BT>
+__global__ void __launch_bounds__(kSimtThreads) k_attn_simt_bwd(const __grid_constant__ AttnBwdArgs b, int key_ctas) {
+  const int cta = blockIdx.x;
+  if (cta < key_ctas) {
+    simt_dkdv<T, DP, BT>(b, cta / b.a.Hk, cta % b.a.Hk);
+  } else {
+    const int heads = b.a.H / b.a.pack;
+    simt_dq<T, DP, BT>(b, (cta - key_ctas) / heads, (cta - key_ctas) % heads);
   }
 }
 

@@ -192,6 +192,9 @@ pc_status_t pc_paged_plan(int B, int width, int page_size, int free_pages, int t
   PC_CHECK(B == 0 || width == 0 || tables, PC_ERR_NULL, "tables must not be NULL");
   PC_CHECK(free_pages == 0 || free_list, PC_ERR_NULL, "free must not be NULL");
   PC_CHECK(tokens == 0 || (positions && slots), PC_ERR_NULL, "positions and slots must not be NULL");
+  const void *in[3] = {cached, added, free_list}, *out[6] = {tables, starts, lengths, positions, slots, taken};
+  for (const void* o : out)
+    for (const void* i : in) PC_CHECK(!o || o != i, PC_ERR_UNSUPPORTED, "an output may not be an input itself");
   pc::PlanArgs a{B, width, page_size, free_pages, tokens, cached, added, free_list, tables, starts, lengths, positions,
                  taken, slots};
   PC_TRY(pc::allow_smem<pc::k_paged_plan>(pc::kMaxRequests * 2 * static_cast<int>(sizeof(int))));

@@ -551,7 +551,8 @@ pc_status_t pc_qk_norm_rotary_fwd(long long tokens, int Hq, int Hk, int dim, int
   PC_CHECK(strides, PC_ERR_NULL, "strides must not be NULL");
   if (Hq) PC_TRY(pc::check_side("q", q, "q_out", q_out, strides, strides + 4, tokens, Hq, dtype));
   if (Hk) PC_TRY(pc::check_side("k", k, "k_out", k_out, strides + 2, strides + 6, tokens, Hk, dtype));
-  PC_CHECK(!Hq || !Hk || q_out != k_out, PC_ERR_UNSUPPORTED, "q_out may not be k_out itself");
+  PC_CHECK(!Hq || !Hk || (q_out != k_out && q_out != k && k_out != q), PC_ERR_UNSUPPORTED,
+           "an output may be its own input, not the other's or the other output");
   pc::RotArgs a{};
   const void* x[2] = {q, k};
   void* y[2] = {q_out, k_out};
@@ -598,7 +599,8 @@ pc_status_t pc_qk_norm_rotary_bwd(long long tokens, int Hq, int Hk, int dim, int
   PC_TRY(pc::check_rot(tokens, Hq, Hk, dim, rotary, layout, positions, frequencies, eps, amplitude, dtype));
   if (tokens > 0) {
     PC_CHECK(strides, PC_ERR_NULL, "strides must not be NULL");
-    PC_CHECK(!Hq || !Hk || dq != dk, PC_ERR_UNSUPPORTED, "dq may not be dk itself");
+    PC_CHECK(!Hq || !Hk || (dq != dk && dq != dk_out && dk != dq_out && (!norm || (dq != k && dk != q))), PC_ERR_UNSUPPORTED,
+             "a gradient may lie where its own input does, not where the other's do or the other gradient");
     if (Hq) PC_TRY(pc::check_side("dq_out", dq_out, "dq", dq, strides, strides + 8, tokens, Hq, dtype));
     if (Hk) PC_TRY(pc::check_side("dk_out", dk_out, "dk", dk, strides + 2, strides + 10, tokens, Hk, dtype));
     if (norm) {

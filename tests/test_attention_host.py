@@ -52,6 +52,7 @@ def test_qk_norm_rotary_fwd(lib):
     assert call(a13=float("nan")) == "PC_ERR_SHAPE"
     assert call(a16=P[0], a7=_replace(st, 4, 1024)) == "PC_ERR_SHAPE" and b"other strides" in lib.pc_last_error()
     assert call(a17=P[4]) == "PC_ERR_UNSUPPORTED"
+    assert call(a17=P[0]) == "PC_ERR_UNSUPPORTED" and call(a16=P[1]) == "PC_ERR_UNSUPPORTED"
     for i in range(4, 8):
         assert call(a7=_replace(st, i, 0)) == "PC_ERR_SHAPE" and b"stride 0" in lib.pc_last_error()
     assert call(a0=0, a5=None) == "PC_OK"
@@ -73,6 +74,9 @@ def test_qk_norm_rotary_bwd(lib):
     assert call(a18=P[2], a9=_replace(st, 8, 1024)) == "PC_ERR_SHAPE"
     assert call(a18=P[0], a9=_replace(st, 9, 128)) == "PC_ERR_SHAPE"
     assert call(a19=P[6]) == "PC_ERR_UNSUPPORTED"
+    for i in (18, 19):
+        for j in ((1, 3) if i == 18 else (0, 2)):
+            assert call(**{f"a{i}": P[j]}) == "PC_ERR_UNSUPPORTED", (i, j)
 
 
 def test_attention_fwd(lib):
@@ -148,6 +152,8 @@ def test_paged_plan_and_write(lib):
     for i in (0, 1, 3, 4):
         assert call(**{f"a{i}": -1}) == "PC_ERR_SHAPE", i
     assert call(a2=0) == "PC_ERR_SHAPE" and call(a0=16385) == "PC_ERR_UNSUPPORTED"
+    for i in range(8, 14):
+        assert call(**{f"a{i}": P[0]}) == "PC_ERR_UNSUPPORTED", i
     st = [128, 64, 128, 64, 2048, 128, 64, 2048, 128, 64]
     call = _caller(lib.pc_paged_write, [10, 2, 64, 7, 16, P[0], P[1], _ll(*st), P[2], P[3], P[4], 1, None])
     for i in (5, 6, 7, 8, 9, 10):
