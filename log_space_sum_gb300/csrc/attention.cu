@@ -8,6 +8,9 @@
 // stored. The gradient forms the probabilities again from lse, in two kernels (dk and dv by tiles of keys,
 // dq by tiles of rows): seven products instead of five, but no sum is left to atomics, whose order
 // would change the bits, and the heads of a group add up in the tile of their keys.
+//
+// Variants: bf16 on the tensor cores (attention_tc.cuh, attention_bwd_tc.cuh: head sizes of whole 16-byte pieces up to 128); few new
+// tokens over a cache by streaming warps (attention_step.cuh); everything else on the CUDA cores (attention_simt.cuh).
 #include <cfloat>
 #include <climits>
 
@@ -243,7 +246,8 @@ pc_status_t try_tc(const AttnArgs& from, pc_dtype_t dt, void* ws, cudaStream_t s
 // Rows of a sequence's unit: 16, or 32 where the sequences' tokens fill more.
 int step_rows(const AttnArgs& a) { return static_cast<long long>(a.T) * a.pack <= 16ll * a.B ? 16 : 32; }
 
-// Where a sequence's rows fill no more than that the cache's bandwidth decides, and tiles of 128 rows would stand empty.
+// Where a sequence's rows fill no more than that the cache's bandwidth decides, and tiles of 128 rows would stand empty (64
+// sequences to 8192, 4 rows each: 205 us against 356 on the tensor cores; the loads there wait for a chain of 128 keys).
 bool step_sizes(const AttnArgs& a, pc_dtype_t dt) {
   return dt == PC_BF16 && a.page && a.page % kStKeys == 0 && a.pages > 0 && a.D % 8 == 0 && a.D <= 128 &&
          static_cast<long long>(a.T) * a.pack <= 32ll * a.B;
@@ -330,7 +334,7 @@ pc_status_t launch_simt_bwd_tile(const AttnBwdArgs& b, cudaStream_t s) {
   return PC_OK;
 }
 
-// Tiles of 32 where those of 64 would leave half of the SMs without a CTA (XX -> XX us for 3 sequences to 333).
+// Tiles of 32 where those of 64 would leave half of the SMs without a CTA (236 -> 205 us for 3 sequences to 333, two launches then).
 template <class T, int DP>
 pc_status_t launch_simt_bwd_dim(const AttnBwdArgs& b, cudaStream_t s) {
   constexpr int BT = simt_bt(DP);

@@ -7,14 +7,16 @@
 //   backward  g = the pairs of dy turned back,  dw = sum over rows of g z,
 //             h = g w,  dx = rstd (h - z avg(h z))
 //
-// Memory-bound: a row (one head of one token) is read once and written once. A row lies in the
-// registers of L = 1 .. 32 lanes, two pieces of V elements a lane: V pairs, whether a pair lies
-// side by side or half a rotation apart, so that no element changes lanes. Angles are reduced in
-// fixed point: f_i / 2 pi as a 64-bit fraction of a turn, whose product with the position wraps to
-// the turn's fraction by itself, exact to 2^-32 of a turn at any int32 position (a float32 angle
-// is off by 0.004 radians at position 131072). They are formed once for all the heads of a token that
-// a warp takes. Norms, sums, rotations and the weights' gradients are float32; the only rounding to
-// bf16 is that of y and dx.
+// Memory-bound: a row (one head of one token) is read once and written once. A row lies in the registers of L = 1 .. 32 lanes,
+// two pieces of V elements a lane: V pairs, whether a pair lies side by side or half a rotation apart, so that no element
+// changes lanes. Angles are reduced in fixed point: f_i / 2 pi as a 64-bit fraction of a turn, whose product with the position
+// wraps to the turn's fraction by itself, exact to 2^-32 of a turn at any int32 position (a float32 angle is off by 0.004
+// radians at position 131072). They are formed once for all the heads of a token that a warp takes. Norms, sums, rotations and the
+// weights' gradients are float32; the only rounding to bf16 is that of y and dx.
+//
+// Measured, bf16, heads of 128: 32768 tokens of 16 + 2 heads 75 us (4.0 TB/s), the gradient of 16384 78 us (2.9 TB/s), bound by
+// issue slots and the latency of a group's chain (loads, sum over lanes, root, products), with as many warps as the registers let
+// stay: 24 an SM forward, 16 in the gradient. 64 tokens of 32 + 8 heads 8 us.
 #include <climits>
 
 #include "pc_device.cuh"

@@ -176,6 +176,32 @@ def test_what_is_not_finite_stays_with_the_rows_that_see_it(dtype):
     assert torch.isfinite(o[:at - 127]).all() and not torch.isfinite(o[at:]).any()
 
 
+def test_a_layer_of_them_by_differences():
+    """Norms with rotation, attention and back, float32: the gradients' products with a direction are the loss's
+    differences along it (in float64; the kernels' own error is 1e-5 of the sums' magnitudes)."""
+    T, H, Hk, D, starts = 150, 4, 2, 40, [0, 90, 150]
+    q, k, v, do = _draw(T, H, Hk, D, "fp32", 20)
+    w = [1 + 0.2 * torch.randn(D, device="cuda") for _ in range(2)]
+    pos, (f, _), dev = torch.arange(T, device="cuda", dtype=torch.int32) * 3, pc.rotary_frequencies(24), _int(starts)
+    qr, kr = pc.qk_norm_rotary_fwd(q, k, pos, f, *w)
+    o, lse = pc.attention_fwd(qr, kr, v, starts=dev)
+    back = pc.attention_bwd(qr, kr, v, o, lse, do, starts=dev)
+    first = pc.qk_norm_rotary_bwd(back["dq"], back["dk"], q, k, pos, f, *w)
+    got = [first["dq"], first["dk"], back["dv"], first["dq_weight"], first["dk_weight"]]
+    P, F, G = _np(pos), _np(f), _np(do)
+
+    def loss(q, k, v, wq, wk):
+        qr, kr = A.norm_rotary_fwd(q, P, F, wq), A.norm_rotary_fwd(k, P, F, wk)
+        return (G * A.packed_fwd(qr, kr, v, starts, D ** -0.5)[0]).sum()
+
+    at, rng = [_np(t) for t in (q, k, v, *w)], np.random.default_rng(1)
+    for i, g in enumerate(got):
+        d, step = rng.normal(size=at[i].shape), 1e-5
+        plus, minus = ([x + sign * step * d if j == i else x for j, x in enumerate(at)] for sign in (1, -1))
+        want = (loss(*plus) - loss(*minus)) / (2 * step)
+        assert abs((_np(g) * d).sum() - want) <= 1e-5 * np.abs(_np(g) * d).sum() + 1e-6 * abs(want), i
+
+
 def test_repeats_streams_and_wide_offsets():
     q, k, v, do = _draw(900, 8, 2, 128, "bf16", 16)
     starts = _int([0, 500, 900])
