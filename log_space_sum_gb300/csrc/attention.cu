@@ -247,7 +247,7 @@ pc_status_t try_tc(const AttnArgs& from, pc_dtype_t dt, void* ws, cudaStream_t s
 int step_rows(const AttnArgs& a) { return static_cast<long long>(a.T) * a.pack <= 16ll * a.B ? 16 : 32; }
 
 // Where a sequence's rows fill no more than that the cache's bandwidth decides, and tiles of 128 rows would stand empty (64
-// sequences to 8192, 4 rows each: 205 us against 356 on the tensor cores; the loads there wait for a chain of 128 keys).
+// sequences to 8192, 4 rows each: 213 us against 279 in tiles of 128 rows cut into the same even ranges).
 bool step_sizes(const AttnArgs& a, pc_dtype_t dt) {
   return dt == PC_BF16 && a.page && a.page % kStKeys == 0 && a.pages > 0 && a.D % 8 == 0 && a.D <= 128 &&
          static_cast<long long>(a.T) * a.pack <= 32ll * a.B;

@@ -14,8 +14,8 @@
 //   dk, dv:  dV(i) S(i+1) | dK(i) dP(i+1)          dq:  dP(j+1) dQ(j) S(j+2)
 // Whole tiles of dq are staged in the place of Q and leave by TMA (456 -> 433 us; dk and dv, of fewer and longer CTAs, do not:
 // 477 us against 504, with registers spilt).
-// Measured: 12 sequences to 4096 (27,873 tokens), 16 / 2 heads of 128, 975 us: dk and dv 480 (tensor pipe 62% busy; without the warps'
-// arithmetic 423), dq 435 (50%; 414, of which about 130 are the starts and ends of 3508 CTAs), delta 51. Not kept: four warpgroups of 32
+// Measured: 12 sequences to 4096 (27,873 tokens), 16 / 2 heads of 128, 975 us; under the profiler dk and dv 488 (tensor pipe 62%
+// busy; without the warps' arithmetic 423), dq 440 (50%, 3508 CTAs; 413), delta 53. Not kept: four warpgroups of 32
 // columns each (1035 us in all), streamed tiles shared by two CTAs through multicast (1119: the pair's lockstep costs more than the
 // L2 reads that it saves).
 // Warps 0-3 take the columns 0 .. 63 of a tile's lanes, warps 4-7 the others; each writes its bf16 operand over columns that

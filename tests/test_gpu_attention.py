@@ -96,6 +96,16 @@ def test_packed_lengths(lengths, H, Hk, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("B", [128, 129, 300])
+@pytest.mark.parametrize("H,Hk,D", [(4, 1, 128), (2, 2, 40)])
+def test_many_sequences(B, H, Hk, D, dtype):
+    rng = np.random.default_rng(B)
+    lengths = rng.integers(0, 9, B) * (rng.random(B) < 0.8)
+    lengths[[5, B // 2, B - 1]] = 200, 131, 257
+    check(*_draw(int(lengths.sum()), H, Hk, D, dtype, B), lengths.tolist(), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("D", [64, 128, 36])
 def test_sequences_do_not_see_one_another_nor_what_lies_behind(dtype, D):
     lengths, T = [130, 61, 257], 500

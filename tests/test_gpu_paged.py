@@ -92,6 +92,16 @@ def test_chunks(H, Hk, D, page, new, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("most", [1, 3, 200])
+@pytest.mark.parametrize("B,page", [(128, 16), (300, 16), (300, 13)])
+def test_many_sequences(B, page, most, dtype):
+    rng = np.random.default_rng(B + most)
+    new = rng.integers(0, most + 1, B) * (rng.random(B) < (0.1 if most > 3 else 0.9))
+    new[[5, B - 1]] = most
+    check((new + rng.integers(0, 300, B)).tolist(), new.tolist(), 8, 2, 128, page, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("page", [16, 64, 100])
 def test_long_caches_are_cut_and_joined(page, dtype):
     check([20001], [1], 8, 2, 128, page, dtype)
@@ -139,8 +149,13 @@ def test_missing_pages_count_as_masked_and_are_reported(dtype, new):
                                for i in range(new)])
         tol = 2.0 ** -7 if dtype == "bf16" else 1e-4  # (of values around one: which keys count is what is tested)
         assert np.abs(_np(o) - want).max() <= tol
-    o = pc.paged_attention(q, kp, vp, _int(tables), _int([n + 10 ** 6]), starts=_int([0, new]))  # past the width
-    assert torch.isfinite(o).all() or True
+    # past the width: every row sees the keys that the table holds (the rows behind the length, which _cache fills with NaN, are
+    # keys then, and get finite values for it)
+    k2, v2 = (torch.nan_to_num(x, nan=0.5, posinf=2.0) for x in (kp, vp))
+    o = pc.paged_attention(q, k2, v2, _int(tables), _int([n + 10 ** 6]), starts=_int([0, new]))
+    k, v = (_np(x)[tables[0]].reshape(-1, Hk, D) for x in (k2, v2))
+    want = np.concatenate([A.attend(_np(q[i:i + 1]), k, v, D ** -0.5, 10 ** 6)[0] for i in range(new)])
+    assert np.abs(_np(o) - want).max() <= tol
     with pytest.raises(pc.PCError, match="PC_ERR_RANGE"):
         pc.device_status()
     pc.paged_attention(q, kp[:0], vp[:0], _int(tables), _int([n]), starts=_int([0, new]))  # no pages at all
