@@ -745,6 +745,10 @@ def qk_norm_rotary_bwd(dq_out, dk_out, q, k, positions=None, frequencies=None, q
     return dict(dq=dq, dk=dk, dq_weight=dq_weight, dk_weight=dk_weight)
 
 
+def _scale(scale, D):
+    return (max(D, 1) ** -0.5) if scale is None else scale  # (the library refuses heads of no features)
+
+
 def _packed_inputs(q, k, v, starts, scale):
     _heads(q, "q")
     dev, dt = q.device, q.dtype
@@ -759,7 +763,7 @@ def _packed_inputs(q, k, v, starts, scale):
         if starts.dim() != 1 or starts.shape[0] < 1:
             raise ValueError("starts must have one dimension and one element at least")
         B = starts.shape[0] - 1
-    return dev, dt, B, T, H, k.shape[1], D, (D ** -0.5 if scale is None and D else scale)
+    return dev, dt, B, T, H, k.shape[1], D, _scale(scale, D)
 
 
 def attention_fwd(q, k, v, starts=None, scale=None, out=None, lse=None):
@@ -829,7 +833,7 @@ def paged_attention(q, k_pages, v_pages, tables, lengths, starts=None, scale=Non
     code, W = DTYPES[dt], tables.shape[1]
     ws = workspace(_query("pc_paged_attention_workspace", B, T, H, Hk, D, P, page, W, code), dev)
     _on(dev, "pc_paged_attention", B, T, H, Hk, D, P, page, W, _ptr(q), _ptr(k_pages), _ptr(v_pages),
-        _strides(q, k_pages, v_pages, out), _ptr(tables), _ptr(lengths), _ptr(starts), D ** -0.5 if scale is None else scale,
+        _strides(q, k_pages, v_pages, out), _ptr(tables), _ptr(lengths), _ptr(starts), _scale(scale, D),
         _ptr(out), _ptr(lse), code, _ptr(ws), ws.numel())
     return out
 

@@ -358,3 +358,11 @@ def test_empty_and_refusals():
         pc.paged_plan(n, n, t, n, 0, 2)
     with pytest.raises(TypeError, match="slots must be torch.int64"):
         pc.paged_write(kp[0], vp[0], kp, vp, n)
+
+
+def test_heads_without_features_are_refused():
+    x, t, n = torch.zeros(2, 1, 0, device="cuda"), _int([[0], [0]]), _int([1, 1])
+    with pytest.raises(pc.PCError, match="head size must be >= 1"):
+        pc.attention_fwd(x, x, x)
+    with pytest.raises(pc.PCError, match="head size must be >= 1"):
+        pc.paged_attention(x, x[:, None], x[:, None], t, n)
