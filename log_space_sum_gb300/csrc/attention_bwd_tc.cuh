@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_dkdv_tc(const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.x % a.Hk, per = args.per, rows = per * a.pack;
   AttnSeq s{0, 0, 0};
-  const AttnTile tile = attn_tile_by_cost<true>(a, blockIdx.x / a.Hk, C, s);
+  const AttnTile tile = attn_tile_by_cost<true, false>(a, blockIdx.x / a.Hk, C, s);
   if (tile.b < 0) return;
   const int j0 = tile.at * C;
   // rows of the tokens from the tile's first key on, for each `pack` heads of the group in turn
@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_dq_tc(const __grid_const
     fence_barrier_init();
   }
   AttnSeq s{0, 0, 0};
-  const AttnTile tile = attn_tile_by_cost<false>(a, blockIdx.x / heads, per, s);
+  const AttnTile tile = attn_tile_by_cost<false, false>(a, blockIdx.x / heads, per, s);
   if (tile.b < 0) return;
   const int t0 = tile.at * per, keys = min(t0 + per, s.n), steps = (keys + C - 1) / C;
   unsigned* status = a.status;

@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kAtThreads, 1) k_attn_tc(const __grid_constant
     fence_barrier_init();
   }
   AttnSeq s{0, 0, 0};
-  const AttnTile tile = attn_tile_by_cost<false>(a, a.splits > 1 ? blockIdx.x / heads / a.splits : blockIdx.x / heads, 2 * args.per, s);
+  const int rank = a.splits > 1 ? blockIdx.x / heads / a.splits : blockIdx.x / heads;
+  const AttnTile tile = a.page ? attn_tile_by_cost<false, true>(a, rank, 2 * args.per, s) : attn_tile_by_cost<false, false>(a, rank, 2 * args.per, s);
   if (tile.b < 0) return;
   const int hk = hp * a.pack / a.group, per = args.per, t0 = tile.at * 2 * per;
   int keys[2], first, last[2];  // the tiles of keys [first, last) are this CTA's
